@@ -20,7 +20,12 @@ Python face of liblinattn (C ABI in include/linattn.h).  The method
 * ``forward_token_decay`` / ``decode_step_token_decay`` — the causal form with
   a decay a_i and input weight b_i per token ("Efficient Transformers II"
   eq (4) with a, b indexed by the token): μ_i = a_i μ_{i−1} + b_i k'_iᵀv_i;
-* ``backward`` — ∂L/∂q, ∂L/∂k, ∂L/∂v and ∂L/∂a of the causal forward.
+* ``backward`` — ∂L/∂q, ∂L/∂k, ∂L/∂v and ∂L/∂a of the causal forward;
+* ``linear``, ``causal_conv`` / ``causal_conv_step``, ``selective_scan`` /
+  ``selective_step`` — the operators of a selective state-space block: a
+  projection with bias, activation and residual, the short depthwise causal
+  convolution and the recurrence with a decay per token, channel and state,
+  over a prompt and for one token.
 
 All work runs in the library's CUDA kernels; PyTorch only allocates device
 memory and provides the stream.
@@ -31,6 +36,7 @@ from ._binding import (EXPORTED, LinAttnError, backward, debug_build, decode_ste
                        last_device_status, launch_count, library_path, load,
                        selftest_device_check, selftest_wait_timeout, shard_entering_state,
                        status_string)
+from ._block import (causal_conv, causal_conv_step, linear, selective_scan, selective_step)
 from .build import build
 
 __all__ = ["forward", "forward_host", "forward_with_state", "forward_from_state", "forward_state",
@@ -38,4 +44,5 @@ __all__ = ["forward", "forward_host", "forward_with_state", "forward_from_state"
            "decode_step_token_decay", "last_device_status", "status_string",
            "LinAttnError", "build", "load", "library_path", "launch_count",
            "selftest_wait_timeout", "debug_build", "last_device_check", "selftest_device_check",
+           "linear", "causal_conv", "causal_conv_step", "selective_scan", "selective_step",
            "EXPORTED"]

@@ -36,7 +36,8 @@ EXPORTED = ("la_forward", "la_forward_with_state", "la_decode_step", "la_status_
             "la_decode_step_fm", "la_forward_token_decay", "la_decode_step_token_decay",
             "la_backward", "la_forward_from_state", "la_forward_state", "la_shard_entering_state",
             "la_forward_host", "la_debug_build", "la_get_last_device_check",
-            "la_selftest_device_check")
+            "la_selftest_device_check", "la_linear", "la_causal_conv", "la_causal_conv_step",
+            "la_selective_scan", "la_selective_step")
 
 
 class LinAttnError(RuntimeError):

@@ -50,14 +50,10 @@ __device__ int g_device_status[2];
 
 constexpr int kMaxDevices = 64;
 
-struct DeviceInfo {
-  bool ready = false;
-  int num_sms = 0;
-  int* status = nullptr;  // device address of g_device_status[0]
-};
-
 std::mutex g_mu;
 DeviceInfo g_dev[kMaxDevices];
+
+}  // namespace
 
 la_status device_info(DeviceInfo* out) {
   int dev = 0;
@@ -78,12 +74,14 @@ la_status device_info(DeviceInfo* out) {
   return LA_OK;
 }
 
+namespace {
 // Workspace memory: stream-ordered allocations from one pool per device owned
 // by the library.  The pool keeps what it has reserved (unlimited release
 // threshold), so repeated calls reuse the same device memory instead of
 // mapping and unmapping it at every synchronisation; the reservation is the
 // largest workspace that calls had in flight at once, held until exit.
 cudaMemPool_t g_pool[kMaxDevices] = {};
+}  // namespace
 
 cudaError_t ws_alloc(void** p, size_t bytes, cudaStream_t s) {
   int dev = 0;
@@ -111,6 +109,8 @@ cudaError_t ws_alloc(void** p, size_t bytes, cudaStream_t s) {
   }
   return cudaMallocFromPoolAsync(p, bytes, pool, s);
 }
+
+namespace {
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
@@ -206,11 +206,15 @@ SegmentPlan plan_segments(int64_t BH, int64_t n, int num_sms, int64_t granule,
   return p;
 }
 
+}  // namespace
+
 la_status to_status(cudaError_t e) {
   if (e == cudaSuccess) return LA_OK;
   if (e == cudaErrorMemoryAllocation) return LA_ERR_OUT_OF_MEMORY;
   return LA_ERR_CUDA;
 }
+
+namespace {
 
 // Kernel family for a validated request and its segment plan: the tcgen05
 // path for what it supports, the fp32 CUDA-core path otherwise.

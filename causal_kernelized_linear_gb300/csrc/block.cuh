@@ -1,0 +1,116 @@
+// Device helpers of the state-space block's kernels: activations, vector
+// loads of 16 bytes as fp32, packed fp32 pairs.
+#pragma once
+
+#include "common.cuh"
+#include "linattn.h"
+#include "tc.cuh"
+
+namespace la {
+namespace block {
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+__device__ __forceinline__ float rcp_f32(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+// x/(1 + e^{−x}) with the hardware's 2^x and 1/x (2 and 1 ulp): about 2e-7
+// relative, against a rounding of 2^-24 (fp32) or 2^-8 (bf16) of the result.
+__device__ __forceinline__ float silu(float x) {
+  return x * rcp_f32(1.f + tc::ex2_f32(-kLog2e * x));
+}
+
+// log(1 + e^x) = max(x, 0) + log1p(e), e = e^{−|x|} ∈ (0, 1].  With
+// s = e/(2 + e) ≤ 1/3, log1p(e) = 2·atanh(s) = 2s·Σ s^{2k}/(2k + 1); nine terms
+// leave (1/9)^9/19 = 1.4e-10 relative.  Relative accuracy matters where x is
+// far below zero (steps of 1e-3): log2(1 + e) would round 1 + e first.
+__device__ __forceinline__ float softplus(float x) {
+  const float e = tc::ex2_f32(-kLog2e * fabsf(x));
+  const float s = e * rcp_f32(2.f + e);
+  const float q = s * s;
+  float p = 1.f / 17.f;
+  p = fmaf(p, q, 1.f / 15.f);
+  p = fmaf(p, q, 1.f / 13.f);
+  p = fmaf(p, q, 1.f / 11.f);
+  p = fmaf(p, q, 1.f / 9.f);
+  p = fmaf(p, q, 1.f / 7.f);
+  p = fmaf(p, q, 1.f / 5.f);
+  p = fmaf(p, q, 1.f / 3.f);
+  p = fmaf(p, q, 1.f);
+  return fmaxf(x, 0.f) + 2.f * s * p;
+}
+
+__device__ __forceinline__ float gelu(float x) {
+  return 0.5f * x * (1.f + erff(x * 0.70710678118654752f));
+}
+
+template <int ACT>
+__device__ __forceinline__ float activate(float x) {
+  if constexpr (ACT == LA_ACT_RELU) return x < 0.f ? 0.f : x;   // keeps NaN
+  if constexpr (ACT == LA_ACT_SILU) return silu(x);
+  if constexpr (ACT == LA_ACT_GELU) return gelu(x);
+  if constexpr (ACT == LA_ACT_SOFTPLUS) return softplus(x);
+  return x;
+}
+
+// Elements of a 16-byte vector.
+template <typename T> constexpr int kVec = 16 / (int)sizeof(T);
+
+template <typename T>
+__device__ __forceinline__ void unpack(const uint4& v, float (&f)[kVec<T>]) {
+  const uint32_t r[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (sizeof(T) == 2) {
+      f[2 * i] = tc::bf16lo_to_f32(r[i]);
+      f[2 * i + 1] = tc::bf16hi_to_f32(r[i]);
+    } else {
+      f[i] = __uint_as_float(r[i]);
+    }
+  }
+}
+
+template <typename T>
+__device__ __forceinline__ uint4 pack(const float (&f)[kVec<T>]) {
+  if constexpr (sizeof(T) == 2)
+    return tc::pack8(f);
+  else
+    return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
+                      __float_as_uint(f[3]));
+}
+
+// Tokens of batch entry b that count: lengths[b] taken into [0, n].
+__device__ __forceinline__ int live_tokens(const int32_t* lengths, int64_t b, int n) {
+  if (!lengths) return n;
+  const int l = lengths[b];
+  return l < 0 ? 0 : (l > n ? n : l);
+}
+
+// Two fp32 values in one 64-bit register pair: one instruction for two
+// lanes' worth of multiply-adds.
+using f32x2 = unsigned long long;
+
+__device__ __forceinline__ f32x2 pack2(float lo, float hi) {
+  f32x2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void unpack2(f32x2 v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+  f32x2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
+}  // namespace block
+}  // namespace la

@@ -1,0 +1,276 @@
+// C ABI of the state-space block's operators (declared in include/linattn.h):
+// argument validation and hand-over to the launchers.
+#include "linattn.h"
+
+#include "internal.h"
+
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+namespace la {
+namespace {
+
+constexpr int64_t kMaxDim = (int64_t)1 << 30;     // tokens, features
+constexpr int64_t kMaxBatch = (int64_t)1 << 24;
+constexpr int64_t kMaxChannels = (int64_t)1 << 20;
+
+bool aligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
+
+int64_t size_of(la_dtype t) { return t == LA_BF16 ? 2 : 4; }
+
+// The rules shared by every la_rows argument: layout and alignment.
+bool valid_rows(const la_rows* r, la_dtype dtype) {
+  if (!r || (r->dtype != LA_BF16 && r->dtype != LA_F32) || r->dtype != dtype) return false;
+  if (r->B < 0 || r->n < 0 || r->d < 1) return false;
+  const int64_t e = size_of(r->dtype);
+  if ((r->d * e) % 16) return false;
+  if (r->B > 1 && (r->stride_b < 0 || (r->stride_b * e) % 16)) return false;
+  if (r->n > 1 && (r->stride_n < 0 || (r->stride_n * e) % 16)) return false;
+  if (r->B > 0 && r->n > 0 && (!r->data || !aligned(r->data, 16))) return false;
+  return true;
+}
+
+// No two elements of a view coincide (outputs).
+bool disjoint_rows(const la_rows* r) {
+  const bool many_b = r->B > 1, many_n = r->n > 1;
+  if (many_b && r->stride_b < r->d) return false;
+  if (many_n && r->stride_n < r->d) return false;
+  if (!many_b || !many_n) return true;
+  // products of 64-bit sizes: compared by division, so that none overflows
+  const bool by_batch = r->stride_n <= (r->stride_b - r->d) / (r->n - 1);
+  const bool by_token = r->stride_b <= (r->stride_n - r->d) / (r->B - 1);
+  return by_batch || by_token;
+}
+
+// The extents are within what the kernels index, the strides within 2^40.
+bool supported_rows(const la_rows* r) {
+  return r->B <= kMaxBatch && r->n <= kMaxDim && r->d <= kMaxDim &&
+         (r->B <= 1 || r->stride_b <= ((int64_t)1 << 40)) &&
+         (r->n <= 1 || r->stride_n <= ((int64_t)1 << 36));
+}
+
+bool same_extent(const la_rows* a, const la_rows* b) {
+  return a->B == b->B && a->n == b->n && a->d == b->d;
+}
+
+bool valid_param(const void* p) { return aligned(p, 16); }
+
+bool valid_activation(la_activation a) { return a >= LA_ACT_NONE && a <= LA_ACT_SOFTPLUS; }
+
+bool overlap(const void* p, const void* q, int64_t bytes) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+  return a < b + (uintptr_t)bytes && b < a + (uintptr_t)bytes;
+}
+
+// Strides of extents 1 are not looked at by the rules: the kernels see 0.
+Rows rows_of(const la_rows* r) {
+  return Rows{r->data, r->B > 1 ? r->stride_b : 0, r->n > 1 ? r->stride_n : 0};
+}
+
+la_status check_conv(const la_rows* x, const void* weight, int width, const void* bias,
+                     la_activation act, la_rows* out, ConvArgs* a) {
+  if (!x || !out || !weight) return LA_ERR_INVALID_ARG;
+  if (!valid_rows(x, x->dtype) || !valid_rows(out, x->dtype) || !same_extent(x, out) ||
+      !disjoint_rows(out))
+    return LA_ERR_INVALID_ARG;
+  if (!valid_param(weight) || !valid_param(bias) || !valid_activation(act))
+    return LA_ERR_INVALID_ARG;
+  if (width < 2 || width > 4 || (act != LA_ACT_NONE && act != LA_ACT_SILU))
+    return LA_ERR_UNSUPPORTED;
+  if (!supported_rows(x) || !supported_rows(out) || x->d > kMaxChannels) return LA_ERR_UNSUPPORTED;
+  *a = ConvArgs{};
+  a->x = rows_of(x);
+  const Rows o = rows_of(out);
+  a->out = out->data;
+  a->out_sb = o.sb;
+  a->out_sn = o.sn;
+  a->weight = weight;
+  a->bias = bias;
+  a->B = x->B;
+  a->n = x->n;
+  a->D = x->d;
+  a->W = width;
+  a->silu = act == LA_ACT_SILU;
+  a->bf16 = x->dtype == LA_BF16;
+  return LA_OK;
+}
+
+la_status check_scan(const la_rows* x, const la_rows* dt, const float* a, int states,
+                     const la_rows* bm, const la_rows* cm, const float* skip, const la_rows* gate,
+                     const float* dt_bias, int softplus, la_rows* out, ScanArgs* s) {
+  if (!x || !dt || !a || !bm || !cm || !out) return LA_ERR_INVALID_ARG;
+  if (!valid_rows(x, x->dtype) || !valid_rows(dt, x->dtype) || !valid_rows(out, x->dtype) ||
+      !valid_rows(bm, x->dtype) || !valid_rows(cm, x->dtype) ||
+      (gate && !valid_rows(gate, x->dtype)))
+    return LA_ERR_INVALID_ARG;
+  if (!same_extent(x, dt) || !same_extent(x, out) || (gate && !same_extent(x, gate)) ||
+      !same_extent(bm, cm) || bm->B != x->B || bm->n != x->n || bm->d != states ||
+      !disjoint_rows(out))
+    return LA_ERR_INVALID_ARG;
+  if (!valid_param(a) || !valid_param(skip) || !valid_param(dt_bias)) return LA_ERR_INVALID_ARG;
+  if (states != 8 && states != 16 && states != 32 && states != 64) return LA_ERR_UNSUPPORTED;
+  for (const la_rows* r : {x, dt, bm, cm, (const la_rows*)out})
+    if (!supported_rows(r)) return LA_ERR_UNSUPPORTED;
+  if ((gate && !supported_rows(gate)) || x->d > kMaxChannels) return LA_ERR_UNSUPPORTED;
+  *s = ScanArgs{};
+  s->x = rows_of(x);
+  s->dt = rows_of(dt);
+  s->b = rows_of(bm);
+  s->c = rows_of(cm);
+  s->gate = gate ? rows_of(gate) : Rows{nullptr, 0, 0};
+  const Rows o = rows_of(out);
+  s->out = out->data;
+  s->out_sb = o.sb;
+  s->out_sn = o.sn;
+  s->a = a;
+  s->skip = skip;
+  s->dt_bias = dt_bias;
+  s->B = x->B;
+  s->n = x->n;
+  s->D = x->d;
+  s->S = states;
+  s->softplus = softplus != 0;
+  s->bf16 = x->dtype == LA_BF16;
+  return LA_OK;
+}
+
+// An empty prompt: the state after it is the one before it.
+cudaError_t copy_state(void* to, const void* from, size_t bytes, cudaStream_t stream) {
+  if (!to || !bytes) return cudaSuccess;
+  return from ? cudaMemcpyAsync(to, from, bytes, cudaMemcpyDeviceToDevice, stream)
+              : cudaMemsetAsync(to, 0, bytes, stream);
+}
+
+}  // namespace
+}  // namespace la
+
+using namespace la;
+
+extern "C" {
+
+la_status la_linear(const la_rows* x, const la_rows* weight, const void* bias,
+                    la_activation activation, const la_rows* residual, la_rows* out,
+                    la_stream stream) {
+  ApiRange range("la_linear");
+  if (!x || !weight || !out) return LA_ERR_INVALID_ARG;
+  if (!valid_rows(x, x->dtype) || !valid_rows(weight, x->dtype) || !valid_rows(out, x->dtype) ||
+      (residual && !valid_rows(residual, x->dtype)))
+    return LA_ERR_INVALID_ARG;
+  if (x->B != 1 || weight->B != 1 || out->B != 1 || weight->d != x->d || out->n != x->n ||
+      out->d != weight->n || weight->n < 1 || (residual && !same_extent(residual, out)) ||
+      !disjoint_rows(out) || !disjoint_rows(x) || !disjoint_rows(weight))
+    return LA_ERR_INVALID_ARG;
+  if (!valid_param(bias) || !valid_activation(activation)) return LA_ERR_INVALID_ARG;
+  for (const la_rows* r : {x, weight, (const la_rows*)out})
+    if (!supported_rows(r)) return LA_ERR_UNSUPPORTED;
+  if (residual && !supported_rows(residual)) return LA_ERR_UNSUPPORTED;
+  if (x->n == 0) return LA_OK;
+  DeviceInfo di;
+  const la_status st = device_info(&di);
+  if (st != LA_OK) return st;
+  LinearArgs a{};
+  a.x = rows_of(x);
+  a.w = rows_of(weight);
+  a.residual = residual ? rows_of(residual) : Rows{nullptr, 0, 0};
+  a.out = out->data;
+  a.out_sn = rows_of(out).sn;
+  a.bias = bias;
+  a.M = x->n;
+  a.N = weight->n;
+  a.K = x->d;
+  a.act = activation;
+  a.bf16 = x->dtype == LA_BF16;
+  a.status = di.status;
+  a.num_sms = di.num_sms;
+  return to_status(linear(a, (cudaStream_t)stream));
+}
+
+la_status la_causal_conv(const la_rows* x, const void* weight, int width, const void* bias,
+                         la_activation activation, const void* state_in, const int32_t* lengths,
+                         la_rows* out, void* state_out, la_stream stream) {
+  ApiRange range("la_causal_conv");
+  ConvArgs a;
+  la_status st = check_conv(x, weight, width, bias, activation, out, &a);
+  if (st != LA_OK) return st;
+  if (!valid_param(state_in) || !valid_param(state_out) || !aligned(lengths, 4))
+    return LA_ERR_INVALID_ARG;
+  const int64_t bytes = a.B * (width - 1) * a.D * size_of(x->dtype);
+  if (state_in && state_out && overlap(state_in, state_out, bytes)) return LA_ERR_INVALID_ARG;
+  a.state_in = state_in;
+  a.state_out = state_out;
+  a.lengths = lengths;
+  if (a.B == 0) return LA_OK;
+  if (a.n == 0) return to_status(copy_state(state_out, state_in, bytes, (cudaStream_t)stream));
+  DeviceInfo di;
+  st = device_info(&di);
+  if (st != LA_OK) return st;
+  a.num_sms = di.num_sms;
+  return to_status(causal_conv(a, (cudaStream_t)stream));
+}
+
+la_status la_causal_conv_step(void* state, const la_rows* x, const void* weight, int width,
+                              const void* bias, la_activation activation, la_rows* out,
+                              la_stream stream) {
+  ApiRange range("la_causal_conv_step");
+  ConvArgs a;
+  la_status st = check_conv(x, weight, width, bias, activation, out, &a);
+  if (st != LA_OK) return st;
+  if (x->n != 1 || !valid_param(state)) return LA_ERR_INVALID_ARG;
+  if (a.B == 0) return LA_OK;
+  if (!state) return LA_ERR_INVALID_ARG;
+  a.state_in = state;
+  a.state_out = state;
+  DeviceInfo di;
+  st = device_info(&di);
+  if (st != LA_OK) return st;
+  a.num_sms = di.num_sms;
+  return to_status(causal_conv_step(a, (cudaStream_t)stream));
+}
+
+la_status la_selective_scan(const la_rows* x, const la_rows* dt, const float* a, int states,
+                            const la_rows* bm, const la_rows* cm, const float* skip,
+                            const la_rows* gate, const float* dt_bias, int softplus,
+                            const float* state_in, const int32_t* lengths, la_rows* out,
+                            float* state_out, la_stream stream) {
+  ApiRange range("la_selective_scan");
+  ScanArgs s;
+  la_status st = check_scan(x, dt, a, states, bm, cm, skip, gate, dt_bias, softplus, out, &s);
+  if (st != LA_OK) return st;
+  if (!valid_param(state_in) || !valid_param(state_out) || !aligned(lengths, 4))
+    return LA_ERR_INVALID_ARG;
+  const int64_t bytes = s.B * s.D * s.S * (int64_t)sizeof(float);
+  if (state_in && state_out && overlap(state_in, state_out, bytes)) return LA_ERR_INVALID_ARG;
+  s.state_in = state_in;
+  s.state_out = state_out;
+  s.lengths = lengths;
+  if (s.B == 0) return LA_OK;
+  if (s.n == 0) return to_status(copy_state(state_out, state_in, bytes, (cudaStream_t)stream));
+  DeviceInfo di;
+  st = device_info(&di);
+  if (st != LA_OK) return st;
+  s.num_sms = di.num_sms;
+  return to_status(selective_scan(s, (cudaStream_t)stream));
+}
+
+la_status la_selective_step(float* state, const la_rows* x, const la_rows* dt, const float* a,
+                            int states, const la_rows* bm, const la_rows* cm, const float* skip,
+                            const la_rows* gate, const float* dt_bias, int softplus,
+                            la_rows* out, la_stream stream) {
+  ApiRange range("la_selective_step");
+  ScanArgs s;
+  la_status st = check_scan(x, dt, a, states, bm, cm, skip, gate, dt_bias, softplus, out, &s);
+  if (st != LA_OK) return st;
+  if (x->n != 1 || !valid_param(state)) return LA_ERR_INVALID_ARG;
+  if (s.B == 0) return LA_OK;
+  if (!state) return LA_ERR_INVALID_ARG;
+  s.state_in = state;
+  s.state_out = state;
+  DeviceInfo di;
+  st = device_info(&di);
+  if (st != LA_OK) return st;
+  s.num_sms = di.num_sms;
+  return to_status(selective_step(s, (cudaStream_t)stream));
+}
+
+}  // extern "C"

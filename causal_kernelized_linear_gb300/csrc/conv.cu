@@ -1,0 +1,167 @@
+// The short depthwise causal convolution of a state-space block:
+//   out_t,c = act(bias_c + Σ_{j<W} w_c,j · X_{t+j,c}),  X = [state | x],
+// over a prompt, and for one token with the state shifted in place.
+//
+// W multiply-adds per value against 2 values moved: bound by HBM.  A thread
+// owns the channels of one 16-byte vector and walks a run of tokens with the
+// last W − 1 inputs in registers, so every input is read once per run (plus
+// W − 1 rows where runs meet, which the neighbouring run has just read into
+// L2) and written once; a warp's accesses are 512 contiguous bytes.
+#include "block.cuh"
+#include "internal.h"
+
+namespace la {
+namespace {
+
+using namespace block;
+
+constexpr int kThreads = 128;
+constexpr int kRun = 32;   // tokens a thread walks
+
+template <typename T, int W>
+__device__ __forceinline__ void load_taps(const ConvArgs& a, int64_t c, float (&w)[W][kVec<T>],
+                                          float (&bias)[kVec<T>]) {
+  constexpr int V = kVec<T>;
+  const T* wp = static_cast<const T*>(a.weight) + c * W;   // V·W consecutive values
+#pragma unroll
+  for (int v = 0; v < W; ++v) {
+    float f[V];
+    unpack<T>(reinterpret_cast<const uint4*>(wp)[v], f);
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int e = v * V + i;
+      w[e % W][e / W] = f[i];
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < V; ++i) bias[i] = 0.f;
+  if (a.bias) unpack<T>(*reinterpret_cast<const uint4*>(static_cast<const T*>(a.bias) + c), bias);
+}
+
+// Row r of X of batch entry b, r counted from the prompt's first token.
+template <typename T, int W>
+__device__ __forceinline__ uint4 row_of(const ConvArgs& a, int64_t b, int64_t r, int64_t c) {
+  if (r >= 0)
+    return __ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(a.x.data) + b * a.x.sb +
+                                                r * a.x.sn + c));
+  if (!a.state_in) return make_uint4(0, 0, 0, 0);
+  return *reinterpret_cast<const uint4*>(static_cast<const T*>(a.state_in) +
+                                         (b * (W - 1) + (W - 1) + r) * a.D + c);
+}
+
+template <typename T, int W, bool SILU>
+__device__ __forceinline__ uint4 taps(const float (&win)[W][kVec<T>],
+                                      const float (&w)[W][kVec<T>],
+                                      const float (&bias)[kVec<T>]) {
+  constexpr int V = kVec<T>;
+  float y[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    y[i] = bias[i];
+#pragma unroll
+    for (int j = 0; j < W; ++j) y[i] = fmaf(w[j][i], win[j][i], y[i]);
+    if constexpr (SILU) y[i] = silu(y[i]);
+  }
+  return pack<T>(y);
+}
+
+template <typename T, int W, bool SILU>
+__global__ void __launch_bounds__(kThreads) conv_kernel(const ConvArgs a, int vecs, int runs) {
+  constexpr int V = kVec<T>;
+  const int64_t item = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+  if (item >= (int64_t)vecs * runs * a.B) return;
+  const int64_t c = (item % vecs) * V;
+  const int run = (int)((item / vecs) % runs);
+  const int64_t b = item / vecs / runs;
+  const int n = (int)a.n;
+  const int len = live_tokens(a.lengths, b, n);
+  float w[W][V], bias[V];
+  load_taps<T, W>(a, c, w, bias);
+  const int t0 = run * kRun;
+  const int t1 = min(t0 + kRun, n);
+  float win[W][V];
+#pragma unroll
+  for (int j = 0; j < W - 1; ++j)
+    unpack<T>(t0 < len ? row_of<T, W>(a, b, t0 - (W - 1) + j, c) : make_uint4(0, 0, 0, 0), win[j]);
+  T* out = static_cast<T*>(a.out) + b * a.out_sb + c;
+  for (int t = t0; t < t1; ++t) {
+    uint4 y = make_uint4(0, 0, 0, 0);
+    if (t < len) {
+      unpack<T>(row_of<T, W>(a, b, t, c), win[W - 1]);
+      y = taps<T, W, SILU>(win, w, bias);
+#pragma unroll
+      for (int j = 0; j < W - 1; ++j)
+#pragma unroll
+        for (int i = 0; i < V; ++i) win[j][i] = win[j + 1][i];
+    }
+    *reinterpret_cast<uint4*>(out + t * a.out_sn) = y;
+  }
+  if (run == 0 && a.state_out) {
+    T* so = static_cast<T*>(a.state_out) + b * (W - 1) * a.D + c;
+#pragma unroll
+    for (int j = 0; j < W - 1; ++j)
+      *reinterpret_cast<uint4*>(so + j * a.D) = row_of<T, W>(a, b, (int64_t)len - (W - 1) + j, c);
+  }
+}
+
+template <typename T, int W, bool SILU>
+__global__ void __launch_bounds__(kThreads) conv_step_kernel(const ConvArgs a, int vecs) {
+  constexpr int V = kVec<T>;
+  const int64_t item = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+  if (item >= vecs * a.B) return;
+  const int64_t c = (item % vecs) * V;
+  const int64_t b = item / vecs;
+  T* st = static_cast<T*>(a.state_out) + b * (W - 1) * a.D + c;
+  uint4 raw[W];
+#pragma unroll
+  for (int j = 0; j < W - 1; ++j) raw[j] = *reinterpret_cast<const uint4*>(st + j * a.D);
+  raw[W - 1] = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.x.data) + b * a.x.sb + c);
+  float w[W][V], bias[V], win[W][V];
+  load_taps<T, W>(a, c, w, bias);
+#pragma unroll
+  for (int j = 0; j < W; ++j) unpack<T>(raw[j], win[j]);
+#pragma unroll
+  for (int j = 0; j < W - 1; ++j) *reinterpret_cast<uint4*>(st + j * a.D) = raw[j + 1];
+  *reinterpret_cast<uint4*>(static_cast<T*>(a.out) + b * a.out_sb + c) =
+      taps<T, W, SILU>(win, w, bias);
+}
+
+template <typename T, int W, bool SILU>
+cudaError_t launch(const ConvArgs& a, bool step, cudaStream_t s) {
+  const int vecs = (int)(a.D / kVec<T>);
+  const int runs = step ? 1 : (int)((a.n + kRun - 1) / kRun);
+  const int64_t blocks = ((int64_t)vecs * runs * a.B + kThreads - 1) / kThreads;
+  if (blocks > INT32_MAX) return cudaErrorInvalidConfiguration;
+  if (step)
+    conv_step_kernel<T, W, SILU><<<(unsigned)blocks, kThreads, 0, s>>>(a, vecs);
+  else
+    conv_kernel<T, W, SILU><<<(unsigned)blocks, kThreads, 0, s>>>(a, vecs, runs);
+  count_launches(1);
+  return cudaGetLastError();
+}
+
+template <typename T, int W>
+cudaError_t by_act(const ConvArgs& a, bool step, cudaStream_t s) {
+  return a.silu ? launch<T, W, true>(a, step, s) : launch<T, W, false>(a, step, s);
+}
+
+template <typename T>
+cudaError_t by_width(const ConvArgs& a, bool step, cudaStream_t s) {
+  switch (a.W) {
+    case 2: return by_act<T, 2>(a, step, s);
+    case 3: return by_act<T, 3>(a, step, s);
+    default: return by_act<T, 4>(a, step, s);
+  }
+}
+
+}  // namespace
+
+cudaError_t causal_conv(const ConvArgs& a, cudaStream_t s) {
+  return a.bf16 ? by_width<__nv_bfloat16>(a, false, s) : by_width<float>(a, false, s);
+}
+
+cudaError_t causal_conv_step(const ConvArgs& a, cudaStream_t s) {
+  return a.bf16 ? by_width<__nv_bfloat16>(a, true, s) : by_width<float>(a, true, s);
+}
+
+}  // namespace la

@@ -164,6 +164,21 @@ la_status forward_in_workspace(const la_tensor* q, const la_tensor* k, const la_
                                la_status (*get_ws)(float**), size_t ws_floats,
                                cudaStream_t stream);
 
+// The current device's attributes, cached per device.
+struct DeviceInfo {
+  bool ready = false;
+  int num_sms = 0;
+  int* status = nullptr;  // device address of the status word
+};
+la_status device_info(DeviceInfo* out);
+
+// Stream-ordered workspace from the library's pool of the current device
+// (release with cudaFreeAsync on the same stream).
+cudaError_t ws_alloc(void** p, size_t bytes, cudaStream_t s);
+
+// The public status of a CUDA runtime result.
+la_status to_status(cudaError_t e);
+
 // Records `k` kernel launches in the process-wide launch counter.
 void count_launches(int k);
 
@@ -208,6 +223,67 @@ cudaError_t backward_da_reduce(const float* parts, float* da, int64_t B, int64_t
 bool tc_backward_supported(const BwdArgs& a);
 size_t tc_backward_ws_floats(const BwdArgs& a);
 cudaError_t tc_backward(const BwdArgs& a, float* ws, int num_sms, int* status, cudaStream_t stream);
+
+// ---------------------------------------------------------------- state-space block
+
+// A strided [B, n, d] view: element (b, t, c) at data[b·sb + t·sn + c].
+struct Rows {
+  const void* data;
+  int64_t sb, sn;
+};
+
+// y = act(x·wᵀ + bias) + residual; x [M, K], w [N, K], y and residual [M, N].
+struct LinearArgs {
+  Rows x, w, residual;  // residual.data may be nullptr
+  void* out;
+  int64_t out_sn;
+  const void* bias;     // [N] or nullptr
+  int64_t M, N, K;
+  la_activation act;
+  bool bf16;
+  int* status;
+  int num_sms;
+};
+cudaError_t linear(const LinearArgs& a, cudaStream_t stream);
+
+// The short depthwise causal convolution over a prompt or one token.
+struct ConvArgs {
+  Rows x;
+  void* out;
+  int64_t out_sb, out_sn;
+  const void* weight;     // [D, W]
+  const void* bias;       // [D] or nullptr
+  const void* state_in;   // [B, W−1, D] or nullptr (zeros)
+  void* state_out;        // [B, W−1, D] or nullptr; the step updates it in place
+  const int32_t* lengths; // [B] or nullptr (all n)
+  int64_t B, n, D;
+  int W;
+  bool silu;
+  bool bf16;
+  int num_sms;
+};
+cudaError_t causal_conv(const ConvArgs& a, cudaStream_t stream);
+cudaError_t causal_conv_step(const ConvArgs& a, cudaStream_t stream);
+
+// The selective state-space scan over a prompt or one token.
+struct ScanArgs {
+  Rows x, dt, b, c, gate;   // gate.data may be nullptr
+  void* out;
+  int64_t out_sb, out_sn;
+  const float* a;           // [D, S]
+  const float* skip;        // [D] or nullptr
+  const float* dt_bias;     // [D] or nullptr
+  const float* state_in;    // [B, D, S] or nullptr (zeros)
+  float* state_out;         // [B, D, S] or nullptr; the step updates it in place
+  const int32_t* lengths;   // [B] or nullptr (all n)
+  int64_t B, n, D;
+  int S;
+  bool softplus;
+  bool bf16;
+  int num_sms;
+};
+cudaError_t selective_scan(const ScanArgs& a, cudaStream_t stream);
+cudaError_t selective_step(const ScanArgs& a, cudaStream_t stream);
 
 // Memory-bound recurrent decode step.
 cudaError_t decode_step(const DecodeArgs& a, cudaStream_t stream);

@@ -363,6 +363,120 @@ la_status la_forward_noalloc(const la_tensor* q, const la_tensor* k, const la_te
  */
 uint64_t la_launch_count(void);
 
+/* ------------------------------------------------------------------------
+ * The operators around the recurrence in a state-space block: a projection,
+ * the short causal convolution and the selective scan (a per-token decay per
+ * state element: the selective step of the Mamba section of "Linear Attention
+ * Research 2026", whose scalar-per-head relative is la_forward_token_decay).
+ *
+ * These take strided views, so that a projection's output can be read in
+ * parts without a copy.  la_rows is a [B, n, d] view: element (b, t, c) at
+ * data[b·stride_b + t·stride_n + c] (strides in elements).  Rules shared by
+ * every la_rows argument:
+ *   - data is 16-byte aligned; d·size, stride_b·size and stride_n·size are
+ *     multiples of 16 bytes (a stride whose extent is 1 is not looked at);
+ *   - strides are not negative; elements of an output view do not coincide;
+ *   - an output shares no memory with an input unless its comment allows it.
+ * "parameter" arrays (bias, skip, …) are dense and 16-byte aligned.
+ * ------------------------------------------------------------------------ */
+typedef struct {
+  void* data;
+  la_dtype dtype;
+  int64_t B, n, d;
+  int64_t stride_b, stride_n;
+} la_rows;
+
+/* relu: max(x, 0); silu: x/(1 + e^{−x}); gelu: x·Φ(x) (the normal
+ * distribution function, no tanh form); softplus: log(1 + e^x). */
+typedef enum {
+  LA_ACT_NONE = 0, LA_ACT_RELU = 1, LA_ACT_SILU = 2, LA_ACT_GELU = 3, LA_ACT_SOFTPLUS = 4
+} la_activation;
+
+/*
+ * la_linear — out = act(x·wᵀ + bias) + residual.
+ *   x         [1, M, K] (B = 1), bf16 or fp32; M ≥ 0 (M = 0 is a no-op).
+ *   weight    [1, N, K], x's dtype: row n holds the weights of output n.
+ *   bias      device [N], x's dtype, or NULL.
+ *   residual  [1, M, N], x's dtype, or NULL; may be the same view as out.
+ *   out       [1, M, N], x's dtype.  Written in full.
+ * K and N are multiples of 8 (bf16) or 4 (fp32); rows of x and of weight do
+ * not overlap (stride_n ≥ K).  Sums, bias, activation and residual are fp32,
+ * rounded once to the output's type.  The sum's order is fixed: equal inputs
+ * give equal bits.
+ * Errors: LA_ERR_INVALID_ARG, LA_ERR_UNSUPPORTED (M, N or K above 2^30),
+ * LA_ERR_OUT_OF_MEMORY, LA_ERR_CUDA.
+ */
+la_status la_linear(const la_rows* x, const la_rows* weight, const void* bias,
+                    la_activation activation, const la_rows* residual, la_rows* out,
+                    la_stream stream);
+
+/*
+ * la_causal_conv — depthwise causal convolution over a prompt:
+ *   out[b,t,c] = act(bias[c] + Σ_{j<W} weight[c,j]·X[b, t + j, c]),
+ * where X is the W − 1 rows of state_in followed by x: the newest input
+ * meets weight[c, W−1].
+ *   x          [B, n, D], bf16 or fp32; n ≥ 0.
+ *   weight     device [D, W] dense, x's dtype; width W ∈ {2, 3, 4}.
+ *   bias       device [D], x's dtype, or NULL.
+ *   activation LA_ACT_NONE or LA_ACT_SILU (others: LA_ERR_UNSUPPORTED).
+ *   state_in   device [B, W−1, D] dense, x's dtype: the inputs before the
+ *              prompt, oldest first; NULL for zeros.
+ *   lengths    device [B] int32, or NULL for n: tokens t ≥ lengths[b] are not
+ *              read, their outputs are 0 (values are taken into [0, n]).
+ *   out        [B, n, D], x's dtype.  Written in full.
+ *   state_out  device [B, W−1, D] dense, x's dtype, or NULL: the last W − 1
+ *              rows of X up to the length.  Must not overlap state_in.
+ * Sums and activation are fp32.  Errors as la_linear; LA_ERR_UNSUPPORTED for
+ * other widths and for D above 2^20.
+ */
+la_status la_causal_conv(const la_rows* x, const void* weight, int width, const void* bias,
+                         la_activation activation, const void* state_in, const int32_t* lengths,
+                         la_rows* out, void* state_out, la_stream stream);
+
+/*
+ * la_causal_conv_step — the convolution's next token.  state [B, W−1, D]
+ * (dense, x's dtype) holds the last W − 1 inputs, oldest first, and is
+ * shifted in place.  x and out are [B, 1, D]; out may be the same view as x.
+ */
+la_status la_causal_conv_step(void* state, const la_rows* x, const void* weight, int width,
+                              const void* bias, la_activation activation, la_rows* out,
+                              la_stream stream);
+
+/*
+ * la_selective_scan — the selective state-space recurrence over a prompt.
+ * For every batch entry b and channel c, with S states per channel:
+ *   Δ_t  = softplus(dt[b,t,c] + dt_bias[c])   (softplus only when asked for)
+ *   h_t,s = exp(Δ_t·a[c,s])·h_{t−1},s + Δ_t·x[b,t,c]·bm[b,t,s]
+ *   out[b,t,c] = (Σ_s cm[b,t,s]·h_t,s + skip[c]·x[b,t,c])·silu(gate[b,t,c])
+ *   x, dt      [B, n, D], bf16 or fp32 (one dtype for all la_rows here).
+ *   a          device fp32 [D, S] (negative for a decay), S ∈ {8, 16, 32, 64}.
+ *   bm, cm     [B, n, S].
+ *   skip       device fp32 [D], or NULL (no such term).
+ *   gate       [B, n, D], or NULL (no gate).
+ *   dt_bias    device fp32 [D], or NULL.
+ *   state_in   device fp32 [B, D, S], or NULL for zeros.
+ *   lengths    as la_causal_conv; the state is the one after the length.
+ *   out        [B, n, D].  Written in full.
+ *   state_out  device fp32 [B, D, S], or NULL.  Must not overlap state_in.
+ * States, sums and the exponentials' arguments are fp32.  Equal inputs give
+ * equal bits.  Errors as la_linear; LA_ERR_UNSUPPORTED for other S.
+ */
+la_status la_selective_scan(const la_rows* x, const la_rows* dt, const float* a, int states,
+                            const la_rows* bm, const la_rows* cm, const float* skip,
+                            const la_rows* gate, const float* dt_bias, int softplus,
+                            const float* state_in, const int32_t* lengths, la_rows* out,
+                            float* state_out, la_stream stream);
+
+/*
+ * la_selective_step — the recurrence's next token: state [B, D, S] fp32 is
+ * updated in place; x, dt, gate, out [B, 1, D], bm, cm [B, 1, S]; the rest
+ * as la_selective_scan.  out may be the same view as x, dt or gate.
+ */
+la_status la_selective_step(float* state, const la_rows* x, const la_rows* dt, const float* a,
+                            int states, const la_rows* bm, const la_rows* cm, const float* skip,
+                            const la_rows* gate, const float* dt_bias, int softplus,
+                            la_rows* out, la_stream stream);
+
 /*
  * la_selftest_wait_timeout — test hook for the failure path of the bounded
  * waits.  Queues on `stream` one small kernel that runs the same bounded
