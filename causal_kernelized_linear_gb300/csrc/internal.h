@@ -122,10 +122,14 @@ cudaError_t tc_performer_forward(const FwdArgs& a, cudaStream_t stream, float* w
 //   tmap_rows:     bf16 [BH, n, D] as a 3-D tensor, box 64 × rows × 1 (rows
 //                  past n read as zero and are not written);
 //   tmap_matrix:   a bf16 row-major [rows, cols] matrix, box 64 × box_rows;
+//   tmap_view:     a bf16 [rows, cols] view with rows row_stride elements apart,
+//                  box 64 × box_rows;
 //   tmap_f32_mats: `count` fp32 row-major [D × D] matrices, contiguous, as a
 //                  3-D tensor, box 32 × D × 1.
 cudaError_t tmap_rows(CUtensorMap* m, const void* base, int64_t BH, int64_t n, int D, int rows);
 cudaError_t tmap_matrix(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, int box_rows);
+cudaError_t tmap_view(CUtensorMap* m, const void* base, int64_t rows, int64_t cols,
+                      int64_t row_stride, int box_rows);
 cudaError_t tmap_f32_mats(CUtensorMap* m, const void* base, int64_t count, int D);
 
 // Exclusive decayed prefix over the per-segment aggregates of every head, in
@@ -245,6 +249,8 @@ struct LinearArgs {
   int num_sms;
 };
 cudaError_t linear(const LinearArgs& a, cudaStream_t stream);
+// The bf16 product on the tensor cores.
+cudaError_t tc_linear(const LinearArgs& a, cudaStream_t stream);
 
 // The short depthwise causal convolution over a prompt or one token.
 struct ConvArgs {

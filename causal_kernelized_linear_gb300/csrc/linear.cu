@@ -82,7 +82,7 @@ cudaError_t simt(const LinearArgs& a, cudaStream_t s) {
 }  // namespace
 
 cudaError_t linear(const LinearArgs& a, cudaStream_t s) {
-  return a.bf16 ? simt<__nv_bfloat16>(a, s) : simt<float>(a, s);
+  return a.bf16 ? tc_linear(a, s) : simt<float>(a, s);
 }
 
 }  // namespace la

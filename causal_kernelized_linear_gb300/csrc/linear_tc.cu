@@ -1,0 +1,478 @@
+// out = act(x·wᵀ + bias) + residual in bf16 on the tcgen05 tensor cores.
+//
+// pair_kernel (many tokens): CTA pairs, persistent, one 256×256 tile of the
+// output per pair at a time.  Each CTA loads its 128 rows of x and 128 rows of
+// w per 64-wide step of K (32 KB, six stages), the even rank issues the
+// cta_group::2 MMAs (256×256×16) for both, and each CTA's TMEM receives its
+// 128 rows × 256 columns in one of two accumulators, so that the epilogue of a
+// tile overlaps the next tile's product.  A pair moves 64 KB per step into
+// shared memory for 2·256·256·64 flops; one CTA on a 128×256 tile would move
+// 48 KB for half of them.
+//
+// few_kernel (few tokens): the product is bound by reading w, so w's rows are
+// the MMA's 128 rows and the tokens its columns (16 to 128, no work on absent
+// ones).  A cluster of CTAs splits K, and adds its partial sums through
+// distributed shared memory in rank order: w is read once, by enough CTAs to
+// keep HBM busy, in one launch, with a fixed order of sums.
+#include "block.cuh"
+#include "internal.h"
+
+#include <atomic>
+
+namespace la {
+namespace {
+
+using namespace block;
+using namespace tc;
+
+using bf16 = __nv_bfloat16;
+
+constexpr int kBK = 64;                 // K per stage: one 128-byte swizzle row
+
+struct LinParams {
+  const bf16* bias;
+  const bf16* residual;
+  int64_t res_sn;
+  bf16* out;
+  int64_t out_sn;
+  int M, N, kblocks;
+  int mtiles, ntiles;
+  int* status;
+};
+
+// bias, activation and residual on 8 neighbouring columns of a row.
+template <int ACT>
+__device__ __forceinline__ void finish8(const LinParams& p, int64_t m, int n, float (&v)[8]) {
+  if (p.bias) {
+    float b[8];
+    unpack<bf16>(__ldg(reinterpret_cast<const uint4*>(p.bias + n)), b);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] += b[i];
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = activate<ACT>(v[i]);
+  if (p.residual) {
+    float r[8];
+    unpack<bf16>(*reinterpret_cast<const uint4*>(p.residual + m * p.res_sn + n), r);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] += r[i];
+  }
+}
+
+// ------------------------------------------------------------------ many tokens
+
+constexpr int kStages = 6;
+constexpr int kTileB = 128 * kBK * 2;               // 16 KB: 128 rows of one operand
+constexpr int kStageB = 2 * kTileB;
+constexpr int kEpiB = 32 * 64 * 2;                  // 4 KB: 32 rows × 64 columns of the output
+constexpr int kPairThreads = 256;
+constexpr int kPairSmem = 1024 + kStages * kStageB + 8 * kEpiB + 256;
+constexpr int kGroupM = 8;                          // row tiles walked together, for L2
+
+struct PairBars {
+  uint64_t full[kStages], empty[kStages], acc_full[2], acc_empty[2];
+  uint32_t tmem;
+  int abort;
+};
+
+// Tile number → (row tile, column tile): columns fastest within groups of
+// kGroupM row tiles, so that the tiles in flight share rows of x and of w.
+__device__ __forceinline__ void tile_at(const LinParams& p, int64_t t, int& mt, int& nt) {
+  const int64_t per = (int64_t)kGroupM * p.ntiles;
+  const int g = (int)(t / per);
+  const int r = (int)(t % per);
+  const int rows = min(kGroupM, p.mtiles - g * kGroupM);
+  mt = g * kGroupM + r % rows;
+  nt = r / rows;
+}
+
+template <int ACT>
+__global__ void __launch_bounds__(kPairThreads, 1)
+pair_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap mw,
+            const __grid_constant__ CUtensorMap mo, const LinParams p) {
+  extern __shared__ uint8_t raw[];
+  uint8_t* base = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
+  uint8_t* epi = base + kStages * kStageB;
+  PairBars* bars = reinterpret_cast<PairBars*>(epi + 8 * kEpiB);
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const uint32_t rank = cluster_rank();
+  const int64_t tiles = (int64_t)p.mtiles * p.ntiles;
+  const int64_t first = blockIdx.x / 2, stride = gridDim.x / 2;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(&bars->full[i], 1);
+      mbar_init(&bars->empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bars->acc_full[i], 1);
+      mbar_init(&bars->acc_empty[i], 8);   // four epilogue warps of each CTA
+    }
+    bars->abort = 0;
+    fence_barrier_init();
+    tma_prefetch_desc(&mx);
+    tma_prefetch_desc(&mw);
+    tma_prefetch_desc(&mo);
+  }
+  if (warp == 2) {
+    tmem_alloc_pair(&bars->tmem, 512);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();          // both CTAs' barriers exist before any remote arrival
+  tc_fence_after();
+  const uint32_t tmem = bars->tmem;
+  volatile int* abort = &bars->abort;
+
+  if (warp == 0 && lane == 0) {
+    // producer: this CTA's rows of x and w; completion is counted by the even rank
+    uint32_t it = 0;
+    for (int64_t t = first; t < tiles && !*abort; t += stride) {
+      int mt, nt;
+      tile_at(p, t, mt, nt);
+      const int m0 = mt * 256 + (int)rank * 128, n0 = nt * 256 + (int)rank * 128;
+      for (int kb = 0; kb < p.kblocks; ++kb, ++it) {
+        const int s = it % kStages;
+        if (it >= kStages &&
+            !mbar_wait(&bars->empty[s], ((it / kStages) & 1) ^ 1, p.status, abort))
+          break;
+        if (rank == 0) mbar_arrive_expect_tx(&bars->full[s], 2 * kStageB);
+        const uint32_t bar = map_to_cta(smem_u32(&bars->full[s]), 0);
+        tma_load_2d_pair(base + s * kStageB, &mx, bar, kb * kBK, m0);
+        tma_load_2d_pair(base + s * kStageB + kTileB, &mw, bar, kb * kBK, n0);
+      }
+    }
+    // an abort leaves loads in flight: let them land before the CTA ends
+    if (*abort && rank == 0)
+      for (uint32_t j = it > kStages ? it - kStages : 0; j < it; ++j)
+        mbar_wait_drain(&bars->full[j % kStages], (j / kStages) & 1);
+  } else if (warp == 1 && lane == 0 && rank == 0) {
+    // MMA issuer, for both CTAs
+    constexpr uint32_t idesc = idesc_bf16_f32(256, 256, false, false);
+    uint32_t it = 0, n = 0;
+    for (int64_t t = first; t < tiles && !*abort; t += stride, ++n) {
+      const int buf = n & 1;
+      if (n >= 2 && !mbar_wait(&bars->acc_empty[buf], ((n >> 1) & 1) ^ 1, p.status, abort)) break;
+      tc_fence_after();
+      const uint32_t d = tmem + buf * 256;
+      bool ok = true;
+      for (int kb = 0; kb < p.kblocks; ++kb, ++it) {
+        const int s = it % kStages;
+        if (!mbar_wait(&bars->full[s], (it / kStages) & 1, p.status, abort)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint64_t da = smem_desc(smem_u32(base + s * kStageB), 16, 1024, kSwizzle128B);
+        const uint64_t db = smem_desc(smem_u32(base + s * kStageB + kTileB), 16, 1024, kSwizzle128B);
+#pragma unroll
+        for (int k = 0; k < kBK / 16; ++k)
+          mma_ss_pair(d, desc_at(da, k * 32), desc_at(db, k * 32), idesc, (kb | k) != 0);
+        mma_commit_pair(&bars->empty[s]);
+      }
+      if (!ok) break;
+      mma_commit_pair(&bars->acc_full[buf]);
+    }
+    if (*abort) {
+      // what was issued ends on its own; the commit tells when
+      mma_commit_pair(&bars->acc_full[0]);
+      mbar_wait_drain(&bars->acc_full[0], 0);
+    }
+  } else if (warp >= 4) {
+    // epilogue: 32 rows per warp, 64 columns at a time through a staging tile
+    const int q = warp - 4;
+    uint8_t* stage = epi + q * 2 * kEpiB;
+    const uint32_t lead_empty[2] = {map_to_cta(smem_u32(&bars->acc_empty[0]), 0),
+                                    map_to_cta(smem_u32(&bars->acc_empty[1]), 0)};
+    uint32_t n = 0, put = 0;
+    for (int64_t t = first; t < tiles; t += stride, ++n) {
+      const int buf = n & 1;
+      if (!warp_wait(&bars->acc_full[buf], (n >> 1) & 1, p.status, abort)) break;
+      tc_fence_after();
+      int mt, nt;
+      tile_at(p, t, mt, nt);
+      const int m0 = mt * 256 + (int)rank * 128 + q * 32, n0 = nt * 256;
+      const int m = m0 + lane;
+      const int cols = min(256, p.N - n0);
+      if (m0 < p.M) {
+        for (int c = 0; c < cols; c += 64, ++put) {
+          uint8_t* st = stage + (put & 1) * kEpiB;
+          const uint32_t sa = smem_u32(st);
+          if (lane == 0) tma_store_wait_read1();
+          __syncwarp();
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            uint32_t r[32];
+            tmem_ld32(tmem_addr(tmem, q * 32, buf * 256 + c + half * 32), r);
+            tmem_ld_wait();
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              float v[8];
+#pragma unroll
+              for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[8 * j + i]);
+              const int nn = n0 + c + half * 32 + 8 * j;
+              if (m < p.M && nn < p.N) finish8<ACT>(p, m, nn, v);
+              sts128(sa + sw_chunk(32, lane, 0, half * 4 + j), pack8(v));
+            }
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            if (LA_DCHECK(p.status, m0 >= 0 && m0 < p.M && n0 + c < p.N, 51))
+              tma_store_2d(&mo, st, n0 + c, m0);
+            tma_store_commit();
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(lead_empty[buf]);
+    }
+    if (lane == 0) tma_store_wait0();
+  }
+  tc_fence_before();
+  __syncwarp();
+  __syncthreads();
+  cluster_sync();          // no CTA leaves while its pair may still signal or read it
+  tc_fence_after();
+  if (warp == 2) tmem_dealloc_pair(tmem, 512);
+}
+
+// ------------------------------------------------------------------ few tokens
+
+constexpr int kFewThreads = 128;
+
+template <int BT> struct FewCfg {
+  static constexpr int kXB = BT * kBK * 2;
+  static constexpr int kStage = kTileB + kXB;
+  static constexpr int kNum = BT <= 32 ? 5 : 4;           // ≤ 113 KB, two CTAs per SM
+  static constexpr int kPart = BT * 128 * 4;              // partial sums, over the stages
+  static constexpr int kBuf = kNum * kStage > kPart ? kNum * kStage : kPart;
+  static constexpr int kSmem = 1024 + kBuf + 256;
+  static constexpr uint32_t kCols = BT < 32 ? 32 : BT;
+};
+
+struct FewBars {
+  uint64_t full[8], empty[8], done;
+  uint32_t tmem;
+  int abort;
+};
+
+// blockIdx: x = feature tile × cluster rank, y = token tile.
+template <int BT, int ACT>
+__global__ void __launch_bounds__(kFewThreads)
+few_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap mw,
+           const LinParams p, const int split) {
+  using C = FewCfg<BT>;
+  extern __shared__ uint8_t raw[];
+  uint8_t* base = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
+  FewBars* bars = reinterpret_cast<FewBars*>(base + C::kBuf);
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int rank = (int)(blockIdx.x % split);
+  const int n0 = (int)(blockIdx.x / split) * 128, m0 = (int)blockIdx.y * BT;
+  const int k0 = (int)((int64_t)p.kblocks * rank / split);
+  const int k1 = (int)((int64_t)p.kblocks * (rank + 1) / split);
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < C::kNum; ++i) {
+      mbar_init(&bars->full[i], 1);
+      mbar_init(&bars->empty[i], 1);
+    }
+    mbar_init(&bars->done, 1);
+    bars->abort = 0;
+    fence_barrier_init();
+    tma_prefetch_desc(&mx);
+    tma_prefetch_desc(&mw);
+  }
+  if (warp == 2) {
+    tmem_alloc(&bars->tmem, C::kCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = bars->tmem;
+  volatile int* abort = &bars->abort;
+
+  if (warp == 0 && lane == 0) {
+    uint32_t it = 0;
+    for (int kb = k0; kb < k1; ++kb, ++it) {
+      const int s = it % C::kNum;
+      if (it >= C::kNum && !mbar_wait(&bars->empty[s], ((it / C::kNum) & 1) ^ 1, p.status, abort))
+        break;
+      mbar_arrive_expect_tx(&bars->full[s], C::kStage);
+      tma_load_2d(base + s * C::kStage, &mw, &bars->full[s], kb * kBK, n0);
+      tma_load_2d(base + s * C::kStage + kTileB, &mx, &bars->full[s], kb * kBK, m0);
+    }
+    if (*abort)
+      for (uint32_t j = it > C::kNum ? it - C::kNum : 0; j < it; ++j)
+        mbar_wait_drain(&bars->full[j % C::kNum], (j / C::kNum) & 1);
+  } else if (warp == 1 && lane == 0) {
+    constexpr uint32_t idesc = idesc_bf16_f32(128, BT, false, false);
+    uint32_t it = 0;
+    for (int kb = k0; kb < k1; ++kb, ++it) {
+      const int s = it % C::kNum;
+      if (!mbar_wait(&bars->full[s], (it / C::kNum) & 1, p.status, abort)) break;
+      tc_fence_after();
+      const uint64_t dw = smem_desc(smem_u32(base + s * C::kStage), 16, 1024, kSwizzle128B);
+      const uint64_t dx = smem_desc(smem_u32(base + s * C::kStage + kTileB), 16, 1024, kSwizzle128B);
+#pragma unroll
+      for (int k = 0; k < kBK / 16; ++k)
+        mma_ss(tmem, desc_at(dw, k * 32), desc_at(dx, k * 32), idesc, it > 0 || k > 0);
+      mma_commit(&bars->empty[s]);
+    }
+    mma_commit(&bars->done);
+  }
+  __syncwarp();
+  // every load has been consumed once `done` completes: the stages become the
+  // partial sums [token][feature]
+  const bool ok = warp_wait(&bars->done, 0, p.status, abort);
+  tc_fence_after();
+  float* part = reinterpret_cast<float*>(base);
+  if (ok) {
+#pragma unroll
+    for (int c = 0; c < BT; c += 16) {
+      uint32_t r[16];
+      tmem_ld16(tmem_addr(tmem, warp * 32, c), r);
+      tmem_ld_wait();
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        part[(c + i) * 128 + warp * 32 + lane] = k0 < k1 ? __uint_as_float(r[i]) : 0.f;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (split > 1) cluster_sync();
+  // rank r finishes its share of the tokens: 16 lanes of 8 features per token
+  const int per = (BT + split - 1) / split;
+  const int tlim = min(min(BT, (rank + 1) * per), p.M - m0);
+  const int f = (threadIdx.x % 16) * 8, n = n0 + f;
+  if (!*abort && n < p.N) {
+    for (int t = rank * per + threadIdx.x / 16; t < tlim; t += kFewThreads / 16) {
+      const uint32_t at = smem_u32(part) + (t * 128 + f) * 4;
+      float v[8] = {};
+      for (int r = 0; r < split; ++r) {
+        const uint32_t pa = split > 1 ? map_to_cta(at, r) : at;
+        const float4 lo = split > 1 ? ld_cluster_f4(pa) : lds128f(pa);
+        const float4 hi = split > 1 ? ld_cluster_f4(pa + 16) : lds128f(pa + 16);
+        v[0] += lo.x, v[1] += lo.y, v[2] += lo.z, v[3] += lo.w;
+        v[4] += hi.x, v[5] += hi.y, v[6] += hi.z, v[7] += hi.w;
+      }
+      finish8<ACT>(p, m0 + t, n, v);
+      if (LA_DCHECK(p.status, m0 + t < p.M && n + 8 <= p.N, 52))
+        *reinterpret_cast<uint4*>(p.out + (int64_t)(m0 + t) * p.out_sn + n) = pack8(v);
+    }
+  }
+  if (split > 1) cluster_sync();   // no CTA leaves while another reads its partial sums
+  if (warp == 2) tmem_dealloc(tmem, C::kCols);
+}
+
+// ------------------------------------------------------------------ launch
+
+template <int ACT>
+cudaError_t launch_pair(const LinearArgs& a, LinParams p, cudaStream_t s) {
+  CUtensorMap mx, mw, mo;
+  cudaError_t e;
+  if ((e = tmap_view(&mx, a.x.data, a.M, a.K, a.x.sn ? a.x.sn : a.K, 128)) != cudaSuccess ||
+      (e = tmap_view(&mw, a.w.data, a.N, a.K, a.w.sn ? a.w.sn : a.K, 128)) != cudaSuccess ||
+      (e = tmap_view(&mo, a.out, a.M, a.N, a.out_sn ? a.out_sn : a.N, 32)) != cudaSuccess)
+    return e;
+  p.mtiles = (p.M + 255) / 256;
+  p.ntiles = (p.N + 255) / 256;
+  const int64_t tiles = (int64_t)p.mtiles * p.ntiles;
+  e = cudaFuncSetAttribute(pair_kernel<ACT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kPairSmem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2);
+  cfg.blockDim = dim3(kPairThreads);
+  cfg.dynamicSmemBytes = kPairSmem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  // as many pairs as can be resident at once (a GPC with an odd number of SMs
+  // leaves one out), each walking its share of the tiles
+  static std::atomic<int> resident{0};
+  int pairs = resident.load(std::memory_order_relaxed);
+  if (pairs == 0) {
+    e = cudaOccupancyMaxActiveClusters(&pairs, pair_kernel<ACT>, &cfg);
+    if (e != cudaSuccess) return e;
+    if (pairs < 1) return cudaErrorInvalidConfiguration;
+    resident.store(pairs, std::memory_order_relaxed);
+  }
+  cfg.gridDim = dim3(2 * (unsigned)(tiles < pairs ? tiles : pairs));
+  e = cudaLaunchKernelEx(&cfg, pair_kernel<ACT>, mx, mw, mo, p);
+  count_launches(1);
+  return e;
+}
+
+template <int BT, int ACT>
+cudaError_t launch_few(const LinearArgs& a, const LinParams& p, cudaStream_t s) {
+  using C = FewCfg<BT>;
+  CUtensorMap mx, mw;
+  cudaError_t e;
+  if ((e = tmap_view(&mx, a.x.data, a.M, a.K, a.x.sn ? a.x.sn : a.K, BT)) != cudaSuccess ||
+      (e = tmap_view(&mw, a.w.data, a.N, a.K, a.w.sn ? a.w.sn : a.K, 128)) != cudaSuccess)
+    return e;
+  const int64_t ft = (a.N + 127) / 128, mt = (a.M + BT - 1) / BT;
+  // split K while CTAs are fewer than two per SM and each keeps four steps
+  int split = 1;
+  while (split < 8 && ft * mt * split * 2 <= 2 * a.num_sms && p.kblocks >= 2 * split * 4) split *= 2;
+  if (mt > 65535 || ft * split > INT32_MAX) return cudaErrorInvalidConfiguration;
+  e = cudaFuncSetAttribute(few_kernel<BT, ACT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(ft * split), (unsigned)mt);
+  cfg.blockDim = dim3(kFewThreads);
+  cfg.dynamicSmemBytes = C::kSmem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)split;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, few_kernel<BT, ACT>, mx, mw, p, split);
+  count_launches(1);
+  return e;
+}
+
+template <int ACT>
+cudaError_t by_shape(const LinearArgs& a, cudaStream_t s) {
+  LinParams p{};
+  p.bias = static_cast<const bf16*>(a.bias);
+  p.residual = static_cast<const bf16*>(a.residual.data);
+  p.res_sn = a.residual.sn;
+  p.out = static_cast<bf16*>(a.out);
+  p.out_sn = a.out_sn;
+  p.M = (int)a.M;
+  p.N = (int)a.N;
+  p.kblocks = (int)((a.K + kBK - 1) / kBK);
+  p.status = a.status;
+  if (a.M <= 16) return launch_few<16, ACT>(a, p, s);
+  if (a.M <= 32) return launch_few<32, ACT>(a, p, s);
+  if (a.M <= 64) return launch_few<64, ACT>(a, p, s);
+  const int64_t tiles = ((a.M + 255) / 256) * ((a.N + 255) / 256);
+  if (a.M <= 128 || tiles < a.num_sms / 4) return launch_few<128, ACT>(a, p, s);
+  return launch_pair<ACT>(a, p, s);
+}
+
+}  // namespace
+
+cudaError_t tc_linear(const LinearArgs& a, cudaStream_t s) {
+  switch (a.act) {
+    case LA_ACT_RELU: return by_shape<LA_ACT_RELU>(a, s);
+    case LA_ACT_SILU: return by_shape<LA_ACT_SILU>(a, s);
+    case LA_ACT_GELU: return by_shape<LA_ACT_GELU>(a, s);
+    case LA_ACT_SOFTPLUS: return by_shape<LA_ACT_SOFTPLUS>(a, s);
+    default: return by_shape<LA_ACT_NONE>(a, s);
+  }
+}
+
+}  // namespace la
