@@ -12,10 +12,11 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import struct
 
 import torch
 
-from ._binding import _DT, _check, _stream_handle, load
+from ._binding import _DT, _check, load
 
 _ACT = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "softplus": 4}
 
@@ -26,8 +27,9 @@ class LaRows(ctypes.Structure):
                 ("stride_n", ctypes.c_int64)]
 
 
-_R = ctypes.POINTER(LaRows)
-_vp, _i = ctypes.c_void_p, ctypes.c_int
+_vp, _i, _R = ctypes.c_void_p, ctypes.c_int, ctypes.c_char_p
+# la_rows arguments are passed as the bytes of the structure: packing them
+# costs a third of building a ctypes structure, and a decoding step makes six
 ARGTYPES = {
     "la_linear": [_R, _R, _vp, _i, _R, _R, _vp],
     "la_causal_conv": [_R, _vp, _i, _vp, _i, _vp, _vp, _R, _vp, _vp],
@@ -47,27 +49,49 @@ def _fn(name):
     return f
 
 
-def _view(name, t, dtype, ndim):
-    """LaRows of a tensor of 1 to 3 axes whose last is contiguous: [d] is not
-    taken, [B, d] with ``ndim`` 2 becomes [B, 1, d], [B, n, d] stays."""
+_pack = struct.Struct("Pi4xqqqqq").pack
+
+
+def _complain(name, t, dtype):
+    """The reason why a tensor was not taken."""
+    if not isinstance(t, torch.Tensor):
+        return TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        return ValueError(f"{name} must be a CUDA tensor (no CPU path exists)")
+    if t.dtype is not dtype:
+        return ValueError(f"{name} must be {dtype}")
+    return ValueError(f"{name}'s last axis must be contiguous")
+
+
+def _view3(name, t, dtype):
+    """The la_rows of a [B, n, d] tensor whose last axis is contiguous."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor (no CPU path exists)")
-    if t.dtype is not dtype:
-        raise ValueError(f"{name} must be {dtype}")
-    shape, stride = t.shape, t.stride()
-    if len(shape) != ndim:
-        raise ValueError(f"{name} must have {ndim} axes, not {len(shape)}")
-    if stride[-1] != 1 and shape[-1] != 1:
-        raise ValueError(f"{name}'s last axis must be contiguous")
-    if ndim == 3:
-        return LaRows(t.data_ptr(), _DT[dtype], shape[0], shape[1], shape[2], stride[0], stride[1])
-    return LaRows(t.data_ptr(), _DT[dtype], shape[0], 1, shape[1], stride[0], 0)
+    if t.dim() != 3:
+        raise ValueError(f"{name} must have 3 axes, not {t.dim()}")
+    B, n, d = t.shape
+    sb, sn, one = t.stride()
+    if t.dtype is not dtype or not t.is_cuda or (one != 1 and d != 1):
+        raise _complain(name, t, dtype)
+    return _pack(t.data_ptr(), _DT[dtype], B, n, d, sb, sn)
+
+
+def _view2(name, t, dtype):
+    """The la_rows [B, 1, d] of a [B, d] tensor."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must have 2 axes, not {t.dim()}")
+    B, d = t.shape
+    sb, one = t.stride()
+    if t.dtype is not dtype or not t.is_cuda or (one != 1 and d != 1):
+        raise _complain(name, t, dtype)
+    return _pack(t.data_ptr(), _DT[dtype], B, 1, d, sb, 0)
 
 
 def _matrix(name, t, dtype):
-    """LaRows [1, rows, d] of a tensor whose leading axes flatten without a copy."""
+    """The la_rows [1, rows, d] of a tensor whose leading axes flatten
+    without a copy."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dim() < 2:
@@ -77,15 +101,11 @@ def _matrix(name, t, dtype):
             t = t.view(-1, t.shape[-1]) if t.numel() else t.new_empty(0, t.shape[-1])
         except RuntimeError:
             raise ValueError(f"{name}'s leading axes must flatten without a copy") from None
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor (no CPU path exists)")
-    if t.dtype is not dtype:
-        raise ValueError(f"{name} must be {dtype}")
     rows, d = t.shape
-    stride = t.stride()
-    if stride[1] != 1 and d != 1:
-        raise ValueError(f"{name}'s last axis must be contiguous")
-    return LaRows(t.data_ptr(), _DT[dtype], 1, rows, d, 0, stride[0])
+    sn, one = t.stride()
+    if t.dtype is not dtype or not t.is_cuda or (one != 1 and d != 1):
+        raise _complain(name, t, dtype)
+    return _pack(t.data_ptr(), _DT[dtype], 1, rows, d, 0, sn)
 
 
 def _dense(name, t, dtype, shape):
@@ -94,10 +114,8 @@ def _dense(name, t, dtype, shape):
         return None
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor (no CPU path exists)")
-    if t.dtype is not dtype:
-        raise ValueError(f"{name} must be {dtype}")
+    if t.dtype is not dtype or not t.is_cuda:
+        raise _complain(name, t, dtype)
     if t.shape != shape:
         raise ValueError(f"{name} must have the shape {tuple(shape)}, not {tuple(t.shape)}")
     if not t.is_contiguous():
@@ -118,6 +136,19 @@ def _act(activation):
         return _ACT[activation]
     except (KeyError, TypeError):
         raise ValueError(f"activation must be one of {sorted(_ACT)}") from None
+
+
+def _stream(stream, x):
+    """The handle of ``stream``, or of the current stream of x's device (whose
+    raw getter is asked first: it costs a thirtieth of building a Stream)."""
+    if stream is None:
+        if _raw_stream is not None:
+            return _raw_stream(x.device.index)
+        return torch.cuda.current_stream(x.device).cuda_stream
+    return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
+
+
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _alloc_on(stream):
@@ -145,10 +176,10 @@ def linear(x, weight, bias=None, activation="none", residual=None, out=None, str
     dt = _dtype_of(x)
     act = _act(activation)
     xd = _matrix("x", x, dt)
+    if not isinstance(weight, torch.Tensor) or weight.dim() != 2:
+        raise ValueError("weight must be an [N, K] tensor")
     wd = _matrix("weight", weight, dt)
-    if weight.dim() != 2:
-        raise ValueError("weight must be [N, K]")
-    N = wd.n
+    N = weight.shape[0]
     shape = x.shape[:-1] + (N,)
     bp = _dense("bias", bias, dt, (N,))
     rd = None
@@ -156,13 +187,12 @@ def linear(x, weight, bias=None, activation="none", residual=None, out=None, str
         rd = _matrix("residual", residual, dt)
         if residual.shape != shape:
             raise ValueError(f"residual must have the shape {tuple(shape)}")
-        rd = ctypes.byref(rd)
     if out is None:
         out = _new(stream, shape, x, dt)
-    elif out.shape != shape:
+    elif isinstance(out, torch.Tensor) and out.shape != shape:
         raise ValueError(f"out must have the shape {tuple(shape)}")
     od = _matrix("out", out, dt)
-    _check("la_linear", _fn("la_linear")(xd, wd, bp, act, rd, od, _stream_handle(stream)))
+    _check("la_linear", _fn("la_linear")(xd, wd, bp, act, rd, od, _stream(stream, x)))
     return out
 
 
@@ -175,7 +205,7 @@ def causal_conv(x, weight, bias=None, activation="silu", state=None, lengths=Non
     and give 0.  Returns out, or (out, state after the prompt)."""
     dt = _dtype_of(x)
     act = _act(activation)
-    xd = _view("x", x, dt, 3)
+    xd = _view3("x", x, dt)
     B, n, D = x.shape
     if not isinstance(weight, torch.Tensor) or weight.dim() != 2:
         raise ValueError("weight must be a [D, W] tensor")
@@ -186,11 +216,11 @@ def causal_conv(x, weight, bias=None, activation="silu", state=None, lengths=Non
     lp = _dense("lengths", lengths, torch.int32, (B,))
     if out is None:
         out = _new(stream, (B, n, D), x, dt)
-    od = _view("out", out, dt, 3)
+    od = _view3("out", out, dt)
     after = _new(stream, (B, max(W - 1, 0), D), x, dt) if return_state else None
     _check("la_causal_conv", _fn("la_causal_conv")(
         xd, wp, W, bp, act, sp, lp, od, after.data_ptr() if return_state else None,
-        _stream_handle(stream)))
+        _stream(stream, x)))
     return (out, after) if return_state else out
 
 
@@ -199,7 +229,7 @@ def causal_conv_step(state, x, weight, bias=None, activation="silu", out=None, s
     shifted in place; x [B, D].  Returns out [B, D]."""
     dt = _dtype_of(x)
     act = _act(activation)
-    xd = _view("x", x, dt, 2)
+    xd = _view2("x", x, dt)
     B, D = x.shape
     if not isinstance(weight, torch.Tensor) or weight.dim() != 2:
         raise ValueError("weight must be a [D, W] tensor")
@@ -211,25 +241,24 @@ def causal_conv_step(state, x, weight, bias=None, activation="silu", out=None, s
     sp = _dense("state", state, dt, (B, W - 1, D))
     if out is None:
         out = _new(stream, (B, D), x, dt)
-    od = _view("out", out, dt, 2)
+    od = _view2("out", out, dt)
     _check("la_causal_conv_step", _fn("la_causal_conv_step")(
-        sp, xd, wp, W, bp, act, od, _stream_handle(stream)))
+        sp, xd, wp, W, bp, act, od, _stream(stream, x)))
     return out
 
 
-def _scan_args(x, dt, a, b, c, skip, gate, dt_bias, ndim):
+def _scan_args(x, dt, a, b, c, skip, gate, dt_bias, view):
     ty = _dtype_of(x)
-    xd = _view("x", x, ty, ndim)
-    dd = _view("dt", dt, ty, ndim)
-    D = xd.d
+    xd = view("x", x, ty)
+    dd = view("dt", dt, ty)
     if not isinstance(a, torch.Tensor) or a.dim() != 2:
         raise ValueError("a must be a [D, S] tensor")
-    S = a.shape[1]
+    D, S = x.shape[-1], a.shape[1]
     ap = _dense("a", a, torch.float32, (D, S))
-    bd = _view("b", b, ty, ndim)
-    cd = _view("c", c, ty, ndim)
+    bd = view("b", b, ty)
+    cd = view("c", c, ty)
     kp = _dense("skip", skip, torch.float32, (D,))
-    gd = ctypes.byref(_view("gate", gate, ty, ndim)) if gate is not None else None
+    gd = view("gate", gate, ty) if gate is not None else None
     tp = _dense("dt_bias", dt_bias, torch.float32, (D,))
     return ty, S, xd, dd, ap, bd, cd, kp, gd, tp
 
@@ -242,17 +271,17 @@ def selective_scan(x, dt, a, b, c, skip=None, gate=None, dt_bias=None, softplus=
     ``state`` [B, D, S] fp32; ``lengths`` [B] int32: later tokens are not read,
     leave the state alone and give 0.  S is 8, 16, 32 or 64.  Returns out, or
     (out, state after the prompt)."""
-    ty, S, xd, dd, ap, bd, cd, kp, gd, tp = _scan_args(x, dt, a, b, c, skip, gate, dt_bias, 3)
+    ty, S, xd, dd, ap, bd, cd, kp, gd, tp = _scan_args(x, dt, a, b, c, skip, gate, dt_bias, _view3)
     B, n, D = x.shape
     sp = _dense("state", state, torch.float32, (B, D, S))
     lp = _dense("lengths", lengths, torch.int32, (B,))
     if out is None:
         out = _new(stream, (B, n, D), x, ty)
-    od = _view("out", out, ty, 3)
+    od = _view3("out", out, ty)
     after = _new(stream, (B, D, S), x, torch.float32) if return_state else None
     _check("la_selective_scan", _fn("la_selective_scan")(
         xd, dd, ap, S, bd, cd, kp, gd, tp, int(bool(softplus)), sp, lp, od,
-        after.data_ptr() if return_state else None, _stream_handle(stream)))
+        after.data_ptr() if return_state else None, _stream(stream, x)))
     return (out, after) if return_state else out
 
 
@@ -261,13 +290,15 @@ def selective_step(state, x, dt, a, b, c, skip=None, gate=None, dt_bias=None, so
     """la_selective_step: the recurrence's next token.  state [B, D, S] fp32 is
     updated in place; x, dt, gate [B, D]; b, c [B, S]; the rest as
     ``selective_scan``.  Returns out [B, D]."""
-    ty, S, xd, dd, ap, bd, cd, kp, gd, tp = _scan_args(x, dt, a, b, c, skip, gate, dt_bias, 2)
+    ty, S, xd, dd, ap, bd, cd, kp, gd, tp = _scan_args(x, dt, a, b, c, skip, gate, dt_bias,
+                                                       _view2)
     if state is None:
         raise TypeError("state must be a torch.Tensor")
-    sp = _dense("state", state, torch.float32, (xd.B, xd.d, S))
+    shape = x.shape
+    sp = _dense("state", state, torch.float32, shape + (S,))
     if out is None:
-        out = _new(stream, (xd.B, xd.d), x, ty)
-    od = _view("out", out, ty, 2)
+        out = _new(stream, shape, x, ty)
+    od = _view2("out", out, ty)
     _check("la_selective_step", _fn("la_selective_step")(
-        sp, xd, dd, ap, S, bd, cd, kp, gd, tp, int(bool(softplus)), od, _stream_handle(stream)))
+        sp, xd, dd, ap, S, bd, cd, kp, gd, tp, int(bool(softplus)), od, _stream(stream, x)))
     return out

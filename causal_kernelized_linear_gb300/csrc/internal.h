@@ -2,6 +2,7 @@
 // Not part of the public ABI (include/linattn.h is).
 #pragma once
 
+#include <atomic>
 #include <cstddef>
 #include <cstdint>
 #include <cuda.h>
@@ -179,6 +180,10 @@ la_status device_info(DeviceInfo* out);
 // Stream-ordered workspace from the library's pool of the current device
 // (release with cudaFreeAsync on the same stream).
 cudaError_t ws_alloc(void** p, size_t bytes, cudaStream_t s);
+
+// Sets a kernel's dynamic shared memory limit, once per kernel and device:
+// `done` is the caller's record, one bit per device.
+cudaError_t allow_smem(const void* kernel, int bytes, std::atomic<uint64_t>* done);
 
 // The public status of a CUDA runtime result.
 la_status to_status(cudaError_t e);

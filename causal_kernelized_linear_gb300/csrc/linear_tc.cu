@@ -381,7 +381,8 @@ cudaError_t launch_pair(const LinearArgs& a, LinParams p, cudaStream_t s) {
   p.mtiles = (p.M + 255) / 256;
   p.ntiles = (p.N + 255) / 256;
   const int64_t tiles = (int64_t)p.mtiles * p.ntiles;
-  e = cudaFuncSetAttribute(pair_kernel<ACT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kPairSmem);
+  static std::atomic<uint64_t> smem_set{0};
+  e = allow_smem((const void*)pair_kernel<ACT>, kPairSmem, &smem_set);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2);
@@ -424,7 +425,8 @@ cudaError_t launch_few(const LinearArgs& a, const LinParams& p, cudaStream_t s) 
   int split = 1;
   while (split < 8 && ft * mt * split * 2 <= 2 * a.num_sms && p.kblocks >= 2 * split * 4) split *= 2;
   if (mt > 65535 || ft * split > INT32_MAX) return cudaErrorInvalidConfiguration;
-  e = cudaFuncSetAttribute(few_kernel<BT, ACT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  static std::atomic<uint64_t> smem_set{0};
+  e = allow_smem((const void*)few_kernel<BT, ACT>, C::kSmem, &smem_set);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(ft * split), (unsigned)mt);

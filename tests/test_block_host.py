@@ -1,7 +1,5 @@
 """State-space block operators, host side: refusals before anything is queued
 (no GPU needed)."""
-import ctypes
-
 import pytest
 import torch
 
@@ -25,7 +23,7 @@ def rows(b=1, n=8, d=64, ptr=P0, dtype=B.LA_BF16, sb=None, sn=None):
 
 
 def ref(r):
-    return ctypes.byref(r) if r is not None else None
+    return bytes(r) if r is not None else None
 
 
 def lin(x=None, w=None, bias=None, act=0, res=None, out=None):
