@@ -3,30 +3,56 @@
 //   y = (Σ_s C_s·h_s + skip·x)·silu(gate),
 // for every channel (a row of a) with S states.
 //
-// Per (token, channel, state): one 2^x and four fp32 multiply-adds.  A group
-// of G = S/K lanes owns two neighbouring channels, K states of each per lane
-// (in registers over the whole prompt, packed in pairs).  Tokens go in
-// batches of G: each lane of a group loads and prepares one token's Δ and
-// Δ·x, the group shares them through shared memory, and the G partial
-// readouts are summed so that lane i ends with token i and writes it.
+// Per (token, channel, state): one 2^x and four fp32 multiply-adds, against a
+// sixteenth of 8 bytes moved: bound by the special-function and fp32 pipes,
+// so a state element is computed once where possible and every other cost is
+// kept off its path.  A group of G = S/K lanes owns two neighbouring channels,
+// K states of each per lane, in registers over the whole prompt, packed in
+// pairs (one instruction for two multiply-adds).  Tokens go in batches of G:
+// each lane of a group prepares one token's Δ and Δ·x, the group shares them
+// through shared memory, and the G partial readouts are summed so that lane i
+// ends with token i, gates it and writes it.
+//
+// A warp is a CTA and waits for nobody: it keeps kAhead tokens of its inputs
+// in flight with cp.async in a ring of its own.  Where channels alone give
+// too few warps, the sequence is cut into chunks: a first launch reaches each
+// chunk's end state from zero (no readout), and the second starts every chunk
+// from the states before it, combined as h ← exp(a·ΣΔ)·h + end.
 #include "block.cuh"
 #include "internal.h"
+
+#include <atomic>
+#include <type_traits>
 
 namespace la {
 namespace {
 
 using namespace block;
 
-constexpr int kThreads = 128;
-constexpr int kWarps = kThreads / 32;
-constexpr int kTile = 32;   // tokens of B and C converted at a time
+constexpr int kTok = 16;      // tokens per stage of the ring
+constexpr int kRing = 4;      // stages; three are in flight while one is used
 
-template <int S> struct Cfg {
+template <typename T, int S> struct Cfg {
   static constexpr int K = S <= 16 ? 4 : 8;        // states per lane and channel
   static constexpr int G = S / K;                  // lanes per channel pair, tokens per batch
   static constexpr int kPairs = 32 / G;            // channel pairs per warp
-  static constexpr int kChannels = 2 * kPairs * kWarps;   // channels per CTA
+  static constexpr int kCh = 2 * kPairs;           // channels per warp
+  static constexpr int kRowB = kCh * (int)sizeof(T);      // bytes of a token's x, dt or gate
+  static constexpr int kStB = S * (int)sizeof(T);         // bytes of a token's B or C
+  static constexpr int kStage = kTok * (3 * kRowB + 2 * kStB);
+  static constexpr int kSmem = kRing * kStage + 2 * kTok * S * 4 + 32 * 32;
+  static_assert(kRowB % 16 == 0 && kStB % 16 == 0 && kTok % G == 0, "scan layout");
 };
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool take) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+               "r"(take ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
 
 template <typename T>
 __device__ __forceinline__ float2 load2(const T* p) {
@@ -46,149 +72,269 @@ __device__ __forceinline__ void store2(T* p, float a, float b) {
     *reinterpret_cast<float2*>(p) = make_float2(a, b);
 }
 
-template <typename T, int S>
-__global__ void __launch_bounds__(kThreads) scan_kernel(const ScanArgs a, int cblocks) {
-  using C = Cfg<S>;
+template <typename T>
+__device__ __forceinline__ float2 lds2(uint32_t at) {
+  if constexpr (sizeof(T) == 2) {
+    uint32_t r;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(r) : "r"(at) : "memory");
+    return make_float2(tc::bf16lo_to_f32(r), tc::bf16hi_to_f32(r));
+  } else {
+    float2 v;
+    asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(at) : "memory");
+    return v;
+  }
+}
+
+__device__ __forceinline__ void lds_pairs(uint32_t at, f32x2& a, f32x2& b) {
+  asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(a), "=l"(b) : "r"(at) : "memory");
+}
+
+struct Chunks {
+  int count;           // chunks per sequence
+  int len;             // tokens per chunk, a multiple of kTok
+  float* end;          // [B][count][D][S]: state reached from zero
+  float* step;         // [B][count][D]: ΣΔ
+};
+
+// ENDS: the first launch of a cut sequence (end states and ΣΔ of the chunks,
+// the last one excepted); otherwise the outputs.
+template <typename T, int S, bool ENDS>
+__global__ void __launch_bounds__(32) scan_kernel(const ScanArgs a, const int cblocks,
+                                                  const Chunks ch) {
+  using C = Cfg<T, S>;
   constexpr int K = C::K, G = C::G;
-  __shared__ float4 bt[kTile][S / 4], ct[kTile][S / 4];
-  __shared__ float4 du[kWarps][32];
-  const int64_t b = blockIdx.x / cblocks;
+  extern __shared__ __align__(16) uint8_t smem[];
+  const uint32_t ring = tc::smem_u32(smem);
+  const uint32_t bt = ring + kRing * C::kStage, ct = bt + kTok * S * 4, du = ct + kTok * S * 4;
   const int cb = blockIdx.x % cblocks;
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const int lg = lane % G, pair = lane / G;
+  const int k = (blockIdx.x / cblocks) % (ENDS ? ch.count - 1 : ch.count);
+  const int64_t b = blockIdx.x / cblocks / (ENDS ? ch.count - 1 : ch.count);
+  const int lane = threadIdx.x, lg = lane % G, pair = lane / G;
   const int D = (int)a.D, n = (int)a.n;
-  const int cw = cb * C::kChannels + (warp * C::kPairs + pair) * 2;
+  const int c0 = cb * C::kCh, cw = c0 + 2 * pair;
   const bool on = cw < D;         // D is even: both channels or none
   const int c = on ? cw : 0;
   const int len = live_tokens(a.lengths, b, n);
+  const int t_lo = k * ch.len;                              // this chunk: [t_lo, t_hi)
+  const int t_hi = ch.count - 1 - k > 0 ? t_lo + ch.len : n;
+  const int live = min(t_hi, len);                          // the tokens of it that count
 
   f32x2 A[2][K / 2], h[2][K / 2];
 #pragma unroll
-  for (int ch = 0; ch < 2; ++ch) {
-    const int64_t at = (int64_t)(c + ch) * S + lg * K;
+  for (int j = 0; j < 2; ++j)
 #pragma unroll
-    for (int k = 0; k < K / 4; ++k) {
-      const float4 v = *reinterpret_cast<const float4*>(a.a + at + 4 * k);
-      A[ch][2 * k] = pack2(v.x * kLog2e, v.y * kLog2e);
-      A[ch][2 * k + 1] = pack2(v.z * kLog2e, v.w * kLog2e);
+    for (int q = 0; q < K / 4; ++q) {
+      const float4 v = *reinterpret_cast<const float4*>(a.a + (int64_t)(c + j) * S + lg * K + 4 * q);
+      A[j][2 * q] = pack2(v.x * kLog2e, v.y * kLog2e);
+      A[j][2 * q + 1] = pack2(v.z * kLog2e, v.w * kLog2e);
       float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (a.state_in) s = *reinterpret_cast<const float4*>(a.state_in + b * D * S + at + 4 * k);
-      h[ch][2 * k] = pack2(s.x, s.y);
-      h[ch][2 * k + 1] = pack2(s.z, s.w);
+      if (!ENDS || k == 0)
+        if (a.state_in)
+          s = *reinterpret_cast<const float4*>(a.state_in + (b * D + c + j) * S + lg * K + 4 * q);
+      h[j][2 * q] = pack2(s.x, s.y);
+      h[j][2 * q + 1] = pack2(s.z, s.w);
     }
-  }
   float bias[2] = {0.f, 0.f}, skip[2] = {0.f, 0.f};
 #pragma unroll
-  for (int ch = 0; ch < 2; ++ch) {
-    if (a.dt_bias) bias[ch] = a.dt_bias[c + ch];
-    if (a.skip) skip[ch] = a.skip[c + ch];
+  for (int j = 0; j < 2; ++j) {
+    if (a.dt_bias) bias[j] = a.dt_bias[c + j];
+    if (a.skip) skip[j] = a.skip[c + j];
   }
-  const T* xp = static_cast<const T*>(a.x.data) + b * a.x.sb + c;
-  const T* dp = static_cast<const T*>(a.dt.data) + b * a.dt.sb + c;
-  const T* zp = a.gate.data ? static_cast<const T*>(a.gate.data) + b * a.gate.sb + c : nullptr;
-  const T* bp = static_cast<const T*>(a.b.data) + b * a.b.sb;
-  const T* cp = static_cast<const T*>(a.c.data) + b * a.c.sb;
-  T* op = static_cast<T*>(a.out) + b * a.out_sb + c;
+  const char* src[5] = {
+      reinterpret_cast<const char*>(static_cast<const T*>(a.x.data) + b * a.x.sb + c0),
+      reinterpret_cast<const char*>(static_cast<const T*>(a.dt.data) + b * a.dt.sb + c0),
+      reinterpret_cast<const char*>(static_cast<const T*>(a.b.data) + b * a.b.sb),
+      reinterpret_cast<const char*>(static_cast<const T*>(a.c.data) + b * a.c.sb),
+      reinterpret_cast<const char*>(static_cast<const T*>(a.gate.data) + b * a.gate.sb + c0)};
+  const bool gated = a.gate.data != nullptr;
+  const int row_ok = min(C::kRowB, (D - c0) * (int)sizeof(T));   // bytes of a row inside D
 
-  for (int t0 = 0; t0 < len; t0 += kTile) {
-    __syncthreads();
-    for (int e = threadIdx.x; e < kTile * S / 2; e += kThreads) {
-      const int t = e / (S / 2), s = (e % (S / 2)) * 2;
-      float2 bv = make_float2(0.f, 0.f), cv = bv;
-      if (t0 + t < len) {
-        bv = load2(bp + (t0 + t) * a.b.sn + s);
-        cv = load2(cp + (t0 + t) * a.c.sn + s);
-      }
-      reinterpret_cast<float2*>(&bt[t][0])[s / 2] = bv;
-      reinterpret_cast<float2*>(&ct[t][0])[s / 2] = cv;
+  // one tensor of a stage: rows of RB bytes into the ring, absent ones as zeros
+  auto fetch = [&](auto rb, uint32_t dst, const char* from, int64_t sn, int ok, int t0) {
+    constexpr int RB = decltype(rb)::value, PER = RB / 16;
+#pragma unroll
+    for (int e = lane; e < kTok * PER; e += 32) {
+      const int t = e / PER, o = (e % PER) * 16;
+      const bool take = t0 + t < live && o < ok;
+      cp_async16(dst + t * RB + o, take ? from + (t0 + t) * sn * (int64_t)sizeof(T) + o : from, take);
     }
-    __syncthreads();
-    const int tn = min(kTile, len - t0);
-    for (int tb = 0; tb < tn; tb += G) {
-      const int t = t0 + tb + lg;
-      float2 x = make_float2(0.f, 0.f), dt = x;
-      if (t < len) {
-        x = load2(xp + t * a.x.sn);
-        dt = load2(dp + t * a.dt.sn);
-        dt.x += bias[0];
-        dt.y += bias[1];
-        if (a.softplus) {
-          dt.x = softplus(dt.x);
-          dt.y = softplus(dt.y);
+  };
+  auto fetch_stage = [&](int slot, int t0) {
+    if (t0 < live) {
+      const uint32_t st = ring + slot * C::kStage;
+      std::integral_constant<int, C::kRowB> rb;
+      std::integral_constant<int, C::kStB> sb;
+      fetch(rb, st, src[0], a.x.sn, row_ok, t0);
+      fetch(rb, st + kTok * C::kRowB, src[1], a.dt.sn, row_ok, t0);
+      fetch(sb, st + 3 * kTok * C::kRowB, src[2], a.b.sn, C::kStB, t0);
+      if (!ENDS) {
+        if (gated) fetch(rb, st + 2 * kTok * C::kRowB, src[4], a.gate.sn, row_ok, t0);
+        fetch(sb, st + 3 * kTok * C::kRowB + kTok * C::kStB, src[3], a.c.sn, C::kStB, t0);
+      }
+    }
+    cp_commit();
+  };
+#pragma unroll
+  for (int i = 0; i < kRing - 1; ++i) fetch_stage(i, t_lo + i * kTok);
+
+  if (!ENDS && k > 0) {
+    // the state entering this chunk; a chunk past the length has ΣΔ = 0 and a
+    // zero end state, and leaves it alone
+    for (int p = 0; p < k; ++p) {
+      const int64_t at = (b * ch.count + p) * D + c;
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const float sd = p > 0 ? ch.step[at + j] : 0.f;
+        const f32x2 s2 = pack2(sd, sd);
+#pragma unroll
+        for (int q = 0; q < K / 2; ++q) {
+          const float2 e = *reinterpret_cast<const float2*>(ch.end + (at + j) * S + lg * K + 2 * q);
+          float e0, e1;
+          unpack2(mul2(s2, A[j][q]), e0, e1);
+          // the first chunk's end state was reached from state_in
+          h[j][q] = p > 0 ? fma2(pack2(tc::ex2_f32(e0), tc::ex2_f32(e1)), h[j][q], pack2(e.x, e.y))
+                          : pack2(e.x, e.y);
         }
       }
+    }
+  }
+
+  float sum[2] = {0.f, 0.f};   // ΣΔ of this lane's tokens (ENDS)
+  T* op = ENDS ? nullptr : static_cast<T*>(a.out) + b * a.out_sb + c;
+  int slot = 0;
+  for (int t0 = t_lo; t0 < live; t0 += kTok) {
+    cp_wait<kRing - 2>();
+    __syncwarp();
+    const uint32_t st = ring + slot * C::kStage;
+    // B and C of the stage as fp32
+    {
+      constexpr int V = kVec<T>, PER = S / V;
+#pragma unroll
+      for (int e = lane; e < kTok * PER; e += 32) {
+        float f[V];
+        unpack<T>(tc::lds128(st + 3 * kTok * C::kRowB + e * 16), f);
+#pragma unroll
+        for (int i = 0; i < V; i += 4)
+          tc::sts128(bt + (e * V + i) * 4, make_uint4(__float_as_uint(f[i]), __float_as_uint(f[i + 1]),
+                                                      __float_as_uint(f[i + 2]), __float_as_uint(f[i + 3])));
+        if (!ENDS) {
+          unpack<T>(tc::lds128(st + 3 * kTok * C::kRowB + kTok * C::kStB + e * 16), f);
+#pragma unroll
+          for (int i = 0; i < V; i += 4)
+            tc::sts128(ct + (e * V + i) * 4, make_uint4(__float_as_uint(f[i]), __float_as_uint(f[i + 1]),
+                                                        __float_as_uint(f[i + 2]), __float_as_uint(f[i + 3])));
+        }
+      }
+    }
+    const int tn = min(kTok, live - t0);
+    for (int tb = 0; tb < tn; tb += G) {
+      const int ti = tb + lg, t = t0 + ti;
+      const uint32_t at = st + ti * C::kRowB + pair * 2 * (int)sizeof(T);
+      const float2 x = lds2<T>(at);
+      float2 dt = lds2<T>(at + kTok * C::kRowB);
+      dt.x += bias[0];
+      dt.y += bias[1];
+      if (a.softplus) {
+        dt.x = softplus(dt.x);
+        dt.y = softplus(dt.y);
+      }
+      if (t >= live) dt = make_float2(0.f, 0.f);   // a step of zero changes nothing
+      if (ENDS) {
+        sum[0] += dt.x;
+        sum[1] += dt.y;
+      }
+      const float u0 = dt.x * x.x, u1 = dt.y * x.y;
       __syncwarp();
-      du[warp][lane] = make_float4(dt.x, dt.y, dt.x * x.x, dt.y * x.y);
+      tc::sts128(du + lane * 32, make_uint4(__float_as_uint(dt.x), __float_as_uint(dt.x),
+                                            __float_as_uint(dt.y), __float_as_uint(dt.y)));
+      tc::sts128(du + lane * 32 + 16, make_uint4(__float_as_uint(u0), __float_as_uint(u0),
+                                                 __float_as_uint(u1), __float_as_uint(u1)));
       __syncwarp();
       float y[2][G];
 #pragma unroll
       for (int i = 0; i < G; ++i) {
-        const float4 v = du[warp][pair * G + i];
-        const f32x2 d2[2] = {pack2(v.x, v.x), pack2(v.y, v.y)};
-        const f32x2 u2[2] = {pack2(v.z, v.z), pack2(v.w, v.w)};
-        f32x2 acc[2] = {0ull, 0ull};
+        f32x2 d2[2], u2[2], acc[2] = {0ull, 0ull};
+        lds_pairs(du + (pair * G + i) * 32, d2[0], d2[1]);
+        lds_pairs(du + (pair * G + i) * 32 + 16, u2[0], u2[1]);
 #pragma unroll
-        for (int k = 0; k < K / 4; ++k) {
-          const float4 B4 = bt[tb + i][lg * (K / 4) + k], C4 = ct[tb + i][lg * (K / 4) + k];
-          const f32x2 B2[2] = {pack2(B4.x, B4.y), pack2(B4.z, B4.w)};
-          const f32x2 C2[2] = {pack2(C4.x, C4.y), pack2(C4.z, C4.w)};
+        for (int q = 0; q < K / 4; ++q) {
+          f32x2 B2[2], C2[2] = {0ull, 0ull};
+          lds_pairs(bt + ((tb + i) * S + lg * K + 4 * q) * 4, B2[0], B2[1]);
+          if (!ENDS) lds_pairs(ct + ((tb + i) * S + lg * K + 4 * q) * 4, C2[0], C2[1]);
 #pragma unroll
-          for (int j = 0; j < 2; ++j)
+          for (int r = 0; r < 2; ++r)
 #pragma unroll
-            for (int ch = 0; ch < 2; ++ch) {
+            for (int j = 0; j < 2; ++j) {
               float e0, e1;
-              unpack2(mul2(d2[ch], A[ch][2 * k + j]), e0, e1);
+              unpack2(mul2(d2[j], A[j][2 * q + r]), e0, e1);
               const f32x2 dec = pack2(tc::ex2_f32(e0), tc::ex2_f32(e1));
-              f32x2& hh = h[ch][2 * k + j];
-              hh = fma2(dec, hh, mul2(u2[ch], B2[j]));
-              acc[ch] = fma2(C2[j], hh, acc[ch]);
+              f32x2& hh = h[j][2 * q + r];
+              hh = fma2(dec, hh, mul2(u2[j], B2[r]));
+              if (!ENDS) acc[j] = fma2(C2[r], hh, acc[j]);
             }
         }
 #pragma unroll
-        for (int ch = 0; ch < 2; ++ch) {
+        for (int j = 0; j < 2; ++j) {
           float lo, hi;
-          unpack2(acc[ch], lo, hi);
-          y[ch][i] = lo + hi;
+          unpack2(acc[j], lo, hi);
+          y[j][i] = lo + hi;
         }
       }
-      // lane i of the group keeps token i: halve the tokens per exchange
+      if constexpr (!ENDS) {
+        // lane i of the group keeps token i: halve the tokens per exchange
 #pragma unroll
-      for (int m = G / 2; m >= 1; m /= 2) {
-        const bool up = (lg & m) != 0;
+        for (int m = G / 2; m >= 1; m /= 2) {
+          const bool up = (lg & m) != 0;
 #pragma unroll
-        for (int i = 0; i < m; ++i)
+          for (int i = 0; i < m; ++i)
 #pragma unroll
-          for (int ch = 0; ch < 2; ++ch) {
-            const float give = up ? y[ch][i] : y[ch][i + m];
-            const float keep = up ? y[ch][i + m] : y[ch][i];
-            y[ch][i] = keep + __shfl_xor_sync(0xffffffffu, give, m);
-          }
-      }
-      if (on && t < len) {
+            for (int j = 0; j < 2; ++j) {
+              const float give = up ? y[j][i] : y[j][i + m];
+              const float keep = up ? y[j][i + m] : y[j][i];
+              y[j][i] = keep + __shfl_xor_sync(0xffffffffu, give, m);
+            }
+        }
         float o0 = fmaf(skip[0], x.x, y[0][0]), o1 = fmaf(skip[1], x.y, y[1][0]);
-        if (zp) {
-          const float2 z = load2(zp + t * a.gate.sn);
+        if (gated) {
+          const float2 z = lds2<T>(at + 2 * kTok * C::kRowB);
           o0 *= silu(z.x);
           o1 *= silu(z.y);
         }
-        store2(op + t * a.out_sn, o0, o1);
+        if (on && t < live) store2(op + t * a.out_sn, o0, o1);
       }
     }
+    __syncwarp();
+    // the stage used before this one is free
+    fetch_stage((slot + kRing - 1) % kRing, t0 + (kRing - 1) * kTok);
+    slot = (slot + 1) % kRing;
   }
-  // tokens past the length
-  if (on)
-    for (int t = len + lg; t < n; t += G) store2(op + t * a.out_sn, 0.f, 0.f);
-  if (on && a.state_out) {
+  cp_wait<0>();
+  float* to = ENDS ? ch.end + ((b * ch.count + k) * D + c) * S
+                   : (a.state_out && k == ch.count - 1 ? a.state_out + (b * D + c) * S : nullptr);
+  if (on && to) {
 #pragma unroll
-    for (int ch = 0; ch < 2; ++ch)
+    for (int j = 0; j < 2; ++j)
 #pragma unroll
-      for (int k = 0; k < K / 4; ++k) {
+      for (int q = 0; q < K / 4; ++q) {
         float4 v;
-        unpack2(h[ch][2 * k], v.x, v.y);
-        unpack2(h[ch][2 * k + 1], v.z, v.w);
-        *reinterpret_cast<float4*>(a.state_out + b * D * S + (int64_t)(c + ch) * S + lg * K +
-                                   4 * k) = v;
+        unpack2(h[j][2 * q], v.x, v.y);
+        unpack2(h[j][2 * q + 1], v.z, v.w);
+        *reinterpret_cast<float4*>(to + j * S + lg * K + 4 * q) = v;
       }
+  }
+  if constexpr (ENDS) {
+#pragma unroll
+    for (int m = G / 2; m >= 1; m /= 2) {
+      sum[0] += __shfl_xor_sync(0xffffffffu, sum[0], m);
+      sum[1] += __shfl_xor_sync(0xffffffffu, sum[1], m);
+    }
+    if (on && lg == 0) {
+      ch.step[(b * ch.count + k) * D + c] = sum[0];
+      ch.step[(b * ch.count + k) * D + c + 1] = sum[1];
+    }
+  } else if (on) {
+    // tokens past the length
+    for (int t = max(t_lo, live) + lg; t < t_hi; t += G) store2(op + t * a.out_sn, 0.f, 0.f);
   }
 }
 
@@ -237,13 +383,55 @@ __global__ void __launch_bounds__(kStepThreads) step_kernel(const ScanArgs a) {
   }
 }
 
+// Warps a sequence should give the GPU before it is cut into chunks.
+constexpr int kWarpsWanted = 4;      // per SM
+
 template <typename T, int S>
 cudaError_t launch_scan(const ScanArgs& a, cudaStream_t s) {
-  const int64_t cblocks = (a.D + Cfg<S>::kChannels - 1) / Cfg<S>::kChannels;
-  if (cblocks * a.B > INT32_MAX) return cudaErrorInvalidConfiguration;
-  scan_kernel<T, S><<<(unsigned)(cblocks * a.B), kThreads, 0, s>>>(a, (int)cblocks);
-  count_launches(1);
-  return cudaGetLastError();
+  using C = Cfg<T, S>;
+  const int64_t cblocks = (a.D + C::kCh - 1) / C::kCh;
+  const int64_t warps = cblocks * a.B;
+  if (warps > INT32_MAX) return cudaErrorInvalidConfiguration;
+  Chunks ch{1, (int)a.n, nullptr, nullptr};
+  const int64_t wanted = (int64_t)kWarpsWanted * a.num_sms;
+  if (warps < wanted && a.n >= 16 * kTok) {
+    int64_t count = (2 * wanted + warps - 1) / warps;
+    count = count < a.n / (8 * kTok) ? count : a.n / (8 * kTok);
+    int64_t len = (a.n + count - 1) / count;
+    len = (len + kTok - 1) / kTok * kTok;
+    ch.len = (int)len;
+    ch.count = (int)((a.n + len - 1) / len);
+  }
+  static std::atomic<uint64_t> set_all{0}, set_ends{0};
+  cudaError_t e = allow_smem((const void*)scan_kernel<T, S, false>, C::kSmem, &set_all);
+  if (e != cudaSuccess) return e;
+  float* ws = nullptr;
+  if (ch.count > 1) {
+    e = allow_smem((const void*)scan_kernel<T, S, true>, C::kSmem, &set_ends);
+    if (e != cudaSuccess) return e;
+    const size_t rows = (size_t)a.B * ch.count * a.D;
+    e = ws_alloc(reinterpret_cast<void**>(&ws), rows * (S + 1) * sizeof(float), s);
+    if (e != cudaSuccess) {
+      cudaGetLastError();
+      return e;
+    }
+    ch.end = ws;
+    ch.step = ws + rows * S;
+    scan_kernel<T, S, true><<<(unsigned)(warps * (ch.count - 1)), 32, C::kSmem, s>>>(
+        a, (int)cblocks, ch);
+    count_launches(1);
+    e = cudaGetLastError();
+  }
+  if (e == cudaSuccess) {
+    scan_kernel<T, S, false><<<(unsigned)(warps * ch.count), 32, C::kSmem, s>>>(a, (int)cblocks, ch);
+    count_launches(1);
+    e = cudaGetLastError();
+  }
+  if (ws) {
+    const cudaError_t f = cudaFreeAsync(ws, s);
+    if (e == cudaSuccess) e = f;
+  }
+  return e;
 }
 
 template <typename T, int S>
