@@ -40,7 +40,8 @@ template <typename T, int S> struct Cfg {
   static constexpr int kRowB = kCh * (int)sizeof(T);      // bytes of a token's x, dt or gate
   static constexpr int kStB = S * (int)sizeof(T);         // bytes of a token's B or C
   static constexpr int kStage = kTok * (3 * kRowB + 2 * kStB);
-  static constexpr int kSmem = kRing * kStage + 2 * kTok * S * 4 + 32 * 32;
+  static constexpr int kDu = kTok * kPairs * 16;          // Δ (and Δ·x) of a stage, each twice
+  static constexpr int kSmem = kRing * kStage + 2 * kTok * S * 4 + 2 * kDu;
   static_assert(kRowB % 16 == 0 && kStB % 16 == 0 && kTok % G == 0, "scan layout");
 };
 
@@ -72,21 +73,23 @@ __device__ __forceinline__ void store2(T* p, float a, float b) {
     *reinterpret_cast<float2*>(p) = make_float2(a, b);
 }
 
+// Two neighbouring values in shared memory.
 template <typename T>
-__device__ __forceinline__ float2 lds2(uint32_t at) {
+__device__ __forceinline__ float2 load2s(const T* p) {
   if constexpr (sizeof(T) == 2) {
-    uint32_t r;
-    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(r) : "r"(at) : "memory");
+    const uint32_t r = *reinterpret_cast<const uint32_t*>(p);
     return make_float2(tc::bf16lo_to_f32(r), tc::bf16hi_to_f32(r));
   } else {
-    float2 v;
-    asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(at) : "memory");
-    return v;
+    return *reinterpret_cast<const float2*>(p);
   }
 }
 
-__device__ __forceinline__ void lds_pairs(uint32_t at, f32x2& a, f32x2& b) {
-  asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(a), "=l"(b) : "r"(at) : "memory");
+// Four fp32 values in shared memory as two pairs.  A plain load: the loop
+// that uses it writes nothing there, so loads move ahead of the arithmetic.
+__device__ __forceinline__ void lds_pairs(const uint8_t* at, f32x2& a, f32x2& b) {
+  const ulonglong2 v = *reinterpret_cast<const ulonglong2*>(at);
+  a = v.x;
+  b = v.y;
 }
 
 struct Chunks {
@@ -105,7 +108,10 @@ __global__ void __launch_bounds__(32) scan_kernel(const ScanArgs a, const int cb
   constexpr int K = C::K, G = C::G;
   extern __shared__ __align__(16) uint8_t smem[];
   const uint32_t ring = tc::smem_u32(smem);
-  const uint32_t bt = ring + kRing * C::kStage, ct = bt + kTok * S * 4, du = ct + kTok * S * 4;
+  uint8_t* const bt = smem + kRing * C::kStage;       // B, C as fp32 [token][state]
+  uint8_t* const ct = bt + kTok * S * 4;
+  uint8_t* const dd = ct + kTok * S * 4;              // [token][pair]: Δ, each value twice
+  uint8_t* const uu = dd + C::kDu;                    // Δ·x likewise
   const int cb = blockIdx.x % cblocks;
   const int k = (blockIdx.x / cblocks) % (ENDS ? ch.count - 1 : ch.count);
   const int64_t b = blockIdx.x / cblocks / (ENDS ? ch.count - 1 : ch.count);
@@ -149,14 +155,18 @@ __global__ void __launch_bounds__(32) scan_kernel(const ScanArgs a, const int cb
   const bool gated = a.gate.data != nullptr;
   const int row_ok = min(C::kRowB, (D - c0) * (int)sizeof(T));   // bytes of a row inside D
 
-  // one tensor of a stage: rows of RB bytes into the ring, absent ones as zeros
+  // A stage's 16-byte pieces of each tensor are dealt to the lanes; absent
+  // ones are written as zeros.
   auto fetch = [&](auto rb, uint32_t dst, const char* from, int64_t sn, int ok, int t0) {
     constexpr int RB = decltype(rb)::value, PER = RB / 16;
 #pragma unroll
-    for (int e = lane; e < kTok * PER; e += 32) {
+    for (int e0 = 0; e0 < kTok * PER; e0 += 32) {
+      const int e = e0 + lane;
       const int t = e / PER, o = (e % PER) * 16;
       const bool take = t0 + t < live && o < ok;
-      cp_async16(dst + t * RB + o, take ? from + (t0 + t) * sn * (int64_t)sizeof(T) + o : from, take);
+      if (kTok * PER % 32 == 0 || e < kTok * PER)
+        cp_async16(dst + t * RB + o, take ? from + (t0 + t) * sn * (int64_t)sizeof(T) + o : from,
+                   take);
     }
   };
   auto fetch_stage = [&](int slot, int t0) {
@@ -205,62 +215,66 @@ __global__ void __launch_bounds__(32) scan_kernel(const ScanArgs a, const int cb
   for (int t0 = t_lo; t0 < live; t0 += kTok) {
     cp_wait<kRing - 2>();
     __syncwarp();
-    const uint32_t st = ring + slot * C::kStage;
+    const uint8_t* st = smem + slot * C::kStage;
     // B and C of the stage as fp32
     {
       constexpr int V = kVec<T>, PER = S / V;
 #pragma unroll
-      for (int e = lane; e < kTok * PER; e += 32) {
-        float f[V];
-        unpack<T>(tc::lds128(st + 3 * kTok * C::kRowB + e * 16), f);
+      for (int e = lane; e < kTok * PER; e += 32)
 #pragma unroll
-        for (int i = 0; i < V; i += 4)
-          tc::sts128(bt + (e * V + i) * 4, make_uint4(__float_as_uint(f[i]), __float_as_uint(f[i + 1]),
-                                                      __float_as_uint(f[i + 2]), __float_as_uint(f[i + 3])));
-        if (!ENDS) {
-          unpack<T>(tc::lds128(st + 3 * kTok * C::kRowB + kTok * C::kStB + e * 16), f);
+        for (int w = 0; w < (ENDS ? 1 : 2); ++w) {
+          float f[V];
+          unpack<T>(*reinterpret_cast<const uint4*>(st + 3 * kTok * C::kRowB + w * kTok * C::kStB + e * 16), f);
+          float4* to = reinterpret_cast<float4*>((w ? ct : bt) + e * V * 4);
 #pragma unroll
-          for (int i = 0; i < V; i += 4)
-            tc::sts128(ct + (e * V + i) * 4, make_uint4(__float_as_uint(f[i]), __float_as_uint(f[i + 1]),
-                                                        __float_as_uint(f[i + 2]), __float_as_uint(f[i + 3])));
+          for (int i = 0; i < V; i += 4) to[i / 4] = make_float4(f[i], f[i + 1], f[i + 2], f[i + 3]);
+        }
+    }
+    // each lane's tokens: Δ and Δ·x for the group; the skip term and the gate
+    // stay with the lane
+    float xs[kTok / G][2], zs[kTok / G][2];
+#pragma unroll
+    for (int bi = 0; bi < kTok / G; ++bi) {
+      const int ti = bi * G + lg;
+      const T* at = reinterpret_cast<const T*>(st + ti * C::kRowB) + 2 * pair;
+      const float2 x = load2s(at);
+      float2 dt = load2s(at + kTok * C::kCh);
+      dt.x += bias[0];
+      dt.y += bias[1];
+      if (a.softplus) dt = softplus2(dt);
+      if (t0 + ti >= live) dt = make_float2(0.f, 0.f);   // a step of zero changes nothing
+      const float u0 = dt.x * x.x, u1 = dt.y * x.y;
+      *reinterpret_cast<float4*>(dd + (ti * C::kPairs + pair) * 16) = make_float4(dt.x, dt.x, dt.y, dt.y);
+      *reinterpret_cast<float4*>(uu + (ti * C::kPairs + pair) * 16) = make_float4(u0, u0, u1, u1);
+      if constexpr (ENDS) {
+        sum[0] += dt.x;
+        sum[1] += dt.y;
+      } else {
+        xs[bi][0] = skip[0] * x.x;
+        xs[bi][1] = skip[1] * x.y;
+        zs[bi][0] = zs[bi][1] = 1.f;
+        if (gated) {
+          const float2 z = load2s(at + 2 * kTok * C::kCh);
+          zs[bi][0] = silu(z.x);
+          zs[bi][1] = silu(z.y);
         }
       }
     }
-    const int tn = min(kTok, live - t0);
-    for (int tb = 0; tb < tn; tb += G) {
-      const int ti = tb + lg, t = t0 + ti;
-      const uint32_t at = st + ti * C::kRowB + pair * 2 * (int)sizeof(T);
-      const float2 x = lds2<T>(at);
-      float2 dt = lds2<T>(at + kTok * C::kRowB);
-      dt.x += bias[0];
-      dt.y += bias[1];
-      if (a.softplus) {
-        dt.x = softplus(dt.x);
-        dt.y = softplus(dt.y);
-      }
-      if (t >= live) dt = make_float2(0.f, 0.f);   // a step of zero changes nothing
-      if (ENDS) {
-        sum[0] += dt.x;
-        sum[1] += dt.y;
-      }
-      const float u0 = dt.x * x.x, u1 = dt.y * x.y;
-      __syncwarp();
-      tc::sts128(du + lane * 32, make_uint4(__float_as_uint(dt.x), __float_as_uint(dt.x),
-                                            __float_as_uint(dt.y), __float_as_uint(dt.y)));
-      tc::sts128(du + lane * 32 + 16, make_uint4(__float_as_uint(u0), __float_as_uint(u0),
-                                                 __float_as_uint(u1), __float_as_uint(u1)));
-      __syncwarp();
+    __syncwarp();
+#pragma unroll
+    for (int bi = 0; bi < kTok / G; ++bi) {
       float y[2][G];
 #pragma unroll
       for (int i = 0; i < G; ++i) {
+        const int ti = bi * G + i;
         f32x2 d2[2], u2[2], acc[2] = {0ull, 0ull};
-        lds_pairs(du + (pair * G + i) * 32, d2[0], d2[1]);
-        lds_pairs(du + (pair * G + i) * 32 + 16, u2[0], u2[1]);
+        lds_pairs(dd + (ti * C::kPairs + pair) * 16, d2[0], d2[1]);
+        lds_pairs(uu + (ti * C::kPairs + pair) * 16, u2[0], u2[1]);
 #pragma unroll
         for (int q = 0; q < K / 4; ++q) {
           f32x2 B2[2], C2[2] = {0ull, 0ull};
-          lds_pairs(bt + ((tb + i) * S + lg * K + 4 * q) * 4, B2[0], B2[1]);
-          if (!ENDS) lds_pairs(ct + ((tb + i) * S + lg * K + 4 * q) * 4, C2[0], C2[1]);
+          lds_pairs(bt + (ti * S + lg * K + 4 * q) * 4, B2[0], B2[1]);
+          if (!ENDS) lds_pairs(ct + (ti * S + lg * K + 4 * q) * 4, C2[0], C2[1]);
 #pragma unroll
           for (int r = 0; r < 2; ++r)
 #pragma unroll
@@ -270,14 +284,16 @@ __global__ void __launch_bounds__(32) scan_kernel(const ScanArgs a, const int cb
               const f32x2 dec = pack2(tc::ex2_f32(e0), tc::ex2_f32(e1));
               f32x2& hh = h[j][2 * q + r];
               hh = fma2(dec, hh, mul2(u2[j], B2[r]));
-              if (!ENDS) acc[j] = fma2(C2[r], hh, acc[j]);
+              if (!ENDS) acc[j] = q + r == 0 ? mul2(C2[r], hh) : fma2(C2[r], hh, acc[j]);
             }
         }
+        if constexpr (!ENDS) {
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          float lo, hi;
-          unpack2(acc[j], lo, hi);
-          y[j][i] = lo + hi;
+          for (int j = 0; j < 2; ++j) {
+            float lo, hi;
+            unpack2(acc[j], lo, hi);
+            y[j][i] = lo + hi;
+          }
         }
       }
       if constexpr (!ENDS) {
@@ -294,13 +310,10 @@ __global__ void __launch_bounds__(32) scan_kernel(const ScanArgs a, const int cb
               y[j][i] = keep + __shfl_xor_sync(0xffffffffu, give, m);
             }
         }
-        float o0 = fmaf(skip[0], x.x, y[0][0]), o1 = fmaf(skip[1], x.y, y[1][0]);
-        if (gated) {
-          const float2 z = lds2<T>(at + 2 * kTok * C::kRowB);
-          o0 *= silu(z.x);
-          o1 *= silu(z.y);
-        }
-        if (on && t < live) store2(op + t * a.out_sn, o0, o1);
+        const int t = t0 + bi * G + lg;
+        if (on && t < live)
+          store2(op + t * a.out_sn, (y[0][0] + xs[bi][0]) * zs[bi][0],
+                 (y[1][0] + xs[bi][1]) * zs[bi][1]);
       }
     }
     __syncwarp();
