@@ -30,7 +30,7 @@ namespace {
 using namespace block;
 
 constexpr int kTok = 16;      // tokens per stage of the ring
-constexpr int kRing = 4;      // stages; three are in flight while one is used
+constexpr int kRing = 3;      // stages; three are in flight while one is used
 
 template <typename T, int S> struct Cfg {
   static constexpr int K = S <= 16 ? 4 : 8;        // states per lane and channel
@@ -40,8 +40,9 @@ template <typename T, int S> struct Cfg {
   static constexpr int kRowB = kCh * (int)sizeof(T);      // bytes of a token's x, dt or gate
   static constexpr int kStB = S * (int)sizeof(T);         // bytes of a token's B or C
   static constexpr int kStage = kTok * (3 * kRowB + 2 * kStB);
-  static constexpr int kDu = kTok * kPairs * 16;          // Δ (and Δ·x) of a stage, each twice
-  static constexpr int kSmem = kRing * kStage + 2 * kTok * S * 4 + 2 * kDu;
+  static constexpr int kDu = kTok * kPairs * 16;          // Δ and Δ·x of a stage
+  static constexpr int kPrep = kDu + 2 * kTok * S * 4;    // and B, C as fp32
+  static constexpr int kSmem = kRing * kStage + 2 * kPrep;
   static_assert(kRowB % 16 == 0 && kStB % 16 == 0 && kTok % G == 0, "scan layout");
 };
 
@@ -108,14 +109,10 @@ __global__ void __launch_bounds__(32) scan_kernel(const ScanArgs a, const int cb
   constexpr int K = C::K, G = C::G;
   extern __shared__ __align__(16) uint8_t smem[];
   const uint32_t ring = tc::smem_u32(smem);
-  uint8_t* const bt = smem + kRing * C::kStage;       // B, C as fp32 [token][state]
-  uint8_t* const ct = bt + kTok * S * 4;
-  uint8_t* const dd = ct + kTok * S * 4;              // [token][pair]: Δ, each value twice
-  uint8_t* const uu = dd + C::kDu;                    // Δ·x likewise
   const int cb = blockIdx.x % cblocks;
   const int k = (blockIdx.x / cblocks) % (ENDS ? ch.count - 1 : ch.count);
   const int64_t b = blockIdx.x / cblocks / (ENDS ? ch.count - 1 : ch.count);
-  const int lane = threadIdx.x, lg = lane % G, pair = lane / G;
+  const int lane = threadIdx.x, lg = lane / C::kPairs, pair = lane % C::kPairs;
   const int D = (int)a.D, n = (int)a.n;
   const int c0 = cb * C::kCh, cw = c0 + 2 * pair;
   const bool on = cw < D;         // D is even: both channels or none
@@ -211,82 +208,90 @@ __global__ void __launch_bounds__(32) scan_kernel(const ScanArgs a, const int cb
 
   float sum[2] = {0.f, 0.f};   // ΣΔ of this lane's tokens (ENDS)
   T* op = ENDS ? nullptr : static_cast<T*>(a.out) + b * a.out_sb + c;
-  int slot = 0;
-  for (int t0 = t_lo; t0 < live; t0 += kTok) {
-    cp_wait<kRing - 2>();
-    __syncwarp();
-    const uint8_t* st = smem + slot * C::kStage;
-    // B and C of the stage as fp32
-    {
-      constexpr int V = kVec<T>, PER = S / V;
+
+  // A stage is prepared while the one before it is scanned, so that the two
+  // chains of dependent instructions fill each other's gaps.  prep: [token]
+  // [pair] Δ and Δ·x, then B and C as fp32; two of them, used in turn.
+  uint8_t* const prep0 = smem + kRing * C::kStage;
+  auto widen = [&](const uint8_t* st, uint8_t* prep) {
+    constexpr int V = kVec<T>, PER = S / V;
 #pragma unroll
-      for (int e = lane; e < kTok * PER; e += 32)
+    for (int e = lane; e < kTok * PER; e += 32)
 #pragma unroll
-        for (int w = 0; w < (ENDS ? 1 : 2); ++w) {
-          float f[V];
-          unpack<T>(*reinterpret_cast<const uint4*>(st + 3 * kTok * C::kRowB + w * kTok * C::kStB + e * 16), f);
-          float4* to = reinterpret_cast<float4*>((w ? ct : bt) + e * V * 4);
+      for (int w = 0; w < (ENDS ? 1 : 2); ++w) {
+        float f[V];
+        unpack<T>(*reinterpret_cast<const uint4*>(st + 3 * kTok * C::kRowB + w * kTok * C::kStB + e * 16), f);
+        float4* to = reinterpret_cast<float4*>(prep + C::kDu + w * kTok * S * 4 + e * V * 4);
 #pragma unroll
-          for (int i = 0; i < V; i += 4) to[i / 4] = make_float4(f[i], f[i + 1], f[i + 2], f[i + 3]);
-        }
-    }
-    // each lane's tokens: Δ and Δ·x for the group; the skip term and the gate
-    // stay with the lane
-    float xs[kTok / G][2], zs[kTok / G][2];
-#pragma unroll
-    for (int bi = 0; bi < kTok / G; ++bi) {
-      const int ti = bi * G + lg;
-      const T* at = reinterpret_cast<const T*>(st + ti * C::kRowB) + 2 * pair;
-      const float2 x = load2s(at);
-      float2 dt = load2s(at + kTok * C::kCh);
-      dt.x += bias[0];
-      dt.y += bias[1];
-      if (a.softplus) dt = softplus2(dt);
-      if (t0 + ti >= live) dt = make_float2(0.f, 0.f);   // a step of zero changes nothing
-      const float u0 = dt.x * x.x, u1 = dt.y * x.y;
-      *reinterpret_cast<float4*>(dd + (ti * C::kPairs + pair) * 16) = make_float4(dt.x, dt.x, dt.y, dt.y);
-      *reinterpret_cast<float4*>(uu + (ti * C::kPairs + pair) * 16) = make_float4(u0, u0, u1, u1);
-      if constexpr (ENDS) {
-        sum[0] += dt.x;
-        sum[1] += dt.y;
-      } else {
-        xs[bi][0] = skip[0] * x.x;
-        xs[bi][1] = skip[1] * x.y;
-        zs[bi][0] = zs[bi][1] = 1.f;
-        if (gated) {
-          const float2 z = load2s(at + 2 * kTok * C::kCh);
-          zs[bi][0] = silu(z.x);
-          zs[bi][1] = silu(z.y);
-        }
+        for (int i = 0; i < V; i += 4) to[i / 4] = make_float4(f[i], f[i + 1], f[i + 2], f[i + 3]);
+      }
+  };
+  // token bi·G + lg of the stage that starts at t0: Δ and Δ·x for the group;
+  // the skip term and the gate stay with the lane
+  float xs[2][kTok / G][2], zs[2][kTok / G][2];
+  auto prepare = [&](const uint8_t* st, uint8_t* prep, int t0, int bi, float (&x1)[2], float (&z1)[2]) {
+    const int ti = bi * G + lg;
+    const T* at = reinterpret_cast<const T*>(st + ti * C::kRowB) + 2 * pair;
+    const float2 x = load2s(at);
+    float2 dt = load2s(at + kTok * C::kCh);
+    dt.x += bias[0];
+    dt.y += bias[1];
+    if (a.softplus) dt = softplus2(dt);
+    if (t0 + ti >= live) dt = make_float2(0.f, 0.f);   // a step of zero changes nothing
+    if constexpr (ENDS) {
+      sum[0] += dt.x;
+      sum[1] += dt.y;
+    } else {
+      x1[0] = skip[0] * x.x;
+      x1[1] = skip[1] * x.y;
+      z1[0] = z1[1] = 1.f;
+      if (gated) {
+        const float2 z = load2s(at + 2 * kTok * C::kCh);
+        z1[0] = silu(z.x);
+        z1[1] = silu(z.y);
       }
     }
-    __syncwarp();
+    return make_float4(dt.x, dt.y, dt.x * x.x, dt.y * x.y);
+  };
+  auto put = [&](uint8_t* prep, int bi, const float4& v) {
+    *reinterpret_cast<float4*>(prep + ((bi * G + lg) * C::kPairs + pair) * 16) = v;
+  };
+  // scans the stage prepared in `prep` and prepares the next one from `st`
+  auto stage = [&](int t0, const uint8_t* prep, uint8_t* next, const uint8_t* st,
+                   const float (&x0)[kTok / G][2], const float (&z0)[kTok / G][2],
+                   float (&x1)[kTok / G][2], float (&z1)[kTok / G][2]) {
+    const uint8_t *bt = prep + C::kDu, *ct = bt + kTok * S * 4;
 #pragma unroll
     for (int bi = 0; bi < kTok / G; ++bi) {
-      float y[2][G];
+      float4 du[G];
+      f32x2 B2[G][K / 2], C2[G][K / 2];
 #pragma unroll
       for (int i = 0; i < G; ++i) {
         const int ti = bi * G + i;
-        f32x2 d2[2], u2[2], acc[2] = {0ull, 0ull};
-        lds_pairs(dd + (ti * C::kPairs + pair) * 16, d2[0], d2[1]);
-        lds_pairs(uu + (ti * C::kPairs + pair) * 16, u2[0], u2[1]);
+        du[i] = *reinterpret_cast<const float4*>(prep + (ti * C::kPairs + pair) * 16);
 #pragma unroll
         for (int q = 0; q < K / 4; ++q) {
-          f32x2 B2[2], C2[2] = {0ull, 0ull};
-          lds_pairs(bt + (ti * S + lg * K + 4 * q) * 4, B2[0], B2[1]);
-          if (!ENDS) lds_pairs(ct + (ti * S + lg * K + 4 * q) * 4, C2[0], C2[1]);
-#pragma unroll
-          for (int r = 0; r < 2; ++r)
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              float e0, e1;
-              unpack2(mul2(d2[j], A[j][2 * q + r]), e0, e1);
-              const f32x2 dec = pack2(tc::ex2_f32(e0), tc::ex2_f32(e1));
-              f32x2& hh = h[j][2 * q + r];
-              hh = fma2(dec, hh, mul2(u2[j], B2[r]));
-              if (!ENDS) acc[j] = q + r == 0 ? mul2(C2[r], hh) : fma2(C2[r], hh, acc[j]);
-            }
+          lds_pairs(bt + (ti * S + lg * K + 4 * q) * 4, B2[i][2 * q], B2[i][2 * q + 1]);
+          if (!ENDS) lds_pairs(ct + (ti * S + lg * K + 4 * q) * 4, C2[i][2 * q], C2[i][2 * q + 1]);
         }
+      }
+      const float4 nx = prepare(st, next, t0 + kTok, bi, x1[bi], z1[bi]);
+      float y[2][G];
+#pragma unroll
+      for (int i = 0; i < G; ++i) {
+        const f32x2 d2[2] = {pack2(du[i].x, du[i].x), pack2(du[i].y, du[i].y)};
+        const f32x2 u2[2] = {pack2(du[i].z, du[i].z), pack2(du[i].w, du[i].w)};
+        f32x2 acc[2] = {0ull, 0ull};
+#pragma unroll
+        for (int q = 0; q < K / 2; ++q)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            float e0, e1;
+            unpack2(mul2(d2[j], A[j][q]), e0, e1);
+            const f32x2 dec = pack2(tc::ex2_f32(e0), tc::ex2_f32(e1));
+            h[j][q] = fma2(dec, h[j][q], mul2(u2[j], B2[i][q]));
+            if (!ENDS) acc[j] = q == 0 ? mul2(C2[i][q], h[j][q]) : fma2(C2[i][q], h[j][q], acc[j]);
+          }
         if constexpr (!ENDS) {
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
@@ -307,19 +312,42 @@ __global__ void __launch_bounds__(32) scan_kernel(const ScanArgs a, const int cb
             for (int j = 0; j < 2; ++j) {
               const float give = up ? y[j][i] : y[j][i + m];
               const float keep = up ? y[j][i + m] : y[j][i];
-              y[j][i] = keep + __shfl_xor_sync(0xffffffffu, give, m);
+              y[j][i] = keep + __shfl_xor_sync(0xffffffffu, give, m * C::kPairs);
             }
         }
         const int t = t0 + bi * G + lg;
         if (on && t < live)
-          store2(op + t * a.out_sn, (y[0][0] + xs[bi][0]) * zs[bi][0],
-                 (y[1][0] + xs[bi][1]) * zs[bi][1]);
+          store2(op + t * a.out_sn, (y[0][0] + x0[bi][0]) * z0[bi][0],
+                 (y[1][0] + x0[bi][1]) * z0[bi][1]);
       }
+      put(next, bi, nx);
     }
+    widen(st, next);
     __syncwarp();
-    // the stage used before this one is free
+  };
+  if (t_lo < live) {
+    cp_wait<kRing - 2>();
+    __syncwarp();
+    widen(smem, prep0);
+#pragma unroll
+    for (int bi = 0; bi < kTok / G; ++bi)
+      put(prep0, bi, prepare(smem, prep0, t_lo, bi, xs[0][bi], zs[0][bi]));
+    __syncwarp();
+  }
+  int slot = 0;   // ring slot of the stage that is scanned
+  auto advance = [&](int t0) {
+    // the prepared stage's slot is free; the next one has to be there
     fetch_stage((slot + kRing - 1) % kRing, t0 + (kRing - 1) * kTok);
+    cp_wait<kRing - 2>();
+    __syncwarp();
     slot = (slot + 1) % kRing;
+  };
+  for (int t0 = t_lo; t0 < live; t0 += 2 * kTok) {
+    advance(t0);
+    stage(t0, prep0, prep0 + C::kPrep, smem + slot * C::kStage, xs[0], zs[0], xs[1], zs[1]);
+    if (t0 + kTok >= live) break;
+    advance(t0 + kTok);
+    stage(t0 + kTok, prep0 + C::kPrep, prep0, smem + slot * C::kStage, xs[1], zs[1], xs[0], zs[0]);
   }
   cp_wait<0>();
   float* to = ENDS ? ch.end + ((b * ch.count + k) * D + c) * S
@@ -338,8 +366,8 @@ __global__ void __launch_bounds__(32) scan_kernel(const ScanArgs a, const int cb
   if constexpr (ENDS) {
 #pragma unroll
     for (int m = G / 2; m >= 1; m /= 2) {
-      sum[0] += __shfl_xor_sync(0xffffffffu, sum[0], m);
-      sum[1] += __shfl_xor_sync(0xffffffffu, sum[1], m);
+      sum[0] += __shfl_xor_sync(0xffffffffu, sum[0], m * C::kPairs);
+      sum[1] += __shfl_xor_sync(0xffffffffu, sum[1], m * C::kPairs);
     }
     if (on && lg == 0) {
       ch.step[(b * ch.count + k) * D + c] = sum[0];
@@ -396,8 +424,9 @@ __global__ void __launch_bounds__(kStepThreads) step_kernel(const ScanArgs a) {
   }
 }
 
-// Warps a sequence should give the GPU before it is cut into chunks.
-constexpr int kWarpsWanted = 4;      // per SM
+constexpr int kWarpsWanted = 4;     // warps per SM below which sequences are cut
+constexpr int kWarpsCut = 16;       // warps per SM that cut sequences should give
+constexpr int kChunkMin = 64;       // tokens
 
 template <typename T, int S>
 cudaError_t launch_scan(const ScanArgs& a, cudaStream_t s) {
@@ -407,9 +436,9 @@ cudaError_t launch_scan(const ScanArgs& a, cudaStream_t s) {
   if (warps > INT32_MAX) return cudaErrorInvalidConfiguration;
   Chunks ch{1, (int)a.n, nullptr, nullptr};
   const int64_t wanted = (int64_t)kWarpsWanted * a.num_sms;
-  if (warps < wanted && a.n >= 16 * kTok) {
-    int64_t count = (2 * wanted + warps - 1) / warps;
-    count = count < a.n / (8 * kTok) ? count : a.n / (8 * kTok);
+  if (warps < wanted && a.n >= 2 * kChunkMin) {
+    int64_t count = (kWarpsCut * (int64_t)a.num_sms + warps - 1) / warps;
+    count = count < a.n / kChunkMin ? count : a.n / kChunkMin;
     int64_t len = (a.n + count - 1) / count;
     len = (len + kTok - 1) / kTok * kTok;
     ch.len = (int)len;
