@@ -44,6 +44,7 @@ template <typename T, int S> struct Cfg {
   static constexpr int kPrep = kDu + 2 * kTok * S * 4;    // and B, C as fp32
   static constexpr int kSmem = kRing * kStage + 2 * kPrep;
   static_assert(kRowB % 16 == 0 && kStB % 16 == 0 && kTok % G == 0, "scan layout");
+  static_assert(32 % (kRowB / 16) == 0 && 32 % (kStB / 16) == 0, "pieces per row");
 };
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool take) {
@@ -153,30 +154,48 @@ __global__ void __launch_bounds__(32) scan_kernel(const ScanArgs a, const int cb
   const int row_ok = min(C::kRowB, (D - c0) * (int)sizeof(T));   // bytes of a row inside D
 
   // A stage's 16-byte pieces of each tensor are dealt to the lanes; absent
-  // ones are written as zeros.
-  auto fetch = [&](auto rb, uint32_t dst, const char* from, int64_t sn, int ok, int t0) {
-    constexpr int RB = decltype(rb)::value, PER = RB / 16;
+  // ones are written as zeros.  Every lane keeps the address of its first
+  // piece of the next stage.
+  const char* next_piece[5];
+  const int64_t sn[5] = {a.x.sn * (int64_t)sizeof(T), a.dt.sn * (int64_t)sizeof(T),
+                         a.b.sn * (int64_t)sizeof(T), a.c.sn * (int64_t)sizeof(T),
+                         a.gate.sn * (int64_t)sizeof(T)};
+#pragma unroll
+  for (int i = 0; i < 5; ++i) {
+    const int per = (i == 2 || i == 3 ? C::kStB : C::kRowB) / 16;
+    next_piece[i] = src[i] + (t_lo + lane / per) * sn[i] + (lane % per) * 16;
+  }
+  auto fetch = [&](auto rb, auto which, uint32_t dst, int ok, int t0, bool whole) {
+    constexpr int RB = decltype(rb)::value, PER = RB / 16, I = decltype(which)::value;
 #pragma unroll
     for (int e0 = 0; e0 < kTok * PER; e0 += 32) {
       const int e = e0 + lane;
-      const int t = e / PER, o = (e % PER) * 16;
-      const bool take = t0 + t < live && o < ok;
-      if (kTok * PER % 32 == 0 || e < kTok * PER)
-        cp_async16(dst + t * RB + o, take ? from + (t0 + t) * sn * (int64_t)sizeof(T) + o : from,
-                   take);
+      const char* from = next_piece[I] + (e0 / PER) * sn[I];
+      if (kTok * PER % 32 == 0 || e < kTok * PER) {
+        if (whole) {
+          cp_async16(dst + e * 16, from, true);
+        } else {
+          const bool take = t0 + e / PER < live && (e % PER) * 16 < ok;
+          cp_async16(dst + e * 16, take ? from : src[I], take);
+        }
+      }
     }
+    next_piece[I] += kTok * sn[I];
   };
   auto fetch_stage = [&](int slot, int t0) {
     if (t0 < live) {
       const uint32_t st = ring + slot * C::kStage;
+      const bool whole = t0 + kTok <= live && row_ok == C::kRowB;
       std::integral_constant<int, C::kRowB> rb;
       std::integral_constant<int, C::kStB> sb;
-      fetch(rb, st, src[0], a.x.sn, row_ok, t0);
-      fetch(rb, st + kTok * C::kRowB, src[1], a.dt.sn, row_ok, t0);
-      fetch(sb, st + 3 * kTok * C::kRowB, src[2], a.b.sn, C::kStB, t0);
+      fetch(rb, std::integral_constant<int, 0>(), st, row_ok, t0, whole);
+      fetch(rb, std::integral_constant<int, 1>(), st + kTok * C::kRowB, row_ok, t0, whole);
+      fetch(sb, std::integral_constant<int, 2>(), st + 3 * kTok * C::kRowB, C::kStB, t0, whole);
       if (!ENDS) {
-        if (gated) fetch(rb, st + 2 * kTok * C::kRowB, src[4], a.gate.sn, row_ok, t0);
-        fetch(sb, st + 3 * kTok * C::kRowB + kTok * C::kStB, src[3], a.c.sn, C::kStB, t0);
+        if (gated)
+          fetch(rb, std::integral_constant<int, 4>(), st + 2 * kTok * C::kRowB, row_ok, t0, whole);
+        fetch(sb, std::integral_constant<int, 3>(), st + 3 * kTok * C::kRowB + kTok * C::kStB,
+              C::kStB, t0, whole);
       }
     }
     cp_commit();
@@ -425,7 +444,7 @@ __global__ void __launch_bounds__(kStepThreads) step_kernel(const ScanArgs a) {
 }
 
 constexpr int kWarpsWanted = 4;     // warps per SM below which sequences are cut
-constexpr int kWarpsCut = 16;       // warps per SM that cut sequences should give
+constexpr int kWarpsCut = 24;       // warps per SM that cut sequences should give
 constexpr int kChunkMin = 64;       // tokens
 
 template <typename T, int S>
