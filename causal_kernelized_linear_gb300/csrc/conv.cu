@@ -17,6 +17,7 @@ using namespace block;
 
 constexpr int kThreads = 128;
 constexpr int kRun = 32;   // tokens a thread walks
+constexpr int kGroup = 8;  // tokens whose loads a thread has in flight
 
 template <typename T, int W>
 __device__ __forceinline__ void load_taps(const ConvArgs& a, int64_t c, float (&w)[W][kVec<T>],
@@ -84,7 +85,26 @@ __global__ void __launch_bounds__(kThreads) conv_kernel(const ConvArgs a, int ve
   for (int j = 0; j < W - 1; ++j)
     unpack<T>(t0 < len ? row_of<T, W>(a, b, t0 - (W - 1) + j, c) : make_uint4(0, 0, 0, 0), win[j]);
   T* out = static_cast<T*>(a.out) + b * a.out_sb + c;
-  for (int t = t0; t < t1; ++t) {
+  int t = t0;
+  // whole groups of kGroup live tokens: their loads are issued together
+  const int whole = t0 + max(0, min(t1, len) - t0) / kGroup * kGroup;
+  const T* xp = static_cast<const T*>(a.x.data) + b * a.x.sb + c;
+  for (; t < whole; t += kGroup) {
+    uint4 raw[kGroup];
+#pragma unroll
+    for (int i = 0; i < kGroup; ++i)
+      raw[i] = __ldg(reinterpret_cast<const uint4*>(xp + (t + i) * a.x.sn));
+#pragma unroll
+    for (int i = 0; i < kGroup; ++i) {
+      unpack<T>(raw[i], win[W - 1]);
+      *reinterpret_cast<uint4*>(out + (t + i) * a.out_sn) = taps<T, W, SILU>(win, w, bias);
+#pragma unroll
+      for (int j = 0; j < W - 1; ++j)
+#pragma unroll
+        for (int k = 0; k < V; ++k) win[j][k] = win[j + 1][k];
+    }
+  }
+  for (; t < t1; ++t) {
     uint4 y = make_uint4(0, 0, 0, 0);
     if (t < len) {
       unpack<T>(row_of<T, W>(a, b, t, c), win[W - 1]);

@@ -398,48 +398,66 @@ __global__ void __launch_bounds__(32) scan_kernel(const ScanArgs a, const int cb
   }
 }
 
-// One token: a lane owns four states of a channel, S/4 lanes a channel.  The
-// state's read and write are nearly all of the traffic (8 bytes per state
-// element); a warp touches 512 contiguous bytes of it.
+// One token: a lane owns four states of a channel (S/4 lanes a channel) in R
+// batch entries, so that it reads a once for all of them and has R loads of
+// the state in flight.  The state's read and write are nearly all of the
+// traffic (8 bytes per state element); a warp touches 512 contiguous bytes.
 constexpr int kStepThreads = 256;
 
-template <typename T, int S>
+template <typename T, int S, int R>
 __global__ void __launch_bounds__(kStepThreads) step_kernel(const ScanArgs a) {
   constexpr int G = S / 4;
   const int64_t item = (int64_t)blockIdx.x * kStepThreads + threadIdx.x;
-  const bool on = item < a.B * a.D * G;
+  const int64_t per = a.D * G, groups = (a.B + R - 1) / R;
+  const bool on = item < groups * per;
   const int64_t it = on ? item : 0;
   const int q = (int)(it % G);
-  const int64_t bc = it / G;
-  const int c = (int)(bc % a.D);
-  const int64_t b = bc / a.D;
-  float* hp = a.state_out + bc * S + 4 * q;
-  const float4 h = *reinterpret_cast<const float4*>(hp);
-  const float4 A = *reinterpret_cast<const float4*>(a.a + (int64_t)c * S + 4 * q);
-  const float x = to_f32(static_cast<const T*>(a.x.data)[b * a.x.sb + c]);
-  float dt = to_f32(static_cast<const T*>(a.dt.data)[b * a.dt.sb + c]);
-  const float2 B0 = load2(static_cast<const T*>(a.b.data) + b * a.b.sb + 4 * q);
-  const float2 B1 = load2(static_cast<const T*>(a.b.data) + b * a.b.sb + 4 * q + 2);
-  const float2 C0 = load2(static_cast<const T*>(a.c.data) + b * a.c.sb + 4 * q);
-  const float2 C1 = load2(static_cast<const T*>(a.c.data) + b * a.c.sb + 4 * q + 2);
-  float z = 0.f;
-  if (a.gate.data) z = to_f32(static_cast<const T*>(a.gate.data)[b * a.gate.sb + c]);
-  if (a.dt_bias) dt += a.dt_bias[c];
-  if (a.softplus) dt = softplus(dt);
-  const float u = dt * x, d2 = dt * kLog2e;
-  float4 r;
-  r.x = fmaf(tc::ex2_f32(d2 * A.x), h.x, u * B0.x);
-  r.y = fmaf(tc::ex2_f32(d2 * A.y), h.y, u * B0.y);
-  r.z = fmaf(tc::ex2_f32(d2 * A.z), h.z, u * B1.x);
-  r.w = fmaf(tc::ex2_f32(d2 * A.w), h.w, u * B1.y);
-  if (on) *reinterpret_cast<float4*>(hp) = r;
-  float y = fmaf(r.x, C0.x, fmaf(r.y, C0.y, fmaf(r.z, C1.x, r.w * C1.y)));
+  const int c = (int)(it % per / G);
+  const int64_t b0 = it / per * R;
+  const int rows = (int)min((int64_t)R, a.B - b0);
+  float4 h[R];
+  float2 Bv[R][2], Cv[R][2];
+  float x[R], dt[R], z[R];
 #pragma unroll
-  for (int m = G / 2; m >= 1; m /= 2) y += __shfl_xor_sync(0xffffffffu, y, m);
-  if (on && q == 0) {
-    if (a.skip) y = fmaf(a.skip[c], x, y);
-    if (a.gate.data) y *= silu(z);
-    static_cast<T*>(a.out)[b * a.out_sb + c] = from_f32<T>(y);
+  for (int r = 0; r < R; ++r) {
+    const int64_t b = b0 + (r < rows ? r : 0);
+    h[r] = __ldcs(reinterpret_cast<const float4*>(a.state_out + (b * a.D + c) * S + 4 * q));
+  }
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const int64_t b = b0 + (r < rows ? r : 0);
+    x[r] = to_f32(static_cast<const T*>(a.x.data)[b * a.x.sb + c]);
+    dt[r] = to_f32(static_cast<const T*>(a.dt.data)[b * a.dt.sb + c]);
+    z[r] = a.gate.data ? to_f32(static_cast<const T*>(a.gate.data)[b * a.gate.sb + c]) : 0.f;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      Bv[r][i] = load2(static_cast<const T*>(a.b.data) + b * a.b.sb + 4 * q + 2 * i);
+      Cv[r][i] = load2(static_cast<const T*>(a.c.data) + b * a.c.sb + 4 * q + 2 * i);
+    }
+  }
+  float4 A = *reinterpret_cast<const float4*>(a.a + (int64_t)c * S + 4 * q);
+  A.x *= kLog2e, A.y *= kLog2e, A.z *= kLog2e, A.w *= kLog2e;
+  const float bias = a.dt_bias ? a.dt_bias[c] : 0.f, skip = a.skip ? a.skip[c] : 0.f;
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    float d = dt[r] + bias;
+    if (a.softplus) d = softplus(d);
+    const float u = d * x[r];
+    float4 n;
+    n.x = fmaf(tc::ex2_f32(d * A.x), h[r].x, u * Bv[r][0].x);
+    n.y = fmaf(tc::ex2_f32(d * A.y), h[r].y, u * Bv[r][0].y);
+    n.z = fmaf(tc::ex2_f32(d * A.z), h[r].z, u * Bv[r][1].x);
+    n.w = fmaf(tc::ex2_f32(d * A.w), h[r].w, u * Bv[r][1].y);
+    float y = fmaf(n.x, Cv[r][0].x, fmaf(n.y, Cv[r][0].y, fmaf(n.z, Cv[r][1].x, n.w * Cv[r][1].y)));
+#pragma unroll
+    for (int m = G / 2; m >= 1; m /= 2) y += __shfl_xor_sync(0xffffffffu, y, m);
+    if (!on || r >= rows) continue;
+    __stcs(reinterpret_cast<float4*>(a.state_out + ((b0 + r) * a.D + c) * S + 4 * q), n);
+    if (q == 0) {
+      y = fmaf(skip, x[r], y);
+      if (a.gate.data) y *= silu(z[r]);
+      static_cast<T*>(a.out)[(b0 + r) * a.out_sb + c] = from_f32<T>(y);
+    }
   }
 }
 
@@ -495,13 +513,21 @@ cudaError_t launch_scan(const ScanArgs& a, cudaStream_t s) {
   return e;
 }
 
-template <typename T, int S>
-cudaError_t launch_step(const ScanArgs& a, cudaStream_t s) {
-  const int64_t blocks = (a.B * a.D * (S / 4) + kStepThreads - 1) / kStepThreads;
+template <typename T, int S, int R>
+cudaError_t launch_step_rows(const ScanArgs& a, cudaStream_t s) {
+  const int64_t blocks = ((a.B + R - 1) / R * a.D * (S / 4) + kStepThreads - 1) / kStepThreads;
   if (blocks > INT32_MAX) return cudaErrorInvalidConfiguration;
-  step_kernel<T, S><<<(unsigned)blocks, kStepThreads, 0, s>>>(a);
+  step_kernel<T, S, R><<<(unsigned)blocks, kStepThreads, 0, s>>>(a);
   count_launches(1);
   return cudaGetLastError();
+}
+
+// Four batch entries per lane where that leaves a thousand threads per SM.
+template <typename T, int S>
+cudaError_t launch_step(const ScanArgs& a, cudaStream_t s) {
+  return a.B >= 4 && a.B / 4 * a.D * (S / 4) >= (int64_t)1024 * a.num_sms
+             ? launch_step_rows<T, S, 4>(a, s)
+             : launch_step_rows<T, S, 1>(a, s);
 }
 
 template <typename T>
