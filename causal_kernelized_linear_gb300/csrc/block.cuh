@@ -78,6 +78,18 @@ __device__ __forceinline__ uint4 pack(const float (&f)[kVec<T>]) {
                       __float_as_uint(f[3]));
 }
 
+// 16 bytes from global to shared memory in the background; `bytes` 0 writes
+// zeros and reads nothing.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes = 16) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// Waits until at most N of this thread's groups are in flight.
+template <int N> __device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 // Tokens of batch entry b that count: lengths[b] taken into [0, n].
 __device__ __forceinline__ int live_tokens(const int32_t* lengths, int64_t b, int n) {
   if (!lengths) return n;

@@ -6,7 +6,9 @@
 // owns the channels of one 16-byte vector and walks a run of tokens with the
 // last W − 1 inputs in registers, so every input is read once per run (plus
 // W − 1 rows where runs meet, which the neighbouring run has just read into
-// L2) and written once; a warp's accesses are 512 contiguous bytes.
+// L2) and written once; a warp's accesses are 512 contiguous bytes.  Rows
+// arrive through a ring in shared memory (cp.async), twelve ahead of the one
+// in use: held in registers they would cost the occupancy that hides HBM.
 #include "block.cuh"
 #include "internal.h"
 
@@ -17,7 +19,23 @@ using namespace block;
 
 constexpr int kThreads = 128;
 constexpr int kRun = 32;   // tokens a thread walks
-constexpr int kGroup = 8;  // tokens whose loads a thread has in flight
+constexpr int kGroup = 4;  // tokens per step of its ring
+constexpr int kRing = 12;  // rows of the ring
+
+// A thread's channels, run and batch entry.
+struct Item {
+  uint32_t vec, run;
+  int64_t b;
+};
+__device__ __forceinline__ Item item_of(int64_t item, uint32_t vecs, uint32_t runs, int64_t B) {
+  if ((int64_t)vecs * runs * B <= UINT32_MAX) {   // 32-bit divisions
+    uint32_t i = (uint32_t)item;
+    const uint32_t v = i % vecs;
+    i /= vecs;
+    return Item{v, i % runs, (int64_t)(i / runs)};
+  }
+  return Item{(uint32_t)(item % vecs), (uint32_t)(item / vecs % runs), item / vecs / runs};
+}
 
 template <typename T, int W>
 __device__ __forceinline__ void load_taps(const ConvArgs& a, int64_t c, float (&w)[W][kVec<T>],
@@ -67,56 +85,56 @@ __device__ __forceinline__ uint4 taps(const float (&win)[W][kVec<T>],
 }
 
 template <typename T, int W, bool SILU>
-__global__ void __launch_bounds__(kThreads) conv_kernel(const ConvArgs a, int vecs, int runs) {
+__global__ void __launch_bounds__(kThreads) conv_kernel(const ConvArgs a, uint32_t vecs,
+                                                        uint32_t runs) {
   constexpr int V = kVec<T>;
+  __shared__ uint4 ring[kRing][kThreads];   // a thread reads only what it copied itself
   const int64_t item = (int64_t)blockIdx.x * kThreads + threadIdx.x;
   if (item >= (int64_t)vecs * runs * a.B) return;
-  const int64_t c = (item % vecs) * V;
-  const int run = (int)((item / vecs) % runs);
-  const int64_t b = item / vecs / runs;
+  const Item at = item_of(item, vecs, runs, a.B);
+  const int64_t c = (int64_t)at.vec * V, b = at.b;
   const int n = (int)a.n;
   const int len = live_tokens(a.lengths, b, n);
+  const int t0 = (int)at.run * kRun;
+  const int t1 = min(t0 + kRun, n), live = min(t1, len);
+  const T* xp = static_cast<const T*>(a.x.data) + b * a.x.sb + c;
+  const uint32_t mine = tc::smem_u32(&ring[0][threadIdx.x]);
+  auto fetch = [&](int t, int slot) {   // kGroup rows from token t
+#pragma unroll
+    for (int i = 0; i < kGroup; ++i)
+      if (t + i < live) cp_async16(mine + (slot + i) * kThreads * 16, xp + (t + i) * a.x.sn);
+    cp_commit();
+  };
+#pragma unroll
+  for (int g = 0; g < kRing / kGroup - 1; ++g) fetch(t0 + g * kGroup, g * kGroup);
   float w[W][V], bias[V];
   load_taps<T, W>(a, c, w, bias);
-  const int t0 = run * kRun;
-  const int t1 = min(t0 + kRun, n);
   float win[W][V];
 #pragma unroll
   for (int j = 0; j < W - 1; ++j)
     unpack<T>(t0 < len ? row_of<T, W>(a, b, t0 - (W - 1) + j, c) : make_uint4(0, 0, 0, 0), win[j]);
   T* out = static_cast<T*>(a.out) + b * a.out_sb + c;
-  int t = t0;
-  // whole groups of kGroup live tokens: their loads are issued together
-  const int whole = t0 + max(0, min(t1, len) - t0) / kGroup * kGroup;
-  const T* xp = static_cast<const T*>(a.x.data) + b * a.x.sb + c;
-  for (; t < whole; t += kGroup) {
-    uint4 raw[kGroup];
-#pragma unroll
-    for (int i = 0; i < kGroup; ++i)
-      raw[i] = __ldg(reinterpret_cast<const uint4*>(xp + (t + i) * a.x.sn));
+  int slot = 0;
+  for (int t = t0; t < t1; t += kGroup) {
+    fetch(t + kRing - kGroup, (slot + kRing - kGroup) % kRing);
+    cp_wait<kRing / kGroup - 1>();
 #pragma unroll
     for (int i = 0; i < kGroup; ++i) {
-      unpack<T>(raw[i], win[W - 1]);
-      *reinterpret_cast<uint4*>(out + (t + i) * a.out_sn) = taps<T, W, SILU>(win, w, bias);
+      uint4 y = make_uint4(0, 0, 0, 0);
+      if (t + i < live) {
+        unpack<T>(ring[slot + i][threadIdx.x], win[W - 1]);
+        y = taps<T, W, SILU>(win, w, bias);
 #pragma unroll
-      for (int j = 0; j < W - 1; ++j)
+        for (int j = 0; j < W - 1; ++j)
 #pragma unroll
-        for (int k = 0; k < V; ++k) win[j][k] = win[j + 1][k];
+          for (int k = 0; k < V; ++k) win[j][k] = win[j + 1][k];
+      }
+      if (t + i < t1) *reinterpret_cast<uint4*>(out + (t + i) * a.out_sn) = y;
     }
+    slot = (slot + kGroup) % kRing;
   }
-  for (; t < t1; ++t) {
-    uint4 y = make_uint4(0, 0, 0, 0);
-    if (t < len) {
-      unpack<T>(row_of<T, W>(a, b, t, c), win[W - 1]);
-      y = taps<T, W, SILU>(win, w, bias);
-#pragma unroll
-      for (int j = 0; j < W - 1; ++j)
-#pragma unroll
-        for (int i = 0; i < V; ++i) win[j][i] = win[j + 1][i];
-    }
-    *reinterpret_cast<uint4*>(out + t * a.out_sn) = y;
-  }
-  if (run == 0 && a.state_out) {
+  cp_wait<0>();
+  if (at.run == 0 && a.state_out) {
     T* so = static_cast<T*>(a.state_out) + b * (W - 1) * a.D + c;
 #pragma unroll
     for (int j = 0; j < W - 1; ++j)
@@ -125,12 +143,12 @@ __global__ void __launch_bounds__(kThreads) conv_kernel(const ConvArgs a, int ve
 }
 
 template <typename T, int W, bool SILU>
-__global__ void __launch_bounds__(kThreads) conv_step_kernel(const ConvArgs a, int vecs) {
+__global__ void __launch_bounds__(kThreads) conv_step_kernel(const ConvArgs a, uint32_t vecs) {
   constexpr int V = kVec<T>;
   const int64_t item = (int64_t)blockIdx.x * kThreads + threadIdx.x;
   if (item >= vecs * a.B) return;
-  const int64_t c = (item % vecs) * V;
-  const int64_t b = item / vecs;
+  const Item at = item_of(item, vecs, 1, a.B);
+  const int64_t c = (int64_t)at.vec * V, b = at.b;
   T* st = static_cast<T*>(a.state_out) + b * (W - 1) * a.D + c;
   uint4 raw[W];
 #pragma unroll
@@ -148,8 +166,8 @@ __global__ void __launch_bounds__(kThreads) conv_step_kernel(const ConvArgs a, i
 
 template <typename T, int W, bool SILU>
 cudaError_t launch(const ConvArgs& a, bool step, cudaStream_t s) {
-  const int vecs = (int)(a.D / kVec<T>);
-  const int runs = step ? 1 : (int)((a.n + kRun - 1) / kRun);
+  const uint32_t vecs = (uint32_t)(a.D / kVec<T>);
+  const uint32_t runs = step ? 1 : (uint32_t)((a.n + kRun - 1) / kRun);
   const int64_t blocks = ((int64_t)vecs * runs * a.B + kThreads - 1) / kThreads;
   if (blocks > INT32_MAX) return cudaErrorInvalidConfiguration;
   if (step)

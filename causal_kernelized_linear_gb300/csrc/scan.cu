@@ -47,16 +47,6 @@ template <typename T, int S> struct Cfg {
   static_assert(32 % (kRowB / 16) == 0 && 32 % (kStB / 16) == 0, "pieces per row");
 };
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool take) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
-               "r"(take ? 16 : 0)
-               : "memory");
-}
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N> __device__ __forceinline__ void cp_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
 template <typename T>
 __device__ __forceinline__ float2 load2(const T* p) {
   if constexpr (sizeof(T) == 2) {
@@ -173,10 +163,10 @@ __global__ void __launch_bounds__(32) scan_kernel(const ScanArgs a, const int cb
       const char* from = next_piece[I] + (e0 / PER) * sn[I];
       if (kTok * PER % 32 == 0 || e < kTok * PER) {
         if (whole) {
-          cp_async16(dst + e * 16, from, true);
+          cp_async16(dst + e * 16, from);
         } else {
           const bool take = t0 + e / PER < live && (e % PER) * 16 < ok;
-          cp_async16(dst + e * 16, take ? from : src[I], take);
+          cp_async16(dst + e * 16, take ? from : src[I], take ? 16 : 0);
         }
       }
     }
@@ -398,37 +388,43 @@ __global__ void __launch_bounds__(32) scan_kernel(const ScanArgs a, const int cb
   }
 }
 
-// One token: a lane owns four states of a channel (S/4 lanes a channel) in R
-// batch entries, so that it reads a once for all of them and has R loads of
+// One token: a lane owns four states of a channel (G = S/4 lanes a channel) in
+// R batch entries, so that it reads a once for all of them and has R loads of
 // the state in flight.  The state's read and write are nearly all of the
 // traffic (8 bytes per state element); a warp touches 512 contiguous bytes.
+// The lanes of a channel share the work per entry: each prepares the entries
+// R/G apart (or one), and passes Δ and Δ·x on by shuffles.
 constexpr int kStepThreads = 256;
 
 template <typename T, int S, int R>
-__global__ void __launch_bounds__(kStepThreads) step_kernel(const ScanArgs a) {
+__global__ void __launch_bounds__(kStepThreads) step_kernel(const ScanArgs a, uint32_t cblocks) {
   constexpr int G = S / 4;
-  const int64_t item = (int64_t)blockIdx.x * kStepThreads + threadIdx.x;
-  const int64_t per = a.D * G, groups = (a.B + R - 1) / R;
-  const bool on = item < groups * per;
-  const int64_t it = on ? item : 0;
-  const int q = (int)(it % G);
-  const int c = (int)(it % per / G);
-  const int64_t b0 = it / per * R;
+  constexpr int P = G < R ? R / G : 1;              // entries a lane prepares
+  const int e = (int)(blockIdx.x % cblocks) * kStepThreads + (int)threadIdx.x;
+  const int64_t b0 = (int64_t)(blockIdx.x / cblocks) * R;
+  const bool on = e < (int)a.D * G;
+  const int q = e % G, c = on ? e / G : 0;
   const int rows = (int)min((int64_t)R, a.B - b0);
+  float* const hp = a.state_out + (b0 * a.D + c) * S + 4 * q;
+  const int64_t hs = a.D * S;
   float4 h[R];
-  float2 Bv[R][2], Cv[R][2];
-  float x[R], dt[R], z[R];
 #pragma unroll
-  for (int r = 0; r < R; ++r) {
-    const int64_t b = b0 + (r < rows ? r : 0);
-    h[r] = __ldcs(reinterpret_cast<const float4*>(a.state_out + (b * a.D + c) * S + 4 * q));
+  for (int r = 0; r < R; ++r)
+    h[r] = __ldcs(reinterpret_cast<const float4*>(hp + (r < rows ? r : 0) * hs));
+  float x[P], dt[P], z[P], u[P];
+  int row[P];
+#pragma unroll
+  for (int p = 0; p < P; ++p) {
+    row[p] = G < R ? p * G + q : q % R;
+    const int64_t b = b0 + (row[p] < rows ? row[p] : 0);
+    x[p] = to_f32(static_cast<const T*>(a.x.data)[b * a.x.sb + c]);
+    dt[p] = to_f32(static_cast<const T*>(a.dt.data)[b * a.dt.sb + c]);
+    z[p] = a.gate.data ? to_f32(static_cast<const T*>(a.gate.data)[b * a.gate.sb + c]) : 0.f;
   }
+  float2 Bv[R][2], Cv[R][2];
 #pragma unroll
   for (int r = 0; r < R; ++r) {
     const int64_t b = b0 + (r < rows ? r : 0);
-    x[r] = to_f32(static_cast<const T*>(a.x.data)[b * a.x.sb + c]);
-    dt[r] = to_f32(static_cast<const T*>(a.dt.data)[b * a.dt.sb + c]);
-    z[r] = a.gate.data ? to_f32(static_cast<const T*>(a.gate.data)[b * a.gate.sb + c]) : 0.f;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       Bv[r][i] = load2(static_cast<const T*>(a.b.data) + b * a.b.sb + 4 * q + 2 * i);
@@ -439,25 +435,34 @@ __global__ void __launch_bounds__(kStepThreads) step_kernel(const ScanArgs a) {
   A.x *= kLog2e, A.y *= kLog2e, A.z *= kLog2e, A.w *= kLog2e;
   const float bias = a.dt_bias ? a.dt_bias[c] : 0.f, skip = a.skip ? a.skip[c] : 0.f;
 #pragma unroll
+  for (int p = 0; p < P; ++p) {
+    dt[p] += bias;
+    if (a.softplus) dt[p] = softplus(dt[p]);
+    u[p] = dt[p] * x[p];
+  }
+  float own[P];
+#pragma unroll
   for (int r = 0; r < R; ++r) {
-    float d = dt[r] + bias;
-    if (a.softplus) d = softplus(d);
-    const float u = d * x[r];
+    const int from = G < R ? r % G : r, slot = G < R ? r / G : 0;
+    const float d = __shfl_sync(0xffffffffu, dt[slot], from, G);
+    const float v = __shfl_sync(0xffffffffu, u[slot], from, G);
     float4 n;
-    n.x = fmaf(tc::ex2_f32(d * A.x), h[r].x, u * Bv[r][0].x);
-    n.y = fmaf(tc::ex2_f32(d * A.y), h[r].y, u * Bv[r][0].y);
-    n.z = fmaf(tc::ex2_f32(d * A.z), h[r].z, u * Bv[r][1].x);
-    n.w = fmaf(tc::ex2_f32(d * A.w), h[r].w, u * Bv[r][1].y);
+    n.x = fmaf(tc::ex2_f32(d * A.x), h[r].x, v * Bv[r][0].x);
+    n.y = fmaf(tc::ex2_f32(d * A.y), h[r].y, v * Bv[r][0].y);
+    n.z = fmaf(tc::ex2_f32(d * A.z), h[r].z, v * Bv[r][1].x);
+    n.w = fmaf(tc::ex2_f32(d * A.w), h[r].w, v * Bv[r][1].y);
+    if (on && r < rows) __stcs(reinterpret_cast<float4*>(hp + r * hs), n);
     float y = fmaf(n.x, Cv[r][0].x, fmaf(n.y, Cv[r][0].y, fmaf(n.z, Cv[r][1].x, n.w * Cv[r][1].y)));
 #pragma unroll
     for (int m = G / 2; m >= 1; m /= 2) y += __shfl_xor_sync(0xffffffffu, y, m);
-    if (!on || r >= rows) continue;
-    __stcs(reinterpret_cast<float4*>(a.state_out + ((b0 + r) * a.D + c) * S + 4 * q), n);
-    if (q == 0) {
-      y = fmaf(skip, x[r], y);
-      if (a.gate.data) y *= silu(z[r]);
-      static_cast<T*>(a.out)[(b0 + r) * a.out_sb + c] = from_f32<T>(y);
-    }
+    if (r == row[slot]) own[slot] = y;
+  }
+#pragma unroll
+  for (int p = 0; p < P; ++p) {
+    if (!on || q >= R || row[p] >= rows) continue;
+    float y = fmaf(skip, x[p], own[p]);
+    if (a.gate.data) y *= silu(z[p]);
+    static_cast<T*>(a.out)[(b0 + row[p]) * a.out_sb + c] = from_f32<T>(y);
   }
 }
 
@@ -515,9 +520,10 @@ cudaError_t launch_scan(const ScanArgs& a, cudaStream_t s) {
 
 template <typename T, int S, int R>
 cudaError_t launch_step_rows(const ScanArgs& a, cudaStream_t s) {
-  const int64_t blocks = ((a.B + R - 1) / R * a.D * (S / 4) + kStepThreads - 1) / kStepThreads;
+  const int64_t cblocks = (a.D * (S / 4) + kStepThreads - 1) / kStepThreads;
+  const int64_t blocks = (a.B + R - 1) / R * cblocks;
   if (blocks > INT32_MAX) return cudaErrorInvalidConfiguration;
-  step_kernel<T, S, R><<<(unsigned)blocks, kStepThreads, 0, s>>>(a);
+  step_kernel<T, S, R><<<(unsigned)blocks, kStepThreads, 0, s>>>(a, (uint32_t)cblocks);
   count_launches(1);
   return cudaGetLastError();
 }
