@@ -1,6 +1,14 @@
-// out = act(x·wᵀ + bias) + residual: choice of kernel, and the fp32 CUDA-core
-// kernel (one thread block per 64×64 tile of the output, K in steps of 16
-// through shared memory, 4×4 outputs per thread).
+// out = act(x·wᵀ + bias) + residual: choice of kernel, and the fp32 kernels on
+// the CUDA cores (TF32 tensor products keep 11 bits of an operand; split into
+// three they would keep 22, but their sums are not rounded like fp32's).
+//
+// tile_kernel: a CTA computes 64×128 outputs, K in steps of 16 through two
+// shared-memory buffers, 8×8 outputs per thread in packed pairs.  Bound by the
+// fp32 pipe: 32 packed multiply-adds against 4 shared loads per step of K.
+//
+// row_kernel (few tokens, or too few tiles to fill the GPU): a warp computes
+// four output features for up to eight tokens, its lanes split K, so that w is
+// read once per eight tokens in 512-byte pieces; bound by reading w.
 #include "block.cuh"
 #include "internal.h"
 
@@ -9,80 +17,185 @@ namespace {
 
 using namespace block;
 
-constexpr int kTile = 64, kStep = 16, kThreads = 256;
+// bias, activation and residual on four neighbouring columns, and the store.
+template <int ACT>
+__device__ __forceinline__ void finish4(const LinearArgs& a, int64_t m, int64_t n, float (&v)[4]) {
+  if (a.bias) {
+    const float4 b = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(a.bias) + n));
+    v[0] += b.x, v[1] += b.y, v[2] += b.z, v[3] += b.w;
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = activate<ACT>(v[i]);
+  if (a.residual.data) {
+    const float4 r = *reinterpret_cast<const float4*>(static_cast<const float*>(a.residual.data) +
+                                                      m * a.residual.sn + n);
+    v[0] += r.x, v[1] += r.y, v[2] += r.z, v[3] += r.w;
+  }
+  *reinterpret_cast<float4*>(static_cast<float*>(a.out) + m * a.out_sn + n) =
+      make_float4(v[0], v[1], v[2], v[3]);
+}
 
-template <typename T, int ACT>
-__global__ void __launch_bounds__(kThreads) linear_simt_kernel(const LinearArgs a) {
-  __shared__ float xs[kStep][kTile + 4], ws[kStep][kTile + 4];
-  const int64_t m0 = (int64_t)blockIdx.y * kTile, n0 = (int64_t)blockIdx.x * kTile;
-  const T* x = static_cast<const T*>(a.x.data);
-  const T* w = static_cast<const T*>(a.w.data);
-  const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
-  const int lr = threadIdx.x / 4, lk = (threadIdx.x % 4) * 4;   // one row, four of K
-  float acc[4][4] = {};
-  for (int64_t k0 = 0; k0 < a.K; k0 += kStep) {
+constexpr int kBM = 64, kBN = 128, kBK = 16, kTileThreads = 128;
+
+template <int ACT>
+__global__ void __launch_bounds__(kTileThreads) tile_kernel(const LinearArgs a, int mtiles) {
+  __shared__ __align__(16) float xs[2][kBK][kBM + 4], ws[2][kBK][kBN + 4];
+  const int64_t m0 = (int64_t)(blockIdx.x % mtiles) * kBM, n0 = (int64_t)(blockIdx.x / mtiles) * kBN;
+  const float* x = static_cast<const float*>(a.x.data);
+  const float* w = static_cast<const float*>(a.w.data);
+  const int tid = threadIdx.x, tx = tid % 16, ty = tid / 16;
+  const int lr = tid / 4, lk = (tid % 4) * 4;      // loads: row lr (+ 32 i), four of K
+  float4 xr[2], wr[4];
+  const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+  auto load = [&](int64_t k) {
+    const bool in = k + lk < a.K;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int64_t m = m0 + lr + 32 * i;
+      xr[i] = in && m < a.M ? __ldg(reinterpret_cast<const float4*>(x + m * a.x.sn + k + lk)) : zero;
+    }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int64_t k = k0 + lk + i;
-      xs[lk + i][lr] = (k < a.K && m0 + lr < a.M) ? to_f32(x[(m0 + lr) * a.x.sn + k]) : 0.f;
-      ws[lk + i][lr] = (k < a.K && n0 + lr < a.N) ? to_f32(w[(n0 + lr) * a.w.sn + k]) : 0.f;
+      const int64_t n = n0 + lr + 32 * i;
+      wr[i] = in && n < a.N ? __ldg(reinterpret_cast<const float4*>(w + n * a.w.sn + k + lk)) : zero;
     }
-    __syncthreads();
+  };
+  auto put = [&](int buf) {
 #pragma unroll
-    for (int k = 0; k < kStep; ++k) {
-      const float4 xv = *reinterpret_cast<const float4*>(&xs[k][ty * 4]);
-      const float4 wv = *reinterpret_cast<const float4*>(&ws[k][tx * 4]);
-      const float xr[4] = {xv.x, xv.y, xv.z, xv.w}, wr[4] = {wv.x, wv.y, wv.z, wv.w};
+    for (int i = 0; i < 2; ++i) {
+      const float v[4] = {xr[i].x, xr[i].y, xr[i].z, xr[i].w};
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(xr[i], wr[j], acc[i][j]);
+      for (int j = 0; j < 4; ++j) xs[buf][lk + j][lr + 32 * i] = v[j];
     }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float v[4] = {wr[i].x, wr[i].y, wr[i].z, wr[i].w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) ws[buf][lk + j][lr + 32 * i] = v[j];
+    }
+  };
+  f32x2 acc[8][4];
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[i][j] = 0ull;
+  load(0);
+  put(0);
+  __syncthreads();
+  int buf = 0;
+  for (int64_t k0 = 0; k0 < a.K; k0 += kBK, buf ^= 1) {
+    const bool more = k0 + kBK < a.K;
+    if (more) load(k0 + kBK);
+#pragma unroll
+    for (int k = 0; k < kBK; ++k) {
+      const float4 xa = *reinterpret_cast<const float4*>(&xs[buf][k][ty * 4]);
+      const float4 xb = *reinterpret_cast<const float4*>(&xs[buf][k][32 + ty * 4]);
+      const ulonglong2 wa = *reinterpret_cast<const ulonglong2*>(&ws[buf][k][tx * 4]);
+      const ulonglong2 wb = *reinterpret_cast<const ulonglong2*>(&ws[buf][k][64 + tx * 4]);
+      const float xv[8] = {xa.x, xa.y, xa.z, xa.w, xb.x, xb.y, xb.z, xb.w};
+      const f32x2 wv[4] = {wa.x, wa.y, wb.x, wb.y};
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const f32x2 d = pack2(xv[i], xv[i]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[i][j] = fma2(d, wv[j], acc[i][j]);
+      }
+    }
+    if (more) put(buf ^ 1);
     __syncthreads();
   }
-  const T* bias = static_cast<const T*>(a.bias);
-  const T* res = static_cast<const T*>(a.residual.data);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int64_t m = m0 + ty * 4 + i;
+  for (int i = 0; i < 8; ++i) {
+    const int64_t m = m0 + (i / 4) * 32 + ty * 4 + i % 4;
     if (m >= a.M) continue;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int64_t n = n0 + tx * 4 + j;
+    for (int j = 0; j < 2; ++j) {
+      const int64_t n = n0 + j * 64 + tx * 4;   // N is a multiple of 4
       if (n >= a.N) continue;
-      float y = acc[i][j];
-      if (bias) y += to_f32(bias[n]);
-      y = activate<ACT>(y);
-      if (res) y += to_f32(res[m * a.residual.sn + n]);
-      static_cast<T*>(a.out)[m * a.out_sn + n] = from_f32<T>(y);
+      float v[4];
+      unpack2(acc[i][2 * j], v[0], v[1]);
+      unpack2(acc[i][2 * j + 1], v[2], v[3]);
+      finish4<ACT>(a, m, n, v);
     }
   }
 }
 
-template <typename T, int ACT>
-cudaError_t launch_simt(const LinearArgs& a, cudaStream_t s) {
-  const int64_t gx = (a.N + kTile - 1) / kTile, gy = (a.M + kTile - 1) / kTile;
-  if (gx > INT32_MAX || gy > 65535) return cudaErrorInvalidConfiguration;
-  linear_simt_kernel<T, ACT><<<dim3((unsigned)gx, (unsigned)gy), kThreads, 0, s>>>(a);
+constexpr int kRowWarps = 4, kRowFeatures = 4;
+
+template <int ACT, int R>
+__global__ void __launch_bounds__(32 * kRowWarps) row_kernel(const LinearArgs a, int fblocks) {
+  const int lane = threadIdx.x % 32;
+  const int64_t n = ((int64_t)(blockIdx.x % fblocks) * kRowWarps + threadIdx.x / 32) * kRowFeatures;
+  const int64_t m0 = (int64_t)(blockIdx.x / fblocks) * R;
+  if (n >= a.N) return;
+  const float* x = static_cast<const float*>(a.x.data);
+  const float* w = static_cast<const float*>(a.w.data) + n * a.w.sn;
+  float acc[R][kRowFeatures] = {};
+#pragma unroll 2
+  for (int64_t k = lane * 4; k < a.K; k += 128) {
+    float4 wv[kRowFeatures];
+#pragma unroll
+    for (int j = 0; j < kRowFeatures; ++j)
+      wv[j] = __ldg(reinterpret_cast<const float4*>(w + j * a.w.sn + k));
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const int64_t m = m0 + r < a.M ? m0 + r : a.M - 1;
+      const float4 xv = __ldg(reinterpret_cast<const float4*>(x + m * a.x.sn + k));
+#pragma unroll
+      for (int j = 0; j < kRowFeatures; ++j) {
+        acc[r][j] = fmaf(xv.x, wv[j].x, acc[r][j]);
+        acc[r][j] = fmaf(xv.y, wv[j].y, acc[r][j]);
+        acc[r][j] = fmaf(xv.z, wv[j].z, acc[r][j]);
+        acc[r][j] = fmaf(xv.w, wv[j].w, acc[r][j]);
+      }
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+#pragma unroll
+    for (int j = 0; j < kRowFeatures; ++j)
+#pragma unroll
+      for (int s = 16; s >= 1; s /= 2) acc[r][j] += __shfl_xor_sync(0xffffffffu, acc[r][j], s);
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+    if (lane == r && m0 + r < a.M) finish4<ACT>(a, m0 + r, n, acc[r]);
+}
+
+template <int ACT, int R>
+cudaError_t launch_rows(const LinearArgs& a, cudaStream_t s) {
+  const int64_t fb = (a.N + kRowWarps * kRowFeatures - 1) / (kRowWarps * kRowFeatures);
+  const int64_t blocks = fb * ((a.M + R - 1) / R);
+  if (blocks > INT32_MAX) return cudaErrorInvalidConfiguration;
+  row_kernel<ACT, R><<<(unsigned)blocks, 32 * kRowWarps, 0, s>>>(a, (int)fb);
   count_launches(1);
   return cudaGetLastError();
 }
 
-template <typename T>
-cudaError_t simt(const LinearArgs& a, cudaStream_t s) {
+template <int ACT>
+cudaError_t launch_f32(const LinearArgs& a, cudaStream_t s) {
+  const int64_t mt = (a.M + kBM - 1) / kBM, nt = (a.N + kBN - 1) / kBN;
+  if (a.M <= 2) return launch_rows<ACT, 2>(a, s);
+  if (a.M <= 32 || (a.M <= 256 && mt * nt < a.num_sms / 2)) return launch_rows<ACT, 8>(a, s);
+  if (mt * nt > INT32_MAX) return cudaErrorInvalidConfiguration;
+  tile_kernel<ACT><<<(unsigned)(mt * nt), kTileThreads, 0, s>>>(a, (int)mt);
+  count_launches(1);
+  return cudaGetLastError();
+}
+
+cudaError_t f32_linear(const LinearArgs& a, cudaStream_t s) {
   switch (a.act) {
-    case LA_ACT_RELU: return launch_simt<T, LA_ACT_RELU>(a, s);
-    case LA_ACT_SILU: return launch_simt<T, LA_ACT_SILU>(a, s);
-    case LA_ACT_GELU: return launch_simt<T, LA_ACT_GELU>(a, s);
-    case LA_ACT_SOFTPLUS: return launch_simt<T, LA_ACT_SOFTPLUS>(a, s);
-    default: return launch_simt<T, LA_ACT_NONE>(a, s);
+    case LA_ACT_RELU: return launch_f32<LA_ACT_RELU>(a, s);
+    case LA_ACT_SILU: return launch_f32<LA_ACT_SILU>(a, s);
+    case LA_ACT_GELU: return launch_f32<LA_ACT_GELU>(a, s);
+    case LA_ACT_SOFTPLUS: return launch_f32<LA_ACT_SOFTPLUS>(a, s);
+    default: return launch_f32<LA_ACT_NONE>(a, s);
   }
 }
 
 }  // namespace
 
 cudaError_t linear(const LinearArgs& a, cudaStream_t s) {
-  return a.bf16 ? tc_linear(a, s) : simt<float>(a, s);
+  return a.bf16 ? tc_linear(a, s) : f32_linear(a, s);
 }
 
 }  // namespace la
