@@ -1,13 +1,13 @@
 // out = act(x·wᵀ + bias) + residual in bf16 on the tcgen05 tensor cores.
 //
-// pair_kernel (many tokens): CTA pairs, persistent, one 256×256 tile of the
-// output per pair at a time.  Each CTA loads its 128 rows of x and 128 rows of
-// w per 64-wide step of K (32 KB, six stages), the even rank issues the
-// cta_group::2 MMAs (256×256×16) for both, and each CTA's TMEM receives its
-// 128 rows × 256 columns in one of two accumulators, so that the epilogue of a
-// tile overlaps the next tile's product.  A pair moves 64 KB per step into
-// shared memory for 2·256·256·64 flops; one CTA on a 128×256 tile would move
-// 48 KB for half of them.
+// pair_kernel (many tokens): CTA pairs, persistent, one 256×BN tile of the
+// output per pair at a time (BN 256, or 128 where that leaves fewer SMs idle).
+// Each CTA loads its 128 rows of x and BN/2 rows of w per 64-wide step of K
+// into a ring, the even rank issues the cta_group::2 MMAs (256×BN×16) for
+// both, and each CTA's TMEM receives its 128 rows × BN columns in one of two
+// accumulators, so that the epilogue of a tile overlaps the next tile's
+// product.  A pair moves 64 KB per step into shared memory for 2·256·256·64
+// flops; one CTA on a 128×256 tile would move 48 KB for half of them.
 //
 // few_kernel (few tokens): the product is bound by reading w, so w's rows are
 // the MMA's 128 rows and the tokens its columns (16 to 128, no work on absent
@@ -40,20 +40,21 @@ struct LinParams {
   int* status;
 };
 
-// bias, activation and residual on 8 neighbouring columns of a row.
+// bias, activation and residual on 8 neighbouring columns of a row; either
+// pointer is null where there is nothing to add.
 template <int ACT>
-__device__ __forceinline__ void finish8(const LinParams& p, int64_t m, int n, float (&v)[8]) {
-  if (p.bias) {
+__device__ __forceinline__ void finish8(const bf16* bias, const bf16* res, float (&v)[8]) {
+  if (bias) {
     float b[8];
-    unpack<bf16>(__ldg(reinterpret_cast<const uint4*>(p.bias + n)), b);
+    unpack<bf16>(__ldg(reinterpret_cast<const uint4*>(bias)), b);
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] += b[i];
   }
 #pragma unroll
   for (int i = 0; i < 8; ++i) v[i] = activate<ACT>(v[i]);
-  if (p.residual) {
+  if (res) {
     float r[8];
-    unpack<bf16>(*reinterpret_cast<const uint4*>(p.residual + m * p.res_sn + n), r);
+    unpack<bf16>(*reinterpret_cast<const uint4*>(res), r);
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] += r[i];
   }
@@ -61,16 +62,21 @@ __device__ __forceinline__ void finish8(const LinParams& p, int64_t m, int n, fl
 
 // ------------------------------------------------------------------ many tokens
 
-constexpr int kStages = 6;
 constexpr int kTileB = 128 * kBK * 2;               // 16 KB: 128 rows of one operand
-constexpr int kStageB = 2 * kTileB;
+constexpr int kEpiWarps = 8;                        // two per quarter of the rows
 constexpr int kEpiB = 32 * 64 * 2;                  // 4 KB: 32 rows × 64 columns of the output
-constexpr int kPairThreads = 256;
-constexpr int kPairSmem = 1024 + kStages * kStageB + 8 * kEpiB + 256;
+constexpr int kPairThreads = 128 + 32 * kEpiWarps;
 constexpr int kGroupM = 8;                          // row tiles walked together, for L2
 
+template <int BN> struct PairCfg {
+  static constexpr int kW = BN / 2 * kBK * 2;       // a CTA's rows of w per step
+  static constexpr int kStage = kTileB + kW;
+  static constexpr int kNum = BN == 256 ? 6 : 8;
+  static constexpr int kSmem = 1024 + kNum * kStage + kEpiWarps * kEpiB + 256;
+};
+
 struct PairBars {
-  uint64_t full[kStages], empty[kStages], acc_full[2], acc_empty[2];
+  uint64_t full[8], empty[8], acc_full[2], acc_empty[2];
   uint32_t tmem;
   int abort;
 };
@@ -86,14 +92,16 @@ __device__ __forceinline__ void tile_at(const LinParams& p, int64_t t, int& mt, 
   nt = r / rows;
 }
 
-template <int ACT>
+template <int BN, int ACT>
 __global__ void __launch_bounds__(kPairThreads, 1)
 pair_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap mw,
             const __grid_constant__ CUtensorMap mo, const LinParams p) {
+  using C = PairCfg<BN>;
+  constexpr int kStages = C::kNum, kStageB = C::kStage;
   extern __shared__ uint8_t raw[];
   uint8_t* base = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
   uint8_t* epi = base + kStages * kStageB;
-  PairBars* bars = reinterpret_cast<PairBars*>(epi + 8 * kEpiB);
+  PairBars* bars = reinterpret_cast<PairBars*>(epi + kEpiWarps * kEpiB);
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const uint32_t rank = cluster_rank();
   const int64_t tiles = (int64_t)p.mtiles * p.ntiles;
@@ -106,7 +114,7 @@ pair_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUte
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bars->acc_full[i], 1);
-      mbar_init(&bars->acc_empty[i], 8);   // four epilogue warps of each CTA
+      mbar_init(&bars->acc_empty[i], 2 * kEpiWarps);   // of both CTAs
     }
     bars->abort = 0;
     fence_barrier_init();
@@ -115,7 +123,7 @@ pair_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUte
     tma_prefetch_desc(&mo);
   }
   if (warp == 2) {
-    tmem_alloc_pair(&bars->tmem, 512);
+    tmem_alloc_pair(&bars->tmem, 2 * BN);
     tmem_relinquish_pair();
   }
   tc_fence_before();
@@ -131,7 +139,7 @@ pair_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUte
     for (int64_t t = first; t < tiles && !*abort; t += stride) {
       int mt, nt;
       tile_at(p, t, mt, nt);
-      const int m0 = mt * 256 + (int)rank * 128, n0 = nt * 256 + (int)rank * 128;
+      const int m0 = mt * 256 + (int)rank * 128, n0 = nt * BN + (int)rank * (BN / 2);
       for (int kb = 0; kb < p.kblocks; ++kb, ++it) {
         const int s = it % kStages;
         if (it >= kStages &&
@@ -149,13 +157,13 @@ pair_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUte
         mbar_wait_drain(&bars->full[j % kStages], (j / kStages) & 1);
   } else if (warp == 1 && lane == 0 && rank == 0) {
     // MMA issuer, for both CTAs
-    constexpr uint32_t idesc = idesc_bf16_f32(256, 256, false, false);
+    constexpr uint32_t idesc = idesc_bf16_f32(256, BN, false, false);
     uint32_t it = 0, n = 0;
     for (int64_t t = first; t < tiles && !*abort; t += stride, ++n) {
       const int buf = n & 1;
       if (n >= 2 && !mbar_wait(&bars->acc_empty[buf], ((n >> 1) & 1) ^ 1, p.status, abort)) break;
       tc_fence_after();
-      const uint32_t d = tmem + buf * 256;
+      const uint32_t d = tmem + buf * BN;
       bool ok = true;
       for (int kb = 0; kb < p.kblocks; ++kb, ++it) {
         const int s = it % kStages;
@@ -180,41 +188,41 @@ pair_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUte
       mbar_wait_drain(&bars->acc_full[0], 0);
     }
   } else if (warp >= 4) {
-    // epilogue: 32 rows per warp, 64 columns at a time through a staging tile
-    const int q = warp - 4;
-    uint8_t* stage = epi + q * 2 * kEpiB;
+    // epilogue: a warp has the rows of its TMEM quarter and half of the
+    // columns, 64 at a time through a staging tile
+    const int q = warp % 4, half = (warp - 4) / 4;
+    uint8_t* st = epi + (warp - 4) * kEpiB;
+    const uint32_t sa = smem_u32(st);
     const uint32_t lead_empty[2] = {map_to_cta(smem_u32(&bars->acc_empty[0]), 0),
                                     map_to_cta(smem_u32(&bars->acc_empty[1]), 0)};
-    uint32_t n = 0, put = 0;
+    uint32_t n = 0;
     for (int64_t t = first; t < tiles; t += stride, ++n) {
       const int buf = n & 1;
       if (!warp_wait(&bars->acc_full[buf], (n >> 1) & 1, p.status, abort)) break;
       tc_fence_after();
       int mt, nt;
       tile_at(p, t, mt, nt);
-      const int m0 = mt * 256 + (int)rank * 128 + q * 32, n0 = nt * 256;
-      const int m = m0 + lane;
-      const int cols = min(256, p.N - n0);
+      const int m0 = mt * 256 + (int)rank * 128 + q * 32, m = m0 + lane;
+      const int c0 = half * (BN / 2), n0 = nt * BN + c0;
+      const int cols = min(BN / 2, p.N - n0);
       if (m0 < p.M) {
-        for (int c = 0; c < cols; c += 64, ++put) {
-          uint8_t* st = stage + (put & 1) * kEpiB;
-          const uint32_t sa = smem_u32(st);
-          if (lane == 0) tma_store_wait_read1();
+        const bf16* res = p.residual && m < p.M ? p.residual + m * p.res_sn + n0 : nullptr;
+        for (int c = 0; c < cols; c += 64) {
+          uint32_t r[64];
+          tmem_ld32(tmem_addr(tmem, q * 32, buf * BN + c0 + c), r);
+          tmem_ld32(tmem_addr(tmem, q * 32, buf * BN + c0 + c + 32), r + 32);
+          tmem_ld_wait();
+          if (lane == 0) tma_store_wait_read0();
           __syncwarp();
 #pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            uint32_t r[32];
-            tmem_ld32(tmem_addr(tmem, q * 32, buf * 256 + c + half * 32), r);
-            tmem_ld_wait();
+          for (int j = 0; j < 8; ++j) {
+            float v[8];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              float v[8];
-#pragma unroll
-              for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[8 * j + i]);
-              const int nn = n0 + c + half * 32 + 8 * j;
-              if (m < p.M && nn < p.N) finish8<ACT>(p, m, nn, v);
-              sts128(sa + sw_chunk(32, lane, 0, half * 4 + j), pack8(v));
-            }
+            for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[8 * j + i]);
+            const bool in = c + 8 * j < cols;
+            finish8<ACT>(p.bias && in ? p.bias + n0 + c + 8 * j : nullptr,
+                         res && in ? res + c + 8 * j : nullptr, v);
+            sts128(sa + sw_chunk(32, lane, 0, j), pack8(v));
           }
           fence_proxy_async_smem();
           __syncwarp();
@@ -236,17 +244,18 @@ pair_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUte
   __syncthreads();
   cluster_sync();          // no CTA leaves while its pair may still signal or read it
   tc_fence_after();
-  if (warp == 2) tmem_dealloc_pair(tmem, 512);
+  if (warp == 2) tmem_dealloc_pair(tmem, 2 * BN);
 }
 
 // ------------------------------------------------------------------ few tokens
 
-constexpr int kFewThreads = 128;
+constexpr int kFewThreads = 256;
 
 template <int BT> struct FewCfg {
   static constexpr int kXB = BT * kBK * 2;
   static constexpr int kStage = kTileB + kXB;
-  static constexpr int kNum = BT <= 32 ? 5 : 4;           // ≤ 113 KB, two CTAs per SM
+  static constexpr int kNum = BT <= 32 ? 5 : (BT == 64 ? 4 : 6);
+  static constexpr int kPerSm = BT <= 64 ? 2 : 1;         // CTAs that fit
   static constexpr int kPart = BT * 128 * 4;              // partial sums, over the stages
   static constexpr int kBuf = kNum * kStage > kPart ? kNum * kStage : kPart;
   static constexpr int kSmem = 1024 + kBuf + 256;
@@ -332,13 +341,13 @@ few_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUten
   float* part = reinterpret_cast<float*>(base);
   if (ok) {
 #pragma unroll
-    for (int c = 0; c < BT; c += 16) {
+    for (int c = warp / 4 * 16; c < BT; c += 32) {
       uint32_t r[16];
-      tmem_ld16(tmem_addr(tmem, warp * 32, c), r);
+      tmem_ld16(tmem_addr(tmem, warp % 4 * 32, c), r);
       tmem_ld_wait();
 #pragma unroll
       for (int i = 0; i < 16; ++i)
-        part[(c + i) * 128 + warp * 32 + lane] = k0 < k1 ? __uint_as_float(r[i]) : 0.f;
+        part[(c + i) * 128 + warp % 4 * 32 + lane] = k0 < k1 ? __uint_as_float(r[i]) : 0.f;
     }
   }
   tc_fence_before();
@@ -352,16 +361,27 @@ few_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUten
     for (int t = rank * per + threadIdx.x / 16; t < tlim; t += kFewThreads / 16) {
       const uint32_t at = smem_u32(part) + (t * 128 + f) * 4;
       float v[8] = {};
-      for (int r = 0; r < split; ++r) {
-        const uint32_t pa = split > 1 ? map_to_cta(at, r) : at;
-        const float4 lo = split > 1 ? ld_cluster_f4(pa) : lds128f(pa);
-        const float4 hi = split > 1 ? ld_cluster_f4(pa + 16) : lds128f(pa + 16);
-        v[0] += lo.x, v[1] += lo.y, v[2] += lo.z, v[3] += lo.w;
-        v[4] += hi.x, v[5] += hi.y, v[6] += hi.z, v[7] += hi.w;
+      for (int r0 = 0; r0 < split; r0 += 4) {   // four ranks' reads in flight
+        float4 lo[4], hi[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (r0 + i < split) {
+            const uint32_t pa = split > 1 ? map_to_cta(at, r0 + i) : at;
+            lo[i] = split > 1 ? ld_cluster_f4(pa) : lds128f(pa);
+            hi[i] = split > 1 ? ld_cluster_f4(pa + 16) : lds128f(pa + 16);
+          }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (r0 + i < split) {
+            v[0] += lo[i].x, v[1] += lo[i].y, v[2] += lo[i].z, v[3] += lo[i].w;
+            v[4] += hi[i].x, v[5] += hi[i].y, v[6] += hi[i].z, v[7] += hi[i].w;
+          }
       }
-      finish8<ACT>(p, m0 + t, n, v);
-      if (LA_DCHECK(p.status, m0 + t < p.M && n + 8 <= p.N, 52))
-        *reinterpret_cast<uint4*>(p.out + (int64_t)(m0 + t) * p.out_sn + n) = pack8(v);
+      const int64_t m = m0 + t;
+      finish8<ACT>(p.bias ? p.bias + n : nullptr,
+                   p.residual ? p.residual + m * p.res_sn + n : nullptr, v);
+      if (LA_DCHECK(p.status, m < p.M && n + 8 <= p.N, 52))
+        *reinterpret_cast<uint4*>(p.out + m * p.out_sn + n) = pack8(v);
     }
   }
   if (split > 1) cluster_sync();   // no CTA leaves while another reads its partial sums
@@ -370,24 +390,24 @@ few_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUten
 
 // ------------------------------------------------------------------ launch
 
-template <int ACT>
+template <int BN, int ACT>
 cudaError_t launch_pair(const LinearArgs& a, LinParams p, cudaStream_t s) {
   CUtensorMap mx, mw, mo;
   cudaError_t e;
   if ((e = tmap_view(&mx, a.x.data, a.M, a.K, a.x.sn ? a.x.sn : a.K, 128)) != cudaSuccess ||
-      (e = tmap_view(&mw, a.w.data, a.N, a.K, a.w.sn ? a.w.sn : a.K, 128)) != cudaSuccess ||
+      (e = tmap_view(&mw, a.w.data, a.N, a.K, a.w.sn ? a.w.sn : a.K, BN / 2)) != cudaSuccess ||
       (e = tmap_view(&mo, a.out, a.M, a.N, a.out_sn ? a.out_sn : a.N, 32)) != cudaSuccess)
     return e;
   p.mtiles = (p.M + 255) / 256;
-  p.ntiles = (p.N + 255) / 256;
+  p.ntiles = (p.N + BN - 1) / BN;
   const int64_t tiles = (int64_t)p.mtiles * p.ntiles;
   static std::atomic<uint64_t> smem_set{0};
-  e = allow_smem((const void*)pair_kernel<ACT>, kPairSmem, &smem_set);
+  e = allow_smem((const void*)pair_kernel<BN, ACT>, PairCfg<BN>::kSmem, &smem_set);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2);
   cfg.blockDim = dim3(kPairThreads);
-  cfg.dynamicSmemBytes = kPairSmem;
+  cfg.dynamicSmemBytes = PairCfg<BN>::kSmem;
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -401,15 +421,23 @@ cudaError_t launch_pair(const LinearArgs& a, LinParams p, cudaStream_t s) {
   static std::atomic<int> resident{0};
   int pairs = resident.load(std::memory_order_relaxed);
   if (pairs == 0) {
-    e = cudaOccupancyMaxActiveClusters(&pairs, pair_kernel<ACT>, &cfg);
+    e = cudaOccupancyMaxActiveClusters(&pairs, pair_kernel<BN, ACT>, &cfg);
     if (e != cudaSuccess) return e;
     if (pairs < 1) return cudaErrorInvalidConfiguration;
     resident.store(pairs, std::memory_order_relaxed);
   }
   cfg.gridDim = dim3(2 * (unsigned)(tiles < pairs ? tiles : pairs));
-  e = cudaLaunchKernelEx(&cfg, pair_kernel<ACT>, mx, mw, mo, p);
+  e = cudaLaunchKernelEx(&cfg, pair_kernel<BN, ACT>, mx, mw, mo, p);
   count_launches(1);
   return e;
+}
+
+// CTAs that share a feature tile's K: as many as are resident at once, while
+// each keeps four steps.
+int few_split(int64_t tiles, int kblocks, int64_t resident) {
+  int split = 1;
+  while (split < 4 && tiles * split * 2 <= resident && kblocks >= split * 8) split *= 2;
+  return split;
 }
 
 template <int BT, int ACT>
@@ -421,9 +449,7 @@ cudaError_t launch_few(const LinearArgs& a, const LinParams& p, cudaStream_t s) 
       (e = tmap_view(&mw, a.w.data, a.N, a.K, a.w.sn ? a.w.sn : a.K, 128)) != cudaSuccess)
     return e;
   const int64_t ft = (a.N + 127) / 128, mt = (a.M + BT - 1) / BT;
-  // split K while CTAs are fewer than two per SM and each keeps four steps
-  int split = 1;
-  while (split < 8 && ft * mt * split * 2 <= 2 * a.num_sms && p.kblocks >= 2 * split * 4) split *= 2;
+  const int split = few_split(ft * mt, p.kblocks, (int64_t)C::kPerSm * a.num_sms);
   if (mt > 65535 || ft * split > INT32_MAX) return cudaErrorInvalidConfiguration;
   static std::atomic<uint64_t> smem_set{0};
   e = allow_smem((const void*)few_kernel<BT, ACT>, C::kSmem, &smem_set);
@@ -445,6 +471,9 @@ cudaError_t launch_few(const LinearArgs& a, const LinParams& p, cudaStream_t s) 
   return e;
 }
 
+constexpr double kFewStep = 600, kPair256Step = 560, kPair128Step = 330;
+constexpr double kFewFixed = 3000, kPairFixed = 5000;
+
 template <int ACT>
 cudaError_t by_shape(const LinearArgs& a, cudaStream_t s) {
   LinParams p{};
@@ -460,9 +489,20 @@ cudaError_t by_shape(const LinearArgs& a, cudaStream_t s) {
   if (a.M <= 16) return launch_few<16, ACT>(a, p, s);
   if (a.M <= 32) return launch_few<32, ACT>(a, p, s);
   if (a.M <= 64) return launch_few<64, ACT>(a, p, s);
-  const int64_t tiles = ((a.M + 255) / 256) * ((a.N + 255) / 256);
-  if (a.M <= 128 || tiles < a.num_sms / 4) return launch_few<128, ACT>(a, p, s);
-  return launch_pair<ACT>(a, p, s);
+  if (a.M <= 128) return launch_few<128, ACT>(a, p, s);
+  // The cheaper of the three by SM cycles per 64-wide step of K, measured where
+  // every SM has a tile (few: 32 KB a step through L2; pair: 256 or 128
+  // columns), times the tiles that follow one another on an SM.
+  const int64_t ft = (a.N + 127) / 128, mt = (a.M + 127) / 128;
+  const int split = few_split(ft * mt, p.kblocks, a.num_sms);
+  auto waves = [](int64_t tiles, int64_t slots) { return (tiles + slots - 1) / slots; };
+  const int64_t pt = (a.M + 255) / 256, pairs = a.num_sms / 2;
+  const double few = waves(ft * mt * split, a.num_sms) * (double)(p.kblocks + split - 1) / split * kFewStep + kFewFixed;
+  const double p256 = waves(pt * ((a.N + 255) / 256), pairs) * (double)p.kblocks * kPair256Step + kPairFixed;
+  const double p128 = waves(pt * ((a.N + 127) / 128), pairs) * (double)p.kblocks * kPair128Step + kPairFixed;
+  if (few <= p256 && few <= p128) return launch_few<128, ACT>(a, p, s);
+  if (p256 <= p128) return launch_pair<256, ACT>(a, p, s);
+  return launch_pair<128, ACT>(a, p, s);
 }
 
 }  // namespace
