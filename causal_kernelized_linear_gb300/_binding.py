@@ -54,6 +54,13 @@ class LaTensor(ctypes.Structure):
                 ("H", ctypes.c_int64), ("n", ctypes.c_int64), ("d", ctypes.c_int64)]
 
 
+class LaRows(ctypes.Structure):
+    """la_rows: a strided [B, n, d] view."""
+    _fields_ = [("data", ctypes.c_void_p), ("dtype", ctypes.c_int), ("B", ctypes.c_int64),
+                ("n", ctypes.c_int64), ("d", ctypes.c_int64), ("stride_b", ctypes.c_int64),
+                ("stride_n", ctypes.c_int64)]
+
+
 _lock = threading.Lock()
 _lib = None
 
@@ -124,6 +131,17 @@ def load():
         lib.la_get_last_device_check.restype = ctypes.c_int
         lib.la_selftest_device_check.argtypes = [vp]
         lib.la_selftest_device_check.restype = ctypes.c_int
+        R, i = ctypes.POINTER(LaRows), ctypes.c_int
+        lib.la_linear.argtypes = [R, R, vp, i, R, R, vp]
+        lib.la_linear.restype = i
+        lib.la_causal_conv.argtypes = [R, vp, i, vp, i, vp, vp, R, vp, vp]
+        lib.la_causal_conv.restype = i
+        lib.la_causal_conv_step.argtypes = [vp, R, vp, i, vp, i, R, vp]
+        lib.la_causal_conv_step.restype = i
+        lib.la_selective_scan.argtypes = [R, R, vp, i, R, R, vp, R, vp, i, vp, vp, R, vp, vp]
+        lib.la_selective_scan.restype = i
+        lib.la_selective_step.argtypes = [vp, R, R, vp, i, R, R, vp, R, vp, i, R, vp]
+        lib.la_selective_step.restype = i
         _lib = lib
         return lib
 

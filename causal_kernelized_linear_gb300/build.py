@@ -2,8 +2,11 @@
 
 Each CUDA translation unit under ``csrc/`` is compiled in parallel, then the
 objects are linked into ``_build/liblinattn.so`` against the shared CUDA
-runtime (the same libcudart.so that PyTorch loads).  Run as a module
-(``python -m causal_kernelized_linear_gb300.build``) or call :func:`build`.
+runtime (the same libcudart.so that PyTorch loads).  Beside them the host
+compiler builds ``_build/la_block.so``, the CPython face of the state-space
+block's operators (it calls the library by address and serves both builds).
+Run as a module (``python -m causal_kernelized_linear_gb300.build``) or call
+:func:`build`.
 """
 from __future__ import annotations
 
@@ -13,6 +16,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG_DIR)
@@ -23,6 +27,10 @@ LIB_PATH = os.path.join(BUILD_DIR, "liblinattn.so")
 # the LA_DEBUG build (device-side index checks), apart from the product library
 DEBUG_BUILD_DIR = os.path.join(PKG_DIR, "_build_debug")
 DEBUG_LIB_PATH = os.path.join(DEBUG_BUILD_DIR, "liblinattn.so")
+
+# the CPython face of the block operators (against the installed PyTorch)
+EXT_SRC = os.path.join(CSRC, "py_block.cpp")
+EXT_PATH = os.path.join(BUILD_DIR, "la_block.so")
 
 ARCH_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a"]
 CXX_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC,-O2",
@@ -41,16 +49,40 @@ def _sources():
 
 
 def _deps():
-    return (_sources() + glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(CSRC, "*.cuh"))
+    return (_sources() + [EXT_SRC] + glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(CSRC, "*.cuh"))
             + glob.glob(os.path.join(INCLUDE, "*.h")) + [os.path.abspath(__file__)])
 
 
 def up_to_date(debug: bool = False) -> bool:
-    path = DEBUG_LIB_PATH if debug else LIB_PATH
-    if not os.path.exists(path):
+    paths = (DEBUG_LIB_PATH if debug else LIB_PATH, EXT_PATH)
+    if not all(os.path.exists(p) for p in paths):
         return False
-    t = os.path.getmtime(path)
+    t = min(os.path.getmtime(p) for p in paths)
     return all(os.path.getmtime(p) <= t for p in _deps())
+
+
+def _build_ext():
+    """Compile ``la_block.so`` with the host compiler; returns its log."""
+    import torch
+    from torch.utils.cpp_extension import include_paths, library_paths
+    cxx = os.environ.get("CXX") or shutil.which("g++") or shutil.which("c++")
+    if not cxx:
+        raise RuntimeError("a C++ compiler is required to build la_block")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(_nvcc())), "include")
+    libs = library_paths()
+    os.makedirs(BUILD_DIR, exist_ok=True)
+    tmp = EXT_PATH + f".tmp{os.getpid()}"
+    cmd = [cxx, "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-I", INCLUDE, *[a for p in include_paths() for a in ("-I", p)],
+           "-I", sysconfig.get_paths()["include"], "-I", cuda, EXT_SRC, "-o", tmp,
+           *[a for p in libs for a in ("-L" + p, "-Wl,-rpath," + p)],
+           "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch", "-ltorch_python"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{cxx} failed for {EXT_SRC}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, EXT_PATH)
+    return r.stdout + r.stderr
 
 
 def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = False,
@@ -77,12 +109,16 @@ def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = Fals
         return obj, r.stdout + r.stderr
 
     srcs = _sources()
-    with cf.ThreadPoolExecutor(max_workers=max(1, min(len(srcs), os.cpu_count() or 4))) as ex:
+    with cf.ThreadPoolExecutor(max_workers=max(1, min(len(srcs) + 1, os.cpu_count() or 4))) as ex:
+        ext = ex.submit(_build_ext)
         results = list(ex.map(compile_one, srcs))
+        results_ext = ext.result()
     if verbose or ptxas_verbose:
         for obj, log in results:
             if log.strip():
                 print(f"== {os.path.basename(obj)}\n{log}", file=sys.stderr)
+        if results_ext.strip():
+            print(f"== la_block.so\n{results_ext}", file=sys.stderr)
     tmp = lib_path + f".tmp{os.getpid()}"
     cmd = [nvcc, *ARCH_FLAGS, "-shared", "-cudart", "shared", "-o", tmp,
            *[o for o, _ in results]]

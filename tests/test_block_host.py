@@ -1,11 +1,12 @@
 """State-space block operators, host side: refusals before anything is queued
 (no GPU needed)."""
+import ctypes
+
 import pytest
 import torch
 
 import causal_kernelized_linear_gb300 as la
 from causal_kernelized_linear_gb300 import _binding as B
-from causal_kernelized_linear_gb300 import _block as K
 
 OK, BAD, UNS = B.LA_OK, B.LA_ERR_INVALID_ARG, B.LA_ERR_UNSUPPORTED
 P0 = 0x10000
@@ -19,23 +20,23 @@ def lib():
 
 def rows(b=1, n=8, d=64, ptr=P0, dtype=B.LA_BF16, sb=None, sn=None):
     sn = d if sn is None else sn
-    return K.LaRows(ptr, dtype, b, n, d, n * sn if sb is None else sb, sn)
+    return B.LaRows(ptr, dtype, b, n, d, n * sn if sb is None else sb, sn)
 
 
 def ref(r):
-    return bytes(r) if r is not None else None
+    return ctypes.byref(r) if r is not None else None
 
 
 def lin(x=None, w=None, bias=None, act=0, res=None, out=None):
     x, w = x or rows(n=8, d=64), w or rows(n=32, d=64)
-    return K._fn("la_linear")(ref(x), ref(w), bias, act, ref(res),
+    return la.load().la_linear(ref(x), ref(w), bias, act, ref(res),
                               ref(out or rows(n=8, d=32)), None)
 
 
 def test_linear_refusals():
-    assert K._fn("la_linear")(None, ref(rows()), None, 0, None, ref(rows()), None) == BAD
-    assert K._fn("la_linear")(ref(rows()), None, None, 0, None, ref(rows()), None) == BAD
-    assert K._fn("la_linear")(ref(rows()), ref(rows()), None, 0, None, None, None) == BAD
+    assert la.load().la_linear(None, ref(rows()), None, 0, None, ref(rows()), None) == BAD
+    assert la.load().la_linear(ref(rows()), None, None, 0, None, ref(rows()), None) == BAD
+    assert la.load().la_linear(ref(rows()), ref(rows()), None, 0, None, None, None) == BAD
     assert lin(x=rows(d=72)) == BAD                            # K differs
     assert lin(out=rows(n=9, d=32)) == BAD                     # M differs
     assert lin(out=rows(n=8, d=40)) == BAD                     # N differs
@@ -59,12 +60,12 @@ def test_linear_refusals():
 
 def conv(x=None, w=0x20000, width=4, bias=None, act=2, sin=None, lens=None, out=None, sout=None):
     x = x or rows(b=2)
-    return K._fn("la_causal_conv")(ref(x), w, width, bias, act, sin, lens,
+    return la.load().la_causal_conv(ref(x), w, width, bias, act, sin, lens,
                                    ref(out or rows(b=2)), sout, None)
 
 
 def test_conv_refusals():
-    assert K._fn("la_causal_conv")(None, P0, 4, None, 2, None, None, ref(rows()), None, None) == BAD
+    assert la.load().la_causal_conv(None, P0, 4, None, 2, None, None, ref(rows()), None, None) == BAD
     assert conv(w=None) == BAD and conv(w=0x20004) == BAD
     assert conv(width=1) == UNS and conv(width=5) == UNS
     assert conv(act=1) == UNS and conv(act=9) == BAD
@@ -83,7 +84,7 @@ def test_conv_refusals():
 
 
 def test_conv_step_refusals():
-    f = K._fn("la_causal_conv_step")
+    f = la.load().la_causal_conv_step
     one = rows(b=2, n=1)
     assert f(None, ref(one), 0x20000, 4, None, 2, ref(one), None) == BAD
     assert f(0x30004, ref(one), 0x20000, 4, None, 2, ref(one), None) == BAD
@@ -93,7 +94,7 @@ def test_conv_step_refusals():
 
 def scan(x=None, dt=None, a=0x20000, S=16, b=None, c=None, skip=None, gate=None, bias=None,
          sin=None, lens=None, out=None, sout=None):
-    return K._fn("la_selective_scan")(
+    return la.load().la_selective_scan(
         ref(x or rows(b=2)), ref(dt or rows(b=2)), a, S, ref(b or rows(b=2, d=16)),
         ref(c or rows(b=2, d=16)), skip, ref(gate), bias, 1, sin, lens, ref(out or rows(b=2)),
         sout, None)
@@ -117,7 +118,7 @@ def test_scan_refusals():
 
 
 def test_step_refusals():
-    f = K._fn("la_selective_step")
+    f = la.load().la_selective_step
     one, bc = rows(b=2, n=1), rows(b=2, n=1, d=16)
 
     def step(state=0x30000, x=one, S=16):
