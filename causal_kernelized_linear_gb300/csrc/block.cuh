@@ -3,6 +3,7 @@
 #pragma once
 
 #include "common.cuh"
+#include "internal.h"
 #include "linattn.h"
 #include "tc.cuh"
 
@@ -50,6 +51,38 @@ __device__ __forceinline__ float activate(float x) {
   if constexpr (ACT == LA_ACT_GELU) return gelu(x);
   if constexpr (ACT == LA_ACT_SOFTPLUS) return softplus(x);
   return x;
+}
+
+// Every kernel of these operators is launched with programmatic stream
+// serialization: its CTAs may start while the kernel before it drains, and
+// nothing of global memory is touched before entry() has returned, which waits
+// until that kernel has completed with its memory visible.  The prologue of a
+// short kernel (launch, barriers, TMEM) overlaps its predecessor's tail.
+__device__ __forceinline__ void entry() {
+  tc::grid_dependency_wait();
+  tc::grid_dependents_launch();
+}
+
+template <typename... P, typename... A>
+cudaError_t launch(void (*kernel)(P...), unsigned grid, unsigned block, size_t smem,
+                   cudaStream_t s, unsigned cluster, A&&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+  if (e == cudaSuccess) count_launches(1);
+  return e;
 }
 
 // Elements of a 16-byte vector.

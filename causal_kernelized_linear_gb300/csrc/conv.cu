@@ -91,6 +91,7 @@ __global__ void __launch_bounds__(kThreads) conv_kernel(const ConvArgs a, uint32
   __shared__ uint4 ring[kRing][kThreads];   // a thread reads only what it copied itself
   const int64_t item = (int64_t)blockIdx.x * kThreads + threadIdx.x;
   if (item >= (int64_t)vecs * runs * a.B) return;
+  entry();
   const Item at = item_of(item, vecs, runs, a.B);
   const int64_t c = (int64_t)at.vec * V, b = at.b;
   const int n = (int)a.n;
@@ -147,6 +148,7 @@ __global__ void __launch_bounds__(kThreads) conv_step_kernel(const ConvArgs a, u
   constexpr int V = kVec<T>;
   const int64_t item = (int64_t)blockIdx.x * kThreads + threadIdx.x;
   if (item >= vecs * a.B) return;
+  entry();
   const Item at = item_of(item, vecs, 1, a.B);
   const int64_t c = (int64_t)at.vec * V, b = at.b;
   T* st = static_cast<T*>(a.state_out) + b * (W - 1) * a.D + c;
@@ -165,22 +167,18 @@ __global__ void __launch_bounds__(kThreads) conv_step_kernel(const ConvArgs a, u
 }
 
 template <typename T, int W, bool SILU>
-cudaError_t launch(const ConvArgs& a, bool step, cudaStream_t s) {
+cudaError_t launch_conv(const ConvArgs& a, bool step, cudaStream_t s) {
   const uint32_t vecs = (uint32_t)(a.D / kVec<T>);
   const uint32_t runs = step ? 1 : (uint32_t)((a.n + kRun - 1) / kRun);
   const int64_t blocks = ((int64_t)vecs * runs * a.B + kThreads - 1) / kThreads;
   if (blocks > INT32_MAX) return cudaErrorInvalidConfiguration;
-  if (step)
-    conv_step_kernel<T, W, SILU><<<(unsigned)blocks, kThreads, 0, s>>>(a, vecs);
-  else
-    conv_kernel<T, W, SILU><<<(unsigned)blocks, kThreads, 0, s>>>(a, vecs, runs);
-  count_launches(1);
-  return cudaGetLastError();
+  return step ? launch(conv_step_kernel<T, W, SILU>, (unsigned)blocks, kThreads, 0, s, 1, a, vecs)
+              : launch(conv_kernel<T, W, SILU>, (unsigned)blocks, kThreads, 0, s, 1, a, vecs, runs);
 }
 
 template <typename T, int W>
 cudaError_t by_act(const ConvArgs& a, bool step, cudaStream_t s) {
-  return a.silu ? launch<T, W, true>(a, step, s) : launch<T, W, false>(a, step, s);
+  return a.silu ? launch_conv<T, W, true>(a, step, s) : launch_conv<T, W, false>(a, step, s);
 }
 
 template <typename T>

@@ -5,12 +5,17 @@
 // tile_kernel: a CTA computes 64×128 outputs, K in steps of 16 through two
 // shared-memory buffers, 8×8 outputs per thread in packed pairs.  Bound by the
 // fp32 pipe: 32 packed multiply-adds against 4 shared loads per step of K.
+// Where tiles are few, 2 or 4 groups of threads of a CTA take K's steps in
+// turn and add their sums in order at the end: one group is one warp per
+// scheduler, which cannot hide its own latencies.
 //
 // row_kernel (few tokens, or too few tiles to fill the GPU): a warp computes
 // four output features for up to eight tokens, its lanes split K, so that w is
 // read once per eight tokens in 512-byte pieces; bound by reading w.
 #include "block.cuh"
 #include "internal.h"
+
+#include <atomic>
 
 namespace la {
 namespace {
@@ -36,15 +41,21 @@ __device__ __forceinline__ void finish4(const LinearArgs& a, int64_t m, int64_t 
 }
 
 constexpr int kBM = 64, kBN = 128, kBK = 16, kTileThreads = 128;
+constexpr int kXF = kBK * (kBM + 4), kWF = kBK * (kBN + 4);   // floats of a buffer
 
-template <int ACT>
-__global__ void __launch_bounds__(kTileThreads) tile_kernel(const LinearArgs a, int mtiles) {
-  __shared__ __align__(16) float xs[2][kBK][kBM + 4], ws[2][kBK][kBN + 4];
+template <int GROUPS> constexpr int kTileSmem = GROUPS * 2 * (kXF + kWF) * 4;
+
+template <int ACT, int GROUPS>
+__global__ void __launch_bounds__(GROUPS * kTileThreads) tile_kernel(const LinearArgs a, int mtiles) {
+  extern __shared__ __align__(16) float tile_smem[];
+  static_assert((GROUPS - 1) * 64 * kTileThreads * 4 <= kTileSmem<GROUPS>, "room for the groups' sums");
   const int64_t m0 = (int64_t)(blockIdx.x % mtiles) * kBM, n0 = (int64_t)(blockIdx.x / mtiles) * kBN;
   const float* x = static_cast<const float*>(a.x.data);
   const float* w = static_cast<const float*>(a.w.data);
-  const int tid = threadIdx.x, tx = tid % 16, ty = tid / 16;
+  const int group = threadIdx.x / kTileThreads, tid = threadIdx.x % kTileThreads;
+  const int tx = tid % 16, ty = tid / 16;
   const int lr = tid / 4, lk = (tid % 4) * 4;      // loads: row lr (+ 32 i), four of K
+  float* const mine = tile_smem + group * 2 * (kXF + kWF);
   float4 xr[2], wr[4];
   const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
   auto load = [&](int64_t k) {
@@ -61,37 +72,43 @@ __global__ void __launch_bounds__(kTileThreads) tile_kernel(const LinearArgs a, 
     }
   };
   auto put = [&](int buf) {
+    float* xs = mine + buf * (kXF + kWF);
+    float* ws = xs + kXF;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const float v[4] = {xr[i].x, xr[i].y, xr[i].z, xr[i].w};
 #pragma unroll
-      for (int j = 0; j < 4; ++j) xs[buf][lk + j][lr + 32 * i] = v[j];
+      for (int j = 0; j < 4; ++j) xs[(lk + j) * (kBM + 4) + lr + 32 * i] = v[j];
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const float v[4] = {wr[i].x, wr[i].y, wr[i].z, wr[i].w};
 #pragma unroll
-      for (int j = 0; j < 4; ++j) ws[buf][lk + j][lr + 32 * i] = v[j];
+      for (int j = 0; j < 4; ++j) ws[(lk + j) * (kBN + 4) + lr + 32 * i] = v[j];
     }
   };
+  entry();
   f32x2 acc[8][4];
 #pragma unroll
   for (int i = 0; i < 8; ++i)
 #pragma unroll
     for (int j = 0; j < 4; ++j) acc[i][j] = 0ull;
-  load(0);
+  load((int64_t)group * kBK);
   put(0);
   __syncthreads();
   int buf = 0;
-  for (int64_t k0 = 0; k0 < a.K; k0 += kBK, buf ^= 1) {
-    const bool more = k0 + kBK < a.K;
-    if (more) load(k0 + kBK);
+  // every group makes the same number of steps; those past K add zeros
+  for (int64_t k0 = 0; k0 < a.K; k0 += GROUPS * kBK, buf ^= 1) {
+    const bool more = k0 + GROUPS * kBK < a.K;
+    if (more) load(k0 + (GROUPS + group) * kBK);
+    const float* xs = mine + buf * (kXF + kWF);
+    const float* ws = xs + kXF;
 #pragma unroll
     for (int k = 0; k < kBK; ++k) {
-      const float4 xa = *reinterpret_cast<const float4*>(&xs[buf][k][ty * 4]);
-      const float4 xb = *reinterpret_cast<const float4*>(&xs[buf][k][32 + ty * 4]);
-      const ulonglong2 wa = *reinterpret_cast<const ulonglong2*>(&ws[buf][k][tx * 4]);
-      const ulonglong2 wb = *reinterpret_cast<const ulonglong2*>(&ws[buf][k][64 + tx * 4]);
+      const float4 xa = *reinterpret_cast<const float4*>(xs + k * (kBM + 4) + ty * 4);
+      const float4 xb = *reinterpret_cast<const float4*>(xs + k * (kBM + 4) + 32 + ty * 4);
+      const ulonglong2 wa = *reinterpret_cast<const ulonglong2*>(ws + k * (kBN + 4) + tx * 4);
+      const ulonglong2 wb = *reinterpret_cast<const ulonglong2*>(ws + k * (kBN + 4) + 64 + tx * 4);
       const float xv[8] = {xa.x, xa.y, xa.z, xa.w, xb.x, xb.y, xb.z, xb.w};
       const f32x2 wv[4] = {wa.x, wa.y, wb.x, wb.y};
 #pragma unroll
@@ -103,6 +120,26 @@ __global__ void __launch_bounds__(kTileThreads) tile_kernel(const LinearArgs a, 
     }
     if (more) put(buf ^ 1);
     __syncthreads();
+  }
+  if constexpr (GROUPS > 1) {
+    // the buffers are done with: the later groups' sums, one row per pair
+    f32x2* sums = reinterpret_cast<f32x2*>(tile_smem);
+    if (group > 0) {
+#pragma unroll
+      for (int i = 0; i < 32; ++i)
+        sums[((group - 1) * 32 + i) * kTileThreads + tid] = acc[i / 4][i % 4];
+    }
+    __syncthreads();
+    if (group > 0) return;
+#pragma unroll
+    for (int g = 0; g < GROUPS - 1; ++g)
+#pragma unroll
+      for (int i = 0; i < 32; ++i) {
+        float s0, s1, t0, t1;
+        unpack2(acc[i / 4][i % 4], s0, s1);
+        unpack2(sums[(g * 32 + i) * kTileThreads + tid], t0, t1);
+        acc[i / 4][i % 4] = pack2(s0 + t0, s1 + t1);
+      }
   }
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
@@ -128,6 +165,7 @@ __global__ void __launch_bounds__(32 * kRowWarps) row_kernel(const LinearArgs a,
   const int64_t n = ((int64_t)(blockIdx.x % fblocks) * kRowWarps + threadIdx.x / 32) * kRowFeatures;
   const int64_t m0 = (int64_t)(blockIdx.x / fblocks) * R;
   if (n >= a.N) return;
+  entry();
   const float* x = static_cast<const float*>(a.x.data);
   const float* w = static_cast<const float*>(a.w.data) + n * a.w.sn;
   float acc[R][kRowFeatures] = {};
@@ -166,20 +204,29 @@ cudaError_t launch_rows(const LinearArgs& a, cudaStream_t s) {
   const int64_t fb = (a.N + kRowWarps * kRowFeatures - 1) / (kRowWarps * kRowFeatures);
   const int64_t blocks = fb * ((a.M + R - 1) / R);
   if (blocks > INT32_MAX) return cudaErrorInvalidConfiguration;
-  row_kernel<ACT, R><<<(unsigned)blocks, 32 * kRowWarps, 0, s>>>(a, (int)fb);
-  count_launches(1);
-  return cudaGetLastError();
+  return launch(row_kernel<ACT, R>, (unsigned)blocks, 32 * kRowWarps, 0, s, 1, a, (int)fb);
+}
+
+template <int ACT, int GROUPS>
+cudaError_t launch_tiles(const LinearArgs& a, int64_t mt, int64_t nt, cudaStream_t s) {
+  static std::atomic<uint64_t> smem_set{0};
+  const cudaError_t e = allow_smem((const void*)tile_kernel<ACT, GROUPS>, kTileSmem<GROUPS>, &smem_set);
+  if (e != cudaSuccess) return e;
+  return launch(tile_kernel<ACT, GROUPS>, (unsigned)(mt * nt), GROUPS * kTileThreads,
+                kTileSmem<GROUPS>, s, 1, a, (int)mt);
 }
 
 template <int ACT>
 cudaError_t launch_f32(const LinearArgs& a, cudaStream_t s) {
   const int64_t mt = (a.M + kBM - 1) / kBM, nt = (a.N + kBN - 1) / kBN;
   if (a.M <= 2) return launch_rows<ACT, 2>(a, s);
-  if (a.M <= 32 || (a.M <= 256 && mt * nt < a.num_sms / 2)) return launch_rows<ACT, 8>(a, s);
+  if (a.M <= 32) return launch_rows<ACT, 8>(a, s);
   if (mt * nt > INT32_MAX) return cudaErrorInvalidConfiguration;
-  tile_kernel<ACT><<<(unsigned)(mt * nt), kTileThreads, 0, s>>>(a, (int)mt);
-  count_launches(1);
-  return cudaGetLastError();
+  // groups until an SM has twelve warps, as long as each has steps to take
+  const int64_t tiles = mt * nt, per_sm = (tiles + a.num_sms - 1) / a.num_sms;
+  if (per_sm == 1 && a.K >= 8 * kBK) return launch_tiles<ACT, 4>(a, mt, nt, s);
+  if (per_sm <= 2 && a.K >= 4 * kBK) return launch_tiles<ACT, 2>(a, mt, nt, s);
+  return launch_tiles<ACT, 1>(a, mt, nt, s);
 }
 
 cudaError_t f32_linear(const LinearArgs& a, cudaStream_t s) {

@@ -130,6 +130,7 @@ pair_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUte
   __syncthreads();
   cluster_sync();          // both CTAs' barriers exist before any remote arrival
   tc_fence_after();
+  entry();
   const uint32_t tmem = bars->tmem;
   volatile int* abort = &bars->abort;
 
@@ -254,11 +255,11 @@ constexpr int kFewThreads = 256;
 template <int BT> struct FewCfg {
   static constexpr int kXB = BT * kBK * 2;
   static constexpr int kStage = kTileB + kXB;
-  static constexpr int kNum = BT <= 32 ? 5 : (BT == 64 ? 4 : 6);
-  static constexpr int kPerSm = BT <= 64 ? 2 : 1;         // CTAs that fit
+  static constexpr int kNum = BT <= 32 ? 5 : (BT == 64 ? 4 : 6);   // most stages of the ring
+  static constexpr int kPerSm = BT <= 64 ? 2 : 1;         // CTAs that fit with all of them
   static constexpr int kPart = BT * 128 * 4;              // partial sums, over the stages
-  static constexpr int kBuf = kNum * kStage > kPart ? kNum * kStage : kPart;
-  static constexpr int kSmem = 1024 + kBuf + 256;
+  static constexpr int buf(int stages) { return stages * kStage > kPart ? stages * kStage : kPart; }
+  static constexpr int smem(int stages) { return 1024 + buf(stages) + 256; }
   static constexpr uint32_t kCols = BT < 32 ? 32 : BT;
 };
 
@@ -268,23 +269,24 @@ struct FewBars {
   int abort;
 };
 
-// blockIdx: x = feature tile × cluster rank, y = token tile.
+// Blocks: cluster rank fastest, then feature tile, then token tile.
 template <int BT, int ACT>
 __global__ void __launch_bounds__(kFewThreads)
 few_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap mw,
-           const LinParams p, const int split) {
+           const LinParams p, const int split, const int ftiles, const int stages) {
   using C = FewCfg<BT>;
   extern __shared__ uint8_t raw[];
   uint8_t* base = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
-  FewBars* bars = reinterpret_cast<FewBars*>(base + C::kBuf);
+  FewBars* bars = reinterpret_cast<FewBars*>(raw + C::smem(stages) - 256);
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int rank = (int)(blockIdx.x % split);
-  const int n0 = (int)(blockIdx.x / split) * 128, m0 = (int)blockIdx.y * BT;
+  const int tile = (int)(blockIdx.x / split);
+  const int n0 = tile % ftiles * 128, m0 = tile / ftiles * BT;
   const int k0 = (int)((int64_t)p.kblocks * rank / split);
   const int k1 = (int)((int64_t)p.kblocks * (rank + 1) / split);
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < C::kNum; ++i) {
+    for (int i = 0; i < stages; ++i) {
       mbar_init(&bars->full[i], 1);
       mbar_init(&bars->empty[i], 1);
     }
@@ -301,28 +303,31 @@ few_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUten
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  entry();
   const uint32_t tmem = bars->tmem;
   volatile int* abort = &bars->abort;
 
+  const int steps = k1 - k0;
   if (warp == 0 && lane == 0) {
-    uint32_t it = 0;
-    for (int kb = k0; kb < k1; ++kb, ++it) {
-      const int s = it % C::kNum;
-      if (it >= C::kNum && !mbar_wait(&bars->empty[s], ((it / C::kNum) & 1) ^ 1, p.status, abort))
-        break;
+    int s = 0, it = 0;
+    uint32_t lap = 0;      // times the ring has been filled
+    for (; it < steps; ++it) {
+      if (it >= stages && !mbar_wait(&bars->empty[s], (lap & 1) ^ 1, p.status, abort)) break;
+      const int kb = k0 + it;
       mbar_arrive_expect_tx(&bars->full[s], C::kStage);
       tma_load_2d(base + s * C::kStage, &mw, &bars->full[s], kb * kBK, n0);
       tma_load_2d(base + s * C::kStage + kTileB, &mx, &bars->full[s], kb * kBK, m0);
+      if (++s == stages) s = 0, ++lap;
     }
     if (*abort)
-      for (uint32_t j = it > C::kNum ? it - C::kNum : 0; j < it; ++j)
-        mbar_wait_drain(&bars->full[j % C::kNum], (j / C::kNum) & 1);
+      for (int j = it > stages ? it - stages : 0; j < it; ++j)
+        mbar_wait_drain(&bars->full[j % stages], (j / stages) & 1);
   } else if (warp == 1 && lane == 0) {
     constexpr uint32_t idesc = idesc_bf16_f32(128, BT, false, false);
-    uint32_t it = 0;
-    for (int kb = k0; kb < k1; ++kb, ++it) {
-      const int s = it % C::kNum;
-      if (!mbar_wait(&bars->full[s], (it / C::kNum) & 1, p.status, abort)) break;
+    int s = 0;
+    uint32_t lap = 0;
+    for (int it = 0; it < steps; ++it) {
+      if (!mbar_wait(&bars->full[s], lap & 1, p.status, abort)) break;
       tc_fence_after();
       const uint64_t dw = smem_desc(smem_u32(base + s * C::kStage), 16, 1024, kSwizzle128B);
       const uint64_t dx = smem_desc(smem_u32(base + s * C::kStage + kTileB), 16, 1024, kSwizzle128B);
@@ -330,6 +335,7 @@ few_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUten
       for (int k = 0; k < kBK / 16; ++k)
         mma_ss(tmem, desc_at(dw, k * 32), desc_at(dx, k * 32), idesc, it > 0 || k > 0);
       mma_commit(&bars->empty[s]);
+      if (++s == stages) s = 0, ++lap;
     }
     mma_commit(&bars->done);
   }
@@ -404,32 +410,29 @@ cudaError_t launch_pair(const LinearArgs& a, LinParams p, cudaStream_t s) {
   static std::atomic<uint64_t> smem_set{0};
   e = allow_smem((const void*)pair_kernel<BN, ACT>, PairCfg<BN>::kSmem, &smem_set);
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(2);
-  cfg.blockDim = dim3(kPairThreads);
-  cfg.dynamicSmemBytes = PairCfg<BN>::kSmem;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 2;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
   // as many pairs as can be resident at once (a GPC with an odd number of SMs
   // leaves one out), each walking its share of the tiles
   static std::atomic<int> resident{0};
   int pairs = resident.load(std::memory_order_relaxed);
   if (pairs == 0) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2);
+    cfg.blockDim = dim3(kPairThreads);
+    cfg.dynamicSmemBytes = PairCfg<BN>::kSmem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
     e = cudaOccupancyMaxActiveClusters(&pairs, pair_kernel<BN, ACT>, &cfg);
     if (e != cudaSuccess) return e;
     if (pairs < 1) return cudaErrorInvalidConfiguration;
     resident.store(pairs, std::memory_order_relaxed);
   }
-  cfg.gridDim = dim3(2 * (unsigned)(tiles < pairs ? tiles : pairs));
-  e = cudaLaunchKernelEx(&cfg, pair_kernel<BN, ACT>, mx, mw, mo, p);
-  count_launches(1);
-  return e;
+  return launch(pair_kernel<BN, ACT>, 2 * (unsigned)(tiles < pairs ? tiles : pairs), kPairThreads,
+                PairCfg<BN>::kSmem, s, 2, mx, mw, mo, p);
 }
 
 // CTAs that share a feature tile's K: as many as are resident at once, while
@@ -449,30 +452,20 @@ cudaError_t launch_few(const LinearArgs& a, const LinParams& p, cudaStream_t s) 
       (e = tmap_view(&mw, a.w.data, a.N, a.K, a.w.sn ? a.w.sn : a.K, 128)) != cudaSuccess)
     return e;
   const int64_t ft = (a.N + 127) / 128, mt = (a.M + BT - 1) / BT;
-  const int split = few_split(ft * mt, p.kblocks, (int64_t)C::kPerSm * a.num_sms);
-  if (mt > 65535 || ft * split > INT32_MAX) return cudaErrorInvalidConfiguration;
+  const int split = few_split(ft * mt, p.kblocks, C::kPerSm * (int64_t)a.num_sms);
+  // no more stages than steps: a short K leaves room for more CTAs per SM
+  const int steps = (p.kblocks + split - 1) / split;
+  const int stages = steps < C::kNum ? steps : C::kNum;
+  if (ft * split * mt > INT32_MAX) return cudaErrorInvalidConfiguration;
   static std::atomic<uint64_t> smem_set{0};
-  e = allow_smem((const void*)few_kernel<BT, ACT>, C::kSmem, &smem_set);
+  e = allow_smem((const void*)few_kernel<BT, ACT>, C::smem(C::kNum), &smem_set);
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(ft * split), (unsigned)mt);
-  cfg.blockDim = dim3(kFewThreads);
-  cfg.dynamicSmemBytes = C::kSmem;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = (unsigned)split;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, few_kernel<BT, ACT>, mx, mw, p, split);
-  count_launches(1);
-  return e;
+  return launch(few_kernel<BT, ACT>, (unsigned)(ft * split * mt), kFewThreads,
+                C::smem(stages), s, (unsigned)split, mx, mw, p, split, (int)ft, stages);
 }
 
-constexpr double kFewStep = 600, kPair256Step = 560, kPair128Step = 330;
-constexpr double kFewFixed = 3000, kPairFixed = 5000;
+constexpr double kFewStep = 520, kPair256Step = 540, kPair128Step = 460;
+constexpr double kFewFixed = 5000, kPairFixed = 7000;
 
 template <int ACT>
 cudaError_t by_shape(const LinearArgs& a, cudaStream_t s) {
@@ -490,16 +483,17 @@ cudaError_t by_shape(const LinearArgs& a, cudaStream_t s) {
   if (a.M <= 32) return launch_few<32, ACT>(a, p, s);
   if (a.M <= 64) return launch_few<64, ACT>(a, p, s);
   if (a.M <= 128) return launch_few<128, ACT>(a, p, s);
-  // The cheaper of the three by SM cycles per 64-wide step of K, measured where
-  // every SM has a tile (few: 32 KB a step through L2; pair: 256 or 128
-  // columns), times the tiles that follow one another on an SM.
+  // The cheapest of the three, in SM cycles: the tiles that follow one another
+  // on an SM, times a tile's steps of K, times a step (each bound by about 64
+  // bytes a cycle into the SM: 32 KB for few and for 256 columns, 24 KB for
+  // 128 columns; measured on shapes that give every SM a tile).
   const int64_t ft = (a.N + 127) / 128, mt = (a.M + 127) / 128;
   const int split = few_split(ft * mt, p.kblocks, a.num_sms);
-  auto waves = [](int64_t tiles, int64_t slots) { return (tiles + slots - 1) / slots; };
+  auto waves = [](int64_t tiles, int64_t slots) { return (double)((tiles + slots - 1) / slots); };
   const int64_t pt = (a.M + 255) / 256, pairs = a.num_sms / 2;
-  const double few = waves(ft * mt * split, a.num_sms) * (double)(p.kblocks + split - 1) / split * kFewStep + kFewFixed;
-  const double p256 = waves(pt * ((a.N + 255) / 256), pairs) * (double)p.kblocks * kPair256Step + kPairFixed;
-  const double p128 = waves(pt * ((a.N + 127) / 128), pairs) * (double)p.kblocks * kPair128Step + kPairFixed;
+  const double few = kFewFixed + waves(ft * mt * split, a.num_sms) * p.kblocks / split * kFewStep;
+  const double p256 = kPairFixed + waves(pt * ((a.N + 255) / 256), pairs) * p.kblocks * kPair256Step;
+  const double p128 = kPairFixed + waves(pt * ((a.N + 127) / 128), pairs) * p.kblocks * kPair128Step;
   if (few <= p256 && few <= p128) return launch_few<128, ACT>(a, p, s);
   if (p256 <= p128) return launch_pair<256, ACT>(a, p, s);
   return launch_pair<128, ACT>(a, p, s);
