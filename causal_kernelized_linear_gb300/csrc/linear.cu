@@ -3,15 +3,18 @@
 // three they would keep 22, but their sums are not rounded like fp32's).
 //
 // tile_kernel: a CTA computes 64×128 outputs, K in steps of 16 through two
-// shared-memory buffers, 8×8 outputs per thread in packed pairs.  Bound by the
-// fp32 pipe: 32 packed multiply-adds against 4 shared loads per step of K.
+// shared-memory buffers, 8×8 outputs per thread in packed pairs: 32 packed
+// multiply-adds against 4 shared loads of 16 bytes per step of K, which keeps
+// the fp32 pipe and the shared-memory pipe equally busy.  Where that leaves SMs
+// idle, 32×64 outputs, 4×4 per thread.
 // Where tiles are few, 2 or 4 groups of threads of a CTA take K's steps in
 // turn and add their sums in order at the end: one group is one warp per
 // scheduler, which cannot hide its own latencies.
 //
-// row_kernel (few tokens, or too few tiles to fill the GPU): a warp computes
+// row_kernel (few tokens, or too few tiles to fill the GPU): a CTA computes
 // four output features for up to eight tokens, its lanes split K, so that w is
-// read once per eight tokens in 512-byte pieces; bound by reading w.
+// read once per eight tokens in 512-byte pieces; bound by reading w for eight
+// tokens, by the loads of x for more.
 #include "block.cuh"
 #include "internal.h"
 
@@ -40,15 +43,22 @@ __device__ __forceinline__ void finish4(const LinearArgs& a, int64_t m, int64_t 
       make_float4(v[0], v[1], v[2], v[3]);
 }
 
-constexpr int kBM = 64, kBN = 128, kBK = 16, kTileThreads = 128;
-constexpr int kXF = kBK * (kBM + 4), kWF = kBK * (kBN + 4);   // floats of a buffer
+constexpr int kBK = 16, kTileThreads = 128;
 
-template <int GROUPS> constexpr int kTileSmem = GROUPS * 2 * (kXF + kWF) * 4;
+// T×T outputs per thread (8 or 4).
+template <int T> struct Tile {
+  static constexpr int kBM = 8 * T, kBN = 16 * T;
+  static constexpr int kXF = kBK * (kBM + 4), kWF = kBK * (kBN + 4);   // floats of a buffer
+};
 
-template <int ACT, int GROUPS>
+template <int T, int GROUPS> constexpr int kTileSmem = GROUPS * 2 * (Tile<T>::kXF + Tile<T>::kWF) * 4;
+
+template <int ACT, int T, int GROUPS>
 __global__ void __launch_bounds__(GROUPS * kTileThreads) tile_kernel(const LinearArgs a, int mtiles) {
   extern __shared__ __align__(16) float tile_smem[];
-  static_assert((GROUPS - 1) * 64 * kTileThreads * 4 <= kTileSmem<GROUPS>, "room for the groups' sums");
+  constexpr int kBM = Tile<T>::kBM, kBN = Tile<T>::kBN, kXF = Tile<T>::kXF, kWF = Tile<T>::kWF;
+  constexpr int P = T / 2;                         // packed pairs per row of a thread
+  static_assert((GROUPS - 1) * T * T * kTileThreads * 4 <= kTileSmem<T, GROUPS>, "room for the groups' sums");
   const int64_t m0 = (int64_t)(blockIdx.x % mtiles) * kBM, n0 = (int64_t)(blockIdx.x / mtiles) * kBN;
   const float* x = static_cast<const float*>(a.x.data);
   const float* w = static_cast<const float*>(a.w.data);
@@ -56,17 +66,17 @@ __global__ void __launch_bounds__(GROUPS * kTileThreads) tile_kernel(const Linea
   const int tx = tid % 16, ty = tid / 16;
   const int lr = tid / 4, lk = (tid % 4) * 4;      // loads: row lr (+ 32 i), four of K
   float* const mine = tile_smem + group * 2 * (kXF + kWF);
-  float4 xr[2], wr[4];
+  float4 xr[T / 4], wr[T / 2];
   const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
   auto load = [&](int64_t k) {
     const bool in = k + lk < a.K;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < T / 4; ++i) {
       const int64_t m = m0 + lr + 32 * i;
       xr[i] = in && m < a.M ? __ldg(reinterpret_cast<const float4*>(x + m * a.x.sn + k + lk)) : zero;
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < T / 2; ++i) {
       const int64_t n = n0 + lr + 32 * i;
       wr[i] = in && n < a.N ? __ldg(reinterpret_cast<const float4*>(w + n * a.w.sn + k + lk)) : zero;
     }
@@ -75,24 +85,24 @@ __global__ void __launch_bounds__(GROUPS * kTileThreads) tile_kernel(const Linea
     float* xs = mine + buf * (kXF + kWF);
     float* ws = xs + kXF;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < T / 4; ++i) {
       const float v[4] = {xr[i].x, xr[i].y, xr[i].z, xr[i].w};
 #pragma unroll
       for (int j = 0; j < 4; ++j) xs[(lk + j) * (kBM + 4) + lr + 32 * i] = v[j];
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < T / 2; ++i) {
       const float v[4] = {wr[i].x, wr[i].y, wr[i].z, wr[i].w};
 #pragma unroll
       for (int j = 0; j < 4; ++j) ws[(lk + j) * (kBN + 4) + lr + 32 * i] = v[j];
     }
   };
   entry();
-  f32x2 acc[8][4];
+  f32x2 acc[T][P];
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
+  for (int i = 0; i < T; ++i)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) acc[i][j] = 0ull;
+    for (int j = 0; j < P; ++j) acc[i][j] = 0ull;
   load((int64_t)group * kBK);
   put(0);
   __syncthreads();
@@ -105,17 +115,23 @@ __global__ void __launch_bounds__(GROUPS * kTileThreads) tile_kernel(const Linea
     const float* ws = xs + kXF;
 #pragma unroll
     for (int k = 0; k < kBK; ++k) {
-      const float4 xa = *reinterpret_cast<const float4*>(xs + k * (kBM + 4) + ty * 4);
-      const float4 xb = *reinterpret_cast<const float4*>(xs + k * (kBM + 4) + 32 + ty * 4);
-      const ulonglong2 wa = *reinterpret_cast<const ulonglong2*>(ws + k * (kBN + 4) + tx * 4);
-      const ulonglong2 wb = *reinterpret_cast<const ulonglong2*>(ws + k * (kBN + 4) + 64 + tx * 4);
-      const float xv[8] = {xa.x, xa.y, xa.z, xa.w, xb.x, xb.y, xb.z, xb.w};
-      const f32x2 wv[4] = {wa.x, wa.y, wb.x, wb.y};
+      float xv[T];
+      f32x2 wv[P];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
+      for (int i = 0; i < T / 4; ++i) {
+        const float4 v = *reinterpret_cast<const float4*>(xs + k * (kBM + 4) + 32 * i + ty * 4);
+        xv[4 * i] = v.x, xv[4 * i + 1] = v.y, xv[4 * i + 2] = v.z, xv[4 * i + 3] = v.w;
+      }
+#pragma unroll
+      for (int i = 0; i < T / 4; ++i) {
+        const ulonglong2 u = *reinterpret_cast<const ulonglong2*>(ws + k * (kBN + 4) + 64 * i + tx * 4);
+        wv[2 * i] = u.x, wv[2 * i + 1] = u.y;
+      }
+#pragma unroll
+      for (int i = 0; i < T; ++i) {
         const f32x2 d = pack2(xv[i], xv[i]);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = fma2(d, wv[j], acc[i][j]);
+        for (int j = 0; j < P; ++j) acc[i][j] = fma2(d, wv[j], acc[i][j]);
       }
     }
     if (more) put(buf ^ 1);
@@ -126,27 +142,27 @@ __global__ void __launch_bounds__(GROUPS * kTileThreads) tile_kernel(const Linea
     f32x2* sums = reinterpret_cast<f32x2*>(tile_smem);
     if (group > 0) {
 #pragma unroll
-      for (int i = 0; i < 32; ++i)
-        sums[((group - 1) * 32 + i) * kTileThreads + tid] = acc[i / 4][i % 4];
+      for (int i = 0; i < T * P; ++i)
+        sums[((group - 1) * T * P + i) * kTileThreads + tid] = acc[i / P][i % P];
     }
     __syncthreads();
     if (group > 0) return;
 #pragma unroll
     for (int g = 0; g < GROUPS - 1; ++g)
 #pragma unroll
-      for (int i = 0; i < 32; ++i) {
+      for (int i = 0; i < T * P; ++i) {
         float s0, s1, t0, t1;
-        unpack2(acc[i / 4][i % 4], s0, s1);
-        unpack2(sums[(g * 32 + i) * kTileThreads + tid], t0, t1);
-        acc[i / 4][i % 4] = pack2(s0 + t0, s1 + t1);
+        unpack2(acc[i / P][i % P], s0, s1);
+        unpack2(sums[(g * T * P + i) * kTileThreads + tid], t0, t1);
+        acc[i / P][i % P] = pack2(s0 + t0, s1 + t1);
       }
   }
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
+  for (int i = 0; i < T; ++i) {
     const int64_t m = m0 + (i / 4) * 32 + ty * 4 + i % 4;
     if (m >= a.M) continue;
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
+    for (int j = 0; j < T / 4; ++j) {
       const int64_t n = n0 + j * 64 + tx * 4;   // N is a multiple of 4
       if (n >= a.N) continue;
       float v[4];
@@ -161,16 +177,16 @@ constexpr int kRowWarps = 4, kRowFeatures = 4;
 
 template <int ACT, int R>
 __global__ void __launch_bounds__(32 * kRowWarps) row_kernel(const LinearArgs a, int fblocks) {
-  const int lane = threadIdx.x % 32;
-  const int64_t n = ((int64_t)(blockIdx.x % fblocks) * kRowWarps + threadIdx.x / 32) * kRowFeatures;
+  __shared__ float sums[kRowWarps][R][kRowFeatures];
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  const int64_t n = (int64_t)(blockIdx.x % fblocks) * kRowFeatures;   // N is a multiple of 4
   const int64_t m0 = (int64_t)(blockIdx.x / fblocks) * R;
-  if (n >= a.N) return;
   entry();
   const float* x = static_cast<const float*>(a.x.data);
   const float* w = static_cast<const float*>(a.w.data) + n * a.w.sn;
   float acc[R][kRowFeatures] = {};
 #pragma unroll 2
-  for (int64_t k = lane * 4; k < a.K; k += 128) {
+  for (int64_t k = (warp * 32 + lane) * 4; k < a.K; k += 128 * kRowWarps) {
     float4 wv[kRowFeatures];
 #pragma unroll
     for (int j = 0; j < kRowFeatures; ++j)
@@ -191,42 +207,69 @@ __global__ void __launch_bounds__(32 * kRowWarps) row_kernel(const LinearArgs a,
 #pragma unroll
   for (int r = 0; r < R; ++r)
 #pragma unroll
-    for (int j = 0; j < kRowFeatures; ++j)
+    for (int j = 0; j < kRowFeatures; ++j) {
 #pragma unroll
       for (int s = 16; s >= 1; s /= 2) acc[r][j] += __shfl_xor_sync(0xffffffffu, acc[r][j], s);
+      if (lane == r * kRowFeatures + j) sums[warp][r][j] = acc[r][j];
+    }
+  __syncthreads();
+  const int64_t m = m0 + threadIdx.x;
+  if (threadIdx.x >= R || m >= a.M) return;
+  float v[4] = {};
 #pragma unroll
-  for (int r = 0; r < R; ++r)
-    if (lane == r && m0 + r < a.M) finish4<ACT>(a, m0 + r, n, acc[r]);
+  for (int i = 0; i < kRowWarps; ++i)
+#pragma unroll
+    for (int j = 0; j < kRowFeatures; ++j) v[j] += sums[i][threadIdx.x][j];
+  finish4<ACT>(a, m, n, v);
 }
 
 template <int ACT, int R>
 cudaError_t launch_rows(const LinearArgs& a, cudaStream_t s) {
-  const int64_t fb = (a.N + kRowWarps * kRowFeatures - 1) / (kRowWarps * kRowFeatures);
+  const int64_t fb = (a.N + kRowFeatures - 1) / kRowFeatures;
   const int64_t blocks = fb * ((a.M + R - 1) / R);
   if (blocks > INT32_MAX) return cudaErrorInvalidConfiguration;
   return launch(row_kernel<ACT, R>, (unsigned)blocks, 32 * kRowWarps, 0, s, 1, a, (int)fb);
 }
 
-template <int ACT, int GROUPS>
-cudaError_t launch_tiles(const LinearArgs& a, int64_t mt, int64_t nt, cudaStream_t s) {
+template <int ACT, int T, int GROUPS>
+cudaError_t launch_groups(const LinearArgs& a, int64_t mt, int64_t nt, cudaStream_t s) {
+  constexpr int smem = kTileSmem<T, GROUPS>;
   static std::atomic<uint64_t> smem_set{0};
-  const cudaError_t e = allow_smem((const void*)tile_kernel<ACT, GROUPS>, kTileSmem<GROUPS>, &smem_set);
+  const cudaError_t e = allow_smem((const void*)tile_kernel<ACT, T, GROUPS>, smem, &smem_set);
   if (e != cudaSuccess) return e;
-  return launch(tile_kernel<ACT, GROUPS>, (unsigned)(mt * nt), GROUPS * kTileThreads,
-                kTileSmem<GROUPS>, s, 1, a, (int)mt);
+  return launch(tile_kernel<ACT, T, GROUPS>, (unsigned)(mt * nt), GROUPS * kTileThreads, smem, s, 1,
+                a, (int)mt);
 }
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// Tiles of T that follow one another on an SM.
+template <int T> int64_t tile_rounds(const LinearArgs& a) {
+  return ceil_div(ceil_div(a.M, Tile<T>::kBM) * ceil_div(a.N, Tile<T>::kBN), a.num_sms);
+}
+
+template <int ACT, int T>
+cudaError_t launch_tiles(const LinearArgs& a, cudaStream_t s) {
+  const int64_t mt = ceil_div(a.M, Tile<T>::kBM), nt = ceil_div(a.N, Tile<T>::kBN);
+  if (mt * nt > INT32_MAX) return cudaErrorInvalidConfiguration;
+  // groups until an SM has about twelve warps, as long as each has steps to take
+  const int64_t rounds = tile_rounds<T>(a);
+  if (rounds == 1 && a.K >= 8 * kBK) return launch_groups<ACT, T, 4>(a, mt, nt, s);
+  if (rounds <= 2 && a.K >= 4 * kBK) return launch_groups<ACT, T, 2>(a, mt, nt, s);
+  return launch_groups<ACT, T, 1>(a, mt, nt, s);
+}
+
+// SM cycles per element of K: rows at kRowRate multiply-adds per SM and cycle,
+// the tiles that follow one another on an SM at what one measured.
+constexpr double kRowRate = 18, kTile8 = 100, kTile4 = 48;
 
 template <int ACT>
 cudaError_t launch_f32(const LinearArgs& a, cudaStream_t s) {
-  const int64_t mt = (a.M + kBM - 1) / kBM, nt = (a.N + kBN - 1) / kBN;
   if (a.M <= 2) return launch_rows<ACT, 2>(a, s);
-  if (a.M <= 32) return launch_rows<ACT, 8>(a, s);
-  if (mt * nt > INT32_MAX) return cudaErrorInvalidConfiguration;
-  // groups until an SM has twelve warps, as long as each has steps to take
-  const int64_t tiles = mt * nt, per_sm = (tiles + a.num_sms - 1) / a.num_sms;
-  if (per_sm == 1 && a.K >= 8 * kBK) return launch_tiles<ACT, 4>(a, mt, nt, s);
-  if (per_sm <= 2 && a.K >= 4 * kBK) return launch_tiles<ACT, 2>(a, mt, nt, s);
-  return launch_tiles<ACT, 1>(a, mt, nt, s);
+  const double rows = (double)a.M * a.N / a.num_sms / kRowRate;
+  const double large = tile_rounds<8>(a) * kTile8, small = tile_rounds<4>(a) * kTile4;
+  if (a.M <= 8 || (rows < large && rows < small)) return launch_rows<ACT, 8>(a, s);
+  return small < large ? launch_tiles<ACT, 4>(a, s) : launch_tiles<ACT, 8>(a, s);
 }
 
 cudaError_t f32_linear(const LinearArgs& a, cudaStream_t s) {
