@@ -464,3 +464,166 @@ def test_streams_and_graph_capture():
     torch.cuda.synchronize()
     assert torch.equal(out, block())
     assert la.last_device_status() == 0
+
+
+# ------------------------------------------------------------------ sizes of the larger kernels
+
+@pytest.mark.parametrize("m,k,n", [
+    (6000, 64, 2056),      # several waves of 256-column pairs, a ragged last column
+    (1024, 520, 2048),     # 128-column pairs, K off 64
+    (2500, 1000, 1288), (700, 2048, 2048), (4099, 8, 4096), (300, 4096, 520), (129, 4096, 4096)])
+@pytest.mark.parametrize("act,use_bias,use_res", [("none", False, False), ("silu", True, True)])
+def test_linear_bf16_kernels(m, k, n, act, use_bias, use_res):
+    g = _gen(m + n)
+    x = _randn(g, m, k, dtype=torch.bfloat16)
+    w = _randn(g, n, k, dtype=torch.bfloat16, scale=k ** -0.5)
+    bias = _randn(g, n, dtype=torch.bfloat16) if use_bias else None
+    res = _randn(g, m, n, dtype=torch.bfloat16) if use_res else None
+    y = la.linear(x, w, bias=bias, activation=act, residual=res)
+    ref, ab = _linear_ref(x, w, bias, act, res)
+    _close(y, ref, ab, k + 2, torch.bfloat16)
+    again = res.clone() if use_res else torch.empty_like(y)
+    la.linear(x, w, bias=bias, activation=act, residual=again if use_res else None, out=again)
+    assert torch.equal(again, y)
+    assert la.last_device_status() == 0
+
+
+@pytest.mark.parametrize("m,k,n", [
+    (9, 36, 20), (100, 2048, 1032), (200, 512, 1024), (400, 1024, 512), (777, 128, 4096),
+    (1000, 1028, 1024), (3000, 68, 1000), (64, 4096, 64)])
+@pytest.mark.parametrize("act,use_bias,use_res", [("none", False, False), ("gelu", True, True)])
+def test_linear_f32_kernels(m, k, n, act, use_bias, use_res):
+    g = _gen(m + n)
+    x = _randn(g, m, k, dtype=torch.float32)
+    w = _randn(g, n, k, dtype=torch.float32, scale=k ** -0.5)
+    bias = _randn(g, n, dtype=torch.float32) if use_bias else None
+    res = _randn(g, m, n, dtype=torch.float32) if use_res else None
+    y = la.linear(x, w, bias=bias, activation=act, residual=res)
+    ref, ab = _linear_ref(x, w, bias, act, res)
+    _close(y, ref, ab, k + 2, torch.float32)
+    assert torch.equal(y, la.linear(x, w, bias=bias, activation=act, residual=res))
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=["bf16", "f32"])
+@pytest.mark.parametrize("S", [16, 32])
+def test_scan_chunks_and_lengths(dtype, S):
+    # a sequence long enough for many chunks; lengths on, before and after a
+    # chunk's border, and in its first chunk
+    n = 2100
+    lens = [n, 0, 64, 65, 1024, 1030, 2090]
+    i = _scan_inputs(_gen(S), len(lens), n, 24, S, dtype, state=True)
+    y, ys, h, hs = _scan_ref(i, lens)
+    got, after = la.selective_scan(**i, return_state=True,
+                                   lengths=torch.tensor(lens, device=DEV, dtype=torch.int32))
+    _close(got, y, 4 * ys, n + S, dtype, "y")
+    _close(after, h, 4 * hs, n + S, torch.float32, "state")
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=["bf16", "f32"])
+@pytest.mark.parametrize("S", [8, 16, 64])
+@pytest.mark.parametrize("B", [4, 9, 300])
+def test_step_batches(dtype, S, B):
+    # enough elements for four batch entries per lane, with a remainder
+    D = 2048
+    i = _scan_inputs(_gen(S + B), B, 1, D, S, dtype, state=True)
+    y, ys, h, hs = _scan_ref(i)
+    one = {k: (v[:, 0] if k in ("x", "dt", "b", "c", "gate") and v is not None else v)
+           for k, v in i.items()}
+    st = one.pop("state").clone()
+    got = la.selective_step(st, **one)
+    _close(got, y[:, 0], 4 * ys[:, 0], S + 1, dtype, "y")
+    _close(st, h, 4 * hs, S + 1, torch.float32, "state")
+
+
+# ------------------------------------------------------------------ offsets past 32 bits
+
+def test_offsets_past_32_bits():
+    g = _gen(21)
+    far = (1 << 31) + 4096
+    big = torch.zeros(far + (1 << 16), device=DEV, dtype=torch.bfloat16)
+    D, n = 64, 40
+
+    def spread(t):       # batch entry 1 lies 2^31 elements after entry 0
+        v = big.as_strided((2, n, D), (far, D, 1))
+        v.copy_(t)
+        return v
+
+    x = _randn(g, 2, n, D, dtype=torch.bfloat16)
+    w = _randn(g, D, 4, dtype=torch.bfloat16)
+    want = la.causal_conv(x, w)
+    assert torch.equal(la.causal_conv(spread(x), w), want)
+    i = _scan_inputs(g, 2, n, D, 16, torch.bfloat16)
+    want, end = la.selective_scan(**i, return_state=True)
+    got, after = la.selective_scan(**dict(i, x=spread(i["x"])), return_state=True)
+    assert torch.equal(got, want) and torch.equal(after, end)
+    out = big.as_strided((2, n, D), (far, D, 1))
+    la.selective_scan(**i, out=out)
+    assert torch.equal(out, want)
+    st = end.clone()
+    one = {k: (v[:, 0] if k in ("x", "dt", "b", "c", "gate") else v) for k, v in i.items()}
+    one.pop("state")
+    y = la.selective_step(st, **one)
+    st2 = end.clone()
+    xs = spread(i["x"])[:, 0]
+    assert torch.equal(la.selective_step(st2, **dict(one, x=xs)), y) and torch.equal(st, st2)
+    # rows of x 2^28 elements apart
+    del out, xs
+    rows = big.as_strided((9, 64), (1 << 28, 1))
+    xl = _randn(g, 9, 64, dtype=torch.bfloat16)
+    rows.copy_(xl)
+    wl = _randn(g, 136, 64, dtype=torch.bfloat16)
+    assert torch.equal(la.linear(rows, wl), la.linear(xl, wl))
+
+
+# ------------------------------------------------------------------ the block as a whole
+
+def test_example_block_prompt_and_tokens_agree():
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples",
+                        "state_space_block.py")
+    spec = importlib.util.spec_from_file_location("state_space_block", path)
+    mod = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(mod)
+    # every value passes through eight bf16 roundings on either path (2^-8 each,
+    # relative to values that the residual keeps near the largest): 2^-5
+    assert mod.run(width=128, batch=3, prompt=70, tokens=5) <= 2.0 ** -5
+    assert mod.run(width=512, batch=2, prompt=300, tokens=3) <= 2.0 ** -5
+
+
+def test_debug_build_gives_the_same_bits():
+    # the LA_DEBUG library in a child process: no check fails, equal outputs
+    import subprocess
+    import sys
+    import tempfile
+    code = (
+        "import sys, torch, causal_kernelized_linear_gb300 as la\n"
+        "g = torch.Generator(device='cuda').manual_seed(5)\n"
+        "r = lambda *s: torch.randn(*s, device='cuda', generator=g).bfloat16()\n"
+        "out = {}\n"
+        "for m, k, n in ((5, 200, 136), (130, 520, 1000), (3000, 264, 2056)):\n"
+        "    out[f'{m}'] = la.linear(r(m, k), r(n, k), bias=r(n), activation='silu', residual=r(m, n))\n"
+        "out['conv'] = la.causal_conv(r(2, 77, 72), r(72, 4))\n"
+        "out['scan'] = la.selective_scan(r(1, 700, 72), r(1, 700, 72), -torch.rand(72, 16,"
+        " device='cuda', generator=g), r(1, 700, 16), r(1, 700, 16))\n"
+        "out['status'] = torch.tensor(la.last_device_check())\n"
+        "out['debug'] = torch.tensor(int(la.debug_build()))\n"
+        "torch.save({k: v.cpu() for k, v in out.items()}, sys.argv[1])\n")
+    import os
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    la.build()
+    la.build(debug=True)
+    got = []
+    with tempfile.TemporaryDirectory() as d:
+        for debug in ("0", "1"):
+            path = os.path.join(d, debug)
+            env = dict(os.environ, LA_DEBUG=debug, PYTHONPATH=root)
+            p = subprocess.run([sys.executable, "-c", code, path], env=env, capture_output=True,
+                               text=True, timeout=300)
+            assert p.returncode == 0, p.stderr[-2000:]
+            got.append(torch.load(path))
+    rel, dbg = got
+    assert rel.pop("debug").item() == 0 and dbg.pop("debug").item() == 1
+    assert rel["status"].tolist() == [0, 0]
+    for k in rel:
+        assert torch.equal(rel[k], dbg[k]), k
