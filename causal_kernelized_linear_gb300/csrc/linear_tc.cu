@@ -255,8 +255,9 @@ constexpr int kFewThreads = 256;
 template <int BT> struct FewCfg {
   static constexpr int kXB = BT * kBK * 2;
   static constexpr int kStage = kTileB + kXB;
-  static constexpr int kNum = BT <= 32 ? 5 : (BT == 64 ? 4 : 6);   // most stages of the ring
-  static constexpr int kPerSm = BT <= 64 ? 2 : 1;         // CTAs that fit with all of them
+  static constexpr int kNum = BT <= 32 ? 8 : 6;           // stages of a CTA alone on its SM
+  static constexpr int kPerSm = BT <= 32 ? 2 : 1;         // CTAs an SM should have
+  static constexpr int kShared = BT <= 32 ? 3 : 6;        // stages where they share it
   static constexpr int kPart = BT * 128 * 4;              // partial sums, over the stages
   static constexpr int buf(int stages) { return stages * kStage > kPart ? stages * kStage : kPart; }
   static constexpr int smem(int stages) { return 1024 + buf(stages) + 256; }
@@ -455,7 +456,8 @@ cudaError_t launch_few(const LinearArgs& a, const LinParams& p, cudaStream_t s) 
   const int split = few_split(ft * mt, p.kblocks, C::kPerSm * (int64_t)a.num_sms);
   // no more stages than steps: a short K leaves room for more CTAs per SM
   const int steps = (p.kblocks + split - 1) / split;
-  const int stages = steps < C::kNum ? steps : C::kNum;
+  const int most = ft * mt * split <= a.num_sms ? C::kNum : C::kShared;
+  const int stages = steps < most ? steps : most;
   if (ft * split * mt > INT32_MAX) return cudaErrorInvalidConfiguration;
   static std::atomic<uint64_t> smem_set{0};
   e = allow_smem((const void*)few_kernel<BT, ACT>, C::smem(C::kNum), &smem_set);
