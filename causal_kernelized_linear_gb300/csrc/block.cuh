@@ -81,7 +81,10 @@ cudaError_t launch(void (*kernel)(P...), unsigned grid, unsigned block, size_t s
   cfg.attrs = attr;
   cfg.numAttrs = cluster > 1 ? 2 : 1;
   const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
-  if (e == cudaSuccess) count_launches(1);
+  if (e == cudaSuccess)
+    count_launches(1);
+  else
+    cudaGetLastError();   // the caller gets the status; nothing is left behind
   return e;
 }
 

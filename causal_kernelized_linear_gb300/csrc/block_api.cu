@@ -135,6 +135,11 @@ la_status check_scan(const la_rows* x, const la_rows* dt, const float* a, int st
   return LA_OK;
 }
 
+// A grid beyond what a launch takes is a request outside the kernels' range.
+la_status launch_status(cudaError_t e) {
+  return e == cudaErrorInvalidConfiguration ? LA_ERR_UNSUPPORTED : to_status(e);
+}
+
 // An empty prompt: the state after it is the one before it.
 cudaError_t copy_state(void* to, const void* from, size_t bytes, cudaStream_t stream) {
   if (!to || !bytes) return cudaSuccess;
@@ -195,7 +200,7 @@ la_status la_linear(const la_rows* x, const la_rows* weight, const void* bias,
   a.bf16 = x->dtype == LA_BF16;
   a.status = di.status;
   a.num_sms = di.num_sms;
-  return to_status(linear(a, (cudaStream_t)stream));
+  return launch_status(linear(a, (cudaStream_t)stream));
 }
 
 la_status la_causal_conv(const la_rows* x, const void* weight, int width, const void* bias,
@@ -218,7 +223,7 @@ la_status la_causal_conv(const la_rows* x, const void* weight, int width, const 
   st = device_info(&di);
   if (st != LA_OK) return st;
   a.num_sms = di.num_sms;
-  return to_status(causal_conv(a, (cudaStream_t)stream));
+  return launch_status(causal_conv(a, (cudaStream_t)stream));
 }
 
 la_status la_causal_conv_step(void* state, const la_rows* x, const void* weight, int width,
@@ -237,7 +242,7 @@ la_status la_causal_conv_step(void* state, const la_rows* x, const void* weight,
   st = device_info(&di);
   if (st != LA_OK) return st;
   a.num_sms = di.num_sms;
-  return to_status(causal_conv_step(a, (cudaStream_t)stream));
+  return launch_status(causal_conv_step(a, (cudaStream_t)stream));
 }
 
 la_status la_selective_scan(const la_rows* x, const la_rows* dt, const float* a, int states,
@@ -262,7 +267,7 @@ la_status la_selective_scan(const la_rows* x, const la_rows* dt, const float* a,
   st = device_info(&di);
   if (st != LA_OK) return st;
   s.num_sms = di.num_sms;
-  return to_status(selective_scan(s, (cudaStream_t)stream));
+  return launch_status(selective_scan(s, (cudaStream_t)stream));
 }
 
 la_status la_selective_step(float* state, const la_rows* x, const la_rows* dt, const float* a,
@@ -282,7 +287,7 @@ la_status la_selective_step(float* state, const la_rows* x, const la_rows* dt, c
   st = device_info(&di);
   if (st != LA_OK) return st;
   s.num_sms = di.num_sms;
-  return to_status(selective_step(s, (cudaStream_t)stream));
+  return launch_status(selective_step(s, (cudaStream_t)stream));
 }
 
 }  // extern "C"

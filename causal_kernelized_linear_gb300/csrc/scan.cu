@@ -33,7 +33,7 @@ constexpr int kTok = 16;      // tokens per stage of the ring
 constexpr int kRing = 3;      // stages; three are in flight while one is used
 
 template <typename T, int S> struct Cfg {
-  static constexpr int K = S <= 16 ? 4 : 8;        // states per lane and channel
+  static constexpr int K = S == 8 ? 2 : (S <= 32 ? 4 : 8);        // states per lane and channel
   static constexpr int G = S / K;                  // lanes per channel pair, tokens per batch
   static constexpr int kPairs = 32 / G;            // channel pairs per warp
   static constexpr int kCh = 2 * kPairs;           // channels per warp
@@ -76,12 +76,30 @@ __device__ __forceinline__ float2 load2s(const T* p) {
   }
 }
 
-// Four fp32 values in shared memory as two pairs.  A plain load: the loop
-// that uses it writes nothing there, so loads move ahead of the arithmetic.
-__device__ __forceinline__ void lds_pairs(const uint8_t* at, f32x2& a, f32x2& b) {
-  const ulonglong2 v = *reinterpret_cast<const ulonglong2*>(at);
-  a = v.x;
-  b = v.y;
+// K fp32 values (2 or a multiple of 4) as pairs, from shared or global memory.
+template <int K>
+__device__ __forceinline__ void load_pairs(const void* at, f32x2 (&p)[K / 2]) {
+  if constexpr (K == 2) {
+    p[0] = *reinterpret_cast<const f32x2*>(at);
+  } else {
+#pragma unroll
+    for (int q = 0; q < K / 4; ++q) {
+      const ulonglong2 v = reinterpret_cast<const ulonglong2*>(at)[q];
+      p[2 * q] = v.x;
+      p[2 * q + 1] = v.y;
+    }
+  }
+}
+
+template <int K>
+__device__ __forceinline__ void store_pairs(void* at, const f32x2 (&p)[K / 2]) {
+  if constexpr (K == 2) {
+    *reinterpret_cast<f32x2*>(at) = p[0];
+  } else {
+#pragma unroll
+    for (int q = 0; q < K / 4; ++q)
+      reinterpret_cast<ulonglong2*>(at)[q] = make_ulonglong2(p[2 * q], p[2 * q + 1]);
+  }
 }
 
 struct Chunks {
@@ -117,20 +135,18 @@ __global__ void __launch_bounds__(32) scan_kernel(const ScanArgs a, const int cb
   const int live = min(t_hi, len);                          // the tokens of it that count
 
   f32x2 A[2][K / 2], h[2][K / 2];
+  const f32x2 log2e = pack2(kLog2e, kLog2e);
 #pragma unroll
-  for (int j = 0; j < 2; ++j)
+  for (int j = 0; j < 2; ++j) {
+    load_pairs<K>(a.a + (int64_t)(c + j) * S + lg * K, A[j]);
 #pragma unroll
-    for (int q = 0; q < K / 4; ++q) {
-      const float4 v = *reinterpret_cast<const float4*>(a.a + (int64_t)(c + j) * S + lg * K + 4 * q);
-      A[j][2 * q] = pack2(v.x * kLog2e, v.y * kLog2e);
-      A[j][2 * q + 1] = pack2(v.z * kLog2e, v.w * kLog2e);
-      float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (!ENDS || k == 0)
-        if (a.state_in)
-          s = *reinterpret_cast<const float4*>(a.state_in + (b * D + c + j) * S + lg * K + 4 * q);
-      h[j][2 * q] = pack2(s.x, s.y);
-      h[j][2 * q + 1] = pack2(s.z, s.w);
+    for (int q = 0; q < K / 2; ++q) {
+      A[j][q] = mul2(A[j][q], log2e);
+      h[j][q] = 0ull;
     }
+    if ((!ENDS || k == 0) && a.state_in)
+      load_pairs<K>(a.state_in + (b * D + c + j) * S + lg * K, h[j]);
+  }
   float bias[2] = {0.f, 0.f}, skip[2] = {0.f, 0.f};
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
@@ -281,11 +297,8 @@ __global__ void __launch_bounds__(32) scan_kernel(const ScanArgs a, const int cb
       for (int i = 0; i < G; ++i) {
         const int ti = bi * G + i;
         du[i] = *reinterpret_cast<const float4*>(prep + (ti * C::kPairs + pair) * 16);
-#pragma unroll
-        for (int q = 0; q < K / 4; ++q) {
-          lds_pairs(bt + (ti * S + lg * K + 4 * q) * 4, B2[i][2 * q], B2[i][2 * q + 1]);
-          if (!ENDS) lds_pairs(ct + (ti * S + lg * K + 4 * q) * 4, C2[i][2 * q], C2[i][2 * q + 1]);
-        }
+        load_pairs<K>(bt + (ti * S + lg * K) * 4, B2[i]);
+        if (!ENDS) load_pairs<K>(ct + (ti * S + lg * K) * 4, C2[i]);
       }
       const float4 nx = prepare(st, next, t0 + kTok, bi, x1[bi], z1[bi]);
       float y[2][G];
@@ -366,14 +379,7 @@ __global__ void __launch_bounds__(32) scan_kernel(const ScanArgs a, const int cb
                    : (a.state_out && k == ch.count - 1 ? a.state_out + (b * D + c) * S : nullptr);
   if (on && to) {
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
-#pragma unroll
-      for (int q = 0; q < K / 4; ++q) {
-        float4 v;
-        unpack2(h[j][2 * q], v.x, v.y);
-        unpack2(h[j][2 * q + 1], v.z, v.w);
-        *reinterpret_cast<float4*>(to + j * S + lg * K + 4 * q) = v;
-      }
+    for (int j = 0; j < 2; ++j) store_pairs<K>(to + j * S + lg * K, h[j]);
   }
   if constexpr (ENDS) {
 #pragma unroll

@@ -515,7 +515,8 @@ int la_debug_build(void);
  * word.  Site numbers: 11–14 the tcgen05 elu+1 forward (tile rows, output
  * rows, the aggregate slot, the entering-state slots), 21–26 the tcgen05
  * backward (item ranges of the loads, rows of the ∂q, ∂k, ∂v stores), 31–32
- * the non-causal readout, 41–42 the Performer forward, 90 the self-test.
+ * the non-causal readout, 41–42 the Performer forward, 51–52 la_linear's
+ * bf16 stores, 90 the self-test.
  * Errors: LA_ERR_INVALID_ARG (site is NULL), LA_ERR_CUDA.
  */
 la_status la_get_last_device_check(la_stream stream, int* site);
