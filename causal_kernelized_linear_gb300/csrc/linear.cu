@@ -25,15 +25,24 @@ namespace {
 
 using namespace block;
 
+// Four neighbouring columns' bias (zeros without one; adding them changes nothing).
+__device__ __forceinline__ float4 bias4(const LinearArgs& a, int64_t n) {
+  return a.bias ? __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(a.bias) + n))
+                : make_float4(0.f, 0.f, 0.f, 0.f);
+}
+
 // bias, activation and residual on four neighbouring columns, and the store.
 template <int ACT>
-__device__ __forceinline__ void finish4(const LinearArgs& a, int64_t m, int64_t n, float (&v)[4]) {
-  if (a.bias) {
-    const float4 b = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(a.bias) + n));
-    v[0] += b.x, v[1] += b.y, v[2] += b.z, v[3] += b.w;
-  }
+__device__ __forceinline__ void finish4(const LinearArgs& a, int64_t m, int64_t n, const float4& b,
+                                        float (&v)[4]) {
+  v[0] += b.x, v[1] += b.y, v[2] += b.z, v[3] += b.w;
+  if constexpr (ACT == LA_ACT_SOFTPLUS) {
+    const float2 lo = softplus2(make_float2(v[0], v[1])), hi = softplus2(make_float2(v[2], v[3]));
+    v[0] = lo.x, v[1] = lo.y, v[2] = hi.x, v[3] = hi.y;
+  } else {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) v[i] = activate<ACT>(v[i]);
+    for (int i = 0; i < 4; ++i) v[i] = activate<ACT>(v[i]);
+  }
   if (a.residual.data) {
     const float4 r = *reinterpret_cast<const float4*>(static_cast<const float*>(a.residual.data) +
                                                       m * a.residual.sn + n);
@@ -48,8 +57,13 @@ constexpr int kBK = 16, kTileThreads = 128;
 // T×T outputs per thread (8 or 4).
 template <int T> struct Tile {
   static constexpr int kBM = 8 * T, kBN = 16 * T;
-  static constexpr int kXF = kBK * (kBM + 4), kWF = kBK * (kBN + 4);   // floats of a buffer
+  static constexpr int kXF = kBK * kBM, kWF = kBK * kBN;   // floats of a buffer
 };
+
+// Column `col` of row k of a buffer.  The four rows that a warp writes at once
+// (k, k + 4, k + 8, k + 12) go to different banks; four neighbouring columns
+// stay together for the 16-byte reads.
+__device__ __forceinline__ int swizzled(int k, int col) { return col ^ ((k >> 2) << 3); }
 
 template <int T, int GROUPS> constexpr int kTileSmem = GROUPS * 2 * (Tile<T>::kXF + Tile<T>::kWF) * 4;
 
@@ -88,13 +102,13 @@ __global__ void __launch_bounds__(GROUPS * kTileThreads) tile_kernel(const Linea
     for (int i = 0; i < T / 4; ++i) {
       const float v[4] = {xr[i].x, xr[i].y, xr[i].z, xr[i].w};
 #pragma unroll
-      for (int j = 0; j < 4; ++j) xs[(lk + j) * (kBM + 4) + lr + 32 * i] = v[j];
+      for (int j = 0; j < 4; ++j) xs[(lk + j) * kBM + swizzled(lk, lr + 32 * i)] = v[j];
     }
 #pragma unroll
     for (int i = 0; i < T / 2; ++i) {
       const float v[4] = {wr[i].x, wr[i].y, wr[i].z, wr[i].w};
 #pragma unroll
-      for (int j = 0; j < 4; ++j) ws[(lk + j) * (kBN + 4) + lr + 32 * i] = v[j];
+      for (int j = 0; j < 4; ++j) ws[(lk + j) * kBN + swizzled(lk, lr + 32 * i)] = v[j];
     }
   };
   entry();
@@ -119,12 +133,12 @@ __global__ void __launch_bounds__(GROUPS * kTileThreads) tile_kernel(const Linea
       f32x2 wv[P];
 #pragma unroll
       for (int i = 0; i < T / 4; ++i) {
-        const float4 v = *reinterpret_cast<const float4*>(xs + k * (kBM + 4) + 32 * i + ty * 4);
+        const float4 v = *reinterpret_cast<const float4*>(xs + k * kBM + 32 * i + swizzled(k, ty * 4));
         xv[4 * i] = v.x, xv[4 * i + 1] = v.y, xv[4 * i + 2] = v.z, xv[4 * i + 3] = v.w;
       }
 #pragma unroll
       for (int i = 0; i < T / 4; ++i) {
-        const ulonglong2 u = *reinterpret_cast<const ulonglong2*>(ws + k * (kBN + 4) + 64 * i + tx * 4);
+        const ulonglong2 u = *reinterpret_cast<const ulonglong2*>(ws + k * kBN + 64 * i + swizzled(k, tx * 4));
         wv[2 * i] = u.x, wv[2 * i + 1] = u.y;
       }
 #pragma unroll
@@ -158,17 +172,18 @@ __global__ void __launch_bounds__(GROUPS * kTileThreads) tile_kernel(const Linea
       }
   }
 #pragma unroll
-  for (int i = 0; i < T; ++i) {
-    const int64_t m = m0 + (i / 4) * 32 + ty * 4 + i % 4;
-    if (m >= a.M) continue;
+  for (int j = 0; j < T / 4; ++j) {
+    const int64_t n = n0 + j * 64 + tx * 4;   // N is a multiple of 4
+    if (n >= a.N) continue;
+    const float4 b = bias4(a, n);
 #pragma unroll
-    for (int j = 0; j < T / 4; ++j) {
-      const int64_t n = n0 + j * 64 + tx * 4;   // N is a multiple of 4
-      if (n >= a.N) continue;
+    for (int i = 0; i < T; ++i) {
+      const int64_t m = m0 + (i / 4) * 32 + ty * 4 + i % 4;
+      if (m >= a.M) continue;
       float v[4];
       unpack2(acc[i][2 * j], v[0], v[1]);
       unpack2(acc[i][2 * j + 1], v[2], v[3]);
-      finish4<ACT>(a, m, n, v);
+      finish4<ACT>(a, m, n, b, v);
     }
   }
 }
@@ -220,7 +235,7 @@ __global__ void __launch_bounds__(32 * kRowWarps) row_kernel(const LinearArgs a,
   for (int i = 0; i < kRowWarps; ++i)
 #pragma unroll
     for (int j = 0; j < kRowFeatures; ++j) v[j] += sums[i][threadIdx.x][j];
-  finish4<ACT>(a, m, n, v);
+  finish4<ACT>(a, m, n, bias4(a, n), v);
 }
 
 template <int ACT, int R>
