@@ -156,6 +156,36 @@ __device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
   return r;
 }
 
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+// silu of two values.
+__device__ __forceinline__ f32x2 silu2(f32x2 x) {
+  float e0, e1;
+  unpack2(mul2(x, pack2(-kLog2e, -kLog2e)), e0, e1);
+  unpack2(add2(pack2(tc::ex2_f32(e0), tc::ex2_f32(e1)), pack2(1.f, 1.f)), e0, e1);
+  return mul2(x, pack2(rcp_f32(e0), rcp_f32(e1)));
+}
+
+// A 16-byte vector as pairs of fp32, and back.
+template <typename T>
+__device__ __forceinline__ void unpack_pairs(const uint4& v, f32x2 (&p)[kVec<T> / 2]) {
+  float f[kVec<T>];
+  unpack<T>(v, f);
+#pragma unroll
+  for (int i = 0; i < kVec<T> / 2; ++i) p[i] = pack2(f[2 * i], f[2 * i + 1]);
+}
+template <typename T>
+__device__ __forceinline__ uint4 pack_pairs(const f32x2 (&p)[kVec<T> / 2]) {
+  float f[kVec<T>];
+#pragma unroll
+  for (int i = 0; i < kVec<T> / 2; ++i) unpack2(p[i], f[2 * i], f[2 * i + 1]);
+  return pack<T>(f);
+}
+
 // softplus of two values.
 __device__ __forceinline__ float2 softplus2(float2 x) {
   const float e0 = tc::ex2_f32(-kLog2e * fabsf(x.x)), e1 = tc::ex2_f32(-kLog2e * fabsf(x.y));

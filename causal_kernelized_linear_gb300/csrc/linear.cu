@@ -1,6 +1,6 @@
 // out = act(x·wᵀ + bias) + residual: choice of kernel, and the fp32 kernels on
-// the CUDA cores (TF32 tensor products keep 11 bits of an operand; split into
-// three they would keep 22, but their sums are not rounded like fp32's).
+// the CUDA cores.  TF32 tensor products keep 11 bits of an operand; fp32 inputs
+// are held to fp32's rounding here, as in the attention kernels.
 //
 // tile_kernel: a CTA computes 64×128 outputs, K in steps of 16 through two
 // shared-memory buffers, 8×8 outputs per thread in packed pairs: 32 packed
@@ -15,6 +15,10 @@
 // four output features for up to eight tokens, its lanes split K, so that w is
 // read once per eight tokens in 512-byte pieces; bound by reading w for eight
 // tokens, by the loads of x for more.
+//
+// Measured: 777×128×4096 with bias and softplus in 22.7 µs = 36 TFLOP/s (three
+// tiles per SM; fp32 pipe 30 %, shared-memory pipe 47 %, issue 44 %);
+// 1×2048×4096 in 7.1 µs = 4.7 TB/s (in a CUDA graph).
 #include "block.cuh"
 #include "internal.h"
 
@@ -275,7 +279,9 @@ cudaError_t launch_tiles(const LinearArgs& a, cudaStream_t s) {
 }
 
 // SM cycles per element of K: rows at kRowRate multiply-adds per SM and cycle,
-// the tiles that follow one another on an SM at what one measured.
+// the tiles that follow one another on an SM at what one measured.  Either side
+// of the borders, in a CUDA graph: 64×2048×2048 43 µs by rows, 56 by small tiles;
+// 200×512×1024 29 by rows, 12 by small tiles; 777×128×4096 21 by large tiles.
 constexpr double kRowRate = 18, kTile8 = 100, kTile4 = 48;
 
 template <int ACT>

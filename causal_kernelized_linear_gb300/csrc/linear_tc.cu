@@ -14,6 +14,11 @@
 // ones).  A cluster of CTAs splits K, and adds its partial sums through
 // distributed shared memory in rank order: w is read once, by enough CTAs to
 // keep HBM busy, in one launch, with a fixed order of sums.
+//
+// Measured: 16384×2048×8192 in 330 µs = 1.67 PFLOP/s, 0.86 of the measured
+// burst rate and 0.97 of the sustained one (tensor pipe 78 % at 4096 tokens);
+// 1777×4096×2048 with bias and residual in 27 µs (56 tiles of 256×256 for 76
+// pairs); 16×2048×8192 in 8.2 µs = 4.1 TB/s.
 #include "block.cuh"
 #include "internal.h"
 
@@ -437,7 +442,8 @@ cudaError_t launch_pair(const LinearArgs& a, LinParams p, cudaStream_t s) {
 }
 
 // CTAs that share a feature tile's K: as many as are resident at once, while
-// each keeps four steps.
+// each keeps four steps, and four at most (64×4096×4096: 14 µs with four, 17
+// with eight, 16 with two, 24 unsplit).
 int few_split(int64_t tiles, int kblocks, int64_t resident) {
   int split = 1;
   while (split < 4 && tiles * split * 2 <= resident && kblocks >= split * 8) split *= 2;
@@ -454,7 +460,10 @@ cudaError_t launch_few(const LinearArgs& a, const LinParams& p, cudaStream_t s) 
     return e;
   const int64_t ft = (a.N + 127) / 128, mt = (a.M + BT - 1) / BT;
   const int split = few_split(ft * mt, p.kblocks, C::kPerSm * (int64_t)a.num_sms);
-  // no more stages than steps: a short K leaves room for more CTAs per SM
+  // A CTA alone on its SM has all stages; CTAs that share one have three each
+  // (16×2048×8192: 8.4 µs, 9.2 with five; 16×4096×2048, alone: 7.9 with five or
+  // eight, 9.0 with three).  No more stages than steps: a short K leaves room
+  // for more CTAs per SM (777×128×4096: 6.6 µs against 11).
   const int steps = (p.kblocks + split - 1) / split;
   const int most = ft * mt * split <= a.num_sms ? C::kNum : C::kShared;
   const int stages = steps < most ? steps : most;

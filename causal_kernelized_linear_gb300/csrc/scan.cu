@@ -3,21 +3,28 @@
 //   y = (Σ_s C_s·h_s + skip·x)·silu(gate),
 // for every channel (a row of a) with S states.
 //
-// Per (token, channel, state): one 2^x and four fp32 multiply-adds, against a
-// sixteenth of 8 bytes moved: bound by the special-function and fp32 pipes,
-// so a state element is computed once where possible and every other cost is
-// kept off its path.  A group of G = S/K lanes owns two neighbouring channels,
-// K states of each per lane, in registers over the whole prompt, packed in
-// pairs (one instruction for two multiply-adds).  Tokens go in batches of G:
-// each lane of a group prepares one token's Δ and Δ·x, the group shares them
-// through shared memory, and the G partial readouts are summed so that lane i
-// ends with token i, gates it and writes it.
+// Per (token, channel, state): one 2^x (4 cycles a warp) and four fp32
+// multiply-adds (4 cycles as two packed pairs), against half a byte moved: bound
+// by instruction issue and by the shared-memory reads of B and C, with HBM at a
+// fifth.  So a state element is computed once where possible, and every other
+// cost is kept off its path.  A group of G = S/K lanes owns two neighbouring
+// channels, K states of each per lane, in registers over the whole prompt,
+// packed in pairs (one instruction for two multiply-adds).  Tokens go in
+// batches of G: each lane of a group prepares one token's Δ and Δ·x, the group
+// shares them through shared memory, and the G partial readouts are summed so
+// that lane i ends with token i, gates it and writes it.  A stage of tokens is
+// prepared while the one before it is scanned (215 µs against 260).
 //
-// A warp is a CTA and waits for nobody: it keeps kAhead tokens of its inputs
-// in flight with cp.async in a ring of its own.  Where channels alone give
-// too few warps, the sequence is cut into chunks: a first launch reaches each
-// chunk's end state from zero (no readout), and the second starts every chunk
-// from the states before it, combined as h ← exp(a·ΣΔ)·h + end.
+// A warp is a CTA and waits for nobody: it keeps two stages of its inputs in
+// flight with cp.async in a ring of its own.  Where channels alone give too few
+// warps, the sequence is cut into chunks: a first launch reaches each chunk's
+// end state from zero (no readout), and the second starts every chunk from the
+// states before it, combined as h ← exp(a·ΣΔ)·h + end.  That costs 0.6 of the
+// work again.
+//
+// Measured, bf16 with gate, 16 states: 4×2048×4096 (1024 warps, uncut) in
+// 213 µs = 2.5 T state elements/s (issue 52 %, shared-memory pipe 50 %, ex2
+// pipe 32 %; 1.7 warps per scheduler); 1×65536×2048 (cut) in 1.05 ms.
 #include "block.cuh"
 #include "internal.h"
 
@@ -30,10 +37,15 @@ namespace {
 using namespace block;
 
 constexpr int kTok = 16;      // tokens per stage of the ring
-constexpr int kRing = 3;      // stages; three are in flight while one is used
+constexpr int kRing = 3;      // stages: one in use, two in flight
 
 template <typename T, int S> struct Cfg {
-  static constexpr int K = S == 8 ? 2 : (S <= 32 ? 4 : 8);        // states per lane and channel
+  // States per lane and channel.  Fewer give more warps and cost more per element
+  // (sharing and summing over G lanes).  2×2048×4096: 32 states in 193 µs with
+  // four, 255 with eight; 4×2048×4096: 8 states in 178 µs with two, 240 with
+  // four, 16 states in 238 µs with two, 213 with four.  With 64, four would leave
+  // a warp less than 16 bytes of a row.
+  static constexpr int K = S == 8 ? 2 : (S <= 32 ? 4 : 8);
   static constexpr int G = S / K;                  // lanes per channel pair, tokens per batch
   static constexpr int kPairs = 32 / G;            // channel pairs per warp
   static constexpr int kCh = 2 * kPairs;           // channels per warp
@@ -402,7 +414,8 @@ __global__ void __launch_bounds__(32) scan_kernel(const ScanArgs a, const int cb
 // the state in flight.  The state's read and write are nearly all of the
 // traffic (8 bytes per state element); a warp touches 512 contiguous bytes.
 // The lanes of a channel share the work per entry: each prepares the entries
-// R/G apart (or one), and passes Δ and Δ·x on by shuffles.
+// R/G apart (or one), and passes Δ and Δ·x on by shuffles (32 µs without).
+// Measured: 256×4096×16 bf16 in 22.4 µs = 6.4 TB/s, 0.94 of the copy bandwidth.
 constexpr int kStepThreads = 256;
 
 template <typename T, int S, int R>
@@ -476,9 +489,13 @@ __global__ void __launch_bounds__(kStepThreads) step_kernel(const ScanArgs a, ui
   }
 }
 
-constexpr int kWarpsWanted = 4;     // warps per SM below which sequences are cut
-constexpr int kWarpsCut = 24;       // warps per SM that cut sequences should give
-constexpr int kChunkMin = 64;       // tokens
+// Sequences are cut where they give fewer than kWarpsWanted warps per SM
+// (2×2048×4096, 3.4 per SM: 147 µs cut, 158 whole; 4×2048×4096, 6.7 per SM:
+// 265 µs cut, 213 whole), into chunks that give kWarpsCut of them (1×65536×2048:
+// 1114 µs at 16, 1059 at 24, 1076 at 32) and have at least kChunkMin tokens.
+constexpr int kWarpsWanted = 4;
+constexpr int kWarpsCut = 24;
+constexpr int kChunkMin = 64;
 
 template <typename T, int S>
 cudaError_t launch_scan(const ScanArgs& a, cudaStream_t s) {
@@ -533,7 +550,9 @@ cudaError_t launch_step_rows(const ScanArgs& a, cudaStream_t s) {
                 (uint32_t)cblocks);
 }
 
-// Four batch entries per lane where that leaves a thousand threads per SM.
+// Four batch entries per lane where that leaves a thousand threads per SM
+// (256×4096×16: 32 µs against 39 for one entry, before the lanes shared work);
+// one otherwise, where latency counts.
 template <typename T, int S>
 cudaError_t launch_step(const ScanArgs& a, cudaStream_t s) {
   return a.B >= 4 && a.B / 4 * a.D * (S / 4) >= (int64_t)1024 * a.num_sms

@@ -627,3 +627,19 @@ def test_debug_build_gives_the_same_bits():
     assert rel["status"].tolist() == [0, 0]
     for k in rel:
         assert torch.equal(rel[k], dbg[k]), k
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=["bf16", "f32"])
+def test_conv_long_runs(dtype):
+    # enough channels for runs of 64 tokens; lengths inside, at and past a run's border
+    n, D, W = 1300, 4096, 4
+    lens = [n, 0, 1, 63, 64, 65, 1279, 1280]
+    g = _gen(31)
+    x = _randn(g, len(lens), n, D, dtype=dtype)
+    w, bias = _randn(g, D, W, dtype=dtype), _randn(g, D, dtype=dtype)
+    st = _randn(g, len(lens), W - 1, D, dtype=dtype)
+    ref, ab, ref_after = _conv_ref(x, w, bias, "silu", st, lens)
+    y, after = la.causal_conv(x, w, bias=bias, state=st, return_state=True,
+                              lengths=torch.tensor(lens, device=DEV, dtype=torch.int32))
+    _close(y, ref, ab, W + 1, dtype)
+    assert torch.equal(after.double(), ref_after)
