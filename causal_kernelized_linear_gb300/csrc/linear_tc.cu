@@ -21,6 +21,7 @@
 // pairs); 16×2048×8192 in 8.2 µs = 4.1 TB/s.
 #include "block.cuh"
 #include "internal.h"
+#include "tc_pair.cuh"
 
 #include <atomic>
 
