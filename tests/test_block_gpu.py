@@ -643,3 +643,65 @@ def test_conv_long_runs(dtype):
                               lengths=torch.tensor(lens, device=DEV, dtype=torch.int32))
     _close(y, ref, ab, W + 1, dtype)
     assert torch.equal(after.double(), ref_after)
+
+
+@pytest.mark.parametrize("n", [50, 700])
+def test_scan_rates_of_minus_infinity_and_lengths(n):
+    # exp(Δ·(−inf)) = 0: such a state holds the newest token only; tokens past
+    # the length still leave it alone
+    lens = [n, 0, 1, n - 7]
+    i = _scan_inputs(_gen(41), len(lens), n, 24, 16, torch.float32, state=True)
+    i["a"][:, 3] = float("-inf")
+    y, ys, h, hs = _scan_ref(i, lens)
+    got, after = la.selective_scan(**i, return_state=True,
+                                   lengths=torch.tensor(lens, device=DEV, dtype=torch.int32))
+    _close(got, y, 4 * ys, n + 16, torch.float32, "y")
+    _close(after, h, 4 * hs, n + 16, torch.float32, "state")
+
+
+def test_refusals_queue_nothing():
+    g = _gen(51)
+    bf = torch.bfloat16
+    x, w = _randn(g, 4, 64, dtype=bf), _randn(g, 32, 64, dtype=bf)
+    seq = _randn(g, 2, 10, 64, dtype=bf)
+    cw = _randn(g, 64, 4, dtype=bf)
+    i = _scan_inputs(g, 2, 10, 64, 16, bf)
+    la.linear(x, w)
+    before = la.launch_count()
+    refused = [
+        lambda: la.linear(x, w[:, :56]),                                  # K differs
+        lambda: la.linear(_randn(g, 4, 72, dtype=bf)[:, 1:65], w),        # not 16-byte aligned
+        lambda: la.linear(_randn(g, 4, 68, dtype=bf)[:, :64], w),         # row stride off 16 bytes
+        lambda: la.linear(x[:, :60], w[:, :60]),                          # K off 16 bytes
+        lambda: la.linear(x[:1].expand(4, 64), w),                        # rows coincide
+        lambda: la.causal_conv(seq, _randn(g, 64, 5, dtype=bf)),          # five taps
+        lambda: la.causal_conv(seq, cw, activation="gelu"),
+        lambda: la.selective_scan(**dict(i, b=i["b"][..., :8], c=i["c"][..., :8])),
+        lambda: la.selective_scan(**dict(i, out=i["x"][:, :1].expand(2, 10, 64))),
+    ]
+    for f in refused:
+        with pytest.raises(la.LinAttnError):
+            f()
+    wrong = [
+        lambda: la.linear(x, w.float()),
+        lambda: la.linear(x.t(), w),
+        lambda: la.linear(x, w, bias=_randn(g, 31, dtype=bf)),
+        lambda: la.linear(x, w, residual=_randn(g, 4, 24, dtype=bf)),
+        lambda: la.linear(x, w, out=torch.empty(4, 24, device=DEV, dtype=bf)),
+        lambda: la.linear(x, w, activation="swish"),
+        lambda: la.linear(x, w.cpu()),
+        lambda: la.causal_conv(seq, cw, lengths=torch.zeros(2, device=DEV, dtype=torch.int64)),
+        lambda: la.causal_conv(seq, cw, lengths=torch.zeros(3, device=DEV, dtype=torch.int32)),
+        lambda: la.causal_conv(seq, cw, state=torch.zeros(2, 4, 64, device=DEV, dtype=bf)),
+        lambda: la.causal_conv(seq[0], cw),
+        lambda: la.selective_scan(**dict(i, a=i["a"].t())),
+        lambda: la.selective_scan(**dict(i, a=i["a"].to(bf))),
+        lambda: la.selective_scan(**dict(i, state=torch.zeros(2, 64, 8, device=DEV))),
+        lambda: la.selective_scan(**dict(i, gate=i["gate"].float())),
+    ]
+    for f in wrong:
+        with pytest.raises(ValueError):
+            f()
+    with pytest.raises(TypeError):
+        la.selective_step(None, *[i[k][:, 0] for k in ("x", "dt")], i["a"], i["b"][:, 0], i["c"][:, 0])
+    assert la.launch_count() == before and la.last_device_status() == 0
