@@ -503,7 +503,12 @@ __global__ void __launch_bounds__(kStepThreads) step_kernel(const ScanArgs a, ui
 // Sequences are cut where they give fewer than kWarpsWanted warps per SM
 // (2×2048×4096, 3.4 per SM: 147 µs cut, 158 whole; 4×2048×4096, 6.7 per SM:
 // 265 µs cut, 213 whole), into chunks that give kWarpsCut of them (1×65536×2048:
-// 1114 µs at 16, 1059 at 24, 1076 at 32) and have at least kChunkMin tokens.
+// 1114 µs at 16, 1059 at 24, 1076 at 32) and have at least kChunkMin tokens
+// (1×300×2048: 17 µs at 64, 20 at 96; 4×500×1024: 26 at 64, 32 at 32).  Short
+// ones are not worth a second launch: with less than two warps per SM
+// 1×130×2048 takes 16 µs cut, 14 whole, and 1×200×2048 16 and 19; with more,
+// 7×333×520 (fp32, 32 states) takes 32 cut and 26 whole.
+constexpr int kCutMin = 160, kCutMinFull = 1024;   // tokens: below and from two warps per SM
 constexpr int kWarpsWanted = 4;
 constexpr int kWarpsCut = 24;
 constexpr int kChunkMin = 64;
@@ -516,7 +521,7 @@ cudaError_t launch_scan(const ScanArgs& a, cudaStream_t s) {
   if (warps > INT32_MAX) return cudaErrorInvalidConfiguration;
   Chunks ch{1, (int)a.n, nullptr, nullptr};
   const int64_t wanted = (int64_t)kWarpsWanted * a.num_sms;
-  if (warps < wanted && a.n >= 2 * kChunkMin) {
+  if (warps < wanted && a.n >= (warps < 2 * a.num_sms ? kCutMin : kCutMinFull)) {
     int64_t count = (kWarpsCut * (int64_t)a.num_sms + warps - 1) / warps;
     count = count < a.n / kChunkMin ? count : a.n / kChunkMin;
     int64_t len = (a.n + count - 1) / count;
