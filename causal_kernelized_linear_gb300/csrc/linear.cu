@@ -278,18 +278,21 @@ cudaError_t launch_tiles(const LinearArgs& a, cudaStream_t s) {
   return launch_groups<ACT, T, 1>(a, mt, nt, s);
 }
 
-// SM cycles per element of K: rows at kRowRate multiply-adds per SM and cycle,
-// the tiles that follow one another on an SM at what one measured.  Either side
-// of the borders, in a CUDA graph: 64×2048×2048 43 µs by rows, 56 by small tiles;
-// 200×512×1024 29 by rows, 12 by small tiles; 777×128×4096 21 by large tiles.
+// SM cycles: rows at kRowRate multiply-adds per SM and cycle, for at least the
+// kRowK elements of K that a CTA's lanes take at once; tiles at what one
+// measured per element of K, times those that follow one another on an SM.
+// Either side of the borders, in a CUDA graph: 64×2048×2048 43 µs by rows, 56 by
+// small tiles; 200×512×1024 29 by rows, 12 by small tiles; 777×128×4096 21 by
+// large tiles; 24×80×4096 4 by small tiles, 13 by rows.
 constexpr double kRowRate = 18, kTile8 = 100, kTile4 = 48;
+constexpr int64_t kRowK = 128 * kRowWarps;
 
 template <int ACT>
 cudaError_t launch_f32(const LinearArgs& a, cudaStream_t s) {
   if (a.M <= 2) return launch_rows<ACT, 2>(a, s);
-  const double rows = (double)a.M * a.N / a.num_sms / kRowRate;
-  const double large = tile_rounds<8>(a) * kTile8, small = tile_rounds<4>(a) * kTile4;
-  if (a.M <= 8 || (rows < large && rows < small)) return launch_rows<ACT, 8>(a, s);
+  const double rows = (double)a.M * a.N / a.num_sms / kRowRate * (a.K > kRowK ? a.K : kRowK);
+  const double large = tile_rounds<8>(a) * kTile8 * a.K, small = tile_rounds<4>(a) * kTile4 * a.K;
+  if ((a.M <= 8 && a.K >= kRowK) || (rows < large && rows < small)) return launch_rows<ACT, 8>(a, s);
   return small < large ? launch_tiles<ACT, 4>(a, s) : launch_tiles<ACT, 8>(a, s);
 }
 
