@@ -23,6 +23,7 @@
 #include "internal.h"
 #include "tc_pair.cuh"
 
+#include <algorithm>
 #include <atomic>
 
 namespace la {
@@ -476,8 +477,27 @@ cudaError_t launch_few(const LinearArgs& a, const LinParams& p, cudaStream_t s) 
                 C::smem(stages), s, (unsigned)split, mx, mw, p, split, (int)ft, stages);
 }
 
-constexpr double kFewStep = 520, kPair256Step = 540, kPair128Step = 460;
-constexpr double kFewFixed = 5000, kPairFixed = 7000;
+// Estimated time of few_kernel<BT>, in SM cycles: a CTA's launch, setup and
+// drain, which grow with the tokens whose partial sums it writes and reads; the
+// steps of K of the CTAs that an SM has, at 64 bytes a cycle into the SM; and
+// the exchange between CTAs that split K.  In a CUDA graph, µs with BT = 32 / 64
+// / 128: 200×64×2048 2.9 / 3.5 / 4.7; 1509×496×296 6.6 / 5.6 / 6.7; 250×1024×2048
+// 8.1 / 6.8 / 8.6; 128×2048×8192 15.7 / 12.1 / 11.9.
+template <int BT> double few_cycles(const LinearArgs& a, int kblocks) {
+  const int64_t tiles = ((a.N + 127) / 128) * ((a.M + BT - 1) / BT);
+  const int split = few_split(tiles, kblocks, FewCfg<BT>::kPerSm * (int64_t)a.num_sms);
+  const double per_sm = (double)((tiles * split + a.num_sms - 1) / a.num_sms);
+  const double fixed = 4300 + 36.5 * BT;
+  return fixed * (0.6 + 0.4 * per_sm) + per_sm * kblocks / split * (FewCfg<BT>::kStage / 64.0) +
+         (split > 1 ? 1000.0 * split : 0.0);
+}
+
+// The same for pair_kernel: the tiles that follow one another on a pair, by
+// what a step of K measured where every SM has a tile.
+template <int BN> double pair_cycles(const LinearArgs& a, int kblocks) {
+  const int64_t tiles = ((a.M + 255) / 256) * ((a.N + BN - 1) / BN), pairs = a.num_sms / 2;
+  return 11000 + (double)((tiles + pairs - 1) / pairs) * kblocks * (BN == 256 ? 540 : 460);
+}
 
 template <int ACT>
 cudaError_t by_shape(const LinearArgs& a, cudaStream_t s) {
@@ -492,23 +512,18 @@ cudaError_t by_shape(const LinearArgs& a, cudaStream_t s) {
   p.kblocks = (int)((a.K + kBK - 1) / kBK);
   p.status = a.status;
   if (a.M <= 16) return launch_few<16, ACT>(a, p, s);
-  if (a.M <= 32) return launch_few<32, ACT>(a, p, s);
-  if (a.M <= 64) return launch_few<64, ACT>(a, p, s);
-  if (a.M <= 128) return launch_few<128, ACT>(a, p, s);
-  // The cheapest of the three, in SM cycles: the tiles that follow one another
-  // on an SM, times a tile's steps of K, times a step (each bound by about 64
-  // bytes a cycle into the SM: 32 KB for few and for 256 columns, 24 KB for
-  // 128 columns; measured on shapes that give every SM a tile).
-  const int64_t ft = (a.N + 127) / 128, mt = (a.M + 127) / 128;
-  const int split = few_split(ft * mt, p.kblocks, a.num_sms);
-  auto waves = [](int64_t tiles, int64_t slots) { return (double)((tiles + slots - 1) / slots); };
-  const int64_t pt = (a.M + 255) / 256, pairs = a.num_sms / 2;
-  const double few = kFewFixed + waves(ft * mt * split, a.num_sms) * p.kblocks / split * kFewStep;
-  const double p256 = kPairFixed + waves(pt * ((a.N + 255) / 256), pairs) * p.kblocks * kPair256Step;
-  const double p128 = kPairFixed + waves(pt * ((a.N + 127) / 128), pairs) * p.kblocks * kPair128Step;
-  if (few <= p256 && few <= p128) return launch_few<128, ACT>(a, p, s);
-  if (p256 <= p128) return launch_pair<256, ACT>(a, p, s);
-  return launch_pair<128, ACT>(a, p, s);
+  // tiles of at most twice the tokens there are
+  const double none = 1e300;
+  const double f32 = few_cycles<32>(a, p.kblocks);
+  const double f64 = a.M > 32 ? few_cycles<64>(a, p.kblocks) : none;
+  const double f128 = a.M > 64 ? few_cycles<128>(a, p.kblocks) : none;
+  const double p128 = a.M > 128 ? pair_cycles<128>(a, p.kblocks) : none;
+  const double p256 = a.M > 128 ? pair_cycles<256>(a, p.kblocks) : none;
+  const double least = std::min({f32, f64, f128, p128, p256});
+  if (f128 == least) return launch_few<128, ACT>(a, p, s);
+  if (f64 == least) return launch_few<64, ACT>(a, p, s);
+  if (f32 == least) return launch_few<32, ACT>(a, p, s);
+  return p256 == least ? launch_pair<256, ACT>(a, p, s) : launch_pair<128, ACT>(a, p, s);
 }
 
 }  // namespace
