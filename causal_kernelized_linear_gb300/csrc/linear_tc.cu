@@ -263,7 +263,9 @@ template <int BT> struct FewCfg {
   static constexpr int kXB = BT * kBK * 2;
   static constexpr int kStage = kTileB + kXB;
   static constexpr int kNum = BT <= 32 ? 8 : 6;           // stages of a CTA alone on its SM
-  static constexpr int kPerSm = BT <= 32 ? 2 : 1;         // CTAs an SM should have
+  // CTAs an SM should have (32×2048×8192: 10 µs with one, 12 with two;
+  // 1×2048×8192: 9.0 with one, 8.6 with two)
+  static constexpr int kPerSm = BT <= 16 ? 2 : 1;
   static constexpr int kShared = BT <= 32 ? 3 : 6;        // stages where they share it
   static constexpr int kPart = BT * 128 * 4;              // partial sums, over the stages
   static constexpr int buf(int stages) { return stages * kStage > kPart ? stages * kStage : kPart; }
