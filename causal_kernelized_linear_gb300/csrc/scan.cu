@@ -141,9 +141,7 @@ __global__ void __launch_bounds__(32) scan_kernel(const ScanArgs a, const int cb
   const int k = (blockIdx.x / cblocks) % (ENDS ? ch.count - 1 : ch.count);
   const int64_t b = blockIdx.x / cblocks / (ENDS ? ch.count - 1 : ch.count);
   const int lane = threadIdx.x, lg = lane / C::kPairs, pair = lane % C::kPairs;
-  // No early trigger for the next kernel: its CTAs would fill the SMs that have
-  // room first and stay there, unevenly (4×2048×4096: 357 µs against 213).
-  tc::grid_dependency_wait();
+  tc::grid_dependency_wait();   // the second launch of a cut sequence starts early
   const int D = (int)a.D, n = (int)a.n;
   const int c0 = cb * C::kCh, cw = c0 + 2 * pair;
   const bool on = cw < D;         // D is even: both channels or none
@@ -544,12 +542,16 @@ cudaError_t launch_scan(const ScanArgs& a, cudaStream_t s) {
     }
     ch.end = ws;
     ch.step = ws + rows * S;
-    e = launch(scan_kernel<T, S, true>, (unsigned)(warps * (ch.count - 1)), 32, C::kSmem, s, 1, a,
-               (int)cblocks, ch);
+    e = launch_in_turn(scan_kernel<T, S, true>, (unsigned)(warps * (ch.count - 1)), 32, C::kSmem, s,
+                       a, (int)cblocks, ch);
   }
+  // The CTAs of a whole scan are resident at once, so it starts in turn: after a
+  // convolution or a product, whose tails free the SMs unevenly, 4×2048×4096 takes
+  // 210 µs, started early 352; 4×500×2048 43 and 90.  The second launch of a cut
+  // one follows the first, which does not let it start before its own end.
   if (e == cudaSuccess)
-    e = launch(scan_kernel<T, S, false>, (unsigned)(warps * ch.count), 32, C::kSmem, s, 1, a,
-               (int)cblocks, ch);
+    e = launch_as(ch.count > 1, scan_kernel<T, S, false>, (unsigned)(warps * ch.count), 32, C::kSmem,
+                  s, 1, a, (int)cblocks, ch);
   if (ws) {
     const cudaError_t f = cudaFreeAsync(ws, s);
     if (e == cudaSuccess) e = f;
