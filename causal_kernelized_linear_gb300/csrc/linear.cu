@@ -250,21 +250,24 @@ cudaError_t launch_rows(const LinearArgs& a, cudaStream_t s) {
   return launch(row_kernel<ACT, R>, (unsigned)blocks, 32 * kRowWarps, 0, s, 1, a, (int)fb);
 }
 
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// Tiles of T that follow one another on an SM.
+template <int T> int64_t tile_rounds(const LinearArgs& a) {
+  return ceil_div(ceil_div(a.M, Tile<T>::kBM) * ceil_div(a.N, Tile<T>::kBN), a.num_sms);
+}
+
+// A grid of one tile per SM or fewer starts in turn: in the tail of a convolution
+// or a product two tiles would share an SM (256×1024×1024: 40 µs, 23 in turn;
+// 200×512×1024: 21 and 12; with more tiles, 1000×1024×1024, no difference).
 template <int ACT, int T, int GROUPS>
 cudaError_t launch_groups(const LinearArgs& a, int64_t mt, int64_t nt, cudaStream_t s) {
   constexpr int smem = kTileSmem<T, GROUPS>;
   static std::atomic<uint64_t> smem_set{0};
   const cudaError_t e = allow_smem((const void*)tile_kernel<ACT, T, GROUPS>, smem, &smem_set);
   if (e != cudaSuccess) return e;
-  return launch(tile_kernel<ACT, T, GROUPS>, (unsigned)(mt * nt), GROUPS * kTileThreads, smem, s, 1,
-                a, (int)mt);
-}
-
-int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
-
-// Tiles of T that follow one another on an SM.
-template <int T> int64_t tile_rounds(const LinearArgs& a) {
-  return ceil_div(ceil_div(a.M, Tile<T>::kBM) * ceil_div(a.N, Tile<T>::kBN), a.num_sms);
+  return launch_as(tile_rounds<T>(a) > 1, tile_kernel<ACT, T, GROUPS>, (unsigned)(mt * nt),
+                   GROUPS * kTileThreads, smem, s, 1, a, (int)mt);
 }
 
 template <int ACT, int T>

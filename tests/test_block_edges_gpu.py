@@ -62,3 +62,15 @@ def test_scan_does_not_start_in_its_predecessors_tail():
     assert _edges(conv_linear) == (1, 1)         # the others still overlap
     assert _edges(conv_scan) == (1, 0)
     assert _edges(linear_scan) == (1, 0)
+
+
+def test_single_round_of_fp32_tiles_does_not_start_in_its_predecessors_tail():
+    g = _gen(2)
+    f32 = torch.float32
+    x = _randn(g, 400, 1024, dtype=f32)
+    w = _randn(g, 512, 1024, dtype=f32, scale=1 / 32)
+    cw = _randn(g, 1024, 4, dtype=f32)
+
+    def conv_linear():
+        la.linear(la.causal_conv(x[None], cw), w)
+    assert _edges(conv_linear) == (1, 0)
