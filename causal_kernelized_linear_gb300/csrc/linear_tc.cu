@@ -80,10 +80,13 @@ template <int BN> struct PairCfg {
   static constexpr int kStage = kTileB + kW;
   static constexpr int kNum = BN == 256 ? 6 : 8;
   static constexpr int kSmem = 1024 + kNum * kStage + kEpiWarps * kEpiB + 256;
+  // Alone on its SM beside anything that uses tensor memory (few_kernel takes the
+  // least, 18 KB), so it may hold its columns while it waits for its predecessor.
+  static_assert(kSmem + 18 * 1024 > 228 * 1024, "tensor memory is not shared");
 };
 
 struct PairBars {
-  uint64_t full[8], empty[8], acc_full[2], acc_empty[2];
+  uint64_t full[8], empty[8], acc_full[2], acc_empty[2], done;
   uint32_t tmem;
   int abort;
 };
@@ -123,6 +126,7 @@ pair_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUte
       mbar_init(&bars->acc_full[i], 1);
       mbar_init(&bars->acc_empty[i], 2 * kEpiWarps);   // of both CTAs
     }
+    mbar_init(&bars->done, 1);
     bars->abort = 0;
     fence_barrier_init();
     tma_prefetch_desc(&mx);
@@ -141,6 +145,7 @@ pair_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUte
   const uint32_t tmem = bars->tmem;
   volatile int* abort = &bars->abort;
 
+  uint32_t issued = 0;     // steps that this CTA's producer has loaded
   if (warp == 0 && lane == 0) {
     // producer: this CTA's rows of x and w; completion is counted by the even rank
     uint32_t it = 0;
@@ -159,10 +164,7 @@ pair_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUte
         tma_load_2d_pair(base + s * kStageB + kTileB, &mw, bar, kb * kBK, n0);
       }
     }
-    // an abort leaves loads in flight: let them land before the CTA ends
-    if (*abort && rank == 0)
-      for (uint32_t j = it > kStages ? it - kStages : 0; j < it; ++j)
-        mbar_wait_drain(&bars->full[j % kStages], (j / kStages) & 1);
+    issued = it;
   } else if (warp == 1 && lane == 0 && rank == 0) {
     // MMA issuer, for both CTAs
     constexpr uint32_t idesc = idesc_bf16_f32(256, BN, false, false);
@@ -189,11 +191,6 @@ pair_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUte
       }
       if (!ok) break;
       mma_commit_pair(&bars->acc_full[buf]);
-    }
-    if (*abort) {
-      // what was issued ends on its own; the commit tells when
-      mma_commit_pair(&bars->acc_full[0]);
-      mbar_wait_drain(&bars->acc_full[0], 0);
     }
   } else if (warp >= 4) {
     // epilogue: a warp has the rows of its TMEM quarter and half of the
@@ -250,6 +247,14 @@ pair_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUte
   tc_fence_before();
   __syncwarp();
   __syncthreads();
+  // after an abort, products and loads in flight end before either CTA does
+  if (threadIdx.x == 32 && rank == 0 && *abort) {
+    mma_commit_pair(&bars->done, 1);
+    mbar_wait_drain(&bars->done, 0);
+  }
+  if (threadIdx.x == 0 && rank == 0 && *abort)
+    for (uint32_t j = issued > kStages ? issued - kStages : 0; j < issued; ++j)
+      mbar_wait_drain(&bars->full[j % kStages], (j / kStages) & 1);
   cluster_sync();          // no CTA leaves while its pair may still signal or read it
   tc_fence_after();
   if (warp == 2) tmem_dealloc_pair(tmem, 2 * BN);
@@ -306,6 +311,20 @@ few_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUten
     tma_prefetch_desc(&mx);
     tma_prefetch_desc(&mw);
   }
+  // Tensor memory is taken after the wait for the predecessor and given back
+  // before the wait for the cluster: a CTA that holds some waits for nothing but
+  // its own loads and products.  A kernel that needs all 512 columns of an SM may
+  // be this one's predecessor or run beside it, so held across either wait they
+  // could make both wait for each other.
+  entry();
+  const int steps = k1 - k0;
+  auto load = [&](int it, int s) {
+    mbar_arrive_expect_tx(&bars->full[s], C::kStage);
+    tma_load_2d(base + s * C::kStage, &mw, &bars->full[s], (k0 + it) * kBK, n0);
+    tma_load_2d(base + s * C::kStage + kTileB, &mx, &bars->full[s], (k0 + it) * kBK, m0);
+  };
+  if (threadIdx.x == 0)
+    for (int it = 0; it < steps && it < stages; ++it) load(it, it);   // the ring's first lap
   if (warp == 2) {
     tmem_alloc(&bars->tmem, C::kCols);
     tmem_relinquish();
@@ -313,25 +332,19 @@ few_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUten
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  entry();
   const uint32_t tmem = bars->tmem;
   volatile int* abort = &bars->abort;
 
-  const int steps = k1 - k0;
+  int issued = 0;          // loads of this CTA (its producer)
   if (warp == 0 && lane == 0) {
-    int s = 0, it = 0;
-    uint32_t lap = 0;      // times the ring has been filled
+    int s = 0, it = stages;
+    uint32_t lap = 1;      // times the ring has been filled
     for (; it < steps; ++it) {
-      if (it >= stages && !mbar_wait(&bars->empty[s], (lap & 1) ^ 1, p.status, abort)) break;
-      const int kb = k0 + it;
-      mbar_arrive_expect_tx(&bars->full[s], C::kStage);
-      tma_load_2d(base + s * C::kStage, &mw, &bars->full[s], kb * kBK, n0);
-      tma_load_2d(base + s * C::kStage + kTileB, &mx, &bars->full[s], kb * kBK, m0);
+      if (!mbar_wait(&bars->empty[s], (lap & 1) ^ 1, p.status, abort)) break;
+      load(it, s);
       if (++s == stages) s = 0, ++lap;
     }
-    if (*abort)
-      for (int j = it > stages ? it - stages : 0; j < it; ++j)
-        mbar_wait_drain(&bars->full[j % stages], (j / stages) & 1);
+    issued = it < steps ? it : steps;
   } else if (warp == 1 && lane == 0) {
     constexpr uint32_t idesc = idesc_bf16_f32(128, BT, false, false);
     int s = 0;
@@ -368,6 +381,18 @@ few_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUten
   }
   tc_fence_before();
   __syncthreads();
+  if (*abort) {
+    // loads and products in flight end before the CTA does
+    if (threadIdx.x == 0)
+      for (int j = issued > stages ? issued - stages : 0; j < issued; ++j)
+        mbar_wait_drain(&bars->full[j % stages], (j / stages) & 1);
+    if (threadIdx.x == 32) mbar_wait_drain(&bars->done, 0);
+    __syncthreads();
+  }
+  if (warp == 2) {
+    tc_fence_after();
+    tmem_dealloc(tmem, C::kCols);
+  }
   if (split > 1) cluster_sync();
   // rank r finishes its share of the tokens: 16 lanes of 8 features per token
   const int per = (BT + split - 1) / split;
@@ -401,7 +426,6 @@ few_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUten
     }
   }
   if (split > 1) cluster_sync();   // no CTA leaves while another reads its partial sums
-  if (warp == 2) tmem_dealloc(tmem, C::kCols);
 }
 
 // ------------------------------------------------------------------ launch

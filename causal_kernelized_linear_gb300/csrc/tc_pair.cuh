@@ -87,13 +87,14 @@ __device__ __forceinline__ void mma_ss_pair(uint32_t d_tmem, uint64_t adesc, uin
       "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
-// Arrives on the barrier at this offset in both CTAs of the pair (ranks 0, 1)
-// once every previously issued pair MMA of this thread has completed.
-__device__ __forceinline__ void mma_commit_pair(uint64_t* bar) {
+// Arrives on the barrier at this offset in both CTAs of the pair (ranks 0, 1; or
+// in those of the mask) once every previously issued pair MMA of this thread has
+// completed.
+__device__ __forceinline__ void mma_commit_pair(uint64_t* bar, uint16_t ranks = 3) {
   asm volatile(
       "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
       " [%0], %1;" ::"r"(smem_u32(bar)),
-      "h"((uint16_t)3)
+      "h"(ranks)
       : "memory");
 }
 

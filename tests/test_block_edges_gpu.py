@@ -74,3 +74,49 @@ def test_single_round_of_fp32_tiles_does_not_start_in_its_predecessors_tail():
     def conv_linear():
         la.linear(la.causal_conv(x[None], cw), w)
     assert _edges(conv_linear) == (1, 0)
+
+
+def test_products_between_the_attention_kernels():
+    """The attention's tensor-core kernels, which take a whole SM's tensor memory
+    and start their own followers early, before, after and beside the products,
+    on one stream and on two: the same bits as one call at a time."""
+    g = _gen(3)
+    B, H, n, d = 1, 8, 1024, 64
+    x = _randn(g, B * H * n, 64)
+    w = [_randn(g, 64, 64, scale=0.125) for _ in range(3)]
+    few = _randn(g, 40, 512)
+    wf = _randn(g, 512, 512, scale=512 ** -0.5)
+    decay = torch.full((H,), 0.98, device=DEV)
+
+    def attend():
+        q, k, v = (la.linear(x, m).view(B, H, n, d) for m in w)
+        la.forward_state(k, v, decay)
+        y = la.linear(few, wf, activation="silu")
+        o = la.forward(q, k, v, decay)
+        la.forward_state(q, o, decay)
+        z = la.linear(y, wf, residual=few)
+        return la.linear(o.view(-1, d), w[0], residual=x), z
+
+    want = []
+    q, k, v = (la.linear(x, m).view(B, H, n, d) for m in w)
+    torch.cuda.synchronize()
+    o = la.forward(q, k, v, decay)
+    torch.cuda.synchronize()
+    y = la.linear(few, wf, activation="silu")
+    torch.cuda.synchronize()
+    want = la.linear(o.view(-1, d), w[0], residual=x), la.linear(y, wf, residual=few)
+    torch.cuda.synchronize()
+    for _ in range(3):
+        got = attend()
+    assert all(torch.equal(p, q) for p, q in zip(got, want))
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = [None, None]
+    for _ in range(3):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i] = attend()
+    torch.cuda.synchronize()
+    for pair in got:
+        assert all(torch.equal(p, q) for p, q in zip(pair, want))
+    assert la.last_device_status() == 0
