@@ -38,6 +38,13 @@ using namespace block;
 
 constexpr float kLargest = 3.0e38f;
 
+// a·log2 e, the decay's exponent per Δ.  Kept finite below: a step of zero, a
+// masked token's among them, leaves the state alone, and 0·(−inf) is not 0.
+__device__ __forceinline__ float rate(float a) {
+  const float r = a * kLog2e;
+  return r < -kLargest ? -kLargest : r;   // keeps NaN
+}
+
 // Added to every decay's exponent.  The hardware's 2^x is low by 2e-8 on average
 // for x in [−0.1, −0.003], a third of an ulp, which a state with a memory of
 // hundreds of tokens adds up (2e-6 after 130 tokens).  With this its mean error
@@ -152,16 +159,15 @@ __global__ void __launch_bounds__(32) scan_kernel(const ScanArgs a, const int cb
   const int live = min(t_hi, len);                          // the tokens of it that count
 
   f32x2 A[2][K / 2], h[2][K / 2];
-  const f32x2 log2e = pack2(kLog2e, kLog2e), centre = pack2(kCentre, kCentre);
+  const f32x2 centre = pack2(kCentre, kCentre);
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
     load_pairs<K>(a.a + (int64_t)(c + j) * S + lg * K, A[j]);
 #pragma unroll
     for (int q = 0; q < K / 2; ++q) {
-      // kept finite: masked tokens pass with Δ = 0, and 0·(−inf) is not 0
       float a0, a1;
-      unpack2(mul2(A[j][q], log2e), a0, a1);
-      A[j][q] = pack2(a0 < -kLargest ? -kLargest : a0, a1 < -kLargest ? -kLargest : a1);
+      unpack2(A[j][q], a0, a1);
+      A[j][q] = pack2(rate(a0), rate(a1));
       h[j][q] = 0ull;
     }
     if ((!ENDS || k == 0) && a.state_in)
@@ -464,7 +470,7 @@ __global__ void __launch_bounds__(kStepThreads) step_kernel(const ScanArgs a, ui
     }
   }
   float4 A = *reinterpret_cast<const float4*>(a.a + (int64_t)c * S + 4 * q);
-  A.x *= kLog2e, A.y *= kLog2e, A.z *= kLog2e, A.w *= kLog2e;
+  A.x = rate(A.x), A.y = rate(A.y), A.z = rate(A.z), A.w = rate(A.w);
   const float bias = a.dt_bias ? a.dt_bias[c] : 0.f, skip = a.skip ? a.skip[c] : 0.f;
 #pragma unroll
   for (int p = 0; p < P; ++p) {

@@ -120,3 +120,30 @@ def test_products_between_the_attention_kernels():
     for pair in got:
         assert all(torch.equal(p, q) for p, q in zip(pair, want))
     assert la.last_device_status() == 0
+
+
+# ------------------------------------------------------------------ rates of minus infinity
+
+@pytest.mark.parametrize("dtype", [BF, torch.float32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("B,D,S", [(2, 72, 16), (300, 2048, 8)])
+def test_step_with_rates_of_minus_infinity(dtype, B, D, S):
+    """exp(Δ·(−inf)) is 0 for Δ > 0, and a step of zero leaves the state alone, as
+    in the scan: the next token's step after the prompt's gives the same state."""
+    g = _gen(4)
+    a = -torch.rand(D, S, device=DEV, generator=g)
+    a[:, 3] = -math.inf
+    state = torch.randn(B, D, S, device=DEV, generator=g)
+    x, b, c = _randn(g, B, D, dtype=dtype), _randn(g, B, S, dtype=dtype), _randn(g, B, S, dtype=dtype)
+    dt = _randn(g, B, D, dtype=dtype).abs()
+    dt[:, ::3] = 0.0
+    st = state.clone()
+    y = la.selective_step(st, x, dt, a, b, c, softplus=False)
+    want = torch.where(dt.double()[..., None] > 0, torch.exp(dt.double()[..., None] * a), 1.0) * state \
+        + (dt.double() * x)[..., None] * b[:, None]
+    assert torch.isfinite(st).all() and torch.isfinite(y).all()
+    assert torch.equal(st[:, ::3], state[:, ::3])
+    # the decay's 2^x and argument: a few ulp of 2^-24 of the largest term, far below 1e-5
+    assert ((st - want).abs() <= 1e-5 * (want.abs() + state.abs() + 1)).all()
+    scan, end = la.selective_scan(x[:, None], dt[:, None], a, b[:, None], c[:, None], softplus=False,
+                                  state=state, return_state=True)
+    assert ((end - st).abs() <= 1e-5 * (st.abs() + state.abs() + 1)).all()
