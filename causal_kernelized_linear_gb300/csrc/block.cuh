@@ -40,15 +40,12 @@ __device__ __forceinline__ float softplus(float x) {
   return fmaf(2.f * s, p, fmaxf(x, 0.f));
 }
 
-__device__ __forceinline__ float gelu(float x) {
-  return 0.5f * x * (1.f + erff(x * 0.70710678118654752f));
-}
-
+// The activations of one value (gelu goes by pairs, below).
 template <int ACT>
 __device__ __forceinline__ float activate(float x) {
+  static_assert(ACT != LA_ACT_GELU, "gelu2");
   if constexpr (ACT == LA_ACT_RELU) return x < 0.f ? 0.f : x;   // keeps NaN
   if constexpr (ACT == LA_ACT_SILU) return silu(x);
-  if constexpr (ACT == LA_ACT_GELU) return gelu(x);
   if constexpr (ACT == LA_ACT_SOFTPLUS) return softplus(x);
   return x;
 }
@@ -220,6 +217,36 @@ __device__ __forceinline__ float2 softplus2(float2 x) {
   float2 r;
   unpack2(p, r.x, r.y);
   return r;
+}
+
+// x·Φ(x) of two values.  Φ(−u) = e^{−u²/2}·t·P(t) for u = |x|, t = 1/(1 + 11u/32):
+// e^{u²/2}·Φ(−u) falls like 1/u, so that P is smooth; it is fitted on [0, 14]
+// (weighted least squares towards the least largest relative error, 6e-8 with
+// fp32 coefficients).  1 + erf(x/√2) would cancel below zero: 1e-3 of the value
+// at −4, all of it at −6.  Within (1.5·x² + 20)·2^-24 of the value for x < 0 (the
+// rounding of u²/2 in the exponent), 20·2^-24 above.  16384×2048×8192 bf16
+// takes 341 µs so, 415 with erfc, 369 with 1 + erf; 777×128×4096 9.1, 14.5 and 10.5.
+__device__ __forceinline__ float2 gelu2(float2 x) {
+  auto both = [](float c) { return pack2(c, c); };
+  const f32x2 u = pack2(fabsf(x.x), fabsf(x.y));
+  float a0, a1;
+  unpack2(fma2(u, both(0.34375f), both(1.f)), a0, a1);
+  const f32x2 t = pack2(rcp_f32(a0), rcp_f32(a1));
+  f32x2 p = fma2(both(-0.027809331193566322f), t, both(0.14384913444519043f));
+  p = fma2(p, t, both(-0.2717140316963196f));
+  p = fma2(p, t, both(0.19092102348804474f));
+  p = fma2(p, t, both(-0.03930721431970596f));
+  p = fma2(p, t, both(0.11265801638364792f));
+  p = fma2(p, t, both(0.11674045026302338f));
+  p = fma2(p, t, both(0.13754227757453918f));
+  p = fma2(p, t, both(0.13711966574192047f));
+  unpack2(mul2(mul2(u, u), both(-0.5f * kLog2e)), a0, a1);
+  const f32x2 q = mul2(mul2(pack2(tc::ex2_f32(a0), tc::ex2_f32(a1)), t), p);   // Φ(−u)
+  const f32x2 h = fma2(q, both(-1.f), both(1.f));
+  float q0, q1, h0, h1;
+  unpack2(q, q0, q1);
+  unpack2(h, h0, h1);
+  return make_float2(x.x * (x.x < 0.f ? q0 : h0), x.y * (x.y < 0.f ? q1 : h1));
 }
 
 }  // namespace block

@@ -43,6 +43,9 @@ __device__ __forceinline__ void finish4(const LinearArgs& a, int64_t m, int64_t 
   if constexpr (ACT == LA_ACT_SOFTPLUS) {
     const float2 lo = softplus2(make_float2(v[0], v[1])), hi = softplus2(make_float2(v[2], v[3]));
     v[0] = lo.x, v[1] = lo.y, v[2] = hi.x, v[3] = hi.y;
+  } else if constexpr (ACT == LA_ACT_GELU) {
+    const float2 lo = gelu2(make_float2(v[0], v[1])), hi = gelu2(make_float2(v[2], v[3]));
+    v[0] = lo.x, v[1] = lo.y, v[2] = hi.x, v[3] = hi.y;
   } else {
 #pragma unroll
     for (int i = 0; i < 4; ++i) v[i] = activate<ACT>(v[i]);

@@ -57,8 +57,16 @@ __device__ __forceinline__ void finish8(const bf16* bias, const bf16* res, float
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] += b[i];
   }
+  if constexpr (ACT == LA_ACT_GELU) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = activate<ACT>(v[i]);
+    for (int i = 0; i < 8; i += 2) {
+      const float2 y = gelu2(make_float2(v[i], v[i + 1]));
+      v[i] = y.x, v[i + 1] = y.y;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = activate<ACT>(v[i]);
+  }
   if (res) {
     float r[8];
     unpack<bf16>(*reinterpret_cast<const uint4*>(res), r);

@@ -147,3 +147,33 @@ def test_step_with_rates_of_minus_infinity(dtype, B, D, S):
     scan, end = la.selective_scan(x[:, None], dt[:, None], a, b[:, None], c[:, None], softplus=False,
                                   state=state, return_state=True)
     assert ((end - st).abs() <= 1e-5 * (st.abs() + state.abs() + 1)).all()
+
+
+# ------------------------------------------------------------------ activations where they are small
+
+def _through_linear(v, act, rows, dtype):
+    """act of the values v, each the only term of its product, in calls of `rows` rows."""
+    v = v.to(dtype)
+    w = torch.eye(64, device=DEV, dtype=dtype)
+    y = torch.empty_like(v)
+    for i in range(0, v.numel(), rows * 64):
+        y[i:i + rows * 64] = la.linear(v[i:i + rows * 64].view(-1, 64), w, activation=act).view(-1)
+    return v.double(), y.double()
+
+
+@pytest.mark.parametrize("dtype", [BF, torch.float32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("rows", [2, 8, 64, 1024])
+def test_gelu_relative_accuracy(dtype, rows):
+    """x·Φ(x) where Φ is small.  Φ(−u) has e^{−u²/2}: the square, its product with
+    log2(e)/2 and that constant round by 2^-24 each at most, which the
+    exponential turns into 1.5·x²·2^-24 relative below zero; 2^x, 1/x, a fitted
+    polynomial and four products stay within 20·2^-24.  Beside it the output's
+    own rounding.  Above zero Φ's small error is relative to 1 − Φ(−x) ≥ 1/2."""
+    x, y = _through_linear(torch.linspace(-12, 12, 64 * 2048, device=DEV), "gelu", rows, dtype)
+    ref = 0.5 * x * torch.special.erfc(-x * math.sqrt(0.5))
+    half = 2.0 ** -8 if dtype == BF else 2.0 ** -24
+    tol = (half + (1.5 * x.clamp(max=0) ** 2 + 20) * 2.0 ** -24) * ref.abs()
+    assert ((y - ref).abs() <= tol).all(), ((y - ref).abs() / ref.abs().clamp_min(1e-300)).max()
+    far = torch.tensor([-1e4, -60.0, -15.0, 0.0, 60.0, 1e4, -1e30, 1e30] * 16, device=DEV)
+    x, y = _through_linear(far, "gelu", rows, dtype)
+    assert (y[x <= 0].abs() <= 1e-30).all() and torch.equal(y[x > 0], x[x > 0])
