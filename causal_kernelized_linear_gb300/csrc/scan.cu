@@ -50,6 +50,14 @@ __device__ __forceinline__ float rate(float a) {
 // hundreds of tokens adds up (2e-6 after 130 tokens).  With this its mean error
 // is within 1.2e-8 of zero for x in [−0.3, 0], and 2^0 is still 1.
 constexpr float kCentre = 2.0e-8f;
+
+// 2^e·h over a whole chunk of growth (a > 0 or negative steps), where 2^e can be
+// past fp32's range although the states are not: h is tiny, or 0 until later tokens.
+__device__ __forceinline__ float grown(float e, float h) {
+  const float half = tc::ex2_f32(0.5f * e);
+  return h == 0.f ? h : half * (half * h);
+}
+
 constexpr int kTok = 16;      // tokens per stage of the ring
 constexpr int kRing = 3;      // stages: one in use, two in flight
 
@@ -241,24 +249,45 @@ __global__ void __launch_bounds__(32) scan_kernel(const ScanArgs a, const int cb
   if (!ENDS && k > 0) {
     // the state entering this chunk; a chunk past the length has ΣΔ = 0 and a
     // zero end state, and leaves it alone
+    auto enter = [&](auto growing) {
 #pragma unroll 4
-    for (int p = 0; p < k; ++p) {
-      const int64_t at = (b * ch.count + p) * D + c;
+      for (int p = 0; p < k; ++p) {
+        const int64_t at = (b * ch.count + p) * D + c;
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const float sd = p > 0 ? ch.step[at + j] : 0.f;
-        const f32x2 s2 = pack2(sd, sd);
+        for (int j = 0; j < 2; ++j) {
+          const float sd = p > 0 ? ch.step[at + j] : 0.f;
+          const f32x2 s2 = pack2(sd, sd);
 #pragma unroll
-        for (int q = 0; q < K / 2; ++q) {
-          const float2 e = *reinterpret_cast<const float2*>(ch.end + (at + j) * S + lg * K + 2 * q);
-          float e0, e1;
-          unpack2(mul2(s2, A[j][q]), e0, e1);
-          // the first chunk's end state was reached from state_in
-          h[j][q] = p > 0 ? fma2(pack2(tc::ex2_f32(e0), tc::ex2_f32(e1)), h[j][q], pack2(e.x, e.y))
-                          : pack2(e.x, e.y);
+          for (int q = 0; q < K / 2; ++q) {
+            const float2 e = *reinterpret_cast<const float2*>(ch.end + (at + j) * S + lg * K + 2 * q);
+            float e0, e1;
+            unpack2(mul2(s2, A[j][q]), e0, e1);
+            // the first chunk's end state was reached from state_in
+            if (p == 0) {
+              h[j][q] = pack2(e.x, e.y);
+            } else if constexpr (decltype(growing)::value) {
+              float h0, h1;
+              unpack2(h[j][q], h0, h1);
+              h[j][q] = add2(pack2(grown(e0, h0), grown(e1, h1)), pack2(e.x, e.y));
+            } else {
+              h[j][q] = fma2(pack2(tc::ex2_f32(e0), tc::ex2_f32(e1)), h[j][q], pack2(e.x, e.y));
+            }
+          }
         }
       }
-    }
+    };
+    enter(std::false_type());
+    // a factor past fp32's range leaves no finite state behind
+    bool lost = false;
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int q = 0; q < K / 2; ++q) {
+        float h0, h1;
+        unpack2(h[j][q], h0, h1);
+        lost |= !(fabsf(h0) <= kLargest) || !(fabsf(h1) <= kLargest);
+      }
+    if (lost) enter(std::true_type());
   }
 
   float sum[2] = {0.f, 0.f};   // ΣΔ of this lane's tokens (ENDS)

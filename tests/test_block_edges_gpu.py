@@ -177,3 +177,30 @@ def test_gelu_relative_accuracy(dtype, rows):
     far = torch.tensor([-1e4, -60.0, -15.0, 0.0, 60.0, 1e4, -1e30, 1e30] * 16, device=DEV)
     x, y = _through_linear(far, "gelu", rows, dtype)
     assert (y[x <= 0].abs() <= 1e-30).all() and torch.equal(y[x > 0], x[x > 0])
+
+
+# ------------------------------------------------------------------ states that grow
+
+@pytest.mark.parametrize("step,first,value", [
+    (2.0, 2070, 1.0),          # e^160 over a chunk whose states are still 0
+    (1.25, 1980, 1e-30)])      # e^100 over a chunk, from 1e-30 to 1e35
+def test_scan_growth_over_chunks(step, first, value):
+    """Positive rates: a chunk's factor can be past fp32's range while the states
+    are not.  Every step's decay is off by at most (|Δ·a| + 3)·2^-24 relative (its
+    argument, its 2^x), 120 steps of it: 4e-5."""
+    n, D, S = 2100, 24, 16
+    x = torch.zeros(1, n, D, device=DEV)
+    x[:, first] = value
+    dt = torch.full((1, n, D), step, device=DEV)
+    a = torch.ones(D, S, device=DEV)
+    a[:, 8:] = -1.0
+    one = torch.ones(1, n, S, device=DEV)
+    y, end = la.selective_scan(x, dt, a, one, one, softplus=False, return_state=True)
+    h = torch.zeros(D, S, device=DEV, dtype=torch.float64)
+    for t in range(n):
+        h = torch.exp(step * a.double()) * h + step * x[0, t, :, None].double()
+        if t in (first - 1, first, first + 20, n - 1):
+            want = h.sum(-1)
+            assert ((y[0, t].double() - want).abs() <= 4e-5 * want.abs()).all(), t
+    assert ((end[0].double() - h).abs() <= 4e-5 * h.abs() + 1e-37).all()
+    assert (y[:, :first] == 0).all()
