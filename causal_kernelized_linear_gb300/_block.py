@@ -7,7 +7,8 @@ Arguments are checked and marshalled in C++ (``csrc/py_block.cpp``, built as
 Python.  Unlike the attention entry points these take strided views: the last
 axis is contiguous, the others may have any stride that is a multiple of 16
 bytes, so the parts of a projection's output are passed as slices.  With an
-explicit ``stream`` the outputs are allocated for that stream.
+explicit ``stream`` the outputs are allocated for that stream.  An ``out`` that
+is given lies on no input, except the same view where a function says so.
 """
 from __future__ import annotations
 
@@ -69,7 +70,7 @@ def causal_conv(x, weight, bias=None, activation="silu", state=None, lengths=Non
 
 def causal_conv_step(state, x, weight, bias=None, activation="silu", out=None, stream=None):
     """la_causal_conv_step: the convolution's next token.  state [B, W−1, D] is
-    shifted in place; x [B, D].  Returns out [B, D]."""
+    shifted in place; x [B, D]; ``out`` may be x.  Returns out [B, D]."""
     return (_ext or _load_ext()).causal_conv_step(state, x, weight, bias, activation, out, stream)
 
 
@@ -79,8 +80,8 @@ def selective_scan(x, dt, a, b, c, skip=None, gate=None, dt_bias=None, softplus=
     with Δ = softplus(dt + dt_bias) (or dt + dt_bias).  x, dt, gate [B, n, D]
     and b, c [B, n, S] bf16 or fp32; a [D, S], skip [D], dt_bias [D] and
     ``state`` [B, D, S] fp32; ``lengths`` [B] int32: later tokens are not read,
-    leave the state alone and give 0.  S is 8, 16, 32 or 64.  Returns out, or
-    (out, state after the prompt)."""
+    leave the state alone and give 0.  S is 8, 16, 32 or 64.  ``out`` may be x, dt
+    or gate.  Returns out, or (out, state after the prompt)."""
     return (_ext or _load_ext()).selective_scan(x, dt, a, b, c, skip, gate, dt_bias, softplus,
                                                 state, lengths, out, return_state, stream)
 
@@ -89,6 +90,6 @@ def selective_step(state, x, dt, a, b, c, skip=None, gate=None, dt_bias=None, so
                    out=None, stream=None):
     """la_selective_step: the recurrence's next token.  state [B, D, S] fp32 is
     updated in place; x, dt, gate [B, D]; b, c [B, S]; the rest as
-    ``selective_scan``.  Returns out [B, D]."""
+    ``selective_scan``, out included.  Returns out [B, D]."""
     return (_ext or _load_ext()).selective_step(state, x, dt, a, b, c, skip, gate, dt_bias,
                                                 softplus, out, stream)

@@ -6,7 +6,9 @@
 
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cstdint>
+#include <utility>
 
 namespace la {
 namespace {
@@ -58,14 +60,88 @@ bool valid_param(const void* p) { return aligned(p, 16); }
 
 bool valid_activation(la_activation a) { return a >= LA_ACT_NONE && a <= LA_ACT_SOFTPLUS; }
 
-bool overlap(const void* p, const void* q, int64_t bytes) {
-  const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
-  return a < b + (uintptr_t)bytes && b < a + (uintptr_t)bytes;
-}
-
 // Strides of extents 1 are not looked at by the rules: the kernels see 0.
 Rows rows_of(const la_rows* r) {
   return Rows{r->data, r->B > 1 ? r->stride_b : 0, r->n > 1 ? r->stride_n : 0};
+}
+
+// Memory that a call reads or writes: a view, or a dense array; its first byte and
+// the one after its last (which passes 64 bits only where no memory can).
+struct Span {
+  const la_rows* view;
+  int64_t lo, hi;
+};
+
+Span span_of(const void* p, int64_t bytes) {
+  const int64_t lo = (int64_t)reinterpret_cast<uintptr_t>(p);
+  return Span{nullptr, lo, p ? lo + bytes : lo};
+}
+
+Span span_of(const la_rows* r) {
+  const int64_t e = size_of(r->dtype), lo = (int64_t)reinterpret_cast<uintptr_t>(r->data);
+  int64_t b = 0, t = 0, hi = 0;
+  if (r->B == 0 || r->n == 0) return Span{r, lo, lo};
+  if (__builtin_mul_overflow(r->B - 1, r->B > 1 ? r->stride_b * e : 0, &b) ||
+      __builtin_mul_overflow(r->n - 1, r->n > 1 ? r->stride_n * e : 0, &t) ||
+      __builtin_add_overflow(b, t, &hi) || __builtin_add_overflow(hi, lo + r->d * e, &hi))
+    hi = INT64_MAX;
+  return Span{r, lo, hi};
+}
+
+// The same memory as B × n rows of `row` bytes, strides in bytes (0 for extents of
+// 1).  Extents times strides pass 64 bits.
+using Wide = __int128;
+struct Region {
+  Wide at, B, n, sb, sn, row;
+};
+
+Region region_of(const Span& s) {
+  const la_rows* r = s.view;
+  if (!r) return Region{s.lo, 1, 1, 0, 0, s.hi - s.lo};
+  const int64_t e = size_of(r->dtype);
+  Region g{s.lo, r->B, r->n, r->B > 1 ? (Wide)r->stride_b * e : 0, r->n > 1 ? (Wide)r->stride_n * e : 0,
+           (Wide)r->d * e};
+  if (g.B > 1 && (g.n == 1 || g.sb == g.n * g.sn)) {   // one level of rows
+    g.sn = g.n == 1 ? g.sb : g.sn;
+    g.n *= g.B, g.B = 1, g.sb = 0;
+  }
+  if (g.n > 1 && g.sn == g.row) g.row *= g.n, g.n = 1, g.sn = 0;   // dense
+  return g;
+}
+
+Wide floor_div(Wide a, Wide b) { return a / b - (a % b < 0); }
+
+// Whether an element of one lies on an element of the other.  Answered exactly
+// where the two have the same strides, or one is dense (the parts of a
+// projection's output among them); otherwise they are taken to be apart.
+bool coincide(const Span& p, const Span& q) {
+  if (p.hi <= q.lo || q.hi <= p.lo || p.lo == p.hi || q.lo == q.hi) return false;
+  const Region a = region_of(p), b = region_of(q);
+  if ((a.sb && b.sb && a.sb != b.sb) || (a.sn && b.sn && a.sn != b.sn)) return false;
+  // a's row meets b's where lo < Σ (difference of their indices)·stride < hi;
+  // the larger stride outside, where few differences are left to try
+  Wide so = a.sb ? a.sb : b.sb, si = a.sn ? a.sn : b.sn;
+  Wide o0 = b.sb ? 1 - b.B : 0, o1 = a.sb ? a.B - 1 : 0;
+  Wide i0 = b.sn ? 1 - b.n : 0, i1 = a.sn ? a.n - 1 : 0;
+  if (si > so) std::swap(so, si), std::swap(o0, i0), std::swap(o1, i1);
+  const Wide lo = b.at - a.at - a.row, hi = b.at - a.at + b.row;
+  if (so > 0) {
+    o0 = std::max(o0, floor_div(lo - i1 * si, so) + 1);
+    o1 = std::min(o1, floor_div(hi - 1 - i0 * si, so));
+  }
+  if (o1 - o0 > 64) return false;   // rows that are not nested: undecided
+  for (Wide o = o0; o <= o1; ++o) {
+    const Wide l = lo - o * so, h = hi - o * so;
+    if (si == 0 ? l < 0 && h > 0
+                : std::max(i0, floor_div(l, si) + 1) <= std::min(i1, floor_div(h - 1, si)))
+      return true;
+  }
+  return false;
+}
+
+bool same_view(const la_rows* a, const la_rows* b) {
+  const Rows p = rows_of(a), q = rows_of(b);
+  return p.data == q.data && p.sb == q.sb && p.sn == q.sn;
 }
 
 la_status check_conv(const la_rows* x, const void* weight, int width, const void* bias,
@@ -79,6 +155,10 @@ la_status check_conv(const la_rows* x, const void* weight, int width, const void
   if (width < 2 || width > 4 || (act != LA_ACT_NONE && act != LA_ACT_SILU))
     return LA_ERR_UNSUPPORTED;
   if (!supported_rows(x) || !supported_rows(out) || x->d > kMaxChannels) return LA_ERR_UNSUPPORTED;
+  const Span o_at = span_of(out);
+  const int64_t e = size_of(x->dtype);
+  if (coincide(o_at, span_of(weight, x->d * width * e)) || coincide(o_at, span_of(bias, x->d * e)))
+    return LA_ERR_INVALID_ARG;
   *a = ConvArgs{};
   a->x = rows_of(x);
   const Rows o = rows_of(out);
@@ -113,6 +193,13 @@ la_status check_scan(const la_rows* x, const la_rows* dt, const float* a, int st
   for (const la_rows* r : {x, dt, bm, cm, (const la_rows*)out})
     if (!supported_rows(r)) return LA_ERR_UNSUPPORTED;
   if ((gate && !supported_rows(gate)) || x->d > kMaxChannels) return LA_ERR_UNSUPPORTED;
+  const Span o_at = span_of(out);
+  for (const la_rows* r : {x, dt, gate})
+    if (r && !same_view(out, r) && coincide(o_at, span_of(r))) return LA_ERR_INVALID_ARG;
+  if (coincide(o_at, span_of(bm)) || coincide(o_at, span_of(cm)) ||
+      coincide(o_at, span_of(a, x->d * states * 4)) || coincide(o_at, span_of(skip, x->d * 4)) ||
+      coincide(o_at, span_of(dt_bias, x->d * 4)))
+    return LA_ERR_INVALID_ARG;
   *s = ScanArgs{};
   s->x = rows_of(x);
   s->dt = rows_of(dt);
@@ -133,6 +220,17 @@ la_status check_scan(const la_rows* x, const la_rows* dt, const float* a, int st
   s->softplus = softplus != 0;
   s->bf16 = x->dtype == LA_BF16;
   return LA_OK;
+}
+
+// Whether a state that is written lies on an input of the scan or its step.
+bool state_meets(const float* state, int64_t bytes, const la_rows* x, const la_rows* dt, const float* a,
+                 int states, const la_rows* bm, const la_rows* cm, const float* skip,
+                 const la_rows* gate, const float* dt_bias) {
+  const Span at = span_of(state, bytes);
+  for (const la_rows* r : {x, dt, bm, cm, gate})
+    if (r && coincide(at, span_of(r))) return true;
+  return coincide(at, span_of(a, x->d * states * 4)) || coincide(at, span_of(skip, x->d * 4)) ||
+         coincide(at, span_of(dt_bias, x->d * 4));
 }
 
 // A grid beyond what a launch takes is a request outside the kernels' range.
@@ -182,6 +280,11 @@ la_status la_linear(const la_rows* x, const la_rows* weight, const void* bias,
   for (const la_rows* r : {x, weight, (const la_rows*)out})
     if (!supported_rows(r)) return LA_ERR_UNSUPPORTED;
   if (residual && !supported_rows(residual)) return LA_ERR_UNSUPPORTED;
+  const Span o_at = span_of(out);
+  if (coincide(o_at, span_of(x)) || coincide(o_at, span_of(weight)) ||
+      coincide(o_at, span_of(bias, weight->n * size_of(x->dtype))) ||
+      (residual && !same_view(out, residual) && coincide(o_at, span_of(residual))))
+    return LA_ERR_INVALID_ARG;
   if (x->n == 0) return LA_OK;
   DeviceInfo di;
   const la_status st = device_info(&di);
@@ -213,7 +316,13 @@ la_status la_causal_conv(const la_rows* x, const void* weight, int width, const 
   if (!valid_param(state_in) || !valid_param(state_out) || !aligned(lengths, 4))
     return LA_ERR_INVALID_ARG;
   const int64_t bytes = a.B * (width - 1) * a.D * size_of(x->dtype);
-  if (state_in && state_out && overlap(state_in, state_out, bytes)) return LA_ERR_INVALID_ARG;
+  const Span o_at = span_of(out), in = span_of(state_in, bytes), after = span_of(state_out, bytes),
+               lens = span_of(lengths, a.B * 4);
+  if (coincide(o_at, span_of(x)) || coincide(o_at, in) || coincide(o_at, after) ||
+      coincide(o_at, lens) || coincide(after, in) || coincide(after, span_of(x)) ||
+      coincide(after, lens) || coincide(after, span_of(weight, a.D * width * size_of(x->dtype))) ||
+      coincide(after, span_of(bias, a.D * size_of(x->dtype))))
+    return LA_ERR_INVALID_ARG;
   a.state_in = state_in;
   a.state_out = state_out;
   a.lengths = lengths;
@@ -236,6 +345,12 @@ la_status la_causal_conv_step(void* state, const la_rows* x, const void* weight,
   if (x->n != 1 || !valid_param(state)) return LA_ERR_INVALID_ARG;
   if (a.B == 0) return LA_OK;
   if (!state) return LA_ERR_INVALID_ARG;
+  const int64_t e = size_of(x->dtype);
+  const Span at = span_of(state, a.B * (width - 1) * a.D * e);
+  if ((!same_view(out, x) && coincide(span_of(out), span_of(x))) || coincide(at, span_of(out)) ||
+      coincide(at, span_of(x)) || coincide(at, span_of(weight, a.D * width * e)) ||
+      coincide(at, span_of(bias, a.D * e)))
+    return LA_ERR_INVALID_ARG;
   a.state_in = state;
   a.state_out = state;
   DeviceInfo di;
@@ -257,7 +372,11 @@ la_status la_selective_scan(const la_rows* x, const la_rows* dt, const float* a,
   if (!valid_param(state_in) || !valid_param(state_out) || !aligned(lengths, 4))
     return LA_ERR_INVALID_ARG;
   const int64_t bytes = s.B * s.D * s.S * (int64_t)sizeof(float);
-  if (state_in && state_out && overlap(state_in, state_out, bytes)) return LA_ERR_INVALID_ARG;
+  const Span o_at = span_of(out), in = span_of(state_in, bytes), lens = span_of(lengths, s.B * 4);
+  if (coincide(o_at, in) || coincide(o_at, span_of(state_out, bytes)) || coincide(o_at, lens) ||
+      state_meets(state_out, bytes, x, dt, a, states, bm, cm, skip, gate, dt_bias) ||
+      coincide(span_of(state_out, bytes), in) || coincide(span_of(state_out, bytes), lens))
+    return LA_ERR_INVALID_ARG;
   s.state_in = state_in;
   s.state_out = state_out;
   s.lengths = lengths;
@@ -281,6 +400,10 @@ la_status la_selective_step(float* state, const la_rows* x, const la_rows* dt, c
   if (x->n != 1 || !valid_param(state)) return LA_ERR_INVALID_ARG;
   if (s.B == 0) return LA_OK;
   if (!state) return LA_ERR_INVALID_ARG;
+  const int64_t bytes = s.B * s.D * s.S * (int64_t)sizeof(float);
+  if (coincide(span_of(state, bytes), span_of(out)) ||
+      state_meets(state, bytes, x, dt, a, states, bm, cm, skip, gate, dt_bias))
+    return LA_ERR_INVALID_ARG;
   s.state_in = state;
   s.state_out = state;
   DeviceInfo di;

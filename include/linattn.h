@@ -376,7 +376,8 @@ uint64_t la_launch_count(void);
  *   - data is 16-byte aligned; d·size, stride_b·size and stride_n·size are
  *     multiples of 16 bytes (a stride whose extent is 1 is not looked at);
  *   - strides are not negative; elements of an output view do not coincide;
- *   - an output shares no memory with an input unless its comment allows it.
+ *   - an output shares no memory with an input unless its comment allows it
+ *     (LA_ERR_INVALID_ARG where the two have the same strides or one is dense).
  * "parameter" arrays (bias, skip, …) are dense and 16-byte aligned.
  * ------------------------------------------------------------------------ */
 typedef struct {
@@ -456,7 +457,8 @@ la_status la_causal_conv_step(void* state, const la_rows* x, const void* weight,
  *   dt_bias    device fp32 [D], or NULL.
  *   state_in   device fp32 [B, D, S], or NULL for zeros.
  *   lengths    as la_causal_conv; the state is the one after the length.
- *   out        [B, n, D].  Written in full.
+ *   out        [B, n, D].  Written in full; may be the same view as x, dt or
+ *              gate.
  *   state_out  device fp32 [B, D, S], or NULL.  Must not overlap state_in.
  * States, sums and the exponentials' arguments are fp32.  Equal inputs give
  * equal bits.  Errors as la_linear; LA_ERR_UNSUPPORTED for other S.

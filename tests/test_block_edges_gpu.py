@@ -204,3 +204,58 @@ def test_scan_growth_over_chunks(step, first, value):
             assert ((y[0, t].double() - want).abs() <= 4e-5 * want.abs()).all(), t
     assert ((end[0].double() - h).abs() <= 4e-5 * h.abs() + 1e-37).all()
     assert (y[:, :first] == 0).all()
+
+
+# ------------------------------------------------------------------ outputs beside and over inputs
+
+def test_outputs_beside_their_inputs_in_one_buffer():
+    """Columns of one buffer that do not meet are let through, whatever lies between."""
+    g = _gen(6)
+    big = _randn(g, 3, 40, 384)
+    keep = big.clone()
+    w, cw = _randn(g, 64, 64, scale=0.125), _randn(g, 64, 4)
+    x, out = big[..., 64:128], big[..., 128:192]
+    want = la.causal_conv(x.clone(), cw)
+    assert la.causal_conv(x, cw, out=out).data_ptr() == out.data_ptr() and torch.equal(out, want)
+    want = la.linear(x.clone(), w)
+    la.linear(x, w, out=out)
+    assert torch.equal(out, want)
+    i = dict(x=x, dt=big[..., :64], gate=big[..., 192:256], b=big[..., 256:272], c=big[..., 272:288],
+             a=-torch.rand(64, 16, device=DEV, generator=g))
+    want, end = la.selective_scan(**{k: v.clone() for k, v in i.items()}, return_state=True)
+    got, after = la.selective_scan(**i, out=out, return_state=True)
+    assert torch.equal(got, want) and torch.equal(after, end)
+    one = {k: (v if k == "a" else v[:, 0]) for k, v in i.items()}
+    s1, s2 = end.clone(), end.clone()
+    want = la.selective_step(s1, **{k: v.clone() for k, v in one.items()})
+    assert torch.equal(la.selective_step(s2, **one, out=big[:, 0, 320:]), want) and torch.equal(s1, s2)
+    assert torch.equal(big[..., :128], keep[..., :128]) and torch.equal(big[:, 1:, 192:], keep[:, 1:, 192:])
+
+
+@pytest.mark.parametrize("B,n,D", [(2, 33, 72), (4, 700, 2048), (1, 2100, 64)])
+@pytest.mark.parametrize("over", ["x", "dt", "gate"])
+def test_scan_output_may_be_an_input(B, n, D, over):
+    g = _gen(7)
+    i = dict(x=_randn(g, B, n, D), dt=_randn(g, B, n, D), gate=_randn(g, B, n, D), b=_randn(g, B, n, 16),
+             c=_randn(g, B, n, 16), a=-torch.rand(D, 16, device=DEV, generator=g))
+    want, end = la.selective_scan(**i, return_state=True)
+    i[over] = i[over].clone()
+    got, after = la.selective_scan(**i, out=i[over], return_state=True)
+    assert torch.equal(got, want) and torch.equal(after, end)
+
+
+def test_output_over_an_input_is_refused():
+    g = _gen(8)
+    x, w, cw = _randn(g, 2, 70, 64), _randn(g, 64, 64), _randn(g, 64, 4)
+    i = dict(x=x, dt=_randn(g, 2, 70, 64), b=_randn(g, 2, 70, 16), c=_randn(g, 2, 70, 16),
+             a=-torch.rand(64, 16, device=DEV, generator=g))
+    wide = _randn(g, 2, 70, 192)
+    before = la.launch_count()
+    for f in (lambda: la.linear(x, w, out=x), lambda: la.causal_conv(x, cw, out=x),
+              lambda: la.linear(x.view(-1, 64)[:64], w, out=w),
+              lambda: la.causal_conv(wide[..., :64], cw, out=wide[..., 56:120]),
+              lambda: la.selective_scan(**dict(i, x=wide[..., :64]), out=wide[..., 32:96]),
+              lambda: la.selective_scan(**dict(i, b=wide[..., :16]), out=wide[..., 8:72])):
+        with pytest.raises(la.LinAttnError):
+            f()
+    assert la.launch_count() == before
