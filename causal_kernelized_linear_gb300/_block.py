@@ -39,6 +39,10 @@ def _load_ext():
             if not os.path.exists(path):
                 raise RuntimeError(f"la_block.so is not built ({path}); run "
                                    "`python -m causal_kernelized_linear_gb300.build`")
+            if _build.ext_built_for() != _build._ext_target():
+                raise RuntimeError(f"la_block.so is built for {_build.ext_built_for() or 'an unknown PyTorch'}, "
+                                   f"this is {_build._ext_target()}; run "
+                                   "`python -m causal_kernelized_linear_gb300.build`")
             loader = importlib.machinery.ExtensionFileLoader("la_block", path)
             ext = importlib.util.module_from_spec(
                 importlib.util.spec_from_file_location("la_block", path, loader=loader))

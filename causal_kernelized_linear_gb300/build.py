@@ -5,8 +5,10 @@ objects are linked into ``_build/liblinattn.so`` against the shared CUDA
 runtime (the same libcudart.so that PyTorch loads).  Beside them the host
 compiler builds ``_build/la_block.so``, the CPython face of the state-space
 block's operators (it calls the library by address and serves both builds).
-Run as a module (``python -m causal_kernelized_linear_gb300.build``) or call
-:func:`build`.
+It needs PyTorch and its headers; the library does not, and is linked first.
+Run as a module (``python -m causal_kernelized_linear_gb300.build``), as a
+script where PyTorch is not installed (``python
+causal_kernelized_linear_gb300/build.py``), or call :func:`build`.
 """
 from __future__ import annotations
 
@@ -31,6 +33,7 @@ DEBUG_LIB_PATH = os.path.join(DEBUG_BUILD_DIR, "liblinattn.so")
 # the CPython face of the block operators (against the installed PyTorch)
 EXT_SRC = os.path.join(CSRC, "py_block.cpp")
 EXT_PATH = os.path.join(BUILD_DIR, "la_block.so")
+EXT_STAMP = EXT_PATH + ".for"   # the PyTorch and Python it was built for
 
 ARCH_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a"]
 CXX_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC,-O2",
@@ -49,16 +52,45 @@ def _sources():
 
 
 def _deps():
-    return (_sources() + [EXT_SRC] + glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(CSRC, "*.cuh"))
+    return (_sources() + glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(CSRC, "*.cuh"))
             + glob.glob(os.path.join(INCLUDE, "*.h")) + [os.path.abspath(__file__)])
 
 
-def up_to_date(debug: bool = False) -> bool:
-    paths = (DEBUG_LIB_PATH if debug else LIB_PATH, EXT_PATH)
-    if not all(os.path.exists(p) for p in paths):
+def _newer(path: str, deps) -> bool:
+    """Whether ``path`` exists and is newer than every one of ``deps``."""
+    if not os.path.exists(path):
         return False
-    t = min(os.path.getmtime(p) for p in paths)
-    return all(os.path.getmtime(p) <= t for p in _deps())
+    t = os.path.getmtime(path)
+    return all(os.path.getmtime(p) <= t for p in deps)
+
+
+def _ext_target() -> str:
+    import torch
+    return (f"PyTorch {torch.__version__}, Python {sys.version.split()[0]} "
+            f"({sysconfig.get_config_var('SOABI')})")
+
+
+def ext_built_for() -> str:
+    """What ``la_block.so`` was built for ("" if that is not known)."""
+    try:
+        with open(EXT_STAMP) as f:
+            return f.read()
+    except OSError:
+        return ""
+
+
+def lib_up_to_date(debug: bool = False) -> bool:
+    return _newer(DEBUG_LIB_PATH if debug else LIB_PATH, _deps())
+
+
+def ext_up_to_date() -> bool:
+    """Whether ``la_block.so`` is built from its source for this PyTorch and Python."""
+    deps = [EXT_SRC, os.path.abspath(__file__)] + glob.glob(os.path.join(INCLUDE, "*.h"))
+    return _newer(EXT_PATH, deps) and ext_built_for() == _ext_target()
+
+
+def up_to_date(debug: bool = False) -> bool:
+    return lib_up_to_date(debug) and ext_up_to_date()
 
 
 def _build_ext():
@@ -82,6 +114,9 @@ def _build_ext():
     if r.returncode != 0:
         raise RuntimeError(f"{cxx} failed for {EXT_SRC}:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, EXT_PATH)
+    with open(tmp, "w") as f:
+        f.write(_ext_target())
+    os.replace(tmp, EXT_STAMP)
     return r.stdout + r.stderr
 
 
@@ -89,11 +124,26 @@ def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = Fals
           debug: bool = False) -> str:
     """Compile every ``csrc/*.cu`` for sm_103a and link liblinattn.so; with
     ``debug``, the LA_DEBUG build (kernels check their indices) in a folder
-    of its own."""
+    of its own.  ``la_block.so`` is left out where PyTorch is not installed; if
+    it fails to compile, that is raised once the library is linked."""
     lib_path = DEBUG_LIB_PATH if debug else LIB_PATH
-    build_dir = DEBUG_BUILD_DIR if debug else BUILD_DIR
-    if not force and up_to_date(debug):
-        return lib_path
+    try:
+        import torch  # noqa: F401
+        want_ext = force or not ext_up_to_date()
+    except ImportError:
+        want_ext = False
+    with cf.ThreadPoolExecutor(max_workers=1) as ex:
+        ext = ex.submit(_build_ext) if want_ext else None
+        if force or not lib_up_to_date(debug):
+            _build_lib(lib_path, debug, verbose, ptxas_verbose)
+        log = ext.result() if ext else ""
+    if (verbose or ptxas_verbose) and log.strip():
+        print(f"== la_block.so\n{log}", file=sys.stderr)
+    return lib_path
+
+
+def _build_lib(lib_path: str, debug: bool, verbose: bool, ptxas_verbose: bool):
+    build_dir = os.path.dirname(lib_path)
     nvcc = _nvcc()
     os.makedirs(build_dir, exist_ok=True)
     extra = ["-Xptxas", "-v"] if ptxas_verbose else []
@@ -109,16 +159,12 @@ def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = Fals
         return obj, r.stdout + r.stderr
 
     srcs = _sources()
-    with cf.ThreadPoolExecutor(max_workers=max(1, min(len(srcs) + 1, os.cpu_count() or 4))) as ex:
-        ext = ex.submit(_build_ext)
+    with cf.ThreadPoolExecutor(max_workers=max(1, min(len(srcs), os.cpu_count() or 4))) as ex:
         results = list(ex.map(compile_one, srcs))
-        results_ext = ext.result()
     if verbose or ptxas_verbose:
         for obj, log in results:
             if log.strip():
                 print(f"== {os.path.basename(obj)}\n{log}", file=sys.stderr)
-        if results_ext.strip():
-            print(f"== la_block.so\n{results_ext}", file=sys.stderr)
     tmp = lib_path + f".tmp{os.getpid()}"
     cmd = [nvcc, *ARCH_FLAGS, "-shared", "-cudart", "shared", "-o", tmp,
            *[o for o, _ in results]]
@@ -126,7 +172,6 @@ def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = Fals
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, lib_path)
-    return lib_path
 
 
 if __name__ == "__main__":
