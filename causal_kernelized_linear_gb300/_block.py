@@ -9,6 +9,11 @@ axis is contiguous, the others may have any stride that is a multiple of 16
 bytes, so the parts of a projection's output are passed as slices.  With an
 explicit ``stream`` the outputs are allocated for that stream.  An ``out`` that
 is given lies on no input, except the same view where a function says so.
+
+They have no backward.  Outputs of inputs that require a gradient carry a node that
+raises when a gradient reaches it; such inputs are refused with a given ``out``,
+and a state that is updated in place may not require one (``torch.no_grad()``
+lifts both).
 """
 from __future__ import annotations
 
@@ -18,7 +23,7 @@ import importlib.util
 import os
 import threading
 
-import torch  # noqa: F401  (la_block links against its libraries)
+import torch
 
 from . import build as _build
 from ._binding import _check, load
@@ -27,6 +32,24 @@ _NAMES = ("la_linear", "la_causal_conv", "la_causal_conv_step", "la_selective_sc
           "la_selective_step")
 _lock = threading.Lock()
 _ext = None
+
+
+class _NoBackward(torch.autograd.Function):
+    """Outputs as they are, behind a node that has no gradient to give."""
+
+    @staticmethod
+    def forward(ctx, name, outs, *inputs):
+        ctx.name = name
+        return outs[0] if len(outs) == 1 else outs
+
+    @staticmethod
+    def backward(ctx, *grads):
+        raise RuntimeError(f"{ctx.name} has no backward: a gradient reached its output "
+                           "(call it under torch.no_grad(), or detach its inputs)")
+
+
+def _no_backward(name, result, inputs):
+    return _NoBackward.apply(name, result if isinstance(result, tuple) else (result,), *inputs)
 
 
 def _load_ext():
@@ -47,7 +70,7 @@ def _load_ext():
             ext = importlib.util.module_from_spec(
                 importlib.util.spec_from_file_location("la_block", path, loader=loader))
             loader.exec_module(ext)
-            ext.bind(_check, *[ctypes.cast(getattr(lib, n), ctypes.c_void_p).value
+            ext.bind(_check, _no_backward, *[ctypes.cast(getattr(lib, n), ctypes.c_void_p).value
                                for n in _NAMES])
             _ext = ext
     return _ext

@@ -10,6 +10,7 @@
 #include <Python.h>
 
 #include <ATen/ATen.h>
+#include <ATen/core/grad_mode.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -27,6 +28,7 @@ decltype(&la_causal_conv_step) p_conv_step = nullptr;
 decltype(&la_selective_scan) p_scan = nullptr;
 decltype(&la_selective_step) p_step = nullptr;
 PyObject* g_fail = nullptr;   // fail(function name, status): raises LinAttnError
+PyObject* g_no_backward = nullptr;   // no_backward(function name, outputs, inputs): see _block.py
 
 // Set when a check has raised a Python error; caught in every entry point.
 struct Raised {};
@@ -192,6 +194,51 @@ PyObject* pair(PyObject* first, at::Tensor&& second) {
   return t;
 }
 
+// Gradients: these functions have no backward.  Before the call, tensors that it
+// would write in place (out, a step's state) may not be part of a graph that is
+// being recorded; after it, what was written says so, and fresh outputs of inputs
+// that require a gradient get a node that raises when it is asked for one.
+struct Grads {
+  PyObject* const* a;
+  Py_ssize_t n;
+  bool wanted = false;
+
+  // the arguments of a call, the stream (the last of them) apart
+  Grads(PyObject* const* args, Py_ssize_t count) : a(args), n(count - 1) {
+    if (!at::GradMode::is_enabled()) return;
+    for (Py_ssize_t i = 0; i < n && !wanted; ++i) wanted = requires_grad(a[i]);
+  }
+  static bool requires_grad(PyObject* o) {
+    if (o == Py_None || PyBool_Check(o) || PyUnicode_Check(o)) return false;   // asking their class is slow
+    return THPVariable_Check(o) && THPVariable_Unpack(o).requires_grad();
+  }
+  void out(PyObject* o) const {
+    if (wanted && o != Py_None)
+      raise(PyExc_ValueError, "no gradient passes through an out that is given, and an argument "
+                              "requires one; call under torch.no_grad()");
+  }
+  void in_place(PyObject* o, const char* name) const {
+    if (wanted && requires_grad(o))
+      raise(PyExc_ValueError, "%s requires a gradient and is updated in place; call under "
+                              "torch.no_grad()", name);
+  }
+  static void written(PyObject* o) {
+    if (o == Py_None) return;
+    const at::Tensor& t = THPVariable_Unpack(o);
+    if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+  }
+  PyObject* result(const char* name, PyObject* r) const {
+    if (!wanted || !r) return r;
+    PyObject* inputs = PyList_New(0);
+    for (Py_ssize_t i = 0; inputs && i < n; ++i)
+      if (requires_grad(a[i]) && PyList_Append(inputs, a[i]) < 0) Py_CLEAR(inputs);
+    PyObject* with = inputs ? PyObject_CallFunction(g_no_backward, "sOO", name, r, inputs) : nullptr;
+    Py_XDECREF(inputs);
+    Py_DECREF(r);
+    return with;
+  }
+};
+
 #define LA_PY_ENTRY(want)                                                        \
   HANDLE_TH_ERRORS                                                               \
   if (n != (want)) {                                                             \
@@ -227,6 +274,8 @@ PyObject* linear(PyObject*, PyObject* const* a, Py_ssize_t n) {
       raise(PyExc_ValueError, "residual must have the shape %s", c10::str(at::IntArrayRef(shape)).c_str());
     rr = call.matrix(r, "residual");
   }
+  const Grads grads(a, n);
+  grads.out(a[5]);
   call.use(a[6]);
   at::Tensor made;
   if (a[5] == Py_None)
@@ -237,7 +286,8 @@ PyObject* linear(PyObject*, PyObject* const* a, Py_ssize_t n) {
   done("la_linear", unlocked([&] {
          return p_linear(&xr, &wr, bias, act, has_res ? &rr : nullptr, &out, call.stream);
        }));
-  return wrap(a[5], std::move(made));
+  grads.written(a[5]);
+  return grads.result("linear", wrap(a[5], std::move(made)));
   LA_PY_END
 }
 
@@ -265,6 +315,8 @@ PyObject* causal_conv(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const auto* lens = static_cast<const int32_t*>(call.dense(a[5], "lengths", at::kInt, {xr.B}));
   const int want = PyObject_IsTrue(a[7]);
   if (want < 0) throw Raised{};
+  const Grads grads(a, n);
+  grads.out(a[6]);
   call.use(a[8]);
   at::Tensor made, after;
   if (a[6] == Py_None) made = call.empty(x.sizes(), call.type);
@@ -274,8 +326,9 @@ PyObject* causal_conv(PyObject*, PyObject* const* a, Py_ssize_t n) {
          return p_conv(&xr, w, W, bias, act, state, lens, &out, want ? after.data_ptr() : nullptr,
                        call.stream);
        }));
+  grads.written(a[6]);
   PyObject* r = wrap(a[6], std::move(made));
-  return want && r ? pair(r, std::move(after)) : r;
+  return grads.result("causal_conv", want && r ? pair(r, std::move(after)) : r);
   LA_PY_END
 }
 
@@ -291,13 +344,18 @@ PyObject* causal_conv_step(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const void* bias = call.dense(a[3], "bias", call.type, {xr.d});
   tensor(a[0], "state");
   void* state = call.dense(a[0], "state", call.type, {xr.B, W > 0 ? W - 1 : 0, xr.d});
+  const Grads grads(a, n);
+  grads.out(a[5]);
+  grads.in_place(a[0], "state");
   call.use(a[6]);
   at::Tensor made;
   if (a[5] == Py_None) made = call.empty(x.sizes(), call.type);
   la_rows out = call.view(a[5] == Py_None ? made : tensor(a[5], "out"), "out", 2);
   done("la_causal_conv_step",
        unlocked([&] { return p_conv_step(state, &xr, w, W, bias, act, &out, call.stream); }));
-  return wrap(a[5], std::move(made));
+  grads.written(a[0]);
+  grads.written(a[5]);
+  return grads.result("causal_conv_step", wrap(a[5], std::move(made)));
   LA_PY_END
 }
 
@@ -339,6 +397,8 @@ PyObject* selective_scan(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const auto* lens = static_cast<const int32_t*>(call.dense(a[10], "lengths", at::kInt, {s.x.B}));
   const int want = PyObject_IsTrue(a[12]);
   if (want < 0) throw Raised{};
+  const Grads grads(a, n);
+  grads.out(a[11]);
   call.use(a[13]);
   at::Tensor made, after;
   if (a[11] == Py_None) made = call.empty(x.sizes(), call.type);
@@ -349,8 +409,9 @@ PyObject* selective_scan(PyObject*, PyObject* const* a, Py_ssize_t n) {
                        s.bias, s.softplus, state, lens, &out,
                        want ? static_cast<float*>(after.data_ptr()) : nullptr, call.stream);
        }));
+  grads.written(a[11]);
   PyObject* r = wrap(a[11], std::move(made));
-  return want && r ? pair(r, std::move(after)) : r;
+  return grads.result("selective_scan", want && r ? pair(r, std::move(after)) : r);
   LA_PY_END
 }
 
@@ -362,6 +423,9 @@ PyObject* selective_step(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const ScanCall s(call, a + 1, 2);
   tensor(a[0], "state");
   auto* state = static_cast<float*>(call.dense(a[0], "state", at::kFloat, {s.x.B, s.x.d, s.S}));
+  const Grads grads(a, n);
+  grads.out(a[10]);
+  grads.in_place(a[0], "state");
   call.use(a[11]);
   at::Tensor made;
   if (a[10] == Py_None) made = call.empty(x.sizes(), call.type);
@@ -370,19 +434,21 @@ PyObject* selective_step(PyObject*, PyObject* const* a, Py_ssize_t n) {
          return p_step(state, &s.x, &s.dt, s.a, (int)s.S, &s.b, &s.c, s.skip,
                        s.gated ? &s.gate : nullptr, s.bias, s.softplus, &out, call.stream);
        }));
-  return wrap(a[10], std::move(made));
+  grads.written(a[0]);
+  grads.written(a[10]);
+  return grads.result("selective_step", wrap(a[10], std::move(made)));
   LA_PY_END
 }
 
-// bind(fail, addresses of the five C functions in the order above)
+// bind(fail, no_backward, addresses of the five C functions in the order above)
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  if (n != 6) {
-    PyErr_SetString(PyExc_TypeError, "bind(fail, five addresses)");
+  if (n != 7) {
+    PyErr_SetString(PyExc_TypeError, "bind(fail, no_backward, five addresses)");
     return nullptr;
   }
   void* p[5];
   for (int i = 0; i < 5; ++i) {
-    p[i] = PyLong_AsVoidPtr(a[i + 1]);
+    p[i] = PyLong_AsVoidPtr(a[i + 2]);
     if (PyErr_Occurred()) return nullptr;
   }
   p_linear = reinterpret_cast<decltype(p_linear)>(p[0]);
@@ -392,6 +458,8 @@ PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
   p_step = reinterpret_cast<decltype(p_step)>(p[4]);
   Py_INCREF(a[0]);
   Py_XSETREF(g_fail, a[0]);
+  Py_INCREF(a[1]);
+  Py_XSETREF(g_no_backward, a[1]);
   Py_RETURN_NONE;
 }
 

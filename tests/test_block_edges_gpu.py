@@ -259,3 +259,65 @@ def test_output_over_an_input_is_refused():
         with pytest.raises(la.LinAttnError):
             f()
     assert la.launch_count() == before
+
+
+# ------------------------------------------------------------------ gradients
+
+def _block_inputs(g, B=2, n=20, D=64):
+    i = dict(x=_randn(g, B, n, D), dt=_randn(g, B, n, D), b=_randn(g, B, n, 16), c=_randn(g, B, n, 16),
+             a=-torch.rand(D, 16, device=DEV, generator=g))
+    return i, _randn(g, D, D, scale=0.125), _randn(g, D, 4)
+
+
+def test_a_gradient_that_reaches_an_output_raises():
+    i, w, cw = _block_inputs(_gen(9))
+    one = {k: (v if k == "a" else v[:, 0].contiguous()) for k, v in i.items()}
+    conv_state = torch.zeros(2, 3, 64, device=DEV, dtype=BF)
+    state = torch.zeros(2, 64, 16, device=DEV)
+    calls = {
+        "linear": lambda p: la.linear(i["x"], p(w)),
+        "causal_conv": lambda p: la.causal_conv(i["x"], p(cw), return_state=True),
+        "causal_conv_step": lambda p: la.causal_conv_step(conv_state.clone(), one["x"], p(cw)),
+        "selective_scan": lambda p: la.selective_scan(**dict(i, a=p(i["a"])), return_state=True),
+        "selective_step": lambda p: la.selective_step(state.clone(), **dict(one, a=p(one["a"])))}
+    for name, f in calls.items():
+        plain = f(lambda t: t)
+        leaf = []
+        got = f(lambda t: leaf.append(t.clone().requires_grad_()) or leaf[0])
+        with torch.no_grad():
+            quiet = f(lambda t: leaf[0])
+        plain, got, quiet = (v if isinstance(v, tuple) else (v,) for v in (plain, got, quiet))
+        for p, q, r in zip(plain, got, quiet):
+            assert torch.equal(p, q) and torch.equal(p, r)
+            assert q.requires_grad and not r.requires_grad and not p.requires_grad
+            with pytest.raises(RuntimeError, match=f"{name} has no backward"):
+                (q.float() * 2).sum().backward(retain_graph=True)
+        assert leaf[0].grad is None
+
+
+def test_given_outputs_and_states_take_no_part_in_a_graph():
+    i, w, cw = _block_inputs(_gen(10))
+    p = w.clone().requires_grad_()
+    out = torch.empty_like(i["x"])
+    with pytest.raises(ValueError, match="no_grad"):
+        la.linear(i["x"], p, out=out)
+    with torch.no_grad():
+        assert torch.equal(la.linear(i["x"], p, out=out), la.linear(i["x"], w))
+    one = {k: (v if k == "a" else v[:, 0].contiguous()) for k, v in i.items()}
+    state = torch.zeros(2, 64, 16, device=DEV, requires_grad=True)
+    with pytest.raises(ValueError, match="state"):
+        la.selective_step(state, **one)
+    with pytest.raises(ValueError, match="state"):
+        la.causal_conv_step(torch.zeros(2, 3, 64, device=DEV, dtype=BF, requires_grad=True), one["x"], cw)
+    # written in place: a graph that has kept the old values notices
+    for s, write in ((torch.zeros(2, 64, 16, device=DEV), lambda s: la.selective_step(s, **one)),
+                     (torch.zeros_like(i["x"]), lambda s: la.selective_scan(**i, out=s))):
+        q = torch.ones_like(s, requires_grad=True)
+        loss = (q * s).sum()
+        write(s)
+        with pytest.raises(RuntimeError, match="inplace"):
+            loss.backward()
+    with torch.inference_mode():         # nothing keeps versions there
+        s = torch.zeros(2, 64, 16, device=DEV)
+        la.selective_step(s, **one)
+        la.linear(i["x"], p, out=torch.empty_like(i["x"]))
