@@ -454,8 +454,10 @@ cudaError_t launch_pair(const LinearArgs& a, LinParams p, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   // as many pairs as can be resident at once (a GPC with an odd number of SMs
   // leaves one out), each walking its share of the tiles
-  static std::atomic<int> resident{0};
-  int pairs = resident.load(std::memory_order_relaxed);
+  static std::atomic<int> resident[64] = {};   // per device
+  int dev = 0;
+  if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
+  int pairs = resident[dev & 63].load(std::memory_order_relaxed);
   if (pairs == 0) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(2);
@@ -471,7 +473,7 @@ cudaError_t launch_pair(const LinearArgs& a, LinParams p, cudaStream_t s) {
     e = cudaOccupancyMaxActiveClusters(&pairs, pair_kernel<BN, ACT>, &cfg);
     if (e != cudaSuccess) return e;
     if (pairs < 1) return cudaErrorInvalidConfiguration;
-    resident.store(pairs, std::memory_order_relaxed);
+    resident[dev & 63].store(pairs, std::memory_order_relaxed);
   }
   return launch(pair_kernel<BN, ACT>, 2 * (unsigned)(tiles < pairs ? tiles : pairs), kPairThreads,
                 PairCfg<BN>::kSmem, s, 2, mx, mw, mo, p);
