@@ -34,7 +34,8 @@ from ._binding import (EXPORTED, LinAttnError, backward, debug_build, decode_ste
                        decode_step_token_decay, forward, forward_from_state, forward_host,
                        forward_state, forward_token_decay, forward_with_state, last_device_check,
                        last_device_status, launch_count, library_path, load,
-                       selftest_device_check, selftest_wait_timeout, shard_entering_state,
+                       selftest_device_check, selftest_linear_kernel, selftest_step_kernel,
+                       selftest_wait_timeout, shard_entering_state,
                        status_string)
 from ._block import (causal_conv, causal_conv_step, linear, selective_scan, selective_step)
 from .build import build
@@ -44,5 +45,6 @@ __all__ = ["forward", "forward_host", "forward_with_state", "forward_from_state"
            "decode_step_token_decay", "last_device_status", "status_string",
            "LinAttnError", "build", "load", "library_path", "launch_count",
            "selftest_wait_timeout", "debug_build", "last_device_check", "selftest_device_check",
+           "selftest_linear_kernel", "selftest_step_kernel",
            "linear", "causal_conv", "causal_conv_step", "selective_scan", "selective_step",
            "EXPORTED"]

@@ -37,7 +37,8 @@ EXPORTED = ("la_forward", "la_forward_with_state", "la_decode_step", "la_status_
             "la_backward", "la_forward_from_state", "la_forward_state", "la_shard_entering_state",
             "la_forward_host", "la_debug_build", "la_get_last_device_check",
             "la_selftest_device_check", "la_linear", "la_causal_conv", "la_causal_conv_step",
-            "la_selective_scan", "la_selective_step")
+            "la_selective_scan", "la_selective_step", "la_selftest_linear_kernel",
+            "la_selftest_step_kernel")
 
 
 class LinAttnError(RuntimeError):
@@ -142,6 +143,11 @@ def load():
         lib.la_selective_scan.restype = i
         lib.la_selective_step.argtypes = [vp, R, R, vp, i, R, R, vp, R, vp, i, R, vp]
         lib.la_selective_step.restype = i
+        L = ctypes.c_int64
+        lib.la_selftest_linear_kernel.argtypes = [i, L, L, L, i]
+        lib.la_selftest_linear_kernel.restype = ctypes.c_char_p
+        lib.la_selftest_step_kernel.argtypes = [L, L, i, i]
+        lib.la_selftest_step_kernel.restype = ctypes.c_char_p
         _lib = lib
         return lib
 
@@ -536,6 +542,29 @@ def selftest_device_check(stream=None) -> int:
     """la_selftest_device_check: queue the LA_DEBUG check self-test kernel
     (LA_ERR_UNSUPPORTED in the release build)."""
     return int(load().la_selftest_device_check(_stream_handle(stream)))
+
+
+def _num_sms(num_sms):
+    return torch.cuda.get_device_properties(torch.cuda.current_device()).multi_processor_count \
+        if num_sms is None else int(num_sms)
+
+
+def selftest_linear_kernel(dtype, m, n, k, num_sms=None):
+    """la_selftest_linear_kernel: the name of the kernel that ``linear`` runs for
+    x [m, k] and weight [n, k] on a GPU with num_sms multiprocessors (default: the
+    current device's)."""
+    name = load().la_selftest_linear_kernel(_DT[dtype], m, n, k, _num_sms(num_sms))
+    if name is None:
+        raise ValueError("sizes out of range")
+    return name.decode()
+
+
+def selftest_step_kernel(batch, channels, states, num_sms=None):
+    """la_selftest_step_kernel: the same for ``selective_step``."""
+    name = load().la_selftest_step_kernel(batch, channels, states, _num_sms(num_sms))
+    if name is None:
+        raise ValueError("sizes out of range")
+    return name.decode()
 
 
 def launch_count() -> int:

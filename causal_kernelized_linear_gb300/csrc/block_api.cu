@@ -413,4 +413,29 @@ la_status la_selective_step(float* state, const la_rows* x, const la_rows* dt, c
   return launch_status(selective_step(s, (cudaStream_t)stream));
 }
 
+const char* la_selftest_linear_kernel(la_dtype dtype, int64_t M, int64_t N, int64_t K, int num_sms) {
+  if ((dtype != LA_BF16 && dtype != LA_F32) || M < 1 || N < 1 || K < 1 || M > kMaxDim || N > kMaxDim ||
+      K > kMaxDim || num_sms < 1)
+    return nullptr;
+  LinearArgs a{};
+  a.M = M;
+  a.N = N;
+  a.K = K;
+  a.bf16 = dtype == LA_BF16;
+  a.num_sms = num_sms;
+  return linear_kernel(a);
+}
+
+const char* la_selftest_step_kernel(int64_t B, int64_t D, int states, int num_sms) {
+  if (B < 1 || D < 1 || B > kMaxBatch || D > kMaxChannels || num_sms < 1 ||
+      (states != 8 && states != 16 && states != 32 && states != 64))
+    return nullptr;
+  ScanArgs s{};
+  s.B = B;
+  s.D = D;
+  s.S = states;
+  s.num_sms = num_sms;
+  return selective_step_kernel(s);
+}
+
 }  // extern "C"

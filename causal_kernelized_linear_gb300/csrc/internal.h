@@ -254,6 +254,9 @@ struct LinearArgs {
   int num_sms;
 };
 cudaError_t linear(const LinearArgs& a, cudaStream_t stream);
+// The name of the kernel that the call would run, by M, N, K, bf16 and num_sms alone.
+const char* linear_kernel(const LinearArgs& a);
+const char* tc_linear_kernel(const LinearArgs& a);
 // The bf16 product on the tensor cores.
 cudaError_t tc_linear(const LinearArgs& a, cudaStream_t stream);
 
@@ -295,6 +298,8 @@ struct ScanArgs {
 };
 cudaError_t selective_scan(const ScanArgs& a, cudaStream_t stream);
 cudaError_t selective_step(const ScanArgs& a, cudaStream_t stream);
+// The name of the step's kernel, by B, D, S and num_sms alone.
+const char* selective_step_kernel(const ScanArgs& a);
 
 // Memory-bound recurrent decode step.
 cudaError_t decode_step(const DecodeArgs& a, cudaStream_t stream);

@@ -273,15 +273,11 @@ cudaError_t launch_groups(const LinearArgs& a, int64_t mt, int64_t nt, cudaStrea
                    GROUPS * kTileThreads, smem, s, 1, a, (int)mt);
 }
 
-template <int ACT, int T>
+template <int ACT, int T, int GROUPS>
 cudaError_t launch_tiles(const LinearArgs& a, cudaStream_t s) {
   const int64_t mt = ceil_div(a.M, Tile<T>::kBM), nt = ceil_div(a.N, Tile<T>::kBN);
   if (mt * nt > INT32_MAX) return cudaErrorInvalidConfiguration;
-  // groups until an SM has about twelve warps, as long as each has steps to take
-  const int64_t rounds = tile_rounds<T>(a);
-  if (rounds == 1 && a.K >= 8 * kBK) return launch_groups<ACT, T, 4>(a, mt, nt, s);
-  if (rounds <= 2 && a.K >= 4 * kBK) return launch_groups<ACT, T, 2>(a, mt, nt, s);
-  return launch_groups<ACT, T, 1>(a, mt, nt, s);
+  return launch_groups<ACT, T, GROUPS>(a, mt, nt, s);
 }
 
 // SM cycles: rows at kRowRate multiply-adds per SM and cycle, for at least the
@@ -293,13 +289,38 @@ cudaError_t launch_tiles(const LinearArgs& a, cudaStream_t s) {
 constexpr double kRowRate = 18, kTile8 = 100, kTile4 = 48;
 constexpr int64_t kRowK = 128 * kRowWarps;
 
-template <int ACT>
-cudaError_t launch_f32(const LinearArgs& a, cudaStream_t s) {
-  if (a.M <= 2) return launch_rows<ACT, 2>(a, s);
+// The kernel for a product: row_kernel<2> or <8>, or tiles of 8×8 or 4×4 outputs per
+// thread with 1, 2 or 4 groups.
+enum Choice { kRows2, kRows8, kTile8x1, kTile8x2, kTile8x4, kTile4x1, kTile4x2, kTile4x4 };
+
+// groups until an SM has about twelve warps, as long as each has steps to take
+template <int T> int tile_groups(const LinearArgs& a) {
+  const int64_t rounds = tile_rounds<T>(a);
+  return rounds == 1 && a.K >= 8 * kBK ? 4 : (rounds <= 2 && a.K >= 4 * kBK ? 2 : 1);
+}
+
+Choice choose(const LinearArgs& a) {
+  if (a.M <= 2) return kRows2;
   const double rows = (double)a.M * a.N / a.num_sms / kRowRate * (a.K > kRowK ? a.K : kRowK);
   const double large = tile_rounds<8>(a) * kTile8 * a.K, small = tile_rounds<4>(a) * kTile4 * a.K;
-  if ((a.M <= 8 && a.K >= kRowK) || (rows < large && rows < small)) return launch_rows<ACT, 8>(a, s);
-  return small < large ? launch_tiles<ACT, 4>(a, s) : launch_tiles<ACT, 8>(a, s);
+  if ((a.M <= 8 && a.K >= kRowK) || (rows < large && rows < small)) return kRows8;
+  const int g = small < large ? tile_groups<4>(a) : tile_groups<8>(a);
+  const Choice first = small < large ? kTile4x1 : kTile8x1;
+  return (Choice)(first + (g == 4 ? 2 : g - 1));
+}
+
+template <int ACT>
+cudaError_t launch_f32(const LinearArgs& a, cudaStream_t s) {
+  switch (choose(a)) {
+    case kRows2: return launch_rows<ACT, 2>(a, s);
+    case kRows8: return launch_rows<ACT, 8>(a, s);
+    case kTile8x1: return launch_tiles<ACT, 8, 1>(a, s);
+    case kTile8x2: return launch_tiles<ACT, 8, 2>(a, s);
+    case kTile8x4: return launch_tiles<ACT, 8, 4>(a, s);
+    case kTile4x1: return launch_tiles<ACT, 4, 1>(a, s);
+    case kTile4x2: return launch_tiles<ACT, 4, 2>(a, s);
+    default: return launch_tiles<ACT, 4, 4>(a, s);
+  }
 }
 
 cudaError_t f32_linear(const LinearArgs& a, cudaStream_t s) {
@@ -313,6 +334,12 @@ cudaError_t f32_linear(const LinearArgs& a, cudaStream_t s) {
 }
 
 }  // namespace
+
+const char* linear_kernel(const LinearArgs& a) {
+  static const char* const names[] = {"rows2", "rows8", "tile8x1", "tile8x2", "tile8x4", "tile4x1",
+                                      "tile4x2", "tile4x4"};
+  return a.bf16 ? tc_linear_kernel(a) : names[choose(a)];
+}
 
 cudaError_t linear(const LinearArgs& a, cudaStream_t s) {
   return a.bf16 ? tc_linear(a, s) : f32_linear(a, s);

@@ -535,6 +535,26 @@ template <int BN> double pair_cycles(const LinearArgs& a, int kblocks) {
   return 11000 + (double)((tiles + pairs - 1) / pairs) * kblocks * (BN == 256 ? 540 : 460);
 }
 
+// The kernel for a product: few_kernel<16> to <128>, or pair_kernel<128> or <256>.
+enum Choice { kFew16, kFew32, kFew64, kFew128, kPair128, kPair256 };
+
+Choice choose(const LinearArgs& a) {
+  const int kblocks = (int)((a.K + kBK - 1) / kBK);
+  if (a.M <= 16) return kFew16;
+  // tiles of at most twice the tokens there are
+  const double none = 1e300;
+  const double f32 = few_cycles<32>(a, kblocks);
+  const double f64 = a.M > 32 ? few_cycles<64>(a, kblocks) : none;
+  const double f128 = a.M > 64 ? few_cycles<128>(a, kblocks) : none;
+  const double p128 = a.M > 128 ? pair_cycles<128>(a, kblocks) : none;
+  const double p256 = a.M > 128 ? pair_cycles<256>(a, kblocks) : none;
+  const double least = std::min({f32, f64, f128, p128, p256});
+  if (f128 == least) return kFew128;
+  if (f64 == least) return kFew64;
+  if (f32 == least) return kFew32;
+  return p256 == least ? kPair256 : kPair128;
+}
+
 template <int ACT>
 cudaError_t by_shape(const LinearArgs& a, cudaStream_t s) {
   LinParams p{};
@@ -547,22 +567,22 @@ cudaError_t by_shape(const LinearArgs& a, cudaStream_t s) {
   p.N = (int)a.N;
   p.kblocks = (int)((a.K + kBK - 1) / kBK);
   p.status = a.status;
-  if (a.M <= 16) return launch_few<16, ACT>(a, p, s);
-  // tiles of at most twice the tokens there are
-  const double none = 1e300;
-  const double f32 = few_cycles<32>(a, p.kblocks);
-  const double f64 = a.M > 32 ? few_cycles<64>(a, p.kblocks) : none;
-  const double f128 = a.M > 64 ? few_cycles<128>(a, p.kblocks) : none;
-  const double p128 = a.M > 128 ? pair_cycles<128>(a, p.kblocks) : none;
-  const double p256 = a.M > 128 ? pair_cycles<256>(a, p.kblocks) : none;
-  const double least = std::min({f32, f64, f128, p128, p256});
-  if (f128 == least) return launch_few<128, ACT>(a, p, s);
-  if (f64 == least) return launch_few<64, ACT>(a, p, s);
-  if (f32 == least) return launch_few<32, ACT>(a, p, s);
-  return p256 == least ? launch_pair<256, ACT>(a, p, s) : launch_pair<128, ACT>(a, p, s);
+  switch (choose(a)) {
+    case kFew16: return launch_few<16, ACT>(a, p, s);
+    case kFew32: return launch_few<32, ACT>(a, p, s);
+    case kFew64: return launch_few<64, ACT>(a, p, s);
+    case kFew128: return launch_few<128, ACT>(a, p, s);
+    case kPair128: return launch_pair<128, ACT>(a, p, s);
+    default: return launch_pair<256, ACT>(a, p, s);
+  }
 }
 
 }  // namespace
+
+const char* tc_linear_kernel(const LinearArgs& a) {
+  static const char* const names[] = {"few16", "few32", "few64", "few128", "pair128", "pair256"};
+  return names[choose(a)];
+}
 
 cudaError_t tc_linear(const LinearArgs& a, cudaStream_t s) {
   switch (a.act) {

@@ -594,6 +594,13 @@ cudaError_t launch_scan(const ScanArgs& a, cudaStream_t s) {
   return e;
 }
 
+// Batch entries per lane of the step: four where that leaves a thousand threads per
+// SM (256×4096×16: 32 µs against 39 for one entry, before the lanes shared work);
+// one otherwise, where latency counts.
+int step_rows(const ScanArgs& a) {
+  return a.B >= 4 && a.B / 4 * a.D * (a.S / 4) >= (int64_t)1024 * a.num_sms ? 4 : 1;
+}
+
 template <typename T, int S, int R>
 cudaError_t launch_step_rows(const ScanArgs& a, cudaStream_t s) {
   const int64_t cblocks = (a.D * (S / 4) + kStepThreads - 1) / kStepThreads;
@@ -603,14 +610,9 @@ cudaError_t launch_step_rows(const ScanArgs& a, cudaStream_t s) {
                 (uint32_t)cblocks);
 }
 
-// Four batch entries per lane where that leaves a thousand threads per SM
-// (256×4096×16: 32 µs against 39 for one entry, before the lanes shared work);
-// one otherwise, where latency counts.
 template <typename T, int S>
 cudaError_t launch_step(const ScanArgs& a, cudaStream_t s) {
-  return a.B >= 4 && a.B / 4 * a.D * (S / 4) >= (int64_t)1024 * a.num_sms
-             ? launch_step_rows<T, S, 4>(a, s)
-             : launch_step_rows<T, S, 1>(a, s);
+  return step_rows(a) == 4 ? launch_step_rows<T, S, 4>(a, s) : launch_step_rows<T, S, 1>(a, s);
 }
 
 template <typename T>
@@ -628,6 +630,8 @@ cudaError_t by_states(const ScanArgs& a, bool step, cudaStream_t s) {
 cudaError_t selective_scan(const ScanArgs& a, cudaStream_t s) {
   return a.bf16 ? by_states<__nv_bfloat16>(a, false, s) : by_states<float>(a, false, s);
 }
+
+const char* selective_step_kernel(const ScanArgs& a) { return step_rows(a) == 4 ? "step4" : "step1"; }
 
 cudaError_t selective_step(const ScanArgs& a, cudaStream_t s) {
   return a.bf16 ? by_states<__nv_bfloat16>(a, true, s) : by_states<float>(a, true, s);

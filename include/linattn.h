@@ -480,6 +480,16 @@ la_status la_selective_step(float* state, const la_rows* x, const la_rows* dt, c
                             la_rows* out, la_stream stream);
 
 /*
+ * la_selftest_linear_kernel, la_selftest_step_kernel — test hooks: the name of the
+ * kernel that la_linear or la_selective_step would run for these sizes on a GPU
+ * with num_sms multiprocessors ("few64", "pair256", "tile8x2", "rows8", "step4",
+ * …; a static string), or NULL for sizes out of range.  Host only: no device is
+ * needed, nothing is queued.
+ */
+const char* la_selftest_linear_kernel(la_dtype dtype, int64_t M, int64_t N, int64_t K, int num_sms);
+const char* la_selftest_step_kernel(int64_t B, int64_t D, int states, int num_sms);
+
+/*
  * la_selftest_wait_timeout — test hook for the failure path of the bounded
  * waits.  Queues on `stream` one small kernel that runs the same bounded
  * wait the tensor-core kernels use (single-thread and whole-warp forms) on a

@@ -8,6 +8,7 @@ import pytest
 import torch
 
 import causal_kernelized_linear_gb300 as la
+from test_block_gpu import _close, _linear_ref, _scan_inputs, _scan_ref
 
 pytestmark = pytest.mark.gpu
 
@@ -321,3 +322,50 @@ def test_given_outputs_and_states_take_no_part_in_a_graph():
         s = torch.zeros(2, 64, 16, device=DEV)
         la.selective_step(s, **one)
         la.linear(i["x"], p, out=torch.empty_like(i["x"]))
+
+
+# ------------------------------------------------------------------ every kernel, at sizes that it is chosen for
+
+@pytest.mark.parametrize("kernel,m,k,n", [
+    ("few16", 11, 208, 264), ("few16", 16, 4096, 160), ("few32", 537, 384, 96), ("few32", 37, 208, 344),
+    ("few64", 604, 328, 1088), ("few64", 175, 1744, 2520), ("few128", 1499, 192, 1208),
+    ("few128", 1170, 1224, 1400), ("pair128", 2619, 352, 1608), ("pair128", 6421, 64, 528),
+    ("pair128", 12611, 112, 376), ("pair256", 9803, 64, 144), ("pair256", 8905, 144, 376),
+    ("rows2", 2, 604, 4100), ("rows8", 41, 476, 1588), ("tile8x1", 4095, 164, 1164),
+    ("tile8x2", 1290, 156, 916), ("tile8x2", 2315, 616, 816), ("tile8x4", 723, 236, 1076),
+    ("tile4x1", 3287, 76, 268), ("tile4x1", 275, 1428, 4092), ("tile4x2", 214, 828, 1692),
+    ("tile4x4", 97, 2044, 1404)])
+@pytest.mark.parametrize("act,use_bias,use_res", [("none", False, False), ("silu", True, True)])
+def test_linear_kernel(kernel, m, k, n, act, use_bias, use_res):
+    dtype = torch.float32 if kernel[:4] in ("rows", "tile") else BF
+    assert la.selftest_linear_kernel(dtype, m, n, k) == kernel
+    g = _gen(m + n)
+    big = _randn(g, m, n + 16, dtype=dtype)           # the output's columns of a wider buffer
+    keep = big.clone()
+    x, w = _randn(g, m, k, dtype=dtype), _randn(g, n, k, dtype=dtype, scale=k ** -0.5)
+    bias = _randn(g, n, dtype=dtype) if use_bias else None
+    res = _randn(g, m, n, dtype=dtype) if use_res else None
+    out = big[:, 8:8 + n]
+    y = la.linear(x, w, bias=bias, activation=act, residual=res, out=out)
+    ref, ab = _linear_ref(x, w, bias, act, res)
+    _close(y, ref, ab, k + 2, dtype, kernel)
+    assert torch.equal(big[:, :8], keep[:, :8]) and torch.equal(big[:, 8 + n:], keep[:, 8 + n:])
+    assert torch.equal(y, la.linear(x, w, bias=bias, activation=act, residual=res))
+    assert la.last_device_status() == 0
+
+
+@pytest.mark.parametrize("dtype", [BF, torch.float32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("S", [8, 16, 32, 64])
+@pytest.mark.parametrize("B", [301, 302, 303])
+def test_step_four_entries_per_lane_and_a_remainder(dtype, S, B):
+    D = 2040
+    assert la.selftest_step_kernel(B, D, S) == "step4"
+    i = _scan_inputs(_gen(S + B), B, 1, D, S, dtype, state=True)
+    y, ys, h, hs = _scan_ref(i)
+    one = {k: (v[:, 0] if k in ("x", "dt", "b", "c", "gate") else v) for k, v in i.items()}
+    room = torch.full((B + 1, D, S), 7.0, device=DEV)          # nothing past the last entry is written
+    st = room[:B].copy_(one.pop("state"))
+    got = la.selective_step(st, **one)
+    _close(got, y[:, 0], 4 * ys[:, 0], S + 1, dtype, "y")
+    _close(st, h, 4 * hs, S + 1, torch.float32, "state")
+    assert (room[B] == 7.0).all()
