@@ -50,39 +50,33 @@ __device__ __forceinline__ float activate(float x) {
   return x;
 }
 
-// Kernels of these operators are launched with programmatic stream
-// serialization where their own grid allows it: the CTAs may start while the
-// kernel before drains, and nothing of global memory is touched before entry()
-// has returned, which waits until that kernel has completed with its memory
-// visible.  The prologue of a short kernel (launch, barriers, TMEM) overlaps its
-// predecessor's tail.
+// Every kernel of these operators is launched with programmatic stream
+// serialization: its CTAs may start while the kernel before it drains, and
+// nothing of global memory is touched before entry() has returned, which waits
+// until that kernel has completed with its memory visible.  The prologue of a
+// short kernel (launch, barriers, TMEM) overlaps its predecessor's tail.
 __device__ __forceinline__ void entry() {
   tc::grid_dependency_wait();
   tc::grid_dependents_launch();
 }
 
 template <typename... P, typename... A>
-cudaError_t launch_as(bool overlap, void (*kernel)(P...), unsigned grid, unsigned block, size_t smem,
-                      cudaStream_t s, unsigned cluster, A&&... args) {
+cudaError_t launch(void (*kernel)(P...), unsigned grid, unsigned block, size_t smem,
+                   cudaStream_t s, unsigned cluster, A&&... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(block);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
-  unsigned n = 0;
-  if (overlap) {
-    attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[n++].val.programmaticStreamSerializationAllowed = 1;
-  }
-  if (cluster > 1) {
-    attr[n].id = cudaLaunchAttributeClusterDimension;
-    attr[n].val.clusterDim.x = cluster;
-    attr[n].val.clusterDim.y = 1;
-    attr[n++].val.clusterDim.z = 1;
-  }
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = n;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
   const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
   if (e == cudaSuccess)
     count_launches(1);
@@ -91,19 +85,16 @@ cudaError_t launch_as(bool overlap, void (*kernel)(P...), unsigned grid, unsigne
   return e;
 }
 
-template <typename K, typename... A>
-cudaError_t launch(K* kernel, unsigned grid, unsigned block, size_t smem, cudaStream_t s,
-                   unsigned cluster, A&&... args) {
-  return launch_as(true, kernel, grid, block, smem, s, cluster, args...);
-}
-
-// For kernels whose CTAs all fit on the GPU at once and stay to the end: started
-// in the predecessor's tail they would fill the SMs that have room first, two or
-// more on one where each SM could have had its share, and stay there.
-template <typename K, typename... A>
-cudaError_t launch_in_turn(K* kernel, unsigned grid, unsigned block, size_t smem, cudaStream_t s,
-                           A&&... args) {
-  return launch_as(false, kernel, grid, block, smem, s, 1, args...);
+// Dynamic shared memory for a grid whose CTAs all fit on the GPU at once and stay to
+// the end: at least `need`, and just so much that one more than an SM's share of
+// them does not fit on it (228 KB per SM, 1 KB of them per CTA, in units of 128
+// bytes).  Started in the predecessor's tail they would otherwise fill the SMs that
+// have room first, and stay there.
+constexpr size_t kSmemMax = 227 * 1024;   // of a CTA; even_smem stays below
+inline size_t even_smem(size_t need, int64_t ctas, int num_sms) {
+  const int64_t per = (ctas + num_sms - 1) / num_sms;
+  const int64_t least = (228 * 1024 / (per + 1) - 1024 + 128) & ~(int64_t)127;
+  return least > (int64_t)need ? (size_t)least : need;
 }
 
 // Elements of a 16-byte vector.

@@ -260,17 +260,17 @@ template <int T> int64_t tile_rounds(const LinearArgs& a) {
   return ceil_div(ceil_div(a.M, Tile<T>::kBM) * ceil_div(a.N, Tile<T>::kBN), a.num_sms);
 }
 
-// A grid of one tile per SM or fewer starts in turn: in the tail of a convolution
-// or a product two tiles would share an SM (256×1024×1024: 40 µs, 23 in turn;
-// 200×512×1024: 21 and 12; with more tiles, 1000×1024×1024, no difference).
+// An even share of the tiles per SM: in the tail of a convolution or a product two
+// of a single round's tiles would share an SM (256×1024×1024: 40 µs, 29 so;
+// 200×512×1024: 21 and 15; with more tiles, 1000×1024×1024, no difference).
 template <int ACT, int T, int GROUPS>
 cudaError_t launch_groups(const LinearArgs& a, int64_t mt, int64_t nt, cudaStream_t s) {
-  constexpr int smem = kTileSmem<T, GROUPS>;
+  constexpr int need = kTileSmem<T, GROUPS>;
   static std::atomic<uint64_t> smem_set{0};
-  const cudaError_t e = allow_smem((const void*)tile_kernel<ACT, T, GROUPS>, smem, &smem_set);
+  const cudaError_t e = allow_smem((const void*)tile_kernel<ACT, T, GROUPS>, kSmemMax, &smem_set);
   if (e != cudaSuccess) return e;
-  return launch_as(tile_rounds<T>(a) > 1, tile_kernel<ACT, T, GROUPS>, (unsigned)(mt * nt),
-                   GROUPS * kTileThreads, smem, s, 1, a, (int)mt);
+  return launch(tile_kernel<ACT, T, GROUPS>, (unsigned)(mt * nt), GROUPS * kTileThreads,
+                even_smem(need, mt * nt, a.num_sms), s, 1, a, (int)mt);
 }
 
 template <int ACT, int T, int GROUPS>

@@ -156,7 +156,9 @@ __global__ void __launch_bounds__(32) scan_kernel(const ScanArgs a, const int cb
   const int k = (blockIdx.x / cblocks) % (ENDS ? ch.count - 1 : ch.count);
   const int64_t b = blockIdx.x / cblocks / (ENDS ? ch.count - 1 : ch.count);
   const int lane = threadIdx.x, lg = lane / C::kPairs, pair = lane % C::kPairs;
-  tc::grid_dependency_wait();   // the second launch of a cut sequence starts early
+  // No early trigger for the next kernel: its CTAs would take their places on the
+  // SMs that have room first.
+  tc::grid_dependency_wait();
   const int D = (int)a.D, n = (int)a.n;
   const int c0 = cb * C::kCh, cw = c0 + 2 * pair;
   const bool on = cw < D;         // D is even: both channels or none
@@ -563,11 +565,11 @@ cudaError_t launch_scan(const ScanArgs& a, cudaStream_t s) {
     ch.count = (int)((a.n + len - 1) / len);
   }
   static std::atomic<uint64_t> set_all{0}, set_ends{0};
-  cudaError_t e = allow_smem((const void*)scan_kernel<T, S, false>, C::kSmem, &set_all);
+  cudaError_t e = allow_smem((const void*)scan_kernel<T, S, false>, kSmemMax, &set_all);
   if (e != cudaSuccess) return e;
   float* ws = nullptr;
   if (ch.count > 1) {
-    e = allow_smem((const void*)scan_kernel<T, S, true>, C::kSmem, &set_ends);
+    e = allow_smem((const void*)scan_kernel<T, S, true>, kSmemMax, &set_ends);
     if (e != cudaSuccess) return e;
     const size_t rows = (size_t)a.B * ch.count * a.D;
     e = ws_alloc(reinterpret_cast<void**>(&ws), rows * (S + 1) * sizeof(float), s);
@@ -577,16 +579,17 @@ cudaError_t launch_scan(const ScanArgs& a, cudaStream_t s) {
     }
     ch.end = ws;
     ch.step = ws + rows * S;
-    e = launch_in_turn(scan_kernel<T, S, true>, (unsigned)(warps * (ch.count - 1)), 32, C::kSmem, s,
-                       a, (int)cblocks, ch);
+    const int64_t ctas = warps * (ch.count - 1);
+    e = launch(scan_kernel<T, S, true>, (unsigned)ctas, 32, even_smem(C::kSmem, ctas, a.num_sms), s, 1,
+               a, (int)cblocks, ch);
   }
-  // The CTAs of a whole scan are resident at once, so it starts in turn: after a
-  // convolution or a product, whose tails free the SMs unevenly, 4×2048×4096 takes
-  // 210 µs, started early 352; 4×500×2048 43 and 90.  The second launch of a cut
-  // one follows the first, which does not let it start before its own end.
+  // An even share of the CTAs per SM, wherever the predecessor's tail leaves room:
+  // after a convolution or a product 4×2048×4096 takes 210 µs, without 352;
+  // 4×500×2048 41 and 90.
+  const int64_t ctas = warps * ch.count;
   if (e == cudaSuccess)
-    e = launch_as(ch.count > 1, scan_kernel<T, S, false>, (unsigned)(warps * ch.count), 32, C::kSmem,
-                  s, 1, a, (int)cblocks, ch);
+    e = launch(scan_kernel<T, S, false>, (unsigned)ctas, 32, even_smem(C::kSmem, ctas, a.num_sms), s, 1,
+               a, (int)cblocks, ch);
   if (ws) {
     const cudaError_t f = cudaFreeAsync(ws, s);
     if (e == cudaSuccess) e = f;

@@ -26,55 +26,76 @@ def _randn(g, *shape, dtype=BF, scale=1.0):
 
 # ------------------------------------------------------------------ order with the kernel before
 
-def _edges(f):
-    """(edges, programmatic ones among them) of the graph that f's calls record."""
+class _Dim3(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_uint), ("y", ctypes.c_uint), ("z", ctypes.c_uint)]
+
+
+class _KernelParams(ctypes.Structure):
+    _fields_ = [("func", ctypes.c_void_p), ("grid", _Dim3), ("block", _Dim3), ("smem", ctypes.c_uint),
+                ("params", ctypes.c_void_p), ("extra", ctypes.c_void_p)]
+
+
+def _second_launch(f):
+    """(starts early, CTAs, dynamic shared memory) of the second of f's two kernels, from
+    the graph that they record."""
     f()
     torch.cuda.synchronize()
     graph = torch.cuda.CUDAGraph(keep_graph=True)
     with torch.cuda.graph(graph):
         f()
-    get = la.load().cudaGraphGetEdges            # from the CUDA runtime that the library is linked to
-    get.argtypes = [ctypes.c_void_p] * 5
+    rt = la.load()                               # the CUDA runtime that the library is linked to
+    rt.cudaGraphGetEdges.argtypes = [ctypes.c_void_p] * 5
+    rt.cudaGraphKernelNodeGetParams.argtypes = [ctypes.c_void_p] * 2
     n = ctypes.c_size_t()
     raw = graph.raw_cuda_graph()
-    assert get(raw, None, None, None, ctypes.byref(n)) == 0
-    ends = [(ctypes.c_void_p * max(1, n.value))() for _ in range(2)]
-    data = (ctypes.c_uint8 * (8 * max(1, n.value)))()   # from_port, to_port, type, reserved
-    assert get(raw, ends[0], ends[1], data, ctypes.byref(n)) == 0
-    return n.value, sum(data[8 * i + 2] == 1 for i in range(n.value))
+    assert rt.cudaGraphGetEdges(raw, None, None, None, ctypes.byref(n)) == 0 and n.value == 1
+    ends = [(ctypes.c_void_p * 1)() for _ in range(2)]
+    data = (ctypes.c_uint8 * 8)()                # from_port, to_port, type, reserved
+    assert rt.cudaGraphGetEdges(raw, ends[0], ends[1], data, ctypes.byref(n)) == 0
+    p = _KernelParams()
+    assert rt.cudaGraphKernelNodeGetParams(ends[1][0], ctypes.byref(p)) == 0
+    return data[2] == 1, p.grid.x * p.grid.y * p.grid.z, p.smem
 
 
-def test_scan_does_not_start_in_its_predecessors_tail():
+def _spread_evenly(launch):
+    """In its predecessor's tail a grid that fits on the GPU at once would crowd the SMs
+    that have room first: it waits, or an SM does not take more than its share of it
+    (228 KB of shared memory, 1 KB of them per CTA)."""
+    early, ctas, smem = launch
+    share = -(-ctas // torch.cuda.get_device_properties(0).multi_processor_count)
+    return not early or (share + 1) * (smem + 1024) > 228 * 1024
+
+
+@pytest.mark.parametrize("dtype", [BF, torch.float32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("B,n,D,S", [(1, 100, 64, 16), (4, 500, 2048, 16), (8, 130, 2048, 8), (5, 400, 1024, 32),
+                                     (3, 200, 2048, 64)])
+def test_scan_is_spread_evenly_in_its_predecessors_tail(dtype, B, n, D, S):
     g = _gen(1)
-    x, dt, gate = (_randn(g, 1, 100, 64) for _ in range(3))
-    b, c = _randn(g, 1, 100, 16), _randn(g, 1, 100, 16)
-    a = -torch.rand(64, 16, device=DEV, generator=g)
-    w, cw = _randn(g, 64, 64), _randn(g, 64, 4)
-    out = torch.empty_like(x)
+    x, dt = (_randn(g, B, n, D, dtype=dtype) for _ in range(2))
+    b, c = _randn(g, B, n, S, dtype=dtype), _randn(g, B, n, S, dtype=dtype)
+    a = -torch.rand(D, S, device=DEV, generator=g)
+    cw = _randn(g, D, 4, dtype=dtype)
+    out, y = torch.empty_like(x), torch.empty_like(x)
 
     def conv_scan():
-        la.selective_scan(la.causal_conv(x, cw), dt, a, b, c, gate=gate, out=out)
-
-    def linear_scan():
-        la.selective_scan(x, la.linear(x, w), a, b, c, gate=gate, out=out)
-
-    def conv_linear():
-        la.linear(la.causal_conv(x, cw), w, out=out)
-    assert _edges(conv_linear) == (1, 1)         # the others still overlap
-    assert _edges(conv_scan) == (1, 0)
-    assert _edges(linear_scan) == (1, 0)
+        la.causal_conv(x, cw, out=y)
+        la.selective_scan(y, dt, a, b, c, out=out)
+    assert _spread_evenly(_second_launch(conv_scan))
 
 
-def test_single_round_of_fp32_tiles_does_not_start_in_its_predecessors_tail():
+@pytest.mark.parametrize("m,k,n", [(400, 1024, 512), (24, 80, 4096), (200, 512, 1024), (777, 256, 2048),
+                                   (723, 236, 1076), (97, 2044, 1404)])
+def test_fp32_tiles_are_spread_evenly_in_their_predecessors_tail(m, k, n):
     g = _gen(2)
     f32 = torch.float32
-    x = _randn(g, 400, 1024, dtype=f32)
-    w = _randn(g, 512, 1024, dtype=f32, scale=1 / 32)
-    cw = _randn(g, 1024, 4, dtype=f32)
+    assert la.selftest_linear_kernel(f32, m, n, k).startswith("tile")
+    x, w, cw = _randn(g, m, k, dtype=f32), _randn(g, n, k, dtype=f32, scale=0.1), _randn(g, k, 4, dtype=f32)
+    out, y = torch.empty(m, n, device=DEV), torch.empty(1, m, k, device=DEV)
 
     def conv_linear():
-        la.linear(la.causal_conv(x[None], cw), w)
-    assert _edges(conv_linear) == (1, 0)
+        la.causal_conv(x[None], cw, out=y)
+        la.linear(y[0], w, out=out)
+    assert _spread_evenly(_second_launch(conv_linear))
 
 
 def test_products_between_the_attention_kernels():
