@@ -201,6 +201,68 @@ def test_gelu_relative_accuracy(dtype, rows):
     assert (y[x <= 0].abs() <= 1e-30).all() and torch.equal(y[x > 0], x[x > 0])
 
 
+def _silu(x):
+    return x * torch.sigmoid(x)
+
+
+def _softplus(x):
+    return x.clamp(min=0) + torch.log1p(torch.exp(-x.abs()))
+
+
+def _relative(x, y, ref, dtype, fixed):
+    """e^{−|x|} comes from an exponent that rounds by 2^-24 of itself and a constant off by
+    a quarter of that: 1.25·|x|·2^-24 relative where it decides the value, below zero;
+    `fixed` roundings of 2^-24 (2^x counts four, 1/x two) beside it, and the output's."""
+    half = 2.0 ** -8 if dtype == BF else 2.0 ** -24
+    tol = (half + (1.25 * (-x).clamp(min=0) + fixed) * 2.0 ** -24) * ref.abs()
+    worst = ((y - ref).abs() - tol).max()
+    assert ((y - ref).abs() <= tol).all(), worst
+
+
+@pytest.mark.parametrize("dtype", [BF, torch.float32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("rows", [2, 8, 64, 1024])
+@pytest.mark.parametrize("act,ref,fixed", [("silu", _silu, 9), ("softplus", _softplus, 12)])
+def test_relative_accuracy_through_linear(dtype, rows, act, ref, fixed):
+    x, y = _through_linear(torch.linspace(-80, 80, 64 * 2048, device=DEV), act, rows, dtype)
+    _relative(x, y, ref(x), dtype, fixed)
+
+
+@pytest.mark.parametrize("dtype", [BF, torch.float32], ids=["bf16", "f32"])
+def test_relative_accuracy_of_the_convolution_and_the_gate(dtype):
+    v = torch.linspace(-80, 80, 64 * 2048, device=DEV).to(dtype)
+    x = v.view(1, -1, 64)
+    w = torch.zeros(64, 2, device=DEV, dtype=dtype)
+    w[:, 1] = 1.0                                    # the newest input alone
+    y = la.causal_conv(x, w, activation="silu")
+    _relative(x.double(), y.double(), _silu(x.double()), dtype, 9)
+    state = torch.zeros(2048, 1, 64, device=DEV, dtype=dtype)
+    y = la.causal_conv_step(state, x[0], w, activation="silu")
+    _relative(x[0].double(), y.double(), _silu(x[0].double()), dtype, 9)
+    # a scan whose state stays 0, so that its output is skip·x·silu(gate), with x = skip = 1
+    one, zero = torch.ones_like(x), torch.zeros(1, 2048, 16, device=DEV, dtype=dtype)
+    a, skip = -torch.ones(64, 16, device=DEV), torch.ones(64, device=DEV)
+    y = la.selective_scan(one, one, a, zero, zero, skip=skip, gate=x)
+    _relative(x.double(), y.double(), _silu(x.double()), dtype, 9 + 2)
+    y = la.selective_step(torch.zeros(2048, 64, 16, device=DEV), one[0], one[0], a, zero[0], zero[0],
+                          skip=skip, gate=x[0])
+    _relative(x[0].double(), y.double(), _silu(x[0].double()), dtype, 9 + 2)
+
+
+@pytest.mark.parametrize("dtype", [BF, torch.float32], ids=["bf16", "f32"])
+def test_relative_accuracy_of_the_step_size(dtype):
+    """softplus(dt) read back from a state: h = Δ·x·b with x = b = 1 and no state before."""
+    dt = torch.linspace(-80, 80, 64 * 2048, device=DEV).to(dtype).view(2048, 1, 64)
+    one, b = torch.ones_like(dt), torch.ones(2048, 1, 16, device=DEV, dtype=dtype)
+    a = -torch.ones(64, 16, device=DEV)
+    want = _softplus(dt.double())[:, 0, :, None].expand(2048, 64, 16)
+    x = dt.double()[:, 0, :, None].expand(2048, 64, 16)
+    _, h = la.selective_scan(one, dt, a, b, b, return_state=True)
+    _relative(x, h.double(), want, torch.float32, 12 + 2)
+    h = torch.zeros(2048, 64, 16, device=DEV)
+    la.selective_step(h, one[:, 0], dt[:, 0], a, b[:, 0], b[:, 0])
+    _relative(x, h.double(), want, torch.float32, 12 + 2)
+
+
 # ------------------------------------------------------------------ states that grow
 
 @pytest.mark.parametrize("step,first,value", [
