@@ -397,11 +397,12 @@ few_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUten
     if (threadIdx.x == 32) mbar_wait_drain(&bars->done, 0);
     __syncthreads();
   }
+  if (split > 1) cluster_arrive();
   if (warp == 2) {
     tc_fence_after();
     tmem_dealloc(tmem, C::kCols);
   }
-  if (split > 1) cluster_sync();
+  if (split > 1) cluster_wait();
   // rank r finishes its share of the tokens: 16 lanes of 8 features per token
   const int per = (BT + split - 1) / split;
   const int tlim = min(min(BT, (rank + 1) * per), p.M - m0);
