@@ -2,9 +2,9 @@
 //   out_t,c = act(bias_c + Σ_{j<W} w_c,j · X_{t+j,c}),  X = [state | x],
 // over a prompt, and for one token with the state shifted in place.
 //
-// W multiply-adds per value against 2 values moved: bound by HBM, with the
-// instructions (73 % of the issue slots before the channels were handled in
-// pairs) close behind.  A thread owns the channels of one 16-byte vector and
+// W multiply-adds per value against 2 values moved: bound by HBM; the
+// instructions take 47 % of the issue slots (73 % before the channels were
+// handled in pairs).  A thread owns the channels of one 16-byte vector and
 // walks a run of tokens with the last W − 1 inputs in registers, so every input
 // is read once per run (plus W − 1 rows where runs meet, which the neighbouring
 // run has just read into L2) and written once; a warp's accesses are 512
@@ -12,7 +12,7 @@
 // sixteen ahead of the one in use: held in registers they cost the occupancy
 // that hides HBM (115 µs against 100 µs for 4×8192×4096 bf16).
 //
-// Measured: 4×8192×4096 bf16, four taps, silu: 87 µs = 6.2 TB/s, 0.91 of the
+// Measured: 4×8192×4096 bf16, four taps, silu: 87 µs = 6.2 TB/s, 0.92 of the
 // copy bandwidth; 3×1501×1000 fp32 with lengths: 6.5 µs.  The step is a
 // launch: 256×4096 in 4.9 µs with the call.
 #include "block.cuh"

@@ -16,8 +16,8 @@
 // read once per eight tokens in 512-byte pieces; bound by reading w for eight
 // tokens, by the loads of x for more.
 //
-// Measured: 777×128×4096 with bias and softplus in 22.7 µs = 36 TFLOP/s (three
-// tiles per SM; fp32 pipe 30 %, shared-memory pipe 47 %, issue 44 %);
+// Measured: 777×128×4096 with bias and softplus in 22.9 µs = 36 TFLOP/s (three
+// tiles per SM; fp32 pipe 30 %, shared-memory pipe 46 %, issue 44 %);
 // 1×2048×4096 in 7.1 µs = 4.7 TB/s (in a CUDA graph).
 #include "block.cuh"
 #include "internal.h"

@@ -16,9 +16,9 @@
 // keep HBM busy, in one launch, with a fixed order of sums.
 //
 // Measured: 16384×2048×8192 in 330 µs = 1.67 PFLOP/s, 0.86 of the measured
-// burst rate and 0.97 of the sustained one (tensor pipe 78 % at 4096 tokens);
+// burst rate and 0.95 of the sustained one (tensor pipe 78 % at 4096 tokens);
 // 1777×4096×2048 with bias and residual in 27 µs (56 tiles of 256×256 for 76
-// pairs); 16×2048×8192 in 8.7 µs = 3.9 TB/s.
+// pairs); 16×2048×8192 in 8.4 to 8.7 µs = 4 TB/s.
 #include "block.cuh"
 #include "internal.h"
 #include "tc_pair.cuh"

@@ -5,8 +5,8 @@
 //
 // Per (token, channel, state): one 2^x (4 cycles a warp) and four fp32
 // multiply-adds (4 cycles as two packed pairs), against half a byte moved: bound
-// by instruction issue and by the shared-memory reads of B and C, with HBM at a
-// fifth.  So a state element is computed once where possible, and every other
+// by the latency of a few warps' dependent instructions and by the shared-memory
+// reads of B and C, with HBM at a fifth.  So a state element is computed once where possible, and every other
 // cost is kept off its path.  A group of G = S/K lanes owns two neighbouring
 // channels, K states of each per lane, in registers over the whole prompt,
 // packed in pairs (one instruction for two multiply-adds).  Tokens go in
@@ -461,7 +461,7 @@ __global__ void __launch_bounds__(32) scan_kernel(const ScanArgs a, const int cb
 // traffic (8 bytes per state element); a warp touches 512 contiguous bytes.
 // The lanes of a channel share the work per entry: each prepares the entries
 // R/G apart (or one), and passes Δ and Δ·x on by shuffles (32 µs without).
-// Measured: 256×4096×16 bf16 in 22.4 µs = 6.4 TB/s, 0.94 of the copy bandwidth.
+// Measured: 256×4096×16 bf16 in 22.4 µs = 6.4 TB/s, 0.95 of the copy bandwidth.
 constexpr int kStepThreads = 256;
 
 template <typename T, int S, int R>
@@ -542,7 +542,8 @@ __global__ void __launch_bounds__(kStepThreads) step_kernel(const ScanArgs a, ui
 // (1×300×2048: 17 µs at 64, 20 at 96; 4×500×1024: 26 at 64, 32 at 32).  Short
 // ones are not worth a second launch: with less than two warps per SM
 // 1×130×2048 takes 16 µs cut, 14 whole, and 1×200×2048 16 and 19; with more,
-// 7×333×520 (fp32, 32 states) takes 32 cut and 26 whole.
+// 7×333×520 (fp32, 32 states) takes 32 cut and 26 whole, and 2×2048×4096 gains;
+// the border between was not measured closer.
 constexpr int kCutMin = 160, kCutMinFull = 1024;   // tokens: below and from two warps per SM
 constexpr int kWarpsWanted = 4;
 constexpr int kWarpsCut = 24;
