@@ -12,8 +12,8 @@ is given lies on no input, except the same view where a function says so.
 
 They have no backward.  Outputs of inputs that require a gradient carry a node that
 raises when a gradient reaches it; such inputs are refused with a given ``out``,
-and a state that is updated in place may not require one (``torch.no_grad()``
-lifts both).
+and a state that is updated in place may not require one unless one of these
+functions returned it (``torch.no_grad()`` lifts both).
 """
 from __future__ import annotations
 

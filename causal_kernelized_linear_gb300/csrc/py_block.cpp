@@ -14,6 +14,7 @@
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
+#include <torch/csrc/autograd/function.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <optional>
@@ -217,8 +218,11 @@ struct Grads {
       raise(PyExc_ValueError, "no gradient passes through an out that is given, and an argument "
                               "requires one; call under torch.no_grad()");
   }
+  // A state that one of these functions returned keeps its raising node.
   void in_place(PyObject* o, const char* name) const {
-    if (wanted && requires_grad(o))
+    if (!wanted || !requires_grad(o)) return;
+    const auto& node = THPVariable_Unpack(o).grad_fn();
+    if (!node || node->name() != "_NoBackwardBackward")
       raise(PyExc_ValueError, "%s requires a gradient and is updated in place; call under "
                               "torch.no_grad()", name);
   }

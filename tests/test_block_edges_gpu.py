@@ -379,6 +379,27 @@ def test_a_gradient_that_reaches_an_output_raises():
         assert leaf[0].grad is None
 
 
+def test_prompts_and_tokens_with_weights_that_require_gradients():
+    """Without torch.no_grad(): the states that a prompt left are stepped as they are."""
+    i, w, cw = _block_inputs(_gen(12))
+    pw, pcw, pa = (t.clone().requires_grad_() for t in (w, cw, i["a"]))
+    x, conv_state = la.causal_conv(la.linear(i["x"], pw), pcw, return_state=True)
+    y, state = la.selective_scan(**dict(i, x=x, a=pa), return_state=True)
+    for t in range(2):
+        u = la.causal_conv_step(conv_state, la.linear(i["x"][:, t], pw), pcw)
+        o = la.selective_step(state, u, i["dt"][:, t], pa, i["b"][:, t], i["c"][:, t])
+    with torch.no_grad():
+        x, conv_ref = la.causal_conv(la.linear(i["x"], w), cw, return_state=True)
+        _, ref = la.selective_scan(**dict(i, x=x), return_state=True)
+        for t in range(2):
+            u = la.causal_conv_step(conv_ref, la.linear(i["x"][:, t], w), cw)
+            want = la.selective_step(ref, u, i["dt"][:, t], i["a"], i["b"][:, t], i["c"][:, t])
+    assert torch.equal(o, want) and torch.equal(state, ref) and torch.equal(conv_state, conv_ref)
+    for v in (o, state, conv_state):
+        with pytest.raises(RuntimeError, match="has no backward"):
+            v.float().sum().backward(retain_graph=True)
+
+
 def test_given_outputs_and_states_take_no_part_in_a_graph():
     i, w, cw = _block_inputs(_gen(10))
     p = w.clone().requires_grad_()
@@ -393,6 +414,9 @@ def test_given_outputs_and_states_take_no_part_in_a_graph():
         la.selective_step(state, **one)
     with pytest.raises(ValueError, match="state"):
         la.causal_conv_step(torch.zeros(2, 3, 64, device=DEV, dtype=BF, requires_grad=True), one["x"], cw)
+    # one that comes from another operator would keep a graph that no longer holds
+    with pytest.raises(ValueError, match="state"):
+        la.selective_step(state * 2, **one)
     # written in place: a graph that has kept the old values notices
     for s, write in ((torch.zeros(2, 64, 16, device=DEV), lambda s: la.selective_step(s, **one)),
                      (torch.zeros_like(i["x"]), lambda s: la.selective_scan(**i, out=s))):
