@@ -25,7 +25,11 @@ Python face of liblinattn (C ABI in include/linattn.h).  The method
   ``selective_step`` — the operators of a selective state-space block: a
   projection with bias, activation and residual, the short depthwise causal
   convolution and the recurrence with a decay per token, channel and state,
-  over a prompt and for one token.
+  over a prompt and for one token;
+* ``gated_delta`` / ``gated_delta_step``, ``rms_norm``, ``linear_e4m3`` — those of a
+  gated delta-rule block beside them: the gated delta rule over a prompt and
+  for one token, the norm with the residual's addition, a gate and an output in
+  16 or 8 bits, and the projection of 8-bit operands.
 
 All work runs in the library's CUDA kernels; PyTorch only allocates device
 memory and provides the stream.
@@ -37,7 +41,8 @@ from ._binding import (EXPORTED, LinAttnError, backward, debug_build, decode_ste
                        selftest_device_check, selftest_linear_kernel, selftest_step_kernel,
                        selftest_wait_timeout, shard_entering_state,
                        status_string)
-from ._block import (causal_conv, causal_conv_step, linear, selective_scan, selective_step)
+from ._block import (causal_conv, causal_conv_step, gated_delta, gated_delta_step, linear,
+                     linear_e4m3, rms_norm, selective_scan, selective_step)
 from .build import build
 
 __all__ = ["forward", "forward_host", "forward_with_state", "forward_from_state", "forward_state",
@@ -47,4 +52,4 @@ __all__ = ["forward", "forward_host", "forward_with_state", "forward_from_state"
            "selftest_wait_timeout", "debug_build", "last_device_check", "selftest_device_check",
            "selftest_linear_kernel", "selftest_step_kernel",
            "linear", "causal_conv", "causal_conv_step", "selective_scan", "selective_step",
-           "EXPORTED"]
+           "gated_delta", "gated_delta_step", "rms_norm", "linear_e4m3", "EXPORTED"]

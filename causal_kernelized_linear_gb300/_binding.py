@@ -25,6 +25,7 @@ LA_ERR_DEVICE_CHECK = 6
 
 LA_BF16 = 0
 LA_F32 = 1
+LA_E4M3 = 2
 LA_FM_ELU1 = 0
 LA_FM_PERFORMER = 1
 
@@ -38,7 +39,8 @@ EXPORTED = ("la_forward", "la_forward_with_state", "la_decode_step", "la_status_
             "la_forward_host", "la_debug_build", "la_get_last_device_check",
             "la_selftest_device_check", "la_linear", "la_causal_conv", "la_causal_conv_step",
             "la_selective_scan", "la_selective_step", "la_selftest_linear_kernel",
-            "la_selftest_step_kernel")
+            "la_selftest_step_kernel", "la_gated_delta", "la_gated_delta_step", "la_rms_norm",
+            "la_linear_e4m3")
 
 
 class LinAttnError(RuntimeError):
@@ -60,6 +62,14 @@ class LaRows(ctypes.Structure):
     _fields_ = [("data", ctypes.c_void_p), ("dtype", ctypes.c_int), ("B", ctypes.c_int64),
                 ("n", ctypes.c_int64), ("d", ctypes.c_int64), ("stride_b", ctypes.c_int64),
                 ("stride_n", ctypes.c_int64)]
+
+
+class LaHeads(ctypes.Structure):
+    """la_heads: a strided [B, n, H, d] view."""
+    _fields_ = [("data", ctypes.c_void_p), ("dtype", ctypes.c_int), ("B", ctypes.c_int64),
+                ("n", ctypes.c_int64), ("H", ctypes.c_int64), ("d", ctypes.c_int64),
+                ("stride_b", ctypes.c_int64), ("stride_n", ctypes.c_int64),
+                ("stride_h", ctypes.c_int64)]
 
 
 _lock = threading.Lock()
@@ -143,6 +153,15 @@ def load():
         lib.la_selective_scan.restype = i
         lib.la_selective_step.argtypes = [vp, R, R, vp, i, R, R, vp, R, vp, i, R, vp]
         lib.la_selective_step.restype = i
+        H, f = ctypes.POINTER(LaHeads), ctypes.c_float
+        lib.la_gated_delta.argtypes = [H, H, H, R, vp, R, vp, i, i, i, f, vp, vp, H, vp, vp]
+        lib.la_gated_delta.restype = i
+        lib.la_gated_delta_step.argtypes = [vp, H, H, H, R, vp, R, vp, i, i, i, f, H, vp]
+        lib.la_gated_delta_step.restype = i
+        lib.la_rms_norm.argtypes = [R, vp, ctypes.c_int64, f, R, R, R, vp, R, vp]
+        lib.la_rms_norm.restype = i
+        lib.la_linear_e4m3.argtypes = [R, vp, R, vp, vp, i, R, R, vp]
+        lib.la_linear_e4m3.restype = i
         L = ctypes.c_int64
         lib.la_selftest_linear_kernel.argtypes = [i, L, L, L, i]
         lib.la_selftest_linear_kernel.restype = ctypes.c_char_p

@@ -1,6 +1,7 @@
-"""The state-space block's operators (``la_linear``, ``la_causal_conv``,
-``la_causal_conv_step``, ``la_selective_scan``, ``la_selective_step`` in
-include/linattn.h).
+"""The operators of state-space and gated-delta blocks (``la_linear``,
+``la_causal_conv``, ``la_causal_conv_step``, ``la_selective_scan``,
+``la_selective_step``, ``la_gated_delta``, ``la_gated_delta_step``,
+``la_rms_norm``, ``la_linear_e4m3`` in include/linattn.h).
 
 Arguments are checked and marshalled in C++ (``csrc/py_block.cpp``, built as
 ``la_block.so``): a decoding step's kernels are shorter than the same work in
@@ -29,7 +30,8 @@ from . import build as _build
 from ._binding import _check, load
 
 _NAMES = ("la_linear", "la_causal_conv", "la_causal_conv_step", "la_selective_scan",
-          "la_selective_step")
+          "la_selective_step", "la_gated_delta", "la_gated_delta_step", "la_rms_norm",
+          "la_linear_e4m3")
 _lock = threading.Lock()
 _ext = None
 
@@ -120,3 +122,53 @@ def selective_step(state, x, dt, a, b, c, skip=None, gate=None, dt_bias=None, so
     ``selective_scan``, out included.  Returns out [B, D]."""
     return (_ext or _load_ext()).selective_step(state, x, dt, a, b, c, skip, gate, dt_bias,
                                                 softplus, out, stream)
+
+
+def gated_delta(q, k, v, dt, a, beta, dt_bias=None, softplus=True, sigmoid=True, normalize=True,
+                scale=None, state=None, lengths=None, out=None, return_state=False, stream=None):
+    """la_gated_delta: S ← α·S + kᵀ·β(v − k·(α·S)), out = scale·q·S, with
+    α = exp(Δ·a), Δ = softplus(dt + dt_bias) (or dt + dt_bias) and β =
+    sigmoid(beta) (or beta).  q, k [B, n, Hk, dk] and v [B, n, Hv, dv] bf16 or
+    fp32, Hv a multiple of Hk (value head h reads query and key head h·Hk/Hv);
+    dt, beta [B, n, Hv] of the same type or fp32; a, dt_bias [Hv] fp32, a ≤ 0;
+    ``normalize`` takes q and k to unit length first; ``scale`` dk^-½ unless
+    given; ``state`` [B, Hv, dk, dv] fp32 (None: zeros); ``lengths`` [B] int32:
+    later tokens are not read, leave the state alone and give 0.  dk and dv
+    are multiples of 8, at most 256 and 512.  Returns out [B, n, Hv, dv], or
+    (out, state after the prompt)."""
+    return (_ext or _load_ext()).gated_delta(q, k, v, dt, a, beta, dt_bias, softplus, sigmoid,
+                                             normalize, scale, state, lengths, out, return_state,
+                                             stream)
+
+
+def gated_delta_step(state, q, k, v, dt, a, beta, dt_bias=None, softplus=True, sigmoid=True,
+                     normalize=True, scale=None, out=None, stream=None):
+    """la_gated_delta_step: the rule's next token.  state [B, Hv, dk, dv] fp32
+    is updated in place; q, k [B, Hk, dk]; v [B, Hv, dv]; dt, beta [B, Hv];
+    the rest as ``gated_delta``.  Returns out [B, Hv, dv]."""
+    return (_ext or _load_ext()).gated_delta_step(state, q, k, v, dt, a, beta, dt_bias, softplus,
+                                                  sigmoid, normalize, scale, out, stream)
+
+
+def rms_norm(x, weight=None, group=None, eps=1e-6, gate=None, residual=None, quantize=False,
+             out=None, sum_out=None, stream=None):
+    """la_rms_norm: h = x + residual, out = h·rsqrt(mean h² + eps)·weight·silu(gate).
+    x, gate, residual [..., D] bf16 or fp32; the mean goes over groups of
+    ``group`` neighbouring features (weight's length, or D), and weight [group]
+    is the same for each.  With ``quantize`` out is float8_e4m3fn, in units of
+    a scale per row (its largest value is 448).  ``out`` may be x, residual or
+    gate, ``sum_out`` (where h goes, rounded) x or residual.  Returns out, or a
+    tuple of out, the scales [...] if quantized, and h if there is a residual."""
+    return (_ext or _load_ext()).rms_norm(x, weight, group, eps, gate, residual, quantize, out,
+                                          sum_out, stream)
+
+
+def linear_e4m3(x, x_scale, weight, weight_scale, bias=None, activation="none", residual=None,
+                out=None, stream=None):
+    """la_linear_e4m3: act(x_scale·weight_scale·(x·weightᵀ) + bias) + residual.
+    x [..., K] and weight [N, K] float8_e4m3fn, x_scale [...] and weight_scale
+    [N] fp32 (one for each row: ``rms_norm(quantize=True)`` gives x and x_scale);
+    bias [N], residual and out [..., N] bf16; the rest as ``linear``.  K is a
+    multiple of 16, N of 8."""
+    return (_ext or _load_ext()).linear_e4m3(x, x_scale, weight, weight_scale, bias, activation,
+                                             residual, out, stream)

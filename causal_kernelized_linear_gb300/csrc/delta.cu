@@ -1,0 +1,257 @@
+// The gated delta rule token by token on the CUDA cores:
+//   w_t = β_t(v_t − k_t(α_t S_{t−1})),  S_t = α_t S_{t−1} + k_tᵀ w_t,  o_t = scale·q_t S_t.
+//
+// The columns of S do not meet: a warp has a few of them (16 for dk = 128) with
+// all their rows, 16 rows by 4 columns to a lane, and walks the tokens with S in
+// registers.  k·S and q·S of the state before the token are summed together over
+// the P = dk/16 lanes that share a column; o_t = scale·(α q·S_{t−1} + (q·k) w_t)
+// needs no second pass over S, so the next token's sums wait for w_t alone.
+// Everything is fp32.
+#include "block.cuh"
+#include "internal.h"
+
+#include <algorithm>
+#include <atomic>
+
+namespace la {
+namespace {
+
+using namespace block;
+using bf16 = __nv_bfloat16;
+
+constexpr int kThreads = 128;
+constexpr unsigned kAll = 0xffffffffu;
+
+struct DeltaParams {
+  Heads q, k, v, out;
+  Rows dt, beta;
+  const float* a;
+  const float* dt_bias;
+  const float* state_in;
+  float* state_out;
+  const int32_t* lengths;
+  int64_t warps;
+  int n, Hk, Hv, dk, dv, slices;
+  float scale;
+  bool gates_f32, softplus, sigmoid, normalize;
+};
+
+// Four neighbouring elements as they are in memory, and as two pairs of fp32.
+template <typename T> struct Raw4;
+template <> struct Raw4<bf16> {
+  uint2 v = {0u, 0u};
+  __device__ __forceinline__ void load(const bf16* p) { v = *reinterpret_cast<const uint2*>(p); }
+  __device__ __forceinline__ f32x2 lo() const { return pack2(tc::bf16lo_to_f32(v.x), tc::bf16hi_to_f32(v.x)); }
+  __device__ __forceinline__ f32x2 hi() const { return pack2(tc::bf16lo_to_f32(v.y), tc::bf16hi_to_f32(v.y)); }
+};
+template <> struct Raw4<float> {
+  float4 v = {0.f, 0.f, 0.f, 0.f};
+  __device__ __forceinline__ void load(const float* p) { v = *reinterpret_cast<const float4*>(p); }
+  __device__ __forceinline__ f32x2 lo() const { return pack2(v.x, v.y); }
+  __device__ __forceinline__ f32x2 hi() const { return pack2(v.z, v.w); }
+};
+
+__device__ __forceinline__ float gate_value(const Rows& r, bool f32, int64_t at) {
+  return f32 ? static_cast<const float*>(r.data)[at] : to_f32(static_cast<const bf16*>(r.data)[at]);
+}
+
+// α and β of a token.  A step of zero leaves the state alone whatever the rate.
+__device__ __forceinline__ float2 gates(const DeltaParams& p, int64_t b, int64_t t, int h) {
+  float d = gate_value(p.dt, p.gates_f32, b * p.dt.sb + t * p.dt.sn + h);
+  if (p.dt_bias) d += p.dt_bias[h];
+  if (p.softplus) d = softplus(d);
+  float be = gate_value(p.beta, p.gates_f32, b * p.beta.sb + t * p.beta.sn + h);
+  if (p.sigmoid) be = 1.f / (1.f + expf(-be));
+  return make_float2(d == 0.f ? 1.f : expf(d * p.a[h]), be);
+}
+
+// Sums over a column's P lanes, of four columns: lane i gets column
+// 2·(i & 1) + (i >> 1 & 1).
+template <int P>
+__device__ __forceinline__ float sum_columns(const float (&c)[4], int lane) {
+  const bool b0 = lane & 1, b1 = lane & 2;
+  const float k0 = b0 ? c[2] : c[0], k1 = b0 ? c[3] : c[1];
+  const float s0 = b0 ? c[0] : c[2], s1 = b0 ? c[1] : c[3];
+  const float x0 = k0 + __shfl_xor_sync(kAll, s0, 1), x1 = k1 + __shfl_xor_sync(kAll, s1, 1);
+  float r = (b1 ? x1 : x0) + __shfl_xor_sync(kAll, b1 ? x0 : x1, 2);
+#pragma unroll
+  for (int m = 4; m < P; m *= 2) r += __shfl_xor_sync(kAll, r, m);
+  return r;
+}
+
+// The way back: every lane gets the four columns' values.
+__device__ __forceinline__ void spread_columns(float w, int lane, float (&c)[4]) {
+  const bool b0 = lane & 1, b1 = lane & 2;
+  const float o = __shfl_xor_sync(kAll, w, 2);
+  const float x0 = b1 ? o : w, x1 = b1 ? w : o;
+  const float y0 = __shfl_xor_sync(kAll, x0, 1), y1 = __shfl_xor_sync(kAll, x1, 1);
+  c[0] = b0 ? y0 : x0, c[1] = b0 ? y1 : x1, c[2] = b0 ? x0 : y0, c[3] = b0 ? x1 : y1;
+}
+
+template <int P>
+__device__ __forceinline__ float sum_lanes(float v) {
+#pragma unroll
+  for (int m = 1; m < P; m *= 2) v += __shfl_xor_sync(kAll, v, m);
+  return v;
+}
+
+__device__ __forceinline__ float both(f32x2 v) {
+  float lo, hi;
+  unpack2(v, lo, hi);
+  return lo + hi;
+}
+
+// One warp: 128/P columns of one (b, head), all tokens.
+template <typename T, int P>
+__global__ void __launch_bounds__(kThreads) recurrent_kernel(const DeltaParams p) {
+  entry();
+  const int64_t wid = (int64_t)blockIdx.x * (kThreads / 32) + threadIdx.x / 32;
+  if (wid >= p.warps) return;
+  const int lane = threadIdx.x % 32, part = lane % P;
+  const int slice = (int)(wid % p.slices);
+  const int64_t bh = wid / p.slices;
+  const int h = (int)(bh % p.Hv);
+  const int64_t b = bh / p.Hv;
+  const int hk = h / (p.Hv / p.Hk);
+  const int col0 = slice * (128 / P) + lane / P * 4;           // this lane's columns
+  const int mine = col0 + 2 * (lane & 1) + (lane >> 1 & 1);    // the one it sums
+  const bool in = col0 < p.dv;                                 // dv is a multiple of 8
+  const int live = live_tokens(p.lengths, b, p.n);
+
+  // rows 4(iP + part) + j of S, in pairs of rows
+  f32x2 S[4][8];
+  bool row_in[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = 4 * (i * P + part);
+    row_in[i] = r < p.dk;
+    float4 m[4] = {};
+    if (p.state_in && in && row_in[i]) {
+      const float* at = p.state_in + (bh * p.dk + r) * p.dv + col0;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) m[j] = *reinterpret_cast<const float4*>(at + (int64_t)j * p.dv);
+    }
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      S[0][2 * i + j] = pack2(m[2 * j].x, m[2 * j + 1].x);
+      S[1][2 * i + j] = pack2(m[2 * j].y, m[2 * j + 1].y);
+      S[2][2 * i + j] = pack2(m[2 * j].z, m[2 * j + 1].z);
+      S[3][2 * i + j] = pack2(m[2 * j].w, m[2 * j + 1].w);
+    }
+  }
+
+  const T* qp = static_cast<const T*>(p.q.data) + b * p.q.sb + (int64_t)hk * p.q.sh;
+  const T* kp = static_cast<const T*>(p.k.data) + b * p.k.sb + (int64_t)hk * p.k.sh;
+  const T* vp = static_cast<const T*>(p.v.data) + b * p.v.sb + (int64_t)h * p.v.sh + mine;
+  T* op = static_cast<T*>(const_cast<void*>(p.out.data)) + b * p.out.sb + (int64_t)h * p.out.sh + mine;
+  Raw4<T> qr[4], kr[4];
+  T vr = from_f32<T>(0.f);
+  auto load = [&](int t) {   // token t's share of this lane
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (row_in[i]) {
+        const int r = 4 * (i * P + part);
+        qr[i].load(qp + t * p.q.sn + r);
+        kr[i].load(kp + t * p.k.sn + r);
+      }
+    if (in) vr = vp[t * p.v.sn];
+  };
+  if (live > 0) load(0);
+  float2 g = {1.f, 0.f};
+  for (int t = 0; t < live; ++t) {
+    if (t % 32 == 0) g = t + lane < live ? gates(p, b, t + lane, h) : make_float2(1.f, 0.f);
+    const float alpha = __shfl_sync(kAll, g.x, t % 32), beta = __shfl_sync(kAll, g.y, t % 32);
+    f32x2 q[8], k[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      q[2 * i] = qr[i].lo(), q[2 * i + 1] = qr[i].hi();
+      k[2 * i] = kr[i].lo(), k[2 * i + 1] = kr[i].hi();
+    }
+    const float v = to_f32(vr);
+    if (t + 1 < live) load(t + 1);
+    f32x2 qk2 = 0, qq2 = 0, kk2 = 0, ks2[4] = {}, qs2[4] = {};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      qk2 = fma2(q[i], k[i], qk2);
+      qq2 = fma2(q[i], q[i], qq2);
+      kk2 = fma2(k[i], k[i], kk2);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        ks2[c] = fma2(k[i], S[c][i], ks2[c]);
+        qs2[c] = fma2(q[i], S[c][i], qs2[c]);
+      }
+    }
+    float ks[4], qs[4];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) ks[c] = both(ks2[c]), qs[c] = both(qs2[c]);
+    float rk = 1.f, rq = p.scale;
+    if (p.normalize) {
+      rk = rsqrtf(sum_lanes<P>(both(kk2)) + 1e-6f);
+      rq *= rsqrtf(sum_lanes<P>(both(qq2)) + 1e-6f);
+    }
+    const float qk = sum_lanes<P>(both(qk2));
+    const float ksum = sum_columns<P>(ks, lane), qsum = sum_columns<P>(qs, lane);
+    const float w = rk * (beta * (v - alpha * (rk * ksum)));
+    float wc[4];
+    spread_columns(w, lane, wc);
+    const f32x2 al = pack2(alpha, alpha);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const f32x2 w2 = pack2(wc[c], wc[c]);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) S[c][i] = fma2(k[i], w2, mul2(al, S[c][i]));
+    }
+    if (in && part < 4) op[t * p.out.sn] = from_f32<T>(rq * (alpha * qsum + qk * w));
+  }
+  if (in && part < 4)
+    for (int t = live; t < p.n; ++t) op[t * p.out.sn] = from_f32<T>(0.f);
+  if (!p.state_out || !in) return;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (!row_in[i]) continue;
+    float* at = p.state_out + (bh * p.dk + 4 * (i * P + part)) * p.dv + col0;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      float4 lo, hi;
+      unpack2(S[0][2 * i + j], lo.x, hi.x);
+      unpack2(S[1][2 * i + j], lo.y, hi.y);
+      unpack2(S[2][2 * i + j], lo.z, hi.z);
+      unpack2(S[3][2 * i + j], lo.w, hi.w);
+      *reinterpret_cast<float4*>(at + (int64_t)(2 * j) * p.dv) = lo;
+      *reinterpret_cast<float4*>(at + (int64_t)(2 * j + 1) * p.dv) = hi;
+    }
+  }
+}
+
+template <typename T, int P>
+cudaError_t launch_recurrent(const DeltaArgs& a, DeltaParams p, cudaStream_t s) {
+  p.slices = (a.dv + 128 / P - 1) / (128 / P);
+  p.warps = a.B * a.Hv * p.slices;
+  const int64_t ctas = (p.warps + kThreads / 32 - 1) / (kThreads / 32);
+  if (ctas > INT32_MAX) return cudaErrorInvalidConfiguration;
+  return launch(recurrent_kernel<T, P>, (unsigned)ctas, kThreads, 0, s, 1, p);
+}
+
+template <typename T>
+cudaError_t by_keys(const DeltaArgs& a, const DeltaParams& p, cudaStream_t s) {
+  if (a.dk <= 64) return launch_recurrent<T, 4>(a, p, s);
+  if (a.dk <= 128) return launch_recurrent<T, 8>(a, p, s);
+  return launch_recurrent<T, 16>(a, p, s);
+}
+
+}  // namespace
+
+cudaError_t gated_delta(const DeltaArgs& a, cudaStream_t s) {
+  DeltaParams p{};
+  p.q = a.q, p.k = a.k, p.v = a.v, p.out = a.out;
+  p.dt = a.dt, p.beta = a.beta;
+  p.a = a.a, p.dt_bias = a.dt_bias;
+  p.state_in = a.state_in, p.state_out = a.state_out, p.lengths = a.lengths;
+  p.n = (int)a.n, p.Hk = (int)a.Hk, p.Hv = (int)a.Hv, p.dk = a.dk, p.dv = a.dv;
+  p.scale = a.scale;
+  p.gates_f32 = a.gates_f32, p.softplus = a.softplus, p.sigmoid = a.sigmoid;
+  p.normalize = a.normalize;
+  return a.bf16 ? by_keys<bf16>(a, p, s) : by_keys<float>(a, p, s);
+}
+
+}  // namespace la

@@ -125,12 +125,15 @@ cudaError_t tc_performer_forward(const FwdArgs& a, cudaStream_t stream, float* w
 //   tmap_matrix:   a bf16 row-major [rows, cols] matrix, box 64 × box_rows;
 //   tmap_view:     a bf16 [rows, cols] view with rows row_stride elements apart,
 //                  box 64 × box_rows;
+//   tmap_bytes:    the same of 8-bit elements, box 128 × box_rows;
 //   tmap_f32_mats: `count` fp32 row-major [D × D] matrices, contiguous, as a
 //                  3-D tensor, box 32 × D × 1.
 cudaError_t tmap_rows(CUtensorMap* m, const void* base, int64_t BH, int64_t n, int D, int rows);
 cudaError_t tmap_matrix(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, int box_rows);
 cudaError_t tmap_view(CUtensorMap* m, const void* base, int64_t rows, int64_t cols,
                       int64_t row_stride, int box_rows);
+cudaError_t tmap_bytes(CUtensorMap* m, const void* base, int64_t rows, int64_t cols,
+                       int64_t row_stride, int box_rows);
 cudaError_t tmap_f32_mats(CUtensorMap* m, const void* base, int64_t count, int D);
 
 // Exclusive decayed prefix over the per-segment aggregates of every head, in
@@ -300,6 +303,61 @@ cudaError_t selective_scan(const ScanArgs& a, cudaStream_t stream);
 cudaError_t selective_step(const ScanArgs& a, cudaStream_t stream);
 // The name of the step's kernel, by B, D, S and num_sms alone.
 const char* selective_step_kernel(const ScanArgs& a);
+
+// ---------------------------------------------------------------- gated delta block
+
+// A strided [B, n, H, d] view: element (b, t, h, c) at data[b·sb + t·sn + h·sh + c].
+struct Heads {
+  const void* data;
+  int64_t sb, sn, sh;
+};
+
+// The gated delta rule over a prompt, or for one token (n = 1, in place).
+struct DeltaArgs {
+  Heads q, k, v, out;
+  Rows dt, beta;            // [B, n, Hv]
+  bool gates_f32;           // the type of dt and beta, else bf16
+  const float* a;           // [Hv]
+  const float* dt_bias;     // [Hv] or nullptr
+  const float* state_in;    // [B, Hv, dk, dv] or nullptr (zeros)
+  float* state_out;         // [B, Hv, dk, dv] or nullptr
+  const int32_t* lengths;   // [B] or nullptr (all n)
+  int64_t B, n, Hk, Hv;
+  int dk, dv;
+  float scale;
+  bool softplus, sigmoid, normalize;
+  bool bf16;
+  int* status;
+  int num_sms;
+};
+cudaError_t gated_delta(const DeltaArgs& a, cudaStream_t stream);
+
+// out = norm(x + residual)·weight·silu(gate) over M rows of D features.
+struct NormArgs {
+  Rows x, residual, gate;   // [M, D]; the latter two may be nullptr
+  void* out;
+  int64_t out_sn;
+  void* sum;                // [M, D] or nullptr: x + residual
+  int64_t sum_sn;
+  float* scale;             // [M]: of an 8-bit out
+  const void* weight;       // [group] or nullptr
+  int64_t M;
+  int D, group;
+  float eps;
+  bool bf16, quantize;
+  int num_sms;
+};
+// Whether a row of D features fits a CTA's registers.
+bool rms_norm_supported(int64_t D, bool bf16);
+cudaError_t rms_norm(const NormArgs& a, cudaStream_t stream);
+
+// LinearArgs with 8-bit x and w, each row with a factor; bf16 otherwise.
+struct LinearE4m3Args {
+  LinearArgs base;
+  const float* x_scale;     // [M]
+  const float* w_scale;     // [N]
+};
+cudaError_t tc_linear_e4m3(const LinearE4m3Args& a, cudaStream_t stream);
 
 // Memory-bound recurrent decode step.
 cudaError_t decode_step(const DecodeArgs& a, cudaStream_t stream);

@@ -1,4 +1,4 @@
-// CPython entry points of the state-space block's operators: argument checks,
+// CPython entry points of the block operators: argument checks,
 // la_rows views of the tensors, output allocation, and the call into the C
 // ABI (include/linattn.h).  No arithmetic.
 //
@@ -17,7 +17,10 @@
 #include <torch/csrc/autograd/function.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <array>
+#include <cmath>
 #include <optional>
+#include <string>
 
 #include "linattn.h"
 
@@ -28,6 +31,10 @@ decltype(&la_causal_conv) p_conv = nullptr;
 decltype(&la_causal_conv_step) p_conv_step = nullptr;
 decltype(&la_selective_scan) p_scan = nullptr;
 decltype(&la_selective_step) p_step = nullptr;
+decltype(&la_gated_delta) p_delta = nullptr;
+decltype(&la_gated_delta_step) p_delta_step = nullptr;
+decltype(&la_rms_norm) p_norm = nullptr;
+decltype(&la_linear_e4m3) p_linear8 = nullptr;
 PyObject* g_fail = nullptr;   // fail(function name, status): raises LinAttnError
 PyObject* g_no_backward = nullptr;   // no_backward(function name, outputs, inputs): see _block.py
 
@@ -49,6 +56,7 @@ const char* type_name(at::ScalarType t) {
   switch (t) {
     case at::kBFloat16: return "torch.bfloat16";
     case at::kFloat: return "torch.float32";
+    case at::kFloat8_e4m3fn: return "torch.float8_e4m3fn";
     default: return "torch.int32";
   }
 }
@@ -62,12 +70,14 @@ struct Call {
   std::optional<c10::cuda::CUDAStreamGuard> on_stream;
   la_stream stream = nullptr;
 
-  explicit Call(const at::Tensor& x) : type(x.scalar_type()) {
+  explicit Call(const at::Tensor& x, const char* name = "x") : type(x.scalar_type()) {
     if (type != at::kBFloat16 && type != at::kFloat)
-      raise(PyExc_ValueError, "x: unsupported dtype (bf16 or fp32 wanted)");
+      raise(PyExc_ValueError, "%s: unsupported dtype (bf16 or fp32 wanted)", name);
     dtype = type == at::kBFloat16 ? LA_BF16 : LA_F32;
     device = x.device();
   }
+  // bf16 results of 8-bit operands
+  Call(const at::Tensor& x, at::ScalarType result) : type(result), dtype(LA_BF16), device(x.device()) {}
 
   void check(const at::Tensor& t, const char* name, at::ScalarType want) const {
     if (!t.is_cuda()) raise(PyExc_ValueError, "%s must be a CUDA tensor (no CPU path exists)", name);
@@ -116,10 +126,11 @@ struct Call {
   }
 
   // [..., d] whose leading axes flatten to rows without a copy.
-  la_rows matrix(const at::Tensor& t, const char* name) const {
+  la_rows matrix(const at::Tensor& t, const char* name) const { return matrix(t, name, type, dtype); }
+  la_rows matrix(const at::Tensor& t, const char* name, at::ScalarType want, la_dtype as) const {
     const int64_t dim = t.dim();
     if (dim < 2) raise(PyExc_ValueError, "%s must have at least two axes", name);
-    check(t, name, type);
+    check(t, name, want);
     last_axis(t, name);
     int64_t rows = 1, stride = t.size(dim - 1);
     bool first = true;
@@ -134,7 +145,33 @@ struct Call {
       }
       rows *= size;
     }
-    return la_rows{t.data_ptr(), dtype, 1, rows, t.size(dim - 1), 0, stride};
+    return la_rows{t.data_ptr(), as, 1, rows, t.size(dim - 1), 0, stride};
+  }
+
+  // [B, n, H, d] (axes 4) or [B, H, d] (axes 3, n = 1).
+  la_heads heads(const at::Tensor& t, const char* name, int axes) const {
+    if (t.dim() != axes)
+      raise(PyExc_ValueError, "%s must have %d axes, not %d", name, axes, (int)t.dim());
+    check(t, name, type);
+    last_axis(t, name);
+    if (axes == 4)
+      return la_heads{t.data_ptr(), dtype, t.size(0), t.size(1), t.size(2), t.size(3),
+                      t.stride(0), t.stride(1), t.stride(2)};
+    return la_heads{t.data_ptr(), dtype, t.size(0), 1, t.size(1), t.size(2),
+                    t.stride(0), 0, t.stride(1)};
+  }
+
+  // [B, n, H] (axes 3) or [B, H] of x's type or fp32.
+  la_rows gate(const at::Tensor& t, const char* name, int axes) const {
+    if (t.dim() != axes)
+      raise(PyExc_ValueError, "%s must have %d axes, not %d", name, axes, (int)t.dim());
+    const bool f32 = t.scalar_type() == at::kFloat;
+    check(t, name, f32 ? at::kFloat : type);
+    last_axis(t, name);
+    const la_dtype as = f32 ? LA_F32 : dtype;
+    if (axes == 3)
+      return la_rows{t.data_ptr(), as, t.size(0), t.size(1), t.size(2), t.stride(0), t.stride(1)};
+    return la_rows{t.data_ptr(), as, t.size(0), 1, t.size(1), t.stride(0), 0};
   }
 
   // A dense array of the given type and shape, or nullptr for None.
@@ -444,14 +481,222 @@ PyObject* selective_step(PyObject*, PyObject* const* a, Py_ssize_t n) {
   LA_PY_END
 }
 
-// bind(fail, no_backward, addresses of the five C functions in the order above)
+float number(PyObject* o, const char* name) {
+  const double v = PyFloat_AsDouble(o);
+  if (v == -1.0 && PyErr_Occurred()) {
+    PyErr_Clear();
+    raise(PyExc_TypeError, "%s must be a number", name);
+  }
+  return (float)v;
+}
+
+int truth(PyObject* o) {
+  const int v = PyObject_IsTrue(o);
+  if (v < 0) throw Raised{};
+  return v;
+}
+
+// What the rule and its step share: q, k, v, dt, a, beta, dt_bias, softplus, sigmoid,
+// normalize, scale.
+struct DeltaCall {
+  la_heads q, k, v;
+  la_rows dt, beta;
+  const float *a, *bias;
+  int softplus, sigmoid, normalize;
+  float scale;
+
+  DeltaCall(const Call& call, PyObject* const* p, int axes) {
+    q = call.heads(tensor(p[0], "q"), "q", axes);
+    k = call.heads(tensor(p[1], "k"), "k", axes);
+    v = call.heads(tensor(p[2], "v"), "v", axes);
+    dt = call.gate(tensor(p[3], "dt"), "dt", axes - 1);
+    tensor(p[4], "a");
+    a = static_cast<const float*>(call.dense(p[4], "a", at::kFloat, {v.H}));
+    beta = call.gate(tensor(p[5], "beta"), "beta", axes - 1);
+    bias = static_cast<const float*>(call.dense(p[6], "dt_bias", at::kFloat, {v.H}));
+    softplus = truth(p[7]);
+    sigmoid = truth(p[8]);
+    normalize = truth(p[9]);
+    scale = p[10] == Py_None ? 1.f / sqrtf((float)q.d) : number(p[10], "scale");
+  }
+  std::array<int64_t, 4> state_shape() const { return {v.B, v.H, q.d, v.d}; }
+};
+
+// q, k, v, dt, a, beta, dt_bias, softplus, sigmoid, normalize, scale, state, lengths, out,
+// return_state, stream
+PyObject* gated_delta(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  LA_PY_ENTRY(16)
+  Call call(tensor(a[0], "q"), "q");
+  const DeltaCall s(call, a, 4);
+  const auto state_shape = s.state_shape();
+  const auto* state = static_cast<const float*>(call.dense(a[11], "state", at::kFloat, state_shape));
+  const auto* lens = static_cast<const int32_t*>(call.dense(a[12], "lengths", at::kInt, {s.v.B}));
+  const int want = truth(a[14]);
+  const Grads grads(a, n);
+  grads.out(a[13]);
+  call.use(a[15]);
+  at::Tensor made, after;
+  if (a[13] == Py_None) made = call.empty({s.v.B, s.v.n, s.v.H, s.v.d}, call.type);
+  la_heads out = call.heads(a[13] == Py_None ? made : tensor(a[13], "out"), "out", 4);
+  if (want) after = call.empty(state_shape, at::kFloat);
+  done("la_gated_delta", unlocked([&] {
+         return p_delta(&s.q, &s.k, &s.v, &s.dt, s.a, &s.beta, s.bias, s.softplus, s.sigmoid,
+                        s.normalize, s.scale, state, lens, &out,
+                        want ? static_cast<float*>(after.data_ptr()) : nullptr, call.stream);
+       }));
+  grads.written(a[13]);
+  PyObject* r = wrap(a[13], std::move(made));
+  return grads.result("gated_delta", want && r ? pair(r, std::move(after)) : r);
+  LA_PY_END
+}
+
+// state, q, k, v, dt, a, beta, dt_bias, softplus, sigmoid, normalize, scale, out, stream
+PyObject* gated_delta_step(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  LA_PY_ENTRY(14)
+  Call call(tensor(a[1], "q"), "q");
+  const DeltaCall s(call, a + 1, 3);
+  tensor(a[0], "state");
+  auto* state = static_cast<float*>(call.dense(a[0], "state", at::kFloat, s.state_shape()));
+  const Grads grads(a, n);
+  grads.out(a[12]);
+  grads.in_place(a[0], "state");
+  call.use(a[13]);
+  at::Tensor made;
+  if (a[12] == Py_None) made = call.empty({s.v.B, s.v.H, s.v.d}, call.type);
+  la_heads out = call.heads(a[12] == Py_None ? made : tensor(a[12], "out"), "out", 3);
+  done("la_gated_delta_step", unlocked([&] {
+         return p_delta_step(state, &s.q, &s.k, &s.v, &s.dt, s.a, &s.beta, s.bias, s.softplus,
+                             s.sigmoid, s.normalize, s.scale, &out, call.stream);
+       }));
+  grads.written(a[0]);
+  grads.written(a[12]);
+  return grads.result("gated_delta_step", wrap(a[12], std::move(made)));
+  LA_PY_END
+}
+
+// x, weight, group, eps, gate, residual, quantize, out, sum_out, stream
+PyObject* rms_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  LA_PY_ENTRY(10)
+  const at::Tensor& x = tensor(a[0], "x");
+  Call call(x);
+  const la_rows xr = call.matrix(x, "x");
+  int64_t group = xr.d;
+  const void* weight = nullptr;
+  if (a[2] != Py_None) {
+    group = PyLong_AsLongLong(a[2]);
+    if (PyErr_Occurred()) throw Raised{};
+  }
+  if (a[1] != Py_None) {
+    const at::Tensor& w = tensor(a[1], "weight");
+    if (w.dim() != 1) raise(PyExc_ValueError, "weight must have one axis");
+    if (a[2] == Py_None) group = w.size(0);
+    weight = call.dense(a[1], "weight", call.type, {group});
+  }
+  if (group < 1 || xr.d % group)
+    raise(PyExc_ValueError, "x's last axis must be a multiple of the norm's group (%lld)", (long long)group);
+  const float eps = number(a[3], "eps");
+  la_rows rows[4];   // gate, residual, sum, out
+  auto like_x = [&](PyObject* o, const char* name, la_rows* to) {
+    if (o == Py_None) return false;
+    const at::Tensor& t = tensor(o, name);
+    if (t.sizes() != x.sizes())
+      raise(PyExc_ValueError, "%s must have the shape %s", name, c10::str(x.sizes()).c_str());
+    *to = call.matrix(t, name);
+    return true;
+  };
+  const bool gated = like_x(a[4], "gate", rows), added = like_x(a[5], "residual", rows + 1);
+  const bool quantize = truth(a[6]);
+  const Grads grads(a, n);
+  grads.out(a[7]);
+  grads.out(a[8]);
+  if (a[8] != Py_None && !added) raise(PyExc_ValueError, "sum_out needs a residual");
+  call.use(a[9]);
+  at::Tensor made, scale, sum;
+  if (a[7] == Py_None) made = call.empty(x.sizes(), quantize ? at::kFloat8_e4m3fn : call.type);
+  const at::Tensor& out = a[7] == Py_None ? made : tensor(a[7], "out");
+  if (out.sizes() != x.sizes())
+    raise(PyExc_ValueError, "out must have the shape %s", c10::str(x.sizes()).c_str());
+  rows[3] = quantize ? call.matrix(out, "out", at::kFloat8_e4m3fn, LA_E4M3) : call.matrix(out, "out");
+  if (quantize) scale = call.empty(x.sizes().slice(0, x.dim() - 1), at::kFloat);
+  if (added && !like_x(a[8], "sum_out", rows + 2)) {
+    sum = call.empty(x.sizes(), call.type);
+    rows[2] = call.matrix(sum, "sum_out");
+  }
+  done("la_rms_norm", unlocked([&] {
+         return p_norm(&xr, weight, group, eps, added ? rows + 1 : nullptr, gated ? rows : nullptr,
+                       rows + 3, quantize ? static_cast<float*>(scale.data_ptr()) : nullptr,
+                       added ? rows + 2 : nullptr, call.stream);
+       }));
+  grads.written(a[7]);
+  grads.written(a[8]);
+  PyObject* r[3] = {wrap(a[7], std::move(made)), nullptr, nullptr};
+  int count = 1;
+  if (quantize) r[count++] = THPVariable_Wrap(std::move(scale));
+  if (added) r[count++] = wrap(a[8], std::move(sum));
+  bool ok = true;
+  for (int i = 0; i < count; ++i) ok = ok && r[i];
+  PyObject* all = !ok ? nullptr : count == 1 ? Py_NewRef(r[0]) : PyTuple_New(count);
+  for (int i = 0; i < count; ++i) {
+    if (all && count > 1)
+      PyTuple_SET_ITEM(all, i, r[i]);
+    else
+      Py_XDECREF(r[i]);
+  }
+  return grads.result("rms_norm", all);
+  LA_PY_END
+}
+
+// x, x_scale, weight, weight_scale, bias, activation, residual, out, stream
+PyObject* linear_e4m3(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  LA_PY_ENTRY(9)
+  const at::Tensor& x = tensor(a[0], "x");
+  Call call(x, at::kBFloat16);
+  const la_activation act = activation(a[5]);
+  const la_rows xr = call.matrix(x, "x", at::kFloat8_e4m3fn, LA_E4M3);
+  tensor(a[1], "x_scale");
+  const auto* xs = static_cast<const float*>(
+      call.dense(a[1], "x_scale", at::kFloat, x.sizes().slice(0, x.dim() - 1)));
+  const at::Tensor& w = tensor(a[2], "weight");
+  if (w.dim() != 2) raise(PyExc_ValueError, "weight must be an [N, K] tensor");
+  const la_rows wr = call.matrix(w, "weight", at::kFloat8_e4m3fn, LA_E4M3);
+  tensor(a[3], "weight_scale");
+  const auto* ws = static_cast<const float*>(call.dense(a[3], "weight_scale", at::kFloat, {wr.n}));
+  c10::SmallVector<int64_t, 5> shape(x.sizes().begin(), x.sizes().end());
+  shape.back() = wr.n;
+  const void* bias = call.dense(a[4], "bias", call.type, {wr.n});
+  la_rows rr{};
+  const bool has_res = a[6] != Py_None;
+  if (has_res) {
+    const at::Tensor& r = tensor(a[6], "residual");
+    if (r.sizes() != at::IntArrayRef(shape))
+      raise(PyExc_ValueError, "residual must have the shape %s", c10::str(at::IntArrayRef(shape)).c_str());
+    rr = call.matrix(r, "residual");
+  }
+  const Grads grads(a, n);
+  grads.out(a[7]);
+  call.use(a[8]);
+  at::Tensor made;
+  if (a[7] == Py_None)
+    made = call.empty(shape, call.type);
+  else if (tensor(a[7], "out").sizes() != at::IntArrayRef(shape))
+    raise(PyExc_ValueError, "out must have the shape %s", c10::str(at::IntArrayRef(shape)).c_str());
+  la_rows out = call.matrix(a[7] == Py_None ? made : tensor(a[7], "out"), "out");
+  done("la_linear_e4m3", unlocked([&] {
+         return p_linear8(&xr, xs, &wr, ws, bias, act, has_res ? &rr : nullptr, &out, call.stream);
+       }));
+  grads.written(a[7]);
+  return grads.result("linear_e4m3", wrap(a[7], std::move(made)));
+  LA_PY_END
+}
+
+// bind(fail, no_backward, addresses of the nine C functions in the order above)
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  if (n != 7) {
-    PyErr_SetString(PyExc_TypeError, "bind(fail, no_backward, five addresses)");
+  if (n != 11) {
+    PyErr_SetString(PyExc_TypeError, "bind(fail, no_backward, nine addresses)");
     return nullptr;
   }
-  void* p[5];
-  for (int i = 0; i < 5; ++i) {
+  void* p[9];
+  for (int i = 0; i < 9; ++i) {
     p[i] = PyLong_AsVoidPtr(a[i + 2]);
     if (PyErr_Occurred()) return nullptr;
   }
@@ -460,6 +705,10 @@ PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
   p_conv_step = reinterpret_cast<decltype(p_conv_step)>(p[2]);
   p_scan = reinterpret_cast<decltype(p_scan)>(p[3]);
   p_step = reinterpret_cast<decltype(p_step)>(p[4]);
+  p_delta = reinterpret_cast<decltype(p_delta)>(p[5]);
+  p_delta_step = reinterpret_cast<decltype(p_delta_step)>(p[6]);
+  p_norm = reinterpret_cast<decltype(p_norm)>(p[7]);
+  p_linear8 = reinterpret_cast<decltype(p_linear8)>(p[8]);
   Py_INCREF(a[0]);
   Py_XSETREF(g_fail, a[0]);
   Py_INCREF(a[1]);
@@ -471,6 +720,8 @@ PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
 PyMethodDef g_methods[] = {LA_PY_METHOD(bind),           LA_PY_METHOD(linear),
                            LA_PY_METHOD(causal_conv),    LA_PY_METHOD(causal_conv_step),
                            LA_PY_METHOD(selective_scan), LA_PY_METHOD(selective_step),
+                           LA_PY_METHOD(gated_delta),    LA_PY_METHOD(gated_delta_step),
+                           LA_PY_METHOD(rms_norm),       LA_PY_METHOD(linear_e4m3),
                            {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "la_block", nullptr, -1, g_methods,
                         nullptr, nullptr, nullptr, nullptr};

@@ -61,7 +61,7 @@ typedef enum {
                                access was skipped (see la_get_last_device_check) */
 } la_status;
 
-typedef enum { LA_BF16 = 0, LA_F32 = 1 } la_dtype;
+typedef enum { LA_BF16 = 0, LA_F32 = 1, LA_E4M3 = 2 /* la_rms_norm, la_linear_e4m3 alone */ } la_dtype;
 
 /* φ: elu(x)+1 ("Linear Transformer", d' = d) or Performer positive random
  * features ("Performer random features", d' = m). */
@@ -478,6 +478,107 @@ la_status la_selective_step(float* state, const la_rows* x, const la_rows* dt, c
                             int states, const la_rows* bm, const la_rows* cm, const float* skip,
                             const la_rows* gate, const float* dt_bias, int softplus,
                             la_rows* out, la_stream stream);
+
+/* ------------------------------------------------------------------------
+ * The operators of a gated delta-rule block, beside la_linear and
+ * la_causal_conv: the gated delta rule (the state of la_forward, decayed per
+ * token, with what a key already recalls taken away before a value is
+ * written: "Efficient Transformers II" eq (10) with a per token and v replaced
+ * by v − k·S), the norm around it, and the product of 8-bit operands.
+ *
+ * la_heads is a [B, n, H, d] view: element (b, t, h, c) at
+ * data[b·stride_b + t·stride_n + h·stride_h + c] (strides in elements).  The
+ * rules are those of la_rows, with stride_h·size a multiple of 16 bytes too.
+ * A [B, H, n, d] tensor is the same view with its strides exchanged.
+ * ------------------------------------------------------------------------ */
+typedef struct {
+  void* data;
+  la_dtype dtype;
+  int64_t B, n, H, d;
+  int64_t stride_b, stride_n, stride_h;
+} la_heads;
+
+/*
+ * la_gated_delta — the gated delta rule over a prompt.  For every batch entry
+ * b and value head h, with a state S [dk, dv] and the query and key head
+ * h·Hk/Hv (rounded down):
+ *   Δ_t = softplus(dt[b,t,h] + dt_bias[h])    (softplus only when asked for)
+ *   α_t = exp(Δ_t·a[h]),  β_t = sigmoid(beta[b,t,h])  (or beta as it is)
+ *   w_t = β_t·(v_t − k_t·(α_t·S_{t−1})),  S_t = α_t·S_{t−1} + k_tᵀ·w_t
+ *   out[b,t,h] = scale·q_t·S_t
+ * With normalize, q_t and k_t are divided by sqrt(Σ x² + 1e-6) first.
+ *   q, k       [B, n, Hk, dk], bf16 or fp32 (one dtype for all la_heads here).
+ *   v, out     [B, n, Hv, dv]; Hv is a multiple of Hk.  out is written in full.
+ *   dt, beta   [B, n, Hv] (la_rows), both of q's dtype or both fp32; here
+ *              strides and data need only be aligned to an element.
+ *   a          device fp32 [Hv], zero or negative (−∞ clears the state).
+ *   dt_bias    device fp32 [Hv], or NULL.
+ *   state_in   device fp32 [B, Hv, dk, dv] dense, or NULL for zeros.
+ *   lengths    device [B] int32, or NULL for n: tokens t ≥ lengths[b] are not
+ *              read, leave the state alone, and their outputs are 0 (values
+ *              are taken into [0, n]).
+ *   state_out  device fp32 [B, Hv, dk, dv] dense, or NULL.  Must not overlap
+ *              state_in.
+ * dk and dv are multiples of 8, dk ≤ 256, dv ≤ 512 (else LA_ERR_UNSUPPORTED).
+ * States, sums, norms and decays are fp32.  Equal inputs give equal bits.
+ * Errors as la_linear.
+ */
+la_status la_gated_delta(const la_heads* q, const la_heads* k, const la_heads* v,
+                         const la_rows* dt, const float* a, const la_rows* beta,
+                         const float* dt_bias, int softplus, int sigmoid, int normalize,
+                         float scale, const float* state_in, const int32_t* lengths,
+                         la_heads* out, float* state_out, la_stream stream);
+
+/*
+ * la_gated_delta_step — the rule's next token: state [B, Hv, dk, dv] fp32
+ * (dense) is updated in place; q, k [B, 1, Hk, dk], v, out [B, 1, Hv, dv],
+ * dt, beta [B, 1, Hv]; the rest as la_gated_delta.
+ */
+la_status la_gated_delta_step(float* state, const la_heads* q, const la_heads* k,
+                              const la_heads* v, const la_rows* dt, const float* a,
+                              const la_rows* beta, const float* dt_bias, int softplus,
+                              int sigmoid, int normalize, float scale, la_heads* out,
+                              la_stream stream);
+
+/*
+ * la_rms_norm — root-mean-square norm of rows, each in groups of `group`
+ * neighbouring features (group = D: one norm per row), after the residual's
+ * addition and before a gate:
+ *   h = x + residual;  y = h·rsqrt(mean over the group of h² + eps)·weight·silu(gate)
+ *   x         [1, M, D] (B = 1), bf16 or fp32; M ≥ 0.
+ *   weight    device [group], x's dtype, or NULL for ones; the same for every
+ *             group of a row.  D is a multiple of group.
+ *   residual  [1, M, D], x's dtype, or NULL.
+ *   gate      [1, M, D], x's dtype, or NULL (no gate).
+ *   out       [1, M, D], x's dtype, or LA_E4M3: y/s rounded to the nearest
+ *             8-bit value, s = max |y| of the row / 448 (at least 2^-126; 1
+ *             for a row of zeros).  Of x's dtype it may be the same view as x, residual or
+ *             gate.
+ *   scale     device fp32 [M]: s (needed with LA_E4M3, else NULL).
+ *   sum       [1, M, D], x's dtype, or NULL: h rounded to x's dtype (the norm
+ *             goes by h before this rounding).  Needs residual; may be the
+ *             same view as x or residual, not as out.
+ * group and D are multiples of 8 (bf16, or LA_E4M3 out) or 4 (fp32); strides
+ * of a LA_E4M3 out of 8 bytes.  Sums are fp32.  Equal inputs give equal bits.
+ * Errors as la_linear; LA_ERR_UNSUPPORTED for D above 65536 (bf16) or 32768.
+ */
+la_status la_rms_norm(const la_rows* x, const void* weight, int64_t group, float eps,
+                      const la_rows* residual, const la_rows* gate, la_rows* out, float* scale,
+                      la_rows* sum, la_stream stream);
+
+/*
+ * la_linear_e4m3 — la_linear on 8-bit operands with scales:
+ *   out[m,n] = act(x_scale[m]·weight_scale[n]·Σ_k x[m,k]·weight[n,k] + bias[n]) + residual[m,n]
+ *   x, weight       [1, M, K] and [1, N, K], LA_E4M3.
+ *   x_scale         device fp32 [M];  weight_scale  device fp32 [N].
+ *   bias, residual, out  as la_linear, bf16.
+ * K is a multiple of 16 and N of 8.  Products are exact and their sums fp32,
+ * as are the scales, bias, activation and residual; rounded once to bf16.
+ * Errors as la_linear.
+ */
+la_status la_linear_e4m3(const la_rows* x, const float* x_scale, const la_rows* weight,
+                         const float* weight_scale, const void* bias, la_activation activation,
+                         const la_rows* residual, la_rows* out, la_stream stream);
 
 /*
  * la_selftest_linear_kernel, la_selftest_step_kernel — test hooks: the name of the
