@@ -242,6 +242,7 @@ cudaError_t by_keys(const DeltaArgs& a, const DeltaParams& p, cudaStream_t s) {
 }  // namespace
 
 cudaError_t gated_delta(const DeltaArgs& a, cudaStream_t s) {
+  if (a.n >= 48 && tc_gated_delta_supported(a)) return tc_gated_delta(a, s);
   DeltaParams p{};
   p.q = a.q, p.k = a.k, p.v = a.v, p.out = a.out;
   p.dt = a.dt, p.beta = a.beta;

@@ -331,6 +331,13 @@ struct DeltaArgs {
   int num_sms;
 };
 cudaError_t gated_delta(const DeltaArgs& a, cudaStream_t stream);
+// In chunks of 64 tokens on the tensor cores (bf16), where the views and sizes allow it.
+bool tc_gated_delta_supported(const DeltaArgs& a);
+cudaError_t tc_gated_delta(const DeltaArgs& a, cudaStream_t stream);
+// A view as a 4-D tensor (d, H, n, B), box 64 × 1 × rows × 1, with the 128-byte
+// swizzle or without.
+cudaError_t tmap_heads(CUtensorMap* m, const Heads& v, int64_t B, int64_t n, int64_t H, int64_t d,
+                       int rows, bool swizzle);
 
 // out = norm(x + residual)·weight·silu(gate) over M rows of D features.
 struct NormArgs {

@@ -81,6 +81,25 @@ cudaError_t tmap_bytes(CUtensorMap* m, const void* base, int64_t rows, int64_t c
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
+cudaError_t tmap_heads(CUtensorMap* m, const Heads& v, int64_t B, int64_t n, int64_t H, int64_t d,
+                       int rows, bool swizzle) {
+  cudaError_t e = get_encoder();
+  if (e != cudaSuccess) return e;
+  // axes that are broadcast (or of extent 1) have one entry, at coordinate 0
+  cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)(v.sh ? H : 1), (cuuint64_t)n,
+                        (cuuint64_t)(v.sb ? B : 1)};
+  const cuuint64_t row = (cuuint64_t)d * 2;
+  cuuint64_t strides[3] = {v.sh ? (cuuint64_t)v.sh * 2 : row, v.sn ? (cuuint64_t)v.sn * 2 : row,
+                           v.sb ? (cuuint64_t)v.sb * 2 : row};
+  cuuint32_t box[4] = {64, 1, (cuuint32_t)rows, 1};
+  cuuint32_t es[4] = {1, 1, 1, 1};
+  CUresult r = g_encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(v.data), dims,
+                        strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
 cudaError_t tmap_f32_mats(CUtensorMap* m, const void* base, int64_t count, int D) {
   cudaError_t e = get_encoder();
   if (e != cudaSuccess) return e;
