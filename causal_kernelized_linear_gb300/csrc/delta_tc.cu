@@ -3,7 +3,7 @@
 // With b_i = Σ_{t≤i} log α_t within a chunk, S the state before it, and k, q of
 // unit length (a factor r per row, so that the rows themselves stay bf16):
 //   A_ij = β_i (k_i·k_j) e^{b_i − b_j} for j < i,   T = (1 + A)^{-1}
-//   w    = T (β v − β e^b (k S))                      the chunk's corrected values
+//   w    = T β (v − e^b (k S))                        the chunk's corrected values
 //   o_i  = scale·(e^{b_i} q_i S + Σ_{j≤i} (q_i·k_j) e^{b_i − b_j} w_j)
 //   S'   = e^{b_C} S + Σ_j e^{b_C − b_j} k_jᵀ w_j
 // Every row and column factor is folded into T, P, w or the output, so q, k and
@@ -13,18 +13,22 @@
 // fp32 registers.  All products on the way of S are transposed, with v's columns
 // as the MMA's 128 rows and the chunk's tokens (or dk) as its columns: Sᵀ, (kS)ᵀ
 // and wᵀ are then A operands in tensor memory, and their conversions never cross
-// lanes.  A chunk is three dependent products: (kS)ᵀ = Sᵀkᵀ, wᵀ = vᵀT1ᵀ +
-// (kS)ᵀT2ᵀ, and wᵀk for the new state; everything else (the gram matrix and the
+// lanes.  A chunk is three dependent products: (kS)ᵀ = Sᵀkᵀ, wᵀ = (vᵀ −
+// (kS)ᵀe^b)(Tβ)ᵀ, and wᵀk for the new state; everything else (the gram matrix and the
 // inverse of the chunk after next, the output) runs beside them.
 //
-// Rounding.  The state, sums, decays, A and T are fp32.  As MMA operands S, kS,
-// T and w are split into two bf16 parts (2^-16 of a value is lost), so that the
-// state stays within about 1e-5 of itself however long the sequence.  What only
-// the output is made of (S in q·S, P, w in P·w) is rounded to bf16 once, as the
-// output is.
+// Rounding.  The state, sums, decays, A and T are fp32.  As MMA operands S, kS and w
+// are split into two bf16 parts (2^-16 of a value is lost) and T into three (2^-24),
+// which keeps the state within about 3e-6 of itself however long the sequence (4e-6
+// with two parts of T, 1e-6 with three of w as well, whose products would take 256
+// more of a chunk's cycles on the tensor cores).  P and the output's w are rounded
+// to bf16 once, as the output is.
 //
-// Roles: warps 0-7 S (two per quarter of the rows), 8-11 the chunk's T and P,
-// 12-15 the output, 16 loads, 17 MMAs (18 and 19 complete a warpgroup).
+// Roles: warps 0-7 S (two per quarter of the rows), 8-11 and 12-15 T and P of every
+// other chunk, 16-19 the output, 20 loads, 21 MMAs, 22 and 23 decays and lengths.  Their loops
+// are kept rolled where they can be: five roles at once run from one instruction
+// cache, and unrolled throughout the kernel spent twice as long on fetching as on
+// issuing (4×4096 tokens of 32 heads in 490 µs).
 #include "block.cuh"
 #include "internal.h"
 #include "tc_pair.cuh"
@@ -41,28 +45,35 @@ using namespace tc;
 using bf16 = __nv_bfloat16;
 
 constexpr int kC = 64;                        // tokens of a chunk
-constexpr int kThreads = 20 * 32;
-constexpr int kStateWarps = 8, kPrepWarp = 8, kOutWarp = 12, kLoadWarp = 16, kMmaWarp = 17;
-constexpr int kKQ = 3, kVS = 2, kTok = 4;     // stages: k and q tiles, v tiles, token factors
+constexpr int kThreads = 24 * 32;
+constexpr int kStateWarps = 8, kPrepWarp = 8, kOutWarp = 16, kLoadWarp = 20, kMmaWarp = 21, kFactorWarp = 22;
+constexpr int kKQ = 3, kVS = 2, kTok = 3, kPS = 2;   // stages: k and q tiles, v tiles, token factors, P
+constexpr int kOutRows = 32;                  // tokens that are stored at once
 constexpr int kSlab = kC * 128;               // 8 KB: 64 tokens × 64 features
 constexpr int kAPitch = 68;                   // floats of a row of A
 
 // Named barriers.
-constexpr uint32_t kBarPrep = 1, kBarOut = 2;
+constexpr uint32_t kBarOut = 1, kBarPrep = 2;   // and 3
 
-struct TokenFactors {
-  float4 pair[kC];      // b (two parts, log2), r_k; the factors of a column of A and P
+struct alignas(16) TokenFactors {
+  // Row i's b and column j's b − log2 r_k, each in two parts: e^{b_i − b_j} r_j is one
+  // exponential of their difference.
+  float bx[kC], by[kC], cx[kC], cy[kC];
+  float far[kC];        // what rows from 32 on make of columns below: e^{b − b_31}, r_k e^{b_31 − b}
+  float a[kC], q[kC];   // β r_k, scale r_q: a row of A, of P
+  float beta[kC];       // a column of T
+  float ks[kC];         // −e^b r_k: a row of k·S
   float left[kC];       // r_k e^{b_C − b}: a row of w for the state
   float out[kC];        // scale r_q e^b: a row of q·S
-  float t1[kC], t2[kC]; // β and −β e^b r_k: a column of T
   float carry;          // e^{b_C}
 };
 
 struct Bars {
-  uint64_t kq_full[kKQ], kq_empty[kKQ], v_full[kVS], v_empty[kVS];
+  uint64_t kq_full[kKQ], kq_empty[kKQ], v_full[kVS], v_empty[kVS], f_ready[kTok];
+  uint64_t g_full[2], w_full[2];              // by the chunk's parity: each prep warpgroup sees every other one
   uint64_t kq_clean, v_clean;                 // the last chunk's rows past the length are zero
-  uint64_t g_full, g_empty, t_ready, s_ready, ks_full, ks_ready, qs_full, qs_read, w_full, w_ready,
-      upd_full, pv_full, done;
+  uint64_t g_empty, t_ready, s_ready, ks_full, ks_ready, qs_full, qs_read, w_ready,
+      upd_full, pv_full, pv_read, done;
   uint32_t tmem;
   int abort;
   int kq_issued, v_issued;                    // loads
@@ -72,11 +83,11 @@ template <int DK> struct Cfg {
   static constexpr int kSlabs = DK / 64;
   static constexpr int kStage = 2 * kSlabs * kSlab;          // k and q: per 64 features, k's rows, then q's
   static constexpr int oV = kKQ * kStage;
-  static constexpr int oT = oV + kVS * 2 * kSlab;            // T1 hi, lo, T2 hi, lo
-  static constexpr int oP = oT + 4 * kSlab;                  // two
-  static constexpr int oOut = oP + 2 * kSlab;
-  static constexpr int oA = oOut + 2 * kSlab;
-  static constexpr int oTok = oA + kC * kAPitch * 4;
+  static constexpr int oT = oV + kVS * 2 * kSlab;            // Tβ in three parts
+  static constexpr int oP = oT + 3 * kSlab;
+  static constexpr int oOut = oP + kPS * kSlab;              // kOutRows tokens, by 64 columns
+  static constexpr int oA = oOut + 2 * kOutRows * 128;
+  static constexpr int oTok = oA + 2 * kC * kAPitch * 4;     // of each prep warpgroup
   static constexpr int oBars = oTok + kTok * (int)sizeof(TokenFactors);
   static constexpr int kSmem = 1024 + oBars + (int)sizeof(Bars);
   static_assert(kSmem <= 227 * 1024, "shared memory of a CTA");
@@ -103,9 +114,22 @@ struct TcParams {
 };
 
 // A pair of fp32 as two bf16 parts each: hi keeps the leading 8 bits, lo the next 8.
-__device__ __forceinline__ void split2(float x, float y, uint32_t& hi, uint32_t& lo) {
+// Returns what hi leaves.
+__device__ __forceinline__ f32x2 split1(f32x2 v, uint32_t& hi) {
+  float x, y;
+  unpack2(v, x, y);
   hi = pack_bf16x2(x, y);
-  lo = pack_bf16x2(x - bf16lo_to_f32(hi), y - bf16hi_to_f32(hi));
+  return fma2(pack2(bf16lo_to_f32(hi), bf16hi_to_f32(hi)), pack2(-1.f, -1.f), v);
+}
+__device__ __forceinline__ void split2(f32x2 v, uint32_t& hi, uint32_t& lo) {
+  float x, y;
+  unpack2(split1(v, hi), x, y);
+  lo = pack_bf16x2(x, y);
+}
+
+// The same with a third part, which keeps the next 8.
+__device__ __forceinline__ void split3(f32x2 v, uint32_t& hi, uint32_t& mid, uint32_t& lo) {
+  split2(split1(v, hi), mid, lo);
 }
 
 // 32 lanes × 8 consecutive columns store (thread i writes lane lane_base + i).
@@ -116,20 +140,38 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t* r) {
       : "memory");
 }
 
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t* r) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+                 "=r"(r[7])
+               : "r"(taddr));
+}
+
+// Two neighbours of what was loaded, as a pair of fp32.
+__device__ __forceinline__ f32x2 pair_of(const uint32_t* r, int i) {
+  return pack2(__uint_as_float(r[i]), __uint_as_float(r[i + 1]));
+}
+
 // The sum of two values that are kept in two parts each.
 __device__ __forceinline__ float2 add_parts(float2 a, float2 b) {
   const float s = a.x + b.x, t = s - a.x;
   return make_float2(s, a.y + b.y + ((a.x - (s - t)) + (b.x - t)));
 }
 
-__device__ __forceinline__ float gate_value(const Rows& r, bool f32, int64_t at) {
-  return f32 ? static_cast<const float*>(r.data)[at] : to_f32(static_cast<const bf16*>(r.data)[at]);
+// A step size or strength as it is in memory, and its value: a load that is used a
+// chunk later, and nothing before that would wait for it.
+__device__ __forceinline__ uint32_t gate_bits(const Rows& r, bool f32, int64_t at) {
+  return f32 ? static_cast<const uint32_t*>(r.data)[at] : static_cast<const uint16_t*>(r.data)[at];
+}
+__device__ __forceinline__ float gate_value(uint32_t bits, bool f32) {
+  return __uint_as_float(f32 ? bits : bits << 16);
 }
 
-// Registers of a thread by role: at launch all have 96, and a warpgroup's share is
-// moved where S is held: 2·120 + 104 + 64 + 72 = 5·96 (dk 128), 2·96 + 104 + 64 + 96.
+// Registers of a thread by role: at launch all have 80, and a warpgroup's share is
+// moved where S is held: 2·120 + 2·64 + 56 + 56 = 6·80
+// (dk 128), 2·112 + 2·72 + 48 + 64.
 template <int N> __device__ __forceinline__ void take_registers() {
-  if constexpr (N > 96)
+  if constexpr (N > 80)
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
   else
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
@@ -144,39 +186,32 @@ struct Ctx {
   bool partial;           // rows of the last chunk lie past the length
 };
 
-// mbar_wait and mbar_wait_drain in line: the compiler refuses calls beside setmaxnreg.
-__device__ __forceinline__ bool wait_in_line(uint64_t* bar, uint32_t parity, int* status,
-                                             volatile int* abort) {
-  if (mbar_try_wait(bar, parity)) return true;
-  const uint64_t t0 = global_timer_ns();
-  for (uint32_t it = 1; !mbar_try_wait(bar, parity); ++it) {
-    if (it % 8) continue;
-    if (*abort) return false;
-    if (global_timer_ns() - t0 > 2000000000ull) {
-      if (status) atomicCAS(status, 0, kStatusTimeout);
+// mbar_wait and mbar_wait_drain in line, since the compiler refuses calls beside
+// setmaxnreg, and in few instructions: the bound is a number of tests, each of up
+// to a microsecond, and the kernel's end reports the timeout.
+constexpr uint32_t kTests = 4000000;
+__device__ __forceinline__ bool wait_in_line(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  uint32_t n = 0;
+  while (!mbar_try_wait(bar, parity))
+    if (*abort || ++n > kTests) {
       *abort = 1;
       return false;
     }
-  }
   return true;
 }
-__device__ __forceinline__ bool warp_wait_in_line(uint64_t* bar, uint32_t parity, int* status,
-                                                  volatile int* abort) {
-  return __all_sync(0xffffffffu, wait_in_line(bar, parity, status, abort));
+__device__ __forceinline__ bool warp_wait_in_line(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  return __all_sync(0xffffffffu, wait_in_line(bar, parity, abort));
 }
-
 __device__ __forceinline__ void drain_in_line(uint64_t* bar, uint32_t parity) {
-  const uint64_t t0 = global_timer_ns();
-  for (uint32_t it = 1; !mbar_try_wait(bar, parity); ++it)
-    if (it % 8 == 0 && global_timer_ns() - t0 > 500000000ull) return;
+  for (uint32_t n = 0; n < kTests / 4 && !mbar_try_wait(bar, parity); ++n) {}
 }
 
 // A role that shares no barrier with other warps returns where a wait gives up;
 // the others (LA_GO_ON) walk on through their remaining barriers, whose waits then
 // end at once: what they write stays within their own buffers and the output.
 #define LA_WAIT(bar, parity) \
-  if (!warp_wait_in_line(&x.bars->bar, (parity) & 1, p.status, abort)) return
-#define LA_GO_ON(bar, parity) warp_wait_in_line(&x.bars->bar, (parity) & 1, p.status, abort)
+  if (!warp_wait_in_line(&x.bars->bar, (parity) & 1, abort)) return
+#define LA_GO_ON(bar, parity) warp_wait_in_line(&x.bars->bar, (parity) & 1, abort)
 
 // ------------------------------------------------------------------ loads
 
@@ -231,7 +266,7 @@ __device__ __forceinline__ void role_load(const Ctx& x, const TcParams& p, const
 
 // ------------------------------------------------------------------ products
 
-// (one thread)
+// (whole warp; one thread issues)
 template <int DK>
 __device__ __forceinline__ void role_mma(const Ctx& x, const TcParams& p) {
   using F = Cfg<DK>;
@@ -241,88 +276,108 @@ __device__ __forceinline__ void role_mma(const Ctx& x, const TcParams& p) {
   constexpr uint32_t id_nn = idesc_bf16_f32(128, kC, false, false);   // K-major A and B, 64 columns
   constexpr uint32_t id_v = idesc_bf16_f32(128, kC, true, false);     // vᵀ from [token][column]
   constexpr uint32_t id_upd = idesc_bf16_f32(128, DK, false, true);   // k as [token][feature]
-  constexpr int KD = DK / 16;
   const uint64_t dT = smem_desc(base + F::oT, 16, 1024, kSwizzle128B);
-  // K-step k of a tile with 64 features per slab
-  auto kstep = [](int k) { return (uint32_t)((k >> 2) * 2 * kSlab + (k & 3) * 32); };
   // K-step k of (kS)ᵀ or wᵀ: 32 tokens' hi parts, then their lo parts
   auto tokens = [](int k) { return (uint32_t)((k >> 1) * 32 + (k & 1) * 8); };
-#define LA_MWAIT(bar, parity) \
-  if (!wait_in_line(&bars->bar, (parity) & 1, p.status, abort)) return
   auto gram = [&](int c) -> bool {   // [k; q]·kᵀ
-    if (!wait_in_line(&bars->kq_full[c % kKQ], (c / kKQ) & 1, p.status, abort)) return false;
-    if (x.partial && c == x.chunks - 1 && !wait_in_line(&bars->kq_clean, 0, p.status, abort)) return false;
-    if (c >= 1 && !wait_in_line(&bars->g_empty, (c - 1) & 1, p.status, abort)) return false;
+    if (!warp_wait_in_line(&bars->kq_full[c % kKQ], (c / kKQ) & 1, abort)) return false;
+    if (x.partial && c == x.chunks - 1 && !warp_wait_in_line(&bars->kq_clean, 0, abort)) return false;
+    if (c >= 1 && !warp_wait_in_line(&bars->g_empty, (c - 1) & 1, abort)) return false;
     tc_fence_after();
-    const uint64_t d = smem_desc(base + c % kKQ * F::kStage, 16, 1024, kSwizzle128B);
+    if (elect_one()) {
+      const uint64_t d = smem_desc(base + c % kKQ * F::kStage, 16, 1024, kSwizzle128B);
+#pragma unroll 1
+      for (int i = 0; i < F::kSlabs; ++i)
 #pragma unroll
-    for (int k = 0; k < KD; ++k)
-      mma_ss(tmem + F::G, desc_at(d, kstep(k)), desc_at(d, kstep(k)), id_nn, k > 0);
-    mma_commit(&bars->g_full);
+        for (int k = 0; k < 4; ++k)
+          mma_ss(tmem + F::G, desc_at(d, i * 2 * kSlab + k * 32), desc_at(d, i * 2 * kSlab + k * 32), id_nn, i | k);
+      mma_commit(&bars->g_full[c & 1]);
+    }
+    __syncwarp();
     return true;
   };
+#pragma unroll 1
   for (int c = 0; c < 2 && c < x.chunks; ++c)
     if (!gram(c)) return;
+#pragma unroll 1
   for (int c = 0; c < x.chunks; ++c) {
     const uint32_t kq = base + c % kKQ * F::kStage;
-    const uint64_t dK = smem_desc(kq, 16, 1024, kSwizzle128B);
-    const uint64_t dQ = smem_desc(kq + kSlab, 16, 1024, kSwizzle128B);
-    const uint64_t dKt = smem_desc(kq, 2 * kSlab, 1024, kSwizzle128B);
-    const uint64_t dV = smem_desc(base + F::oV + c % kVS * 2 * kSlab, kSlab, 1024, kSwizzle128B);
-    const uint64_t dP = smem_desc(base + F::oP + c % 2 * kSlab, 16, 1024, kSwizzle128B);
-    // wᵀ = vᵀ T1ᵀ
-    LA_MWAIT(t_ready, c);
-    LA_MWAIT(v_full[c % kVS], c / kVS);
-    if (x.partial && c == x.chunks - 1) LA_MWAIT(v_clean, 0);
+    // (kS)ᵀ = Sᵀ kᵀ
+    LA_WAIT(s_ready, c);
     tc_fence_after();
+    auto of_state = [&](uint32_t to, uint64_t d) {   // S's hi parts, its lo parts
+#pragma unroll 1
+      for (int i = 0; i < 2 * F::kSlabs; ++i) {
+        const uint64_t di = desc_at(d, i % F::kSlabs * 2 * kSlab);
+        const uint32_t from = tmem + F::SH + i * 32;
 #pragma unroll
-    for (int part = 0; part < 2; ++part)
-#pragma unroll
-      for (int k = 0; k < kC / 16; ++k)
-        mma_ss(tmem + F::W, desc_at(dV, k * 2048), desc_at(dT, part * kSlab + k * 32), id_v, part | k);
-    mma_commit(&bars->v_empty[c % kVS]);
-    // (kS)ᵀ = Sᵀ kᵀ, and (qS)ᵀ
-    LA_MWAIT(s_ready, c);
+        for (int k = 0; k < 4; ++k) mma_ts(to, from + k * 8, desc_at(di, k * 32), id_nn, i | k);
+      }
+    };
+    if (elect_one()) {
+      of_state(tmem + F::KS, smem_desc(kq, 16, 1024, kSwizzle128B));
+      mma_commit(&bars->ks_full);
+    }
+    __syncwarp();
+    // wᵀ = vᵀ (Tβ)ᵀ; its columns are free since S is there, which waited for (P w)ᵀ
+    LA_WAIT(t_ready, c);
+    LA_WAIT(v_full[c % kVS], c / kVS);
+    if (x.partial && c == x.chunks - 1) LA_WAIT(v_clean, 0);
     tc_fence_after();
+    if (elect_one()) {
+      const uint64_t dV = smem_desc(base + F::oV + c % kVS * 2 * kSlab, kSlab, 1024, kSwizzle128B);
+#pragma unroll 1
+      for (int part = 0; part < 3; ++part)
 #pragma unroll
-    for (int part = 0; part < 2; ++part)
-#pragma unroll
-      for (int k = 0; k < KD; ++k)
-        mma_ts(tmem + F::KS, tmem + (part ? F::SL : F::SH) + k * 8, desc_at(dK, kstep(k)), id_nn, part | k);
-    mma_commit(&bars->ks_full);
-#pragma unroll
-    for (int k = 0; k < KD; ++k)
-      mma_ts(tmem + F::UPD, tmem + F::SH + k * 8, desc_at(dQ, kstep(k)), id_nn, k > 0);
-    mma_commit(&bars->qs_full);
-    // wᵀ += (kS)ᵀ T2ᵀ
-    LA_MWAIT(ks_ready, c);
+        for (int k = 0; k < kC / 16; ++k)
+          mma_ss(tmem + F::W, desc_at(dV, k * 2048), desc_at(dT, part * kSlab + k * 32), id_v, part | k);
+      mma_commit(&bars->v_empty[c % kVS]);
+    }
+    __syncwarp();
+    // wᵀ −= (e^b kS)ᵀ (Tβ)ᵀ, and (qS)ᵀ
+    LA_WAIT(ks_ready, c);
+    if (c >= 1) LA_WAIT(pv_read, c - 1);
     tc_fence_after();
+    if (elect_one()) {
+#pragma unroll 1
+      for (int part = 0; part < 3; ++part) {   // hi·hi, hi·mid, lo·hi
+        const uint32_t from = tmem + F::KS + (part == 2 ? 16 : 0);
+        const uint64_t d = desc_at(dT, part == 1 ? kSlab : 0);
 #pragma unroll
-    for (int part = 0; part < 3; ++part)   // hi·hi, hi·lo, lo·hi
-#pragma unroll
-      for (int k = 0; k < kC / 16; ++k)
-        mma_ts(tmem + F::W, tmem + F::KS + tokens(k) + (part == 2 ? 16 : 0),
-               desc_at(dT, (part == 1 ? 3 : 2) * kSlab + k * 32), id_nn, 1);
-    mma_commit(&bars->w_full);
-    if (c + 2 < x.chunks && !gram(c + 2)) return;
+        for (int k = 0; k < kC / 16; ++k) mma_ts(tmem + F::W, from + tokens(k), desc_at(d, k * 32), id_nn, 1);
+      }
+      mma_commit(&bars->w_full[c & 1]);
+      of_state(tmem + F::PV, smem_desc(kq + kSlab, 16, 1024, kSwizzle128B));
+      mma_commit(&bars->qs_full);
+    }
+    __syncwarp();
     // the state's wᵀk
-    LA_MWAIT(w_ready, c);
-    LA_MWAIT(qs_read, c);
+    LA_WAIT(w_ready, c);
     tc_fence_after();
+    if (elect_one()) {
+      const uint64_t dKt = smem_desc(kq, 2 * kSlab, 1024, kSwizzle128B);
+#pragma unroll 1
+      for (int part = 0; part < 2; ++part)
 #pragma unroll
-    for (int part = 0; part < 2; ++part)
+        for (int k = 0; k < kC / 16; ++k)
+          mma_ts(tmem + F::UPD, tmem + F::KS + part * 16 + tokens(k), desc_at(dKt, k * 2048), id_upd, part | k);
+      mma_commit(&bars->upd_full);
+    }
+    __syncwarp();
+    // (P w)ᵀ on top of what the output's warps have put there
+    LA_WAIT(qs_read, c);
+    tc_fence_after();
+    if (elect_one()) {
+      const uint64_t dP = smem_desc(base + F::oP + c % kPS * kSlab, 16, 1024, kSwizzle128B);
 #pragma unroll
       for (int k = 0; k < kC / 16; ++k)
-        mma_ts(tmem + F::UPD, tmem + F::KS + tokens(k) + part * 16, desc_at(dKt, k * 2048), id_upd, part | k);
-    mma_commit(&bars->upd_full);
-    mma_commit(&bars->kq_empty[c % kKQ]);
-    // (P w)ᵀ on top of what the output's warps have put there
-#pragma unroll
-    for (int k = 0; k < kC / 16; ++k)
-      mma_ts(tmem + F::PV, tmem + F::SL + k * 8, desc_at(dP, k * 32), id_nn, 1);
-    mma_commit(&bars->pv_full);
+        mma_ts(tmem + F::PV, tmem + F::W + (k >> 1) * 32 + (k & 1) * 8, desc_at(dP, k * 32), id_nn, 1);
+      mma_commit(&bars->pv_full);
+      mma_commit(&bars->kq_empty[c % kKQ]);   // and the chunk's factors
+    }
+    __syncwarp();
+    if (c + 2 < x.chunks && !gram(c + 2)) return;
   }
-#undef LA_MWAIT
 }
 
 // ------------------------------------------------------------------ the state
@@ -338,17 +393,37 @@ __device__ __forceinline__ void role_state(const Ctx& x, const TcParams& p, int 
   const uint32_t at = tmem_addr(x.tmem, warp % 4 * 32, 0);
   const int col = x.tile * 128 + warp % 4 * 32 + lane;
   const int64_t head = (int64_t)x.b * p.Hv + x.h;
-  float S[kCols];
+  // between global memory and S by way of the columns of the update, so that these
+  // loops stay small
+  const uint32_t mine = at + F::UPD + k0;
+  const int64_t first = (head * p.dk + k0) * p.dv + col;
+  const int rows = min(kCols, p.dk - k0);   // multiples of 8
+#pragma unroll 1
+  for (int i = 0; i < kCols; i += 8) {
+    uint32_t r[8] = {};
+    if (p.state_in && col < p.dv && i < rows)
 #pragma unroll
-  for (int i = 0; i < kCols; ++i)
-    S[i] = p.state_in && col < p.dv && k0 + i < p.dk ? p.state_in[(head * p.dk + k0 + i) * p.dv + col] : 0.f;
+      for (int j = 0; j < 8; ++j) r[j] = __float_as_uint(p.state_in[first + (int64_t)(i + j) * p.dv]);
+    __syncwarp();
+    tmem_st8(mine + i, r);
+  }
+  tmem_st_wait();
+  f32x2 S[kCols / 2];
+#pragma unroll
+  for (int j = 0; j < kCols; j += 32) {
+    uint32_t r[32];
+    tmem_ld32(mine + j, r);
+    tmem_ld_wait();
+#pragma unroll
+    for (int i = 0; i < 16; ++i) S[j / 2 + i] = pair_of(r, 2 * i);
+  }
 
   auto publish = [&] {   // S as the next products' operand
 #pragma unroll
     for (int j = 0; j < kCols; j += 16) {
       uint32_t hi[8], lo[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) split2(S[j + 2 * i], S[j + 2 * i + 1], hi[i], lo[i]);
+      for (int i = 0; i < 8; ++i) split2(S[j / 2 + i], hi[i], lo[i]);
       tmem_st8(at + F::SH + (k0 + j) / 2, hi);
       tmem_st8(at + F::SL + (k0 + j) / 2, lo);
     }
@@ -357,9 +432,11 @@ __device__ __forceinline__ void role_state(const Ctx& x, const TcParams& p, int 
     __syncwarp();
     if (lane == 0) mbar_arrive(&bars->s_ready);
   };
-  if (x.chunks) publish();
+#pragma unroll 1
   for (int c = 0; c < x.chunks; ++c) {
-    const TokenFactors& tok = x.tok[c % kTok];
+    publish();
+    const TokenFactors& tok = x.tok[c % kTok];   // overwritten after the chunk's last product
+    LA_WAIT(f_ready[c % kTok], c / kTok);
     LA_WAIT(ks_full, c);
     tc_fence_after();
     {
@@ -370,8 +447,11 @@ __device__ __forceinline__ void role_state(const Ctx& x, const TcParams& p, int 
       for (int j = 0; j < 16; j += 8) {
         uint32_t hi[8], lo[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          split2(__uint_as_float(r[2 * (j + i)]), __uint_as_float(r[2 * (j + i) + 1]), hi[i], lo[i]);
+        for (int i = 0; i < 8; i += 2) {
+          const ulonglong2 f = *reinterpret_cast<const ulonglong2*>(&tok.ks[half * 32 + 2 * (j + i)]);
+          split2(mul2(pair_of(r, 2 * (j + i)), f.x), hi[i], lo[i]);
+          split2(mul2(pair_of(r, 2 * (j + i) + 2), f.y), hi[i + 1], lo[i + 1]);
+        }
         tmem_st8(at + F::KS + half * 32 + j, hi);
         tmem_st8(at + F::KS + half * 32 + 16 + j, lo);
       }
@@ -380,8 +460,9 @@ __device__ __forceinline__ void role_state(const Ctx& x, const TcParams& p, int 
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars->ks_ready);
     }
-    LA_WAIT(w_full, c);
+    LA_WAIT(w_full[c & 1], c / 2);
     tc_fence_after();
+    const f32x2 carry = pack2(tok.carry, tok.carry);
     {
       uint32_t r[32];
       tmem_ld32(at + F::W + half * 32, r);
@@ -392,13 +473,12 @@ __device__ __forceinline__ void role_state(const Ctx& x, const TcParams& p, int 
 #pragma unroll
         for (int i = 0; i < 8; ++i)
           hi[i] = pack_bf16x2(__uint_as_float(r[2 * (j + i)]), __uint_as_float(r[2 * (j + i) + 1]));
-        tmem_st8(at + F::SL + half * 16 + j, hi);   // for the output; (kS)ᵀ is done with S's lo parts
+        tmem_st8(at + F::W + half * 32 + j, hi);   // for the output
 #pragma unroll
         for (int i = 0; i < 8; i += 2) {
-          const uint32_t* v = r + 2 * (j + i);
-          const float4 f = *reinterpret_cast<const float4*>(&tok.left[half * 32 + 2 * (j + i)]);
-          split2(__uint_as_float(v[0]) * f.x, __uint_as_float(v[1]) * f.y, hi[i], lo[i]);
-          split2(__uint_as_float(v[2]) * f.z, __uint_as_float(v[3]) * f.w, hi[i + 1], lo[i + 1]);
+          const ulonglong2 f = *reinterpret_cast<const ulonglong2*>(&tok.left[half * 32 + 2 * (j + i)]);
+          split2(mul2(pair_of(r, 2 * (j + i)), f.x), hi[i], lo[i]);
+          split2(mul2(pair_of(r, 2 * (j + i) + 2), f.y), hi[i + 1], lo[i + 1]);
         }
         tmem_st8(at + F::KS + half * 32 + j, hi);
         tmem_st8(at + F::KS + half * 32 + 16 + j, lo);
@@ -408,7 +488,6 @@ __device__ __forceinline__ void role_state(const Ctx& x, const TcParams& p, int 
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars->w_ready);
     }
-    const float carry = tok.carry;
     LA_WAIT(upd_full, c);
     tc_fence_after();
 #pragma unroll
@@ -417,15 +496,32 @@ __device__ __forceinline__ void role_state(const Ctx& x, const TcParams& p, int 
       tmem_ld32(at + F::UPD + k0 + j, r);
       tmem_ld_wait();
 #pragma unroll
-      for (int i = 0; i < 32; ++i) S[j + i] = fmaf(S[j + i], carry, __uint_as_float(r[i]));
+      for (int i = 0; i < 16; ++i) S[j / 2 + i] = fma2(S[j / 2 + i], carry, pair_of(r, 2 * i));
     }
-    LA_WAIT(pv_full, c);   // done with w where S's lo parts go
-    if (c + 1 < x.chunks) publish();
+    LA_WAIT(pv_full, c);   // so that the next chunk's w may start
   }
-  if (p.state_out && col < p.dv) {
+  if (!p.state_out) return;
 #pragma unroll
-    for (int i = 0; i < kCols; ++i)
-      if (k0 + i < p.dk) p.state_out[(head * p.dk + k0 + i) * p.dv + col] = S[i];
+  for (int j = 0; j < kCols; j += 8) {
+    uint32_t r[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float lo, hi;
+      unpack2(S[j / 2 + i], lo, hi);
+      r[2 * i] = __float_as_uint(lo), r[2 * i + 1] = __float_as_uint(hi);
+    }
+    tmem_st8(mine + j, r);
+  }
+  tmem_st_wait();
+#pragma unroll 1
+  for (int i = 0; i < rows; i += 8) {
+    uint32_t r[8];
+    tmem_ld8(mine + i, r);
+    tmem_ld_wait();
+    if (col < p.dv)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) p.state_out[first + (int64_t)(i + j) * p.dv] = __uint_as_float(r[j]);
+    __syncwarp();
   }
 }
 
@@ -442,16 +538,18 @@ __device__ __forceinline__ void role_out(const Ctx& x, const TcParams& p, const 
   const int d = warp % 4 * 32 + lane;
   const bool lead = warp == kOutWarp && lane == 0;
   uint8_t* stage = x.sm + F::oOut;
-  const uint32_t mine = smem_u32(stage) + d / 64 * kSlab + d % 64 * 2;
+  const uint32_t mine = smem_u32(stage) + d / 64 * kOutRows * 128 + d % 64 * 2;
+#pragma unroll 1
   for (int c = 0; c < x.chunks; ++c) {
     const TokenFactors& tok = x.tok[c % kTok];
     // scale e^{b_i} q_i S is what P·w is added to
+    LA_GO_ON(f_ready[c % kTok], c / kTok);
     LA_GO_ON(qs_full, c);
     tc_fence_after();
-#pragma unroll
+#pragma unroll 1
     for (int j = 0; j < kC; j += 32) {
       uint32_t r[32];
-      tmem_ld32(at + F::UPD + j, r);
+      tmem_ld32(at + F::PV + j, r);
       tmem_ld_wait();
 #pragma unroll
       for (int i = 0; i < 32; i += 4) {
@@ -469,32 +567,36 @@ __device__ __forceinline__ void role_out(const Ctx& x, const TcParams& p, const 
     if (lane == 0) mbar_arrive(&bars->qs_read);
     LA_GO_ON(pv_full, c);
     tc_fence_after();
-    if (lead) tma_store_wait_read0();
-    named_bar_sync(kBarOut, 128);
     const int rows = min(kC, x.live - c * kC);
-#pragma unroll
-    for (int j = 0; j < kC; j += 32) {
-      uint32_t r[32];
-      tmem_ld32(at + F::PV + j, r);
+#pragma unroll 1
+    for (int j = 0; j < kC; j += kOutRows) {
+      uint32_t v[32];
+      tmem_ld32(at + F::PV + j, v);
       tmem_ld_wait();
+      if (j) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->pv_read);
+      }
+      if (lead) tma_store_wait_read0();
+      named_bar_sync(kBarOut, 128);
 #pragma unroll
-      for (int i = 0; i < 32; ++i) {
-        const float o = j + i < rows ? __uint_as_float(r[i]) : 0.f;
-        asm volatile("st.shared.b16 [%0], %1;" ::"r"(mine + (j + i) * 128),
+      for (int i = 0; i < kOutRows; ++i) {
+        const float o = j + i < rows ? __uint_as_float(v[i]) : 0.f;
+        asm volatile("st.shared.b16 [%0], %1;" ::"r"(mine + i * 128),
                      "h"((uint16_t)(pack_bf16x2(o, 0.f) & 0xffffu))
                      : "memory");
       }
-    }
-    tc_fence_before();
-    fence_proxy_async_smem();
-    named_bar_sync(kBarOut, 128);
-    if (lead) {
-      for (int i = 0; i < 2; ++i) {
-        const int col = x.tile * 128 + i * 64;
-        if (col < p.dv && LA_DCHECK(p.status, c * kC < p.n, 61))
-          tma_store_4d(mo, stage + i * kSlab, col, x.h * p.o_h, c * kC, x.b * p.o_b);
+      fence_proxy_async_smem();
+      named_bar_sync(kBarOut, 128);
+      if (lead) {
+        for (int i = 0; i < 2; ++i) {
+          const int col = x.tile * 128 + i * 64;
+          if (col < p.dv && c * kC + j < p.n && LA_DCHECK(p.status, c * kC + j >= 0, 61))
+            tma_store_4d(mo, stage + i * kOutRows * 128, col, x.h * p.o_h, c * kC + j, x.b * p.o_b);
+        }
+        tma_store_commit();
       }
-      tma_store_commit();
     }
   }
   if (lead) tma_store_wait0();
@@ -516,22 +618,16 @@ __device__ __forceinline__ float log2_decay(const TcParams& p, float dt, float b
   return g < -1048576.f ? -1048576.f : g;
 }
 
-// One column of the inverse of a unit lower triangular 16×16 block.
+// One column of the inverse of a unit lower triangular 16×16 block, by the columns
+// of A: what is known of v is taken from all rows below at once.
 __device__ __forceinline__ void invert16(float* A, int lane) {
   float v[16];
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    float s = lane == i ? 1.f : 0.f;
+  for (int i = 0; i < 16; ++i) v[i] = lane == i ? 1.f : 0.f;
 #pragma unroll
-    for (int j = 0; j < i; j += 4) {
-      const float4 a = *reinterpret_cast<const float4*>(A + i * kAPitch + j);
-      s = fmaf(-a.x, v[j], s);
-      if (j + 1 < i) s = fmaf(-a.y, v[j + 1], s);
-      if (j + 2 < i) s = fmaf(-a.z, v[j + 2], s);
-      if (j + 3 < i) s = fmaf(-a.w, v[j + 3], s);
-    }
-    v[i] = s;
-  }
+  for (int j = 0; j < 15; ++j)
+#pragma unroll
+    for (int i = j + 1; i < 16; ++i) v[i] = fmaf(-A[i * kAPitch + j], v[j], v[i]);
   __syncwarp();
   if (lane < 16)
 #pragma unroll
@@ -568,160 +664,214 @@ __device__ __forceinline__ void small_product(const float* X, const float* Y, in
         make_float4(sign * z[r].x, sign * z[r].y, sign * z[r].z, sign * z[r].w);
 }
 
+// Decays, strengths and lengths of each chunk's tokens, of k by warp 19 and of q by
+// warp 18; lane i has tokens i and i + 32.
+template <int DK>
+__device__ __forceinline__ void role_factors(const Ctx& x, const TcParams& p, int warp, int lane) {
+  using F = Cfg<DK>;
+  volatile int* abort = &x.bars->abort;
+  const bool keys = warp == kFactorWarp + 1;
+  const float rate = p.a[x.h], bias = p.dt_bias ? p.dt_bias[x.h] : 0.f;
+  uint32_t dt[2], be[2];
+  auto fetch = [&](int c) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int64_t t = (int64_t)c * kC + i * 32 + lane;
+      const bool in = t < x.live;
+      dt[i] = in ? gate_bits(p.dt, p.gates_f32, x.b * p.dt.sb + t * p.dt.sn + x.h) : 0u;
+      be[i] = in ? gate_bits(p.beta, p.gates_f32, x.b * p.beta.sb + t * p.beta.sn + x.h) : 0u;
+    }
+  };
+  if (x.chunks) fetch(0);
+#pragma unroll 1
+  for (int c = 0; c < x.chunks; ++c) {
+    TokenFactors& tok = x.tok[c % kTok];
+    const int count = x.live - c * kC;
+    float2 b[2];                        // inclusive sums
+    float beta[2], r[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const bool live = i * 32 + lane < count;
+      b[i] = make_float2(live ? log2_decay(p, gate_value(dt[i], p.gates_f32), bias, rate) : 0.f, 0.f);
+      const float strength = gate_value(be[i], p.gates_f32);
+      beta[i] = !live ? 0.f : p.sigmoid ? rcp_f32(1.f + ex2_f32(-kLog2e * strength)) : strength;
+    }
+    if (c + 1 < x.chunks) fetch(c + 1);
+#pragma unroll 1
+    for (int m = 1; m < 32; m *= 2)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float2 o = make_float2(__shfl_up_sync(0xffffffffu, b[i].x, m), __shfl_up_sync(0xffffffffu, b[i].y, m));
+        if (lane >= m) b[i] = add_parts(o, b[i]);
+      }
+    const float2 mid = make_float2(__shfl_sync(0xffffffffu, b[0].x, 31), __shfl_sync(0xffffffffu, b[0].y, 31));
+    b[1] = add_parts(b[1], mid);
+    const float2 last = make_float2(__shfl_sync(0xffffffffu, b[1].x, 31), __shfl_sync(0xffffffffu, b[1].y, 31));
+    LA_WAIT(kq_full[c % kKQ], c / kKQ);
+    r[0] = r[1] = 1.f;
+    if (p.normalize) {
+      const uint32_t slab = smem_u32(x.sm + c % kKQ * F::kStage + !keys * kSlab);
+      f32x2 sum[2][2] = {};
+#pragma unroll 2
+      for (int j = 0; j < 8 * F::kSlabs; ++j) {
+        const uint32_t at = slab + (j / 8) * 2 * kSlab + sw_chunk(kC, lane, 0, j % 8);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const uint4 v = lds128(at + i * 32 * 128);
+          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const f32x2 f = pack2(bf16lo_to_f32(w[e]), bf16hi_to_f32(w[e]));
+            sum[i][e & 1] = fma2(f, f, sum[i][e & 1]);
+          }
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        float lo, hi;
+        unpack2(add2(sum[i][0], sum[i][1]), lo, hi);
+        r[i] = rsqrtf(lo + hi + 1e-6f);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int t = i * 32 + lane;
+      if (t >= count) r[i] = 0.f;
+      const float eb = ex2_f32(b[i].x + b[i].y);
+      if (keys) {
+        const float off = (mid.x - b[i].x) + (mid.y - b[i].y);
+        tok.bx[t] = tok.cx[t] = b[i].x;
+        tok.by[t] = b[i].y;
+        tok.cy[t] = b[i].y - lg2_f32(r[i]);
+        tok.far[t] = i ? ex2_f32(-off) : r[i] * ex2_f32(off);
+        tok.a[t] = beta[i] * r[i];
+        tok.beta[t] = beta[i];
+        tok.ks[t] = -eb * r[i];
+        tok.left[t] = r[i] * ex2_f32((last.x - b[i].x) + (last.y - b[i].y));
+      } else {
+        tok.out[t] = p.scale * r[i] * eb;
+        tok.q[t] = p.scale * r[i];
+      }
+    }
+    if (keys && lane == 0) tok.carry = ex2_f32(last.x + last.y);
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&x.bars->f_ready[c % kTok]);
+  }
+}
+
 // Thread t < 64 has token t's row of k·kᵀ, thread 64 + t that of q·kᵀ.
 template <int DK>
 __device__ __forceinline__ void role_prep(const Ctx& x, const TcParams& p, int warp, int lane) {
   using F = Cfg<DK>;
   Bars* bars = x.bars;
   volatile int* abort = &bars->abort;
-  const int t = (warp - kPrepWarp) * 32 + lane, row = t % kC;
+  const int group = (warp - kPrepWarp) / 4, t = warp % 4 * 32 + lane, row = t % kC;
+  const uint32_t bar = kBarPrep + group;
   const bool keys = t < kC;
   const uint32_t at = tmem_addr(x.tmem, warp % 4 * 32, 0);
-  float* A = reinterpret_cast<float*>(x.sm + F::oA);
-  const float rate = p.a[x.h], bias = p.dt_bias ? p.dt_bias[x.h] : 0.f;
-  // step and strength of tokens lane and lane + 32 of a chunk
-  float dt[2], be[2];
-  auto fetch = [&](int c) {
+  float* A = reinterpret_cast<float*>(x.sm + F::oA) + group * kC * kAPitch;
+#pragma unroll 1
+  for (int c = group; c < x.chunks; c += 2) {
+    const TokenFactors& tok = x.tok[c % kTok];
+    LA_GO_ON(f_ready[c % kTok], c / kTok);
+    const float bx = tok.bx[row], by = tok.by[row];
+    const float factor = keys ? tok.a[row] : tok.q[row];
+    const int upto = row - keys;      // A below the diagonal, P with it
+    const uint32_t P = smem_u32(x.sm + F::oP + c % kPS * kSlab);
+    named_bar_sync(bar, 128);    // the last chunk's T has been read from A
+    // this row of A, or of P, 16 columns at a time
+    LA_GO_ON(g_full[c & 1], c / 2);
+    tc_fence_after();
+    const float far = factor * tok.far[row];
+    const f32x2 f2 = pack2(factor, factor), bx2 = pack2(bx, bx), by2 = pack2(by, by), minus = pack2(-1.f, -1.f);
+#pragma unroll 1
+    for (int j0 = 0; j0 < kC; j0 += 16) {
+      float v[16] = {};
+      if (j0 <= (row | 31)) {         // (the same for the whole warp)
+        uint32_t g[16];
+        tmem_ld16(at + F::G + j0, g);
+        tmem_ld_wait();
+        if (row >= 32 && j0 < 32) {
+          const f32x2 far2 = pack2(far, far);
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int64_t tt = (int64_t)c * kC + i * 32 + lane;
-      const bool in = tt < x.live;
-      dt[i] = in ? gate_value(p.dt, p.gates_f32, x.b * p.dt.sb + tt * p.dt.sn + x.h) : 0.f;
-      be[i] = in ? gate_value(p.beta, p.gates_f32, x.b * p.beta.sb + tt * p.beta.sn + x.h) : 0.f;
-    }
-  };
-  if (x.chunks) fetch(0);
-  for (int c = 0; c < x.chunks; ++c) {
-    TokenFactors& tok = x.tok[c % kTok];
-    const bool live = c * kC + row < x.live;
-    // b, inclusive, of both halves of the chunk
-    float2 b[2];
+          for (int j = 0; j < 16; j += 4) {
+            const ulonglong2 f = *reinterpret_cast<const ulonglong2*>(&tok.far[j0 + j]);
+            unpack2(mul2(far2, mul2(pair_of(g, j), f.x)), v[j], v[j + 1]);
+            unpack2(mul2(far2, mul2(pair_of(g, j + 2), f.y)), v[j + 2], v[j + 3]);
+          }
+        } else {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      b[i] = make_float2(c * kC + i * 32 + lane < x.live ? log2_decay(p, dt[i], bias, rate) : 0.f, 0.f);
+          for (int j = 0; j < 16; j += 4) {
+            const ulonglong2 cx = *reinterpret_cast<const ulonglong2*>(&tok.cx[j0 + j]);
+            const ulonglong2 cy = *reinterpret_cast<const ulonglong2*>(&tok.cy[j0 + j]);
+            const f32x2 d0 = add2(fma2(cx.x, minus, bx2), fma2(cy.x, minus, by2));
+            const f32x2 d1 = add2(fma2(cx.y, minus, bx2), fma2(cy.y, minus, by2));
+            float e[4];
+            unpack2(d0, e[0], e[1]);
+            unpack2(d1, e[2], e[3]);
+            unpack2(mul2(mul2(pair_of(g, j), f2), pack2(ex2_f32(e[0]), ex2_f32(e[1]))), v[j], v[j + 1]);
+            unpack2(mul2(mul2(pair_of(g, j + 2), f2), pack2(ex2_f32(e[2]), ex2_f32(e[3]))), v[j + 2], v[j + 3]);
+          }
 #pragma unroll
-      for (int m = 1; m < 32; m *= 2) {
-        const float2 o = make_float2(__shfl_up_sync(0xffffffffu, b[i].x, m), __shfl_up_sync(0xffffffffu, b[i].y, m));
-        if (lane >= m) b[i] = add_parts(o, b[i]);
+          for (int j = 0; j < 16; ++j) v[j] = j0 + j <= upto ? v[j] : 0.f;
+        }
+      }
+      if (keys) {
+        float4* to = reinterpret_cast<float4*>(A + row * kAPitch + j0);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) to[j] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 16; j += 8) {
+          const float w[8] = {v[j], v[j + 1], v[j + 2], v[j + 3], v[j + 4], v[j + 5], v[j + 6], v[j + 7]};
+          sts128(P + sw_chunk(kC, row, 0, (j0 + j) / 8), pack8(w));
+        }
       }
     }
-    b[1] = add_parts(b[1], make_float2(__shfl_sync(0xffffffffu, b[0].x, 31), __shfl_sync(0xffffffffu, b[0].y, 31)));
-    const float2 last = make_float2(__shfl_sync(0xffffffffu, b[1].x, 31), __shfl_sync(0xffffffffu, b[1].y, 31));
-    const float2 mine = row < 32 ? b[0] : b[1];
-    float beta = row < 32 ? be[0] : be[1];
-    if (p.sigmoid) beta = 1.f / (1.f + expf(-beta));
-    if (!live) beta = 0.f;
-    if (c + 1 < x.chunks) fetch(c + 1);
-    // 1 / length of this thread's row of k or q
-    LA_GO_ON(kq_full[c % kKQ], c / kKQ);
-    float r = 1.f;
-    if (p.normalize) {
-      f32x2 s2 = 0;
-#pragma unroll
-      for (int i = 0; i < F::kSlabs; ++i)
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          f32x2 v[4];
-          unpack_pairs<bf16>(lds128(smem_u32(x.sm + c % kKQ * F::kStage + (2 * i + !keys) * kSlab) +
-                                    sw_chunk(kC, row, 0, j)), v);
-#pragma unroll
-          for (int u = 0; u < 4; ++u) s2 = fma2(v[u], v[u], s2);
-        }
-      float lo, hi;
-      unpack2(s2, lo, hi);
-      r = rsqrtf(lo + hi + 1e-6f);
-    }
-    if (!live) r = 0.f;
-    const float eb = ex2_f32(mine.x + mine.y);
-    if (keys) {
-      tok.pair[row] = make_float4(mine.x, mine.y, r, 0.f);
-      tok.left[row] = r * ex2_f32((last.x - mine.x) + (last.y - mine.y));
-      tok.t1[row] = beta;
-      tok.t2[row] = -beta * eb * r;
-      if (row == 0) tok.carry = ex2_f32(last.x + last.y);
-    } else {
-      tok.out[row] = p.scale * r * eb;
-    }
-    named_bar_sync(kBarPrep, 128);   // and the last chunk's T has been read from A
-    // this row of A, or of P
-    LA_GO_ON(g_full, c);
-    tc_fence_after();
-    uint32_t g[64];
-    tmem_ld32(at + F::G, g);
-    tmem_ld32(at + F::G + 32, g + 32);
-    tmem_ld_wait();
     tc_fence_before();
     __syncwarp();
     if (lane == 0) mbar_arrive(&bars->g_empty);
-    const float factor = keys ? beta * r : p.scale * r;
-    const int upto = row - keys;      // A below the diagonal, P with it
-    const int cols = row / 32 ? 64 : 32;
-    uint32_t pk[32] = {};
-#pragma unroll
-    for (int j = 0; j < 64; j += 2) {
-      if (j >= cols) break;           // (the same for the whole warp)
-      float v[2];
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const float4 f = tok.pair[j + u];
-        const float e = ex2_f32((mine.x - f.x) + (mine.y - f.y));
-        v[u] = j + u <= upto ? factor * (__uint_as_float(g[j + u]) * f.z) * e : 0.f;
-      }
-      if (keys)
-        *reinterpret_cast<float2*>(A + row * kAPitch + j) = make_float2(v[0], v[1]);
-      else
-        pk[j / 2] = pack_bf16x2(v[0], v[1]);
-    }
-    named_bar_sync(kBarPrep, 128);
+    named_bar_sync(bar, 128);
     // T in A's place: blocks of 16, then 32, then 64; the upper blocks hold what is
     // between two products
     invert16(A + (t / 32) * 16 * (kAPitch + 1), lane);
-    named_bar_sync(kBarPrep, 128);
+    named_bar_sync(bar, 128);
     {
       const int o = t / 64 * 32, u = t % 64, r0 = u / 4, c0 = u % 4 * 4;
       float* B = A + o * (kAPitch + 1);
       small_product<1>(B + (16 + r0) * kAPitch, B + c0, 0, 16, 1.f, B + r0 * kAPitch + 16 + c0);
-      named_bar_sync(kBarPrep, 128);
+      named_bar_sync(bar, 128);
       small_product<1>(B + (16 + r0) * kAPitch + 16, B + 16 + c0, 0, 16, -1.f, B + (16 + r0) * kAPitch + c0);
     }
-    named_bar_sync(kBarPrep, 128);
+    named_bar_sync(bar, 128);
     {
       const int r0 = t / 8 * 2, c0 = t % 8 * 4;
       small_product<2>(A + (32 + r0) * kAPitch, A + c0, c0 < 16 ? 0 : 16, 32, 1.f, A + r0 * kAPitch + 32 + c0);
-      named_bar_sync(kBarPrep, 128);
+      named_bar_sync(bar, 128);
       small_product<2>(A + (32 + r0) * kAPitch + 32, A + 32 + c0, 0, r0 < 16 ? 16 : 32, -1.f,
                        A + (32 + r0) * kAPitch + c0);
     }
-    named_bar_sync(kBarPrep, 128);
-    // T1 and T2 where the last chunk's were, P where that of the one before was
-    if (c >= 1) LA_GO_ON(w_full, c - 1);
+    named_bar_sync(bar, 128);
+    // Tβ where the last chunk's was; its w is complete, and so is every product that
+    // was issued before it, with the P of the chunk before
+    if (c >= 1) LA_GO_ON(w_full[(c - 1) & 1], (c - 1) / 2);
     const uint32_t T = smem_u32(x.sm + F::oT);
     const int h0 = keys ? 0 : 32;     // half of the row's columns
+#pragma unroll 1
+    for (int j = h0; j < h0 + 32; j += 8) {
+      uint4 o[3] = {};
+      if (j / 16 <= row / 16) {       // (above, blocks hold what was between two products)
+        uint32_t* u = reinterpret_cast<uint32_t*>(o);
 #pragma unroll
-    for (int j = 0; j < 32; j += 8) {
-      uint4 o[4];
-      uint32_t* w = reinterpret_cast<uint32_t*>(o);
-#pragma unroll
-      for (int i = 0; i < 8; i += 4) {
-        const int k = h0 + j + i;
-        const float4 a = *reinterpret_cast<const float4*>(A + row * kAPitch + k);
-        const float4 f1 = *reinterpret_cast<const float4*>(&tok.t1[k]);
-        const float4 f2 = *reinterpret_cast<const float4*>(&tok.t2[k]);
-        const float v0 = k <= row ? a.x : 0.f, v1 = k + 1 <= row ? a.y : 0.f;
-        const float v2 = k + 2 <= row ? a.z : 0.f, v3 = k + 3 <= row ? a.w : 0.f;
-        split2(v0 * f1.x, v1 * f1.y, w[i / 2], w[4 + i / 2]);
-        split2(v2 * f1.z, v3 * f1.w, w[i / 2 + 1], w[4 + i / 2 + 1]);
-        split2(v0 * f2.x, v1 * f2.y, w[8 + i / 2], w[12 + i / 2]);
-        split2(v2 * f2.z, v3 * f2.w, w[8 + i / 2 + 1], w[12 + i / 2 + 1]);
+        for (int i = 0; i < 8; i += 4) {
+          const ulonglong2 a = *reinterpret_cast<const ulonglong2*>(A + row * kAPitch + j + i);
+          const ulonglong2 f = *reinterpret_cast<const ulonglong2*>(&tok.beta[j + i]);
+          split3(mul2(a.x, f.x), u[i / 2], u[4 + i / 2], u[8 + i / 2]);
+          split3(mul2(a.y, f.y), u[i / 2 + 1], u[4 + i / 2 + 1], u[8 + i / 2 + 1]);
+        }
       }
 #pragma unroll
-      for (int m = 0; m < 4; ++m) sts128(T + m * kSlab + sw_chunk(kC, row, 0, (h0 + j) / 8), o[m]);
-    }
-    if (!keys) {
-      const uint32_t P = smem_u32(x.sm + F::oP + c % 2 * kSlab);
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        sts128(P + sw_chunk(kC, row, 0, j), make_uint4(pk[4 * j], pk[4 * j + 1], pk[4 * j + 2], pk[4 * j + 3]));
+      for (int m = 0; m < 3; ++m) sts128(T + m * kSlab + sw_chunk(kC, row, 0, j / 8), o[m]);
     }
     fence_proxy_async_smem();
     __syncwarp();
@@ -746,10 +896,11 @@ chunk_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUt
   if (threadIdx.x == 0) {
     for (int i = 0; i < kKQ; ++i) mbar_init(&bars->kq_full[i], 1), mbar_init(&bars->kq_empty[i], 1);
     for (int i = 0; i < kVS; ++i) mbar_init(&bars->v_full[i], 1), mbar_init(&bars->v_empty[i], 1);
-    for (uint64_t* b : {&bars->kq_clean, &bars->v_clean, &bars->g_full, &bars->ks_full, &bars->qs_full,
-                        &bars->w_full, &bars->upd_full, &bars->pv_full, &bars->done})
+    for (uint64_t* b : {&bars->kq_clean, &bars->v_clean, &bars->g_full[0], &bars->g_full[1], &bars->ks_full,
+                        &bars->qs_full, &bars->w_full[0], &bars->w_full[1], &bars->upd_full, &bars->pv_full, &bars->done})
       mbar_init(b, 1);
-    for (uint64_t* b : {&bars->g_empty, &bars->t_ready, &bars->qs_read}) mbar_init(b, 4);
+    for (int i = 0; i < kTok; ++i) mbar_init(&bars->f_ready[i], 2);
+    for (uint64_t* b : {&bars->g_empty, &bars->t_ready, &bars->qs_read, &bars->pv_read}) mbar_init(b, 4);
     for (uint64_t* b : {&bars->s_ready, &bars->ks_ready, &bars->w_ready}) mbar_init(b, kStateWarps);
     bars->abort = bars->kq_issued = bars->v_issued = 0;
     fence_barrier_init();
@@ -769,7 +920,7 @@ chunk_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUt
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  x.tmem = bars->tmem;
+  x.tmem = __shfl_sync(0xffffffffu, bars->tmem, 0);   // (known to be the same for the warp)
   x.tile = blockIdx.x % p.tiles;
   const int64_t bh = blockIdx.x / p.tiles;
   x.h = (int)(bh % p.Hv);
@@ -779,25 +930,27 @@ chunk_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUt
   x.partial = x.live % kC != 0 && x.live < p.n;
 
   if (warp < kStateWarps) {
-    take_registers<DK == 128 ? 120 : 96>();
+    take_registers<DK == 128 ? 120 : 112>();
     role_state<DK>(x, p, warp, lane);
   } else if (warp < kOutWarp) {
-    take_registers<104>();
+    take_registers<DK == 128 ? 64 : 72>();
     role_prep<DK>(x, p, warp, lane);
   } else if (warp < kLoadWarp) {
-    take_registers<64>();
+    take_registers<DK == 128 ? 56 : 48>();
     role_out<DK>(x, p, &mo, warp, lane);
   } else {
-    take_registers<DK == 128 ? 72 : 96>();
+    take_registers<DK == 128 ? 56 : 64>();
     if (warp == kLoadWarp)
       role_load<DK>(x, p, &mq, &mk, &mv, lane);
-    else if (warp == kMmaWarp && lane == 0)
+    else if (warp == kMmaWarp)
       role_mma<DK>(x, p);
+    else
+      role_factors<DK>(x, p, warp, lane);
   }
   __syncwarp();
   tc_fence_before();
   __syncthreads();
-  if (*(volatile int*)&bars->abort) {   // copies and products in flight end before the CTA does
+  if (*(volatile int*)&bars->abort) {   // a wait gave up: copies and products in flight end before the CTA does
     if (warp == kMmaWarp && lane == 0) {
       mma_commit(&bars->done);
       drain_in_line(&bars->done, 0);
@@ -807,7 +960,10 @@ chunk_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUt
       for (int j = max(0, kq_issued - kKQ); j < kq_issued; ++j) drain_in_line(&bars->kq_full[j % kKQ], (j / kKQ) & 1);
       for (int j = max(0, v_issued - kVS); j < v_issued; ++j) drain_in_line(&bars->v_full[j % kVS], (j / kVS) & 1);
     }
-    if (warp == kOutWarp && lane == 0) tma_store_wait0();
+    if (warp == kOutWarp && lane == 0) {
+      tma_store_wait0();
+      atomicCAS(p.status, 0, kStatusTimeout);
+    }
     __syncthreads();
   }
   tc_fence_after();
@@ -821,7 +977,7 @@ cudaError_t launch_chunks(const DeltaArgs& a, const TcParams& p, cudaStream_t s)
   if ((e = tmap_heads(&mq, a.q, a.B, a.n, a.Hk, a.dk, kC, true)) != cudaSuccess ||
       (e = tmap_heads(&mk, a.k, a.B, a.n, a.Hk, a.dk, kC, true)) != cudaSuccess ||
       (e = tmap_heads(&mv, a.v, a.B, a.n, a.Hv, a.dv, kC, true)) != cudaSuccess ||
-      (e = tmap_heads(&mo, a.out, a.B, a.n, a.Hv, a.dv, kC, false)) != cudaSuccess)
+      (e = tmap_heads(&mo, a.out, a.B, a.n, a.Hv, a.dv, kOutRows, false)) != cudaSuccess)
     return e;
   const int64_t ctas = a.B * a.Hv * p.tiles;
   if (ctas > INT32_MAX) return cudaErrorInvalidConfiguration;
