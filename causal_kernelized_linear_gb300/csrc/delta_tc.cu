@@ -72,7 +72,7 @@ struct Bars {
   uint64_t kq_full[kKQ], kq_empty[kKQ], v_full[kVS], v_empty[kVS], f_ready[kTok];
   uint64_t g_full[2], w_full[2];              // by the chunk's parity: each prep warpgroup sees every other one
   uint64_t kq_clean, v_clean;                 // the last chunk's rows past the length are zero
-  uint64_t g_empty, t_ready, s_ready, ks_full, ks_ready, qs_full, qs_read, w_ready,
+  uint64_t g_empty, t_ready, s_ready[2], ks_full, ks_ready, qs_full, qs_read, w_ready,
       upd_full, pv_full, pv_read, done;
   uint32_t tmem;
   int abort;
@@ -104,6 +104,11 @@ struct TcParams {
   const float* state_in;
   float* state_out;
   const int32_t* lengths;
+  // sequences in `segs` parts of seg_tokens each: what each but the last makes of a
+  // zero state and of the identity, and the states that enter the others
+  int segs, seg_tokens;
+  float *added, *transition;
+  const float* entering;
   bf16* out;
   int64_t out_sb, out_sn, out_sh;
   int n, Hk, Hv, dk, dv, tiles;
@@ -182,8 +187,13 @@ struct Ctx {
   Bars* bars;
   TokenFactors* tok;
   uint32_t tmem;
-  int b, h, tile, live, chunks;
+  // the CTA's part of a sequence: its first token, how many exist, how many count
+  int b, h, tile, t0, end, live, chunks;
   bool partial;           // rows of the last chunk lie past the length
+  bool identity;          // from the identity without v: the transition over the part
+  const float* s_in;      // the state before and after, [dk, cols], or nullptr
+  float* s_out;
+  int cols;
 };
 
 // mbar_wait and mbar_wait_drain in line, since the compiler refuses calls beside
@@ -216,7 +226,7 @@ __device__ __forceinline__ void drain_in_line(uint64_t* bar, uint32_t parity) {
 // ------------------------------------------------------------------ loads
 
 // (whole warp)
-template <int DK>
+template <int DK, bool SUMMARY>
 __device__ __forceinline__ void role_load(const Ctx& x, const TcParams& p, const CUtensorMap* mq,
                                           const CUtensorMap* mk, const CUtensorMap* mv, int lane) {
   using F = Cfg<DK>;
@@ -224,7 +234,7 @@ __device__ __forceinline__ void role_load(const Ctx& x, const TcParams& p, const
   const int hk = x.h / (p.Hv / p.Hk);
   const int vslabs = p.dv - x.tile * 128 > 64 ? 2 : 1;
   for (int c = 0; c < x.chunks; ++c) {
-    const int s = c % kKQ, vs = c % kVS, t = c * kC;
+    const int s = c % kKQ, vs = c % kVS, t = x.t0 + c * kC;
     if (c >= kKQ) LA_WAIT(kq_empty[s], c / kKQ - 1);
     if (lane == 0) {
       uint8_t* to = x.sm + s * F::kStage;
@@ -236,6 +246,7 @@ __device__ __forceinline__ void role_load(const Ctx& x, const TcParams& p, const
       }
     }
     if (lane == 0) x.bars->kq_issued = c + 1;
+    if (SUMMARY && x.identity) continue;
     if (c >= kVS) LA_WAIT(v_empty[vs], c / kVS - 1);
     if (lane == 0) {
       uint8_t* to = x.sm + F::oV + vs * 2 * kSlab;
@@ -257,6 +268,7 @@ __device__ __forceinline__ void role_load(const Ctx& x, const TcParams& p, const
   fence_proxy_async_smem();
   __syncwarp();
   if (lane == 0) mbar_arrive(&x.bars->kq_clean);
+  if (SUMMARY && x.identity) return;
   LA_WAIT(v_full[c % kVS], c / kVS);
   for (int i = 0; i < vslabs; ++i) clear(x.sm + F::oV + (c % kVS * 2 + i) * kSlab);
   fence_proxy_async_smem();
@@ -266,8 +278,29 @@ __device__ __forceinline__ void role_load(const Ctx& x, const TcParams& p, const
 
 // ------------------------------------------------------------------ products
 
-// (whole warp; one thread issues)
-template <int DK>
+// D[tmem] (+)= A·B by the one thread of the warp for which `lead` is set, without a
+// branch: what the warp has in common then stays in its uniform registers, where
+// the instruction wants its operands.
+__device__ __forceinline__ void warp_mma_ss(uint32_t lead, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                            uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(lead)
+      : "memory");
+}
+__device__ __forceinline__ void warp_mma_ts(uint32_t lead, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
+                                            uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(lead)
+      : "memory");
+}
+
+// (whole warp)  The loops over products are unrolled: an MMA of these takes 32 to 64
+// cycles, and with its operands' addresses computed in a loop it is issued in 130.
+template <int DK, bool SUMMARY>
 __device__ __forceinline__ void role_mma(const Ctx& x, const TcParams& p) {
   using F = Cfg<DK>;
   Bars* bars = x.bars;
@@ -276,114 +309,124 @@ __device__ __forceinline__ void role_mma(const Ctx& x, const TcParams& p) {
   constexpr uint32_t id_nn = idesc_bf16_f32(128, kC, false, false);   // K-major A and B, 64 columns
   constexpr uint32_t id_v = idesc_bf16_f32(128, kC, true, false);     // vᵀ from [token][column]
   constexpr uint32_t id_upd = idesc_bf16_f32(128, DK, false, true);   // k as [token][feature]
+  constexpr int KD = DK / 16, KC = kC / 16;
+  const uint32_t lead = elect_one();
   const uint64_t dT = smem_desc(base + F::oT, 16, 1024, kSwizzle128B);
+  // K-step k of a tile with 64 features per slab
+  auto kstep = [](int k) { return (uint32_t)((k >> 2) * 2 * kSlab + (k & 3) * 32); };
   // K-step k of (kS)ᵀ or wᵀ: 32 tokens' hi parts, then their lo parts
   auto tokens = [](int k) { return (uint32_t)((k >> 1) * 32 + (k & 1) * 8); };
-  auto gram = [&](int c) -> bool {   // [k; q]·kᵀ
-    if (!warp_wait_in_line(&bars->kq_full[c % kKQ], (c / kKQ) & 1, abort)) return false;
-    if (x.partial && c == x.chunks - 1 && !warp_wait_in_line(&bars->kq_clean, 0, abort)) return false;
-    if (c >= 1 && !warp_wait_in_line(&bars->g_empty, (c - 1) & 1, abort)) return false;
-    tc_fence_after();
-    if (elect_one()) {
-      const uint64_t d = smem_desc(base + c % kKQ * F::kStage, 16, 1024, kSwizzle128B);
 #pragma unroll 1
-      for (int i = 0; i < F::kSlabs; ++i)
+  for (int c = -2; c < x.chunks; ++c) {
+    if (c >= 0) {
+      const uint32_t kq = base + c % kKQ * F::kStage;
+      const uint64_t dK = smem_desc(kq, 16, 1024, kSwizzle128B);
+      // (kS)ᵀ = Sᵀ kᵀ
+      LA_WAIT(s_ready[0], c);
+      tc_fence_after();
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          mma_ss(tmem + F::G, desc_at(d, i * 2 * kSlab + k * 32), desc_at(d, i * 2 * kSlab + k * 32), id_nn, i | k);
-      mma_commit(&bars->g_full[c & 1]);
-    }
-    __syncwarp();
-    return true;
-  };
-#pragma unroll 1
-  for (int c = 0; c < 2 && c < x.chunks; ++c)
-    if (!gram(c)) return;
-#pragma unroll 1
-  for (int c = 0; c < x.chunks; ++c) {
-    const uint32_t kq = base + c % kKQ * F::kStage;
-    // (kS)ᵀ = Sᵀ kᵀ
-    LA_WAIT(s_ready, c);
-    tc_fence_after();
-    auto of_state = [&](uint32_t to, uint64_t d) {   // S's hi parts, its lo parts
-#pragma unroll 1
-      for (int i = 0; i < 2 * F::kSlabs; ++i) {
-        const uint64_t di = desc_at(d, i % F::kSlabs * 2 * kSlab);
-        const uint32_t from = tmem + F::SH + i * 32;
+      for (int k = 0; k < KD; ++k)
+        warp_mma_ts(lead, tmem + F::KS, tmem + F::SH + k * 8, desc_at(dK, kstep(k)), id_nn, k > 0);
+      LA_WAIT(s_ready[1], c);
+      tc_fence_after();
 #pragma unroll
-        for (int k = 0; k < 4; ++k) mma_ts(to, from + k * 8, desc_at(di, k * 32), id_nn, i | k);
-      }
-    };
-    if (elect_one()) {
-      of_state(tmem + F::KS, smem_desc(kq, 16, 1024, kSwizzle128B));
-      mma_commit(&bars->ks_full);
-    }
-    __syncwarp();
-    // wᵀ = vᵀ (Tβ)ᵀ; its columns are free since S is there, which waited for (P w)ᵀ
-    LA_WAIT(t_ready, c);
-    LA_WAIT(v_full[c % kVS], c / kVS);
-    if (x.partial && c == x.chunks - 1) LA_WAIT(v_clean, 0);
-    tc_fence_after();
-    if (elect_one()) {
-      const uint64_t dV = smem_desc(base + F::oV + c % kVS * 2 * kSlab, kSlab, 1024, kSwizzle128B);
-#pragma unroll 1
+      for (int k = 0; k < KD; ++k)
+        warp_mma_ts(lead, tmem + F::KS, tmem + F::SL + k * 8, desc_at(dK, kstep(k)), id_nn, 1);
+      if (lead) mma_commit(&bars->ks_full);
+      __syncwarp();
+      // wᵀ −= (e^b kS)ᵀ (Tβ)ᵀ: hi·hi, hi·mid, lo·hi; and (qS)ᵀ
+      LA_WAIT(ks_ready, c);
+      if (!SUMMARY && c >= 1) LA_WAIT(pv_read, c - 1);
+      tc_fence_after();
+#pragma unroll
       for (int part = 0; part < 3; ++part)
 #pragma unroll
-        for (int k = 0; k < kC / 16; ++k)
-          mma_ss(tmem + F::W, desc_at(dV, k * 2048), desc_at(dT, part * kSlab + k * 32), id_v, part | k);
-      mma_commit(&bars->v_empty[c % kVS]);
-    }
-    __syncwarp();
-    // wᵀ −= (e^b kS)ᵀ (Tβ)ᵀ, and (qS)ᵀ
-    LA_WAIT(ks_ready, c);
-    if (c >= 1) LA_WAIT(pv_read, c - 1);
-    tc_fence_after();
-    if (elect_one()) {
-#pragma unroll 1
-      for (int part = 0; part < 3; ++part) {   // hi·hi, hi·mid, lo·hi
-        const uint32_t from = tmem + F::KS + (part == 2 ? 16 : 0);
-        const uint64_t d = desc_at(dT, part == 1 ? kSlab : 0);
+        for (int k = 0; k < KC; ++k)
+          warp_mma_ts(lead, tmem + F::W, tmem + F::KS + tokens(k) + (part == 2 ? 16 : 0),
+                      desc_at(dT, (part == 1 ? kSlab : 0) + k * 32), id_nn, 1);
+      if (lead) mma_commit(&bars->w_full[c & 1]);
+      __syncwarp();
+      if constexpr (!SUMMARY) {
 #pragma unroll
-        for (int k = 0; k < kC / 16; ++k) mma_ts(tmem + F::W, from + tokens(k), desc_at(d, k * 32), id_nn, 1);
+        for (int part = 0; part < 2; ++part)
+#pragma unroll
+          for (int k = 0; k < KD; ++k)
+            warp_mma_ts(lead, tmem + F::PV, tmem + (part ? F::SL : F::SH) + k * 8, desc_at(dK, kSlab + kstep(k)),
+                        id_nn, part | k);
+        if (lead) mma_commit(&bars->qs_full);
+        __syncwarp();
       }
-      mma_commit(&bars->w_full[c & 1]);
-      of_state(tmem + F::PV, smem_desc(kq + kSlab, 16, 1024, kSwizzle128B));
-      mma_commit(&bars->qs_full);
-    }
-    __syncwarp();
-    // the state's wᵀk
-    LA_WAIT(w_ready, c);
-    tc_fence_after();
-    if (elect_one()) {
+      // the state's wᵀk
+      LA_WAIT(w_ready, c);
+      tc_fence_after();
       const uint64_t dKt = smem_desc(kq, 2 * kSlab, 1024, kSwizzle128B);
-#pragma unroll 1
+#pragma unroll
       for (int part = 0; part < 2; ++part)
 #pragma unroll
-        for (int k = 0; k < kC / 16; ++k)
-          mma_ts(tmem + F::UPD, tmem + F::KS + part * 16 + tokens(k), desc_at(dKt, k * 2048), id_upd, part | k);
-      mma_commit(&bars->upd_full);
-    }
-    __syncwarp();
-    // (P w)ᵀ on top of what the output's warps have put there
-    LA_WAIT(qs_read, c);
-    tc_fence_after();
-    if (elect_one()) {
-      const uint64_t dP = smem_desc(base + F::oP + c % kPS * kSlab, 16, 1024, kSwizzle128B);
+        for (int k = 0; k < KC; ++k)
+          warp_mma_ts(lead, tmem + F::UPD, tmem + F::KS + part * 16 + tokens(k), desc_at(dKt, k * 2048), id_upd,
+                      part | k);
+      if (lead) {
+        mma_commit(&bars->upd_full);
+        if (SUMMARY) mma_commit(&bars->kq_empty[c % kKQ]);
+      }
+      __syncwarp();
+      // (P w)ᵀ on top of what the output's warps have put there
+      if constexpr (!SUMMARY) {
+        LA_WAIT(qs_read, c);
+        tc_fence_after();
+        const uint64_t dP = smem_desc(base + F::oP + c % kPS * kSlab, 16, 1024, kSwizzle128B);
 #pragma unroll
-      for (int k = 0; k < kC / 16; ++k)
-        mma_ts(tmem + F::PV, tmem + F::W + (k >> 1) * 32 + (k & 1) * 8, desc_at(dP, k * 32), id_nn, 1);
-      mma_commit(&bars->pv_full);
-      mma_commit(&bars->kq_empty[c % kKQ]);   // and the chunk's factors
+        for (int k = 0; k < KC; ++k)
+          warp_mma_ts(lead, tmem + F::PV, tmem + F::W + tokens(k), desc_at(dP, k * 32), id_nn, 1);
+        if (lead) {
+          mma_commit(&bars->pv_full);
+          mma_commit(&bars->kq_empty[c % kKQ]);   // and the chunk's factors
+        }
+        __syncwarp();
+      }
     }
-    __syncwarp();
-    if (c + 2 < x.chunks && !gram(c + 2)) return;
+    // while S is on its way: the products of the chunks ahead that go without it.
+    // [k; q]·kᵀ
+    if (c + 2 < x.chunks) {
+      const int g = c + 2;
+      LA_WAIT(kq_full[g % kKQ], g / kKQ);
+      if (x.partial && g == x.chunks - 1) LA_WAIT(kq_clean, 0);
+      if (g >= 1) LA_WAIT(g_empty, g - 1);
+      tc_fence_after();
+      const uint64_t d = smem_desc(base + g % kKQ * F::kStage, 16, 1024, kSwizzle128B);
+#pragma unroll
+      for (int k = 0; k < KD; ++k)
+        warp_mma_ss(lead, tmem + F::G, desc_at(d, kstep(k)), desc_at(d, kstep(k)), id_nn, k > 0);
+      if (lead) mma_commit(&bars->g_full[g & 1]);
+      __syncwarp();
+    }
+    // wᵀ = vᵀ (Tβ)ᵀ, whose columns (P w)ᵀ has read
+    if (c >= -1 && c + 1 < x.chunks) {
+      const int n = c + 1;
+      LA_WAIT(t_ready, n);
+      if (!(SUMMARY && x.identity)) {
+        LA_WAIT(v_full[n % kVS], n / kVS);
+        if (x.partial && n == x.chunks - 1) LA_WAIT(v_clean, 0);
+      }
+      if (!SUMMARY && n >= 1) LA_WAIT(pv_full, n - 1);   // (else the state's warps have read them)
+      tc_fence_after();
+      const uint64_t dV = smem_desc(base + F::oV + n % kVS * 2 * kSlab, kSlab, 1024, kSwizzle128B);
+#pragma unroll
+      for (int part = 0; part < 3; ++part)
+#pragma unroll
+        for (int k = 0; k < KC; ++k)
+          warp_mma_ss(lead, tmem + F::W, desc_at(dV, k * 2048), desc_at(dT, part * kSlab + k * 32), id_v, part | k);
+      if (lead) mma_commit(&bars->v_empty[n % kVS]);
+      __syncwarp();
+    }
   }
 }
 
 // ------------------------------------------------------------------ the state
 
 // Warp w has rows 32(w % 4) … of Sᵀ (columns of v) and half of its columns.
-template <int DK>
+template <int DK, bool SUMMARY>
 __device__ __forceinline__ void role_state(const Ctx& x, const TcParams& p, int warp, int lane) {
   using F = Cfg<DK>;
   constexpr int kCols = DK / 2;
@@ -391,19 +434,22 @@ __device__ __forceinline__ void role_state(const Ctx& x, const TcParams& p, int 
   volatile int* abort = &bars->abort;
   const int half = warp / 4, k0 = half * kCols;
   const uint32_t at = tmem_addr(x.tmem, warp % 4 * 32, 0);
-  const int col = x.tile * 128 + warp % 4 * 32 + lane;
-  const int64_t head = (int64_t)x.b * p.Hv + x.h;
+  const int col = (SUMMARY && x.identity ? 0 : x.tile * 128) + warp % 4 * 32 + lane;
   // between global memory and S by way of the columns of the update, so that these
   // loops stay small
   const uint32_t mine = at + F::UPD + k0;
-  const int64_t first = (head * p.dk + k0) * p.dv + col;
+  const int64_t first = (int64_t)k0 * x.cols + col;
   const int rows = min(kCols, p.dk - k0);   // multiples of 8
 #pragma unroll 1
   for (int i = 0; i < kCols; i += 8) {
     uint32_t r[8] = {};
-    if (p.state_in && col < p.dv && i < rows)
+    if (SUMMARY && x.identity) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) r[j] = __float_as_uint(p.state_in[first + (int64_t)(i + j) * p.dv]);
+      for (int j = 0; j < 8; ++j) r[j] = __float_as_uint(k0 + i + j == col ? 1.f : 0.f);
+    } else if (x.s_in && col < x.cols && i < rows) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) r[j] = __float_as_uint(x.s_in[first + (int64_t)(i + j) * x.cols]);
+    }
     __syncwarp();
     tmem_st8(mine + i, r);
   }
@@ -418,19 +464,31 @@ __device__ __forceinline__ void role_state(const Ctx& x, const TcParams& p, int 
     for (int i = 0; i < 16; ++i) S[j / 2 + i] = pair_of(r, 2 * i);
   }
 
-  auto publish = [&] {   // S as the next products' operand
+  // S as the next products' operand: the hi parts first, for which they start
+  auto publish = [&] {
 #pragma unroll
-    for (int j = 0; j < kCols; j += 16) {
-      uint32_t hi[8], lo[8];
+    for (int part = 0; part < 2; ++part) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) split2(S[j / 2 + i], hi[i], lo[i]);
-      tmem_st8(at + F::SH + (k0 + j) / 2, hi);
-      tmem_st8(at + F::SL + (k0 + j) / 2, lo);
+      for (int j = 0; j < kCols; j += 16) {
+        uint32_t w[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          float v0, v1;
+          if (part == 0) {
+            unpack2(S[j / 2 + i], v0, v1);
+            w[i] = pack_bf16x2(v0, v1);
+          } else {
+            uint32_t hi;
+            split2(S[j / 2 + i], hi, w[i]);
+          }
+        }
+        tmem_st8(at + (part ? F::SL : F::SH) + (k0 + j) / 2, w);
+      }
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars->s_ready[part]);
     }
-    tmem_st_wait();
-    tc_fence_before();
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&bars->s_ready);
   };
 #pragma unroll 1
   for (int c = 0; c < x.chunks; ++c) {
@@ -473,7 +531,7 @@ __device__ __forceinline__ void role_state(const Ctx& x, const TcParams& p, int 
 #pragma unroll
         for (int i = 0; i < 8; ++i)
           hi[i] = pack_bf16x2(__uint_as_float(r[2 * (j + i)]), __uint_as_float(r[2 * (j + i) + 1]));
-        tmem_st8(at + F::W + half * 32 + j, hi);   // for the output
+        if (!SUMMARY) tmem_st8(at + F::W + half * 32 + j, hi);   // for the output
 #pragma unroll
         for (int i = 0; i < 8; i += 2) {
           const ulonglong2 f = *reinterpret_cast<const ulonglong2*>(&tok.left[half * 32 + 2 * (j + i)]);
@@ -498,9 +556,9 @@ __device__ __forceinline__ void role_state(const Ctx& x, const TcParams& p, int 
 #pragma unroll
       for (int i = 0; i < 16; ++i) S[j / 2 + i] = fma2(S[j / 2 + i], carry, pair_of(r, 2 * i));
     }
-    LA_WAIT(pv_full, c);   // so that the next chunk's w may start
+    if (!SUMMARY) LA_WAIT(pv_full, c);   // so that the next chunk's w may start
   }
-  if (!p.state_out) return;
+  if (!x.s_out) return;
 #pragma unroll
   for (int j = 0; j < kCols; j += 8) {
     uint32_t r[8];
@@ -518,9 +576,9 @@ __device__ __forceinline__ void role_state(const Ctx& x, const TcParams& p, int 
     uint32_t r[8];
     tmem_ld8(mine + i, r);
     tmem_ld_wait();
-    if (col < p.dv)
+    if (col < x.cols)
 #pragma unroll
-      for (int j = 0; j < 8; ++j) p.state_out[first + (int64_t)(i + j) * p.dv] = __uint_as_float(r[j]);
+      for (int j = 0; j < 8; ++j) x.s_out[first + (int64_t)(i + j) * x.cols] = __uint_as_float(r[j]);
     __syncwarp();
   }
 }
@@ -581,19 +639,23 @@ __device__ __forceinline__ void role_out(const Ctx& x, const TcParams& p, const 
       if (lead) tma_store_wait_read0();
       named_bar_sync(kBarOut, 128);
 #pragma unroll
-      for (int i = 0; i < kOutRows; ++i) {
-        const float o = j + i < rows ? __uint_as_float(v[i]) : 0.f;
-        asm volatile("st.shared.b16 [%0], %1;" ::"r"(mine + i * 128),
-                     "h"((uint16_t)(pack_bf16x2(o, 0.f) & 0xffffu))
-                     : "memory");
+      for (int i = 0; i < kOutRows; i += 2) {
+        const uint32_t o = pack_bf16x2(__uint_as_float(v[i]), __uint_as_float(v[i + 1]));
+        asm volatile("st.shared.b16 [%0], %1;" ::"r"(mine + i * 128), "h"((uint16_t)(o & 0xffffu)) : "memory");
+        asm volatile("st.shared.b16 [%0], %1;" ::"r"(mine + i * 128 + 128), "h"((uint16_t)(o >> 16)) : "memory");
       }
+      if (rows < kC)   // what q·S made of the rows past the length
+#pragma unroll 1
+        for (int i = max(0, rows - j); i < kOutRows; ++i)
+          asm volatile("st.shared.b16 [%0], %1;" ::"r"(mine + i * 128), "h"((uint16_t)0) : "memory");
       fence_proxy_async_smem();
       named_bar_sync(kBarOut, 128);
       if (lead) {
         for (int i = 0; i < 2; ++i) {
           const int col = x.tile * 128 + i * 64;
-          if (col < p.dv && c * kC + j < p.n && LA_DCHECK(p.status, c * kC + j >= 0, 61))
-            tma_store_4d(mo, stage + i * kOutRows * 128, col, x.h * p.o_h, c * kC + j, x.b * p.o_b);
+          const int t = x.t0 + c * kC + j;
+          if (col < p.dv && t < p.n && LA_DCHECK(p.status, t >= 0, 61))
+            tma_store_4d(mo, stage + i * kOutRows * 128, col, x.h * p.o_h, t, x.b * p.o_b);
         }
         tma_store_commit();
       }
@@ -602,8 +664,8 @@ __device__ __forceinline__ void role_out(const Ctx& x, const TcParams& p, const 
   if (lead) tma_store_wait0();
   // chunks past the length
   const int cols = min(128, p.dv - x.tile * 128) / 8, lanes = (warp - kOutWarp) * 32 + lane;
-  bf16* o = p.out + x.b * p.out_sb + x.h * p.out_sh + x.tile * 128;
-  for (int64_t t = x.chunks * kC + lanes / 16; t < p.n; t += 8)
+  bf16* o = p.out + x.b * p.out_sb + x.t0 * p.out_sn + x.h * p.out_sh + x.tile * 128;
+  for (int64_t t = x.chunks * kC + lanes / 16; t < x.end; t += 8)
     if (lanes % 16 < cols) *reinterpret_cast<uint4*>(o + t * p.out_sn + lanes % 16 * 8) = make_uint4(0, 0, 0, 0);
 }
 
@@ -618,20 +680,33 @@ __device__ __forceinline__ float log2_decay(const TcParams& p, float dt, float b
   return g < -1048576.f ? -1048576.f : g;
 }
 
-// One column of the inverse of a unit lower triangular 16×16 block, by the columns
-// of A: what is known of v is taken from all rows below at once.
+// One column of the inverse of a unit lower triangular 16×16 block, whose diagonal
+// holds zeros: v_i = [i is the column] − Σ_{j<i} A_ij v_j, two terms at a time.
 __device__ __forceinline__ void invert16(float* A, int lane) {
-  float v[16];
+  f32x2 v[8] = {};
 #pragma unroll
-  for (int i = 0; i < 16; ++i) v[i] = lane == i ? 1.f : 0.f;
+  for (int i = 0; i < 16; ++i) {
+    f32x2 s = pack2(lane == i ? -1.f : 0.f, 0.f);
 #pragma unroll
-  for (int j = 0; j < 15; ++j)
-#pragma unroll
-    for (int i = j + 1; i < 16; ++i) v[i] = fmaf(-A[i * kAPitch + j], v[j], v[i]);
+    for (int j = 0; j < i; j += 4) {
+      const ulonglong2 a = *reinterpret_cast<const ulonglong2*>(A + i * kAPitch + j);
+      s = fma2(a.x, v[j / 2], s);
+      if (j + 2 < i) s = fma2(a.y, v[j / 2 + 1], s);
+    }
+    float s0, s1, lo, hi;
+    unpack2(s, s0, s1);
+    unpack2(v[i / 2], lo, hi);
+    v[i / 2] = i % 2 ? pack2(lo, -(s0 + s1)) : pack2(-(s0 + s1), 0.f);
+  }
   __syncwarp();
   if (lane < 16)
 #pragma unroll
-    for (int i = 0; i < 16; ++i) A[i * kAPitch + lane] = v[i];
+    for (int i = 0; i < 8; ++i) {
+      float lo, hi;
+      unpack2(v[i], lo, hi);
+      A[2 * i * kAPitch + lane] = lo;
+      A[(2 * i + 1) * kAPitch + lane] = hi;
+    }
 }
 
 // ROWS rows × 4 columns of X·Y over K of [K0, K1), all at the A's pitch.
@@ -676,8 +751,8 @@ __device__ __forceinline__ void role_factors(const Ctx& x, const TcParams& p, in
   auto fetch = [&](int c) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const int64_t t = (int64_t)c * kC + i * 32 + lane;
-      const bool in = t < x.live;
+      const bool in = c * kC + i * 32 + lane < x.live;
+      const int64_t t = (int64_t)x.t0 + c * kC + i * 32 + lane;
       dt[i] = in ? gate_bits(p.dt, p.gates_f32, x.b * p.dt.sb + t * p.dt.sn + x.h) : 0u;
       be[i] = in ? gate_bits(p.beta, p.gates_f32, x.b * p.beta.sb + t * p.beta.sn + x.h) : 0u;
     }
@@ -760,7 +835,7 @@ __device__ __forceinline__ void role_factors(const Ctx& x, const TcParams& p, in
 }
 
 // Thread t < 64 has token t's row of k·kᵀ, thread 64 + t that of q·kᵀ.
-template <int DK>
+template <int DK, bool SUMMARY>
 __device__ __forceinline__ void role_prep(const Ctx& x, const TcParams& p, int warp, int lane) {
   using F = Cfg<DK>;
   Bars* bars = x.bars;
@@ -824,7 +899,7 @@ __device__ __forceinline__ void role_prep(const Ctx& x, const TcParams& p, int w
 #pragma unroll
         for (int j = 0; j < 16; j += 8) {
           const float w[8] = {v[j], v[j + 1], v[j + 2], v[j + 3], v[j + 4], v[j + 5], v[j + 6], v[j + 7]};
-          sts128(P + sw_chunk(kC, row, 0, (j0 + j) / 8), pack8(w));
+          if (!SUMMARY) sts128(P + sw_chunk(kC, row, 0, (j0 + j) / 8), pack8(w));
         }
       }
     }
@@ -881,7 +956,8 @@ __device__ __forceinline__ void role_prep(const Ctx& x, const TcParams& p, int w
 
 // ------------------------------------------------------------------ kernel
 
-template <int DK>
+// SUMMARY: no output, and one more CTA for each part, which starts from the identity.
+template <int DK, bool SUMMARY>
 __global__ void __launch_bounds__(kThreads, 1)
 chunk_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
              const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mo, const TcParams p) {
@@ -901,16 +977,20 @@ chunk_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUt
       mbar_init(b, 1);
     for (int i = 0; i < kTok; ++i) mbar_init(&bars->f_ready[i], 2);
     for (uint64_t* b : {&bars->g_empty, &bars->t_ready, &bars->qs_read, &bars->pv_read}) mbar_init(b, 4);
-    for (uint64_t* b : {&bars->s_ready, &bars->ks_ready, &bars->w_ready}) mbar_init(b, kStateWarps);
+    for (uint64_t* b : {&bars->s_ready[0], &bars->s_ready[1], &bars->ks_ready, &bars->w_ready}) mbar_init(b, kStateWarps);
     bars->abort = bars->kq_issued = bars->v_issued = 0;
     fence_barrier_init();
     for (const CUtensorMap* m : {&mq, &mk, &mv, &mo}) tma_prefetch_desc(m);
   }
-  // nothing reads v's second slab from global memory where the tile has one: zeros
-  if (p.dv - (int)(blockIdx.x % p.tiles) * 128 <= 64)
-    for (int i = threadIdx.x; i < kVS * kSlab / 16; i += kThreads)
-      *reinterpret_cast<uint4*>(x.sm + F::oV + (2 * (i / (kSlab / 16)) + 1) * kSlab + i % (kSlab / 16) * 16) =
-          make_uint4(0, 0, 0, 0);
+  const int tiles = p.tiles + SUMMARY, parts = p.segs - SUMMARY;
+  x.tile = blockIdx.x % tiles;
+  x.identity = SUMMARY && x.tile == p.tiles;
+  const int part = blockIdx.x / tiles % parts;
+  const int64_t bh = blockIdx.x / tiles / parts;
+  // what is not loaded of the v tiles: zeros
+  const int rest = x.identity ? 0 : p.dv - x.tile * 128 <= 64 ? 1 : 2;
+  for (int i = threadIdx.x; i < kVS * 2 * kSlab / 16; i += kThreads)
+    if (i / (kSlab / 16) % 2 >= rest) *reinterpret_cast<uint4*>(x.sm + F::oV + i * 16) = make_uint4(0, 0, 0, 0);
   fence_proxy_async_smem();
   entry();
   if (warp == kMmaWarp) {
@@ -921,29 +1001,39 @@ chunk_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUt
   __syncthreads();
   tc_fence_after();
   x.tmem = __shfl_sync(0xffffffffu, bars->tmem, 0);   // (known to be the same for the warp)
-  x.tile = blockIdx.x % p.tiles;
-  const int64_t bh = blockIdx.x / p.tiles;
   x.h = (int)(bh % p.Hv);
   x.b = (int)(bh / p.Hv);
-  x.live = live_tokens(p.lengths, x.b, p.n);
+  x.t0 = part * p.seg_tokens;
+  x.end = min(p.n - x.t0, p.seg_tokens);
+  x.live = max(0, min(live_tokens(p.lengths, x.b, p.n) - x.t0, x.end));
   x.chunks = (x.live + kC - 1) / kC;
-  x.partial = x.live % kC != 0 && x.live < p.n;
+  x.partial = x.live % kC != 0 && x.t0 + x.live < p.n;
+  const int64_t state = (int64_t)p.dk * p.dv;
+  x.cols = x.identity ? p.dk : p.dv;
+  if (SUMMARY) {
+    x.s_in = nullptr;
+    x.s_out = x.identity ? p.transition + (bh * parts + part) * p.dk * p.dk : p.added + (bh * parts + part) * state;
+  } else {
+    x.s_in = part ? p.entering + (bh * (parts - 1) + part - 1) * state
+                  : p.state_in ? p.state_in + bh * state : nullptr;
+    x.s_out = part == parts - 1 && p.state_out ? p.state_out + bh * state : nullptr;
+  }
 
   if (warp < kStateWarps) {
     take_registers<DK == 128 ? 120 : 112>();
-    role_state<DK>(x, p, warp, lane);
+    role_state<DK, SUMMARY>(x, p, warp, lane);
   } else if (warp < kOutWarp) {
     take_registers<DK == 128 ? 64 : 72>();
-    role_prep<DK>(x, p, warp, lane);
+    role_prep<DK, SUMMARY>(x, p, warp, lane);
   } else if (warp < kLoadWarp) {
     take_registers<DK == 128 ? 56 : 48>();
-    role_out<DK>(x, p, &mo, warp, lane);
+    if (!SUMMARY) role_out<DK>(x, p, &mo, warp, lane);
   } else {
     take_registers<DK == 128 ? 56 : 64>();
     if (warp == kLoadWarp)
-      role_load<DK>(x, p, &mq, &mk, &mv, lane);
+      role_load<DK, SUMMARY>(x, p, &mq, &mk, &mv, lane);
     else if (warp == kMmaWarp)
-      role_mma<DK>(x, p);
+      role_mma<DK, SUMMARY>(x, p);
     else
       role_factors<DK>(x, p, warp, lane);
   }
@@ -970,8 +1060,89 @@ chunk_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUt
   if (warp == kMmaWarp) tmem_dealloc(x.tmem, 512);
 }
 
+// The states that enter the parts of a sequence, S ← M·S + N over them: a CTA has
+// kJoinCols columns of a head's state, and the next part's M under way while it
+// multiplies with this one's.
+constexpr int kJoinCols = 16, kJoinThreads = 256, kMPitch = 132;
+constexpr int kJoinSmem = (2 * 128 * kMPitch + 2 * 128 * kJoinCols) * 4;
+
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(const float* state_in, const float* added,
+                                                            const float* transition, float* entering, int dk, int dv,
+                                                            int parts) {
+  extern __shared__ float sm[];
+  float* S = sm + 2 * 128 * kMPitch;        // [2][128][kJoinCols]
+  entry();
+  const int blocks = (dv + kJoinCols - 1) / kJoinCols;
+  const int64_t bh = blockIdx.x / blocks;
+  const int c0 = blockIdx.x % blocks * kJoinCols;
+  const int k = threadIdx.x / 2, c = threadIdx.x % 2 * 8;   // this thread's row and columns
+  const bool in = k < dk && c0 + c < dv;                    // dv is a multiple of 8
+  auto fetch = [&](int g) {
+    const float* M = transition + (bh * parts + g) * dk * dk;
+    for (int i = threadIdx.x; i < dk * dk / 4; i += kJoinThreads)
+      cp_async16(smem_u32(sm + (g & 1) * 128 * kMPitch + i / (dk / 4) * kMPitch + i % (dk / 4) * 4), M + i * 4);
+    cp_commit();
+  };
+  auto load8 = [&](const float* p, float (&v)[8]) {
+    const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+  };
+  auto store8 = [&](float* p, const float (&v)[8]) {
+    reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+    reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+  };
+  const int64_t at = (int64_t)k * dv + c0 + c, state = (int64_t)dk * dv;
+  float v[8] = {};
+  if (state_in && in) load8(state_in + bh * state + at, v);
+  store8(S + k * kJoinCols + c, v);
+  fetch(0);
+  for (int g = 0; g < parts; ++g) {
+    if (g + 1 < parts) fetch(g + 1);
+    if (in) load8(added + (bh * parts + g) * state + at, v);
+    if (g + 1 < parts) cp_wait<1>(); else cp_wait<0>();
+    __syncthreads();
+    const float* M = sm + (g & 1) * 128 * kMPitch + k * kMPitch;
+    const float* from = S + (g & 1) * 128 * kJoinCols + c;
+    if (in) {
+      for (int j = 0; j < dk; j += 4) {
+        const float4 m = *reinterpret_cast<const float4*>(M + j);
+        const float mv[4] = {m.x, m.y, m.z, m.w};
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          float w[8];
+          load8(from + (j + u) * kJoinCols, w);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[i] = fmaf(mv[u], w[i], v[i]);
+        }
+      }
+      store8(entering + (bh * parts + g) * state + at, v);
+    }
+    store8(S + ((g + 1) & 1) * 128 * kJoinCols + k * kJoinCols + c, v);
+    __syncthreads();   // before this part's M is overwritten
+  }
+}
+
+// Parts of a sequence: with few heads most SMs would have none, so each sequence is
+// walked twice, first for what every part makes of a state (one CTA more for each
+// part, and no output), then with the states that enter them.  By the µs of a chunk
+// (4.0, and 3.3 without the output) and of joining two parts.
+int parts_of(const DeltaArgs& a, int tiles) {
+  const int64_t heads = a.B * a.Hv, chunks = (a.n + kC - 1) / kC;
+  auto rounds = [&](int64_t ctas) { return (double)((ctas + a.num_sms - 1) / a.num_sms); };
+  int best = 1;
+  double least = rounds(heads * tiles) * chunks * 4.0;
+  for (int g = 2; g <= 64 && g * 4 <= chunks; ++g) {
+    const int64_t part = (chunks + g - 1) / g;
+    if ((chunks + part - 1) / part != g) continue;
+    const double t = rounds(heads * (g - 1) * (tiles + 1)) * part * 3.3 + rounds(heads * g * tiles) * part * 4.0 +
+                     20.0 + rounds(heads * ((a.dv + kJoinCols - 1) / kJoinCols)) * (g - 1) * 3.0;
+    if (t < least) least = t, best = g;
+  }
+  return best;
+}
+
 template <int DK>
-cudaError_t launch_chunks(const DeltaArgs& a, const TcParams& p, cudaStream_t s) {
+cudaError_t launch_chunks(const DeltaArgs& a, TcParams p, cudaStream_t s) {
   CUtensorMap mq, mk, mv, mo;
   cudaError_t e;
   if ((e = tmap_heads(&mq, a.q, a.B, a.n, a.Hk, a.dk, kC, true)) != cudaSuccess ||
@@ -979,11 +1150,41 @@ cudaError_t launch_chunks(const DeltaArgs& a, const TcParams& p, cudaStream_t s)
       (e = tmap_heads(&mv, a.v, a.B, a.n, a.Hv, a.dv, kC, true)) != cudaSuccess ||
       (e = tmap_heads(&mo, a.out, a.B, a.n, a.Hv, a.dv, kOutRows, false)) != cudaSuccess)
     return e;
-  const int64_t ctas = a.B * a.Hv * p.tiles;
-  if (ctas > INT32_MAX) return cudaErrorInvalidConfiguration;
-  static std::atomic<uint64_t> smem_set{0};
-  if ((e = allow_smem((const void*)chunk_kernel<DK>, Cfg<DK>::kSmem, &smem_set)) != cudaSuccess) return e;
-  return launch(chunk_kernel<DK>, (unsigned)ctas, kThreads, Cfg<DK>::kSmem, s, 1, mq, mk, mv, mo, p);
+  const int64_t heads = a.B * a.Hv;
+  p.segs = parts_of(a, p.tiles);
+  p.seg_tokens = (int)(((a.n + kC - 1) / kC + p.segs - 1) / p.segs) * kC;
+  const int64_t ctas = heads * p.segs * p.tiles, first = heads * (p.segs - 1) * (p.tiles + 1);
+  if (ctas > INT32_MAX || first > INT32_MAX) return cudaErrorInvalidConfiguration;
+  static std::atomic<uint64_t> smem_set[3];
+  constexpr int kSmem = Cfg<DK>::kSmem;
+  if ((e = allow_smem((const void*)chunk_kernel<DK, false>, kSmem, smem_set)) != cudaSuccess) return e;
+  float* ws = nullptr;
+  if (p.segs > 1) {
+    if ((e = allow_smem((const void*)chunk_kernel<DK, true>, kSmem, smem_set + 1)) != cudaSuccess ||
+        (e = allow_smem((const void*)join_kernel, kJoinSmem, smem_set + 2)) != cudaSuccess)
+      return e;
+    const int64_t state = (int64_t)a.dk * a.dv, each = heads * (p.segs - 1);
+    if ((e = ws_alloc((void**)&ws, each * (2 * state + (int64_t)a.dk * a.dk) * sizeof(float), s)) != cudaSuccess) {
+      cudaGetLastError();
+      return e;
+    }
+    float* entering = ws + each * state;
+    p.added = ws;
+    p.entering = entering;
+    p.transition = entering + each * state;
+    e = launch(chunk_kernel<DK, true>, (unsigned)first, kThreads, kSmem, s, 1, mq, mk, mv, mo, p);
+    const int64_t blocks = (a.dv + kJoinCols - 1) / kJoinCols;
+    if (e == cudaSuccess)
+      e = launch(join_kernel, (unsigned)(heads * blocks), kJoinThreads, kJoinSmem, s, 1, p.state_in, p.added,
+                 p.transition, entering, a.dk, a.dv, p.segs - 1);
+  }
+  if (e == cudaSuccess)
+    e = launch(chunk_kernel<DK, false>, (unsigned)ctas, kThreads, kSmem, s, 1, mq, mk, mv, mo, p);
+  if (ws) {
+    const cudaError_t f = cudaFreeAsync(ws, s);
+    if (e == cudaSuccess) e = f;
+  }
+  return e;
 }
 
 }  // namespace
