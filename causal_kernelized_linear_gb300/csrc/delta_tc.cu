@@ -72,7 +72,7 @@ struct Bars {
   uint64_t kq_full[kKQ], kq_empty[kKQ], v_full[kVS], v_empty[kVS], f_ready[kTok];
   uint64_t g_full[2], w_full[2];              // by the chunk's parity: each prep warpgroup sees every other one
   uint64_t kq_clean, v_clean;                 // the last chunk's rows past the length are zero
-  uint64_t g_empty, t_ready, s_ready[2], ks_full, ks_ready, qs_full, qs_read, w_ready,
+  uint64_t g_empty, t_ready, s_ready, ks_full, ks_ready, qs_full, qs_read, w_ready,
       upd_full, pv_full, pv_read, done;
   uint32_t tmem;
   int abort;
@@ -197,13 +197,25 @@ struct Ctx {
 };
 
 // mbar_wait and mbar_wait_drain in line, since the compiler refuses calls beside
-// setmaxnreg, and in few instructions: the bound is a number of tests, each of up
-// to a microsecond, and the kernel's end reports the timeout.
-constexpr uint32_t kTests = 4000000;
+// setmaxnreg, and in few instructions.  The bound is a number of tests, of some 50
+// cycles each; the kernel's end reports the timeout.
+constexpr uint32_t kRounds = 20000;
+__device__ __forceinline__ bool round_of_tests(uint64_t* bar, uint32_t parity) {   // 4096 at most
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t.reg .u32 n;\n\tmov.u32 n, 4096;\n"
+      "W:\n\tmbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t@p bra D;\n\t"
+      "sub.u32 n, n, 1;\n\tsetp.ne.u32 q, n, 0;\n\t@q bra W;\n"
+      "D:\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
 __device__ __forceinline__ bool wait_in_line(uint64_t* bar, uint32_t parity, volatile int* abort) {
-  uint32_t n = 0;
-  while (!mbar_try_wait(bar, parity))
-    if (*abort || ++n > kTests) {
+#pragma unroll 1
+  for (uint32_t n = 0; !round_of_tests(bar, parity); ++n)
+    if (*abort || n > kRounds) {
       *abort = 1;
       return false;
     }
@@ -213,14 +225,16 @@ __device__ __forceinline__ bool warp_wait_in_line(uint64_t* bar, uint32_t parity
   return __all_sync(0xffffffffu, wait_in_line(bar, parity, abort));
 }
 __device__ __forceinline__ void drain_in_line(uint64_t* bar, uint32_t parity) {
-  for (uint32_t n = 0; n < kTests / 4 && !mbar_try_wait(bar, parity); ++n) {}
+#pragma unroll 1
+  for (uint32_t n = 0; n < kRounds / 4 && !round_of_tests(bar, parity); ++n) {}
 }
 
 // A role that shares no barrier with other warps returns where a wait gives up;
 // the others (LA_GO_ON) walk on through their remaining barriers, whose waits then
 // end at once: what they write stays within their own buffers and the output.
-#define LA_WAIT(bar, parity) \
-  if (!warp_wait_in_line(&x.bars->bar, (parity) & 1, abort)) return
+#define LA_WAIT_AT(bar, parity) \
+  if (!warp_wait_in_line(bar, (parity) & 1, abort)) return
+#define LA_WAIT(bar, parity) LA_WAIT_AT(&x.bars->bar, parity)
 #define LA_GO_ON(bar, parity) warp_wait_in_line(&x.bars->bar, (parity) & 1, abort)
 
 // ------------------------------------------------------------------ loads
@@ -278,26 +292,34 @@ __device__ __forceinline__ void role_load(const Ctx& x, const TcParams& p, const
 
 // ------------------------------------------------------------------ products
 
-// D[tmem] (+)= A·B by the one thread of the warp for which `lead` is set, without a
-// branch: what the warp has in common then stays in its uniform registers, where
-// the instruction wants its operands.
-__device__ __forceinline__ void warp_mma_ss(uint32_t lead, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
-                                            uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
-      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(lead)
-      : "memory");
-}
-__device__ __forceinline__ void warp_mma_ts(uint32_t lead, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
-                                            uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
-      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(lead)
-      : "memory");
-}
+// A shared-memory operand: of its descriptor (smem_desc) the low word, which holds the
+// address, and the high one, which is the same for a layout.
+struct Operand {
+  uint32_t lo, hi;
+  __device__ __forceinline__ Operand(uint32_t saddr, uint32_t lbo) {
+    const uint64_t d = smem_desc(saddr, lbo, 1024, kSwizzle128B);
+    lo = (uint32_t)d, hi = (uint32_t)(d >> 32);
+  }
+};
 
+// D[tmem] (+)= A·B, B `at_b` bytes (and A `at_a`) into its operand.
+template <bool ACC>
+__device__ __forceinline__ void issue_ss(uint32_t d, const Operand& a, uint32_t at_a, const Operand& b, uint32_t at_b,
+                                         uint32_t idesc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 x, y;\n\tsetp.ne.b32 p, %6, 0;\n\tmov.b64 x, {%1, %2};\n\t"
+      "mov.b64 y, {%3, %4};\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %5, p;\n\t}" ::"r"(d),
+      "r"(a.lo + at_a / 16), "r"(a.hi), "r"(b.lo + at_b / 16), "r"(b.hi), "r"(idesc), "n"(ACC ? 1 : 0)
+      : "memory");
+}
+template <bool ACC>
+__device__ __forceinline__ void issue_ts(uint32_t d, uint32_t a, const Operand& b, uint32_t at_b, uint32_t idesc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 y;\n\tsetp.ne.b32 p, %5, 0;\n\tmov.b64 y, {%2, %3};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %4, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b.lo + at_b / 16), "r"(b.hi), "r"(idesc), "n"(ACC ? 1 : 0)
+      : "memory");
+}
 // (whole warp)  The loops over products are unrolled: an MMA of these takes 32 to 64
 // cycles, and with its operands' addresses computed in a loop it is issued in 130.
 template <int DK, bool SUMMARY>
@@ -311,62 +333,57 @@ __device__ __forceinline__ void role_mma(const Ctx& x, const TcParams& p) {
   constexpr uint32_t id_upd = idesc_bf16_f32(128, DK, false, true);   // k as [token][feature]
   constexpr int KD = DK / 16, KC = kC / 16;
   const uint32_t lead = elect_one();
-  const uint64_t dT = smem_desc(base + F::oT, 16, 1024, kSwizzle128B);
+  const Operand T(base + F::oT, 16);
   // K-step k of a tile with 64 features per slab
   auto kstep = [](int k) { return (uint32_t)((k >> 2) * 2 * kSlab + (k & 3) * 32); };
-  // K-step k of (kS)ᵀ or wᵀ: 32 tokens' hi parts, then their lo parts
-  auto tokens = [](int k) { return (uint32_t)((k >> 1) * 32 + (k & 1) * 8); };
+  // S's hi parts, then its lo parts, with k (at 0) or q
+  auto of_state = [&](uint32_t to, const Operand& b, uint32_t at) {
+    issue_ts<false>(to, tmem + F::SH, b, at, id_nn);
+#pragma unroll
+    for (int i = 1; i < 2 * KD; ++i) issue_ts<true>(to, tmem + F::SH + i * 8, b, at + kstep(i % KD), id_nn);
+  };
+  // K-step k of (kS)ᵀ or wᵀ: 16 tokens' hi parts, then their lo parts
+  auto tokens = [](int k) { return (uint32_t)(k * 16); };
 #pragma unroll 1
   for (int c = -2; c < x.chunks; ++c) {
     if (c >= 0) {
       const uint32_t kq = base + c % kKQ * F::kStage;
-      const uint64_t dK = smem_desc(kq, 16, 1024, kSwizzle128B);
+      const Operand K(kq, 16);
       // (kS)ᵀ = Sᵀ kᵀ
-      LA_WAIT(s_ready[0], c);
+      LA_WAIT(s_ready, c);
       tc_fence_after();
-#pragma unroll
-      for (int k = 0; k < KD; ++k)
-        warp_mma_ts(lead, tmem + F::KS, tmem + F::SH + k * 8, desc_at(dK, kstep(k)), id_nn, k > 0);
-      LA_WAIT(s_ready[1], c);
-      tc_fence_after();
-#pragma unroll
-      for (int k = 0; k < KD; ++k)
-        warp_mma_ts(lead, tmem + F::KS, tmem + F::SL + k * 8, desc_at(dK, kstep(k)), id_nn, 1);
-      if (lead) mma_commit(&bars->ks_full);
+      if (lead) {
+        of_state(tmem + F::KS, K, 0);
+        mma_commit(&bars->ks_full);
+      }
       __syncwarp();
       // wᵀ −= (e^b kS)ᵀ (Tβ)ᵀ: hi·hi, hi·mid, lo·hi; and (qS)ᵀ
       LA_WAIT(ks_ready, c);
       if (!SUMMARY && c >= 1) LA_WAIT(pv_read, c - 1);
       tc_fence_after();
+      if (lead) {
 #pragma unroll
-      for (int part = 0; part < 3; ++part)
+        for (int part = 0; part < 3; ++part)
 #pragma unroll
-        for (int k = 0; k < KC; ++k)
-          warp_mma_ts(lead, tmem + F::W, tmem + F::KS + tokens(k) + (part == 2 ? 16 : 0),
-                      desc_at(dT, (part == 1 ? kSlab : 0) + k * 32), id_nn, 1);
-      if (lead) mma_commit(&bars->w_full[c & 1]);
-      __syncwarp();
-      if constexpr (!SUMMARY) {
-#pragma unroll
-        for (int part = 0; part < 2; ++part)
-#pragma unroll
-          for (int k = 0; k < KD; ++k)
-            warp_mma_ts(lead, tmem + F::PV, tmem + (part ? F::SL : F::SH) + k * 8, desc_at(dK, kSlab + kstep(k)),
-                        id_nn, part | k);
-        if (lead) mma_commit(&bars->qs_full);
-        __syncwarp();
+          for (int k = 0; k < KC; ++k)
+            issue_ts<true>(tmem + F::W, tmem + F::KS + tokens(k) + (part == 2 ? 8 : 0), T,
+                           (part == 1 ? kSlab : 0) + k * 32, id_nn);
+        mma_commit(&bars->w_full[c & 1]);
+        if constexpr (!SUMMARY) {
+          of_state(tmem + F::PV, K, kSlab);
+          mma_commit(&bars->qs_full);
+        }
       }
+      __syncwarp();
       // the state's wᵀk
       LA_WAIT(w_ready, c);
       tc_fence_after();
-      const uint64_t dKt = smem_desc(kq, 2 * kSlab, 1024, kSwizzle128B);
-#pragma unroll
-      for (int part = 0; part < 2; ++part)
-#pragma unroll
-        for (int k = 0; k < KC; ++k)
-          warp_mma_ts(lead, tmem + F::UPD, tmem + F::KS + part * 16 + tokens(k), desc_at(dKt, k * 2048), id_upd,
-                      part | k);
       if (lead) {
+        const Operand Kt(kq, 2 * kSlab);
+        issue_ts<false>(tmem + F::UPD, tmem + F::KS, Kt, 0, id_upd);
+#pragma unroll
+        for (int i = 1; i < 2 * KC; ++i)
+          issue_ts<true>(tmem + F::UPD, tmem + F::KS + tokens(i % KC) + i / KC * 8, Kt, i % KC * 2048, id_upd);
         mma_commit(&bars->upd_full);
         if (SUMMARY) mma_commit(&bars->kq_empty[c % kKQ]);
       }
@@ -375,11 +392,10 @@ __device__ __forceinline__ void role_mma(const Ctx& x, const TcParams& p) {
       if constexpr (!SUMMARY) {
         LA_WAIT(qs_read, c);
         tc_fence_after();
-        const uint64_t dP = smem_desc(base + F::oP + c % kPS * kSlab, 16, 1024, kSwizzle128B);
-#pragma unroll
-        for (int k = 0; k < KC; ++k)
-          warp_mma_ts(lead, tmem + F::PV, tmem + F::W + tokens(k), desc_at(dP, k * 32), id_nn, 1);
         if (lead) {
+          const Operand P(base + F::oP + c % kPS * kSlab, 16);
+#pragma unroll
+          for (int k = 0; k < KC; ++k) issue_ts<true>(tmem + F::PV, tmem + F::W + tokens(k), P, k * 32, id_nn);
           mma_commit(&bars->pv_full);
           mma_commit(&bars->kq_empty[c % kKQ]);   // and the chunk's factors
         }
@@ -394,11 +410,13 @@ __device__ __forceinline__ void role_mma(const Ctx& x, const TcParams& p) {
       if (x.partial && g == x.chunks - 1) LA_WAIT(kq_clean, 0);
       if (g >= 1) LA_WAIT(g_empty, g - 1);
       tc_fence_after();
-      const uint64_t d = smem_desc(base + g % kKQ * F::kStage, 16, 1024, kSwizzle128B);
+      if (lead) {
+        const Operand d(base + g % kKQ * F::kStage, 16);
+        issue_ss<false>(tmem + F::G, d, 0, d, 0, id_nn);
 #pragma unroll
-      for (int k = 0; k < KD; ++k)
-        warp_mma_ss(lead, tmem + F::G, desc_at(d, kstep(k)), desc_at(d, kstep(k)), id_nn, k > 0);
-      if (lead) mma_commit(&bars->g_full[g & 1]);
+        for (int k = 1; k < KD; ++k) issue_ss<true>(tmem + F::G, d, kstep(k), d, kstep(k), id_nn);
+        mma_commit(&bars->g_full[g & 1]);
+      }
       __syncwarp();
     }
     // wᵀ = vᵀ (Tβ)ᵀ, whose columns (P w)ᵀ has read
@@ -411,13 +429,14 @@ __device__ __forceinline__ void role_mma(const Ctx& x, const TcParams& p) {
       }
       if (!SUMMARY && n >= 1) LA_WAIT(pv_full, n - 1);   // (else the state's warps have read them)
       tc_fence_after();
-      const uint64_t dV = smem_desc(base + F::oV + n % kVS * 2 * kSlab, kSlab, 1024, kSwizzle128B);
+      if (lead) {
+        const Operand V(base + F::oV + n % kVS * 2 * kSlab, kSlab);
+        issue_ss<false>(tmem + F::W, V, 0, T, 0, id_v);
 #pragma unroll
-      for (int part = 0; part < 3; ++part)
-#pragma unroll
-        for (int k = 0; k < KC; ++k)
-          warp_mma_ss(lead, tmem + F::W, desc_at(dV, k * 2048), desc_at(dT, part * kSlab + k * 32), id_v, part | k);
-      if (lead) mma_commit(&bars->v_empty[n % kVS]);
+        for (int i = 1; i < 3 * KC; ++i)
+          issue_ss<true>(tmem + F::W, V, i % KC * 2048, T, i / KC * kSlab + i % KC * 32, id_v);
+        mma_commit(&bars->v_empty[n % kVS]);
+      }
       __syncwarp();
     }
   }
@@ -464,87 +483,53 @@ __device__ __forceinline__ void role_state(const Ctx& x, const TcParams& p, int 
     for (int i = 0; i < 16; ++i) S[j / 2 + i] = pair_of(r, 2 * i);
   }
 
-  // S as the next products' operand: the hi parts first, for which they start
-  auto publish = [&] {
-#pragma unroll
-    for (int part = 0; part < 2; ++part) {
-#pragma unroll
-      for (int j = 0; j < kCols; j += 16) {
-        uint32_t w[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          float v0, v1;
-          if (part == 0) {
-            unpack2(S[j / 2 + i], v0, v1);
-            w[i] = pack_bf16x2(v0, v1);
-          } else {
-            uint32_t hi;
-            split2(S[j / 2 + i], hi, w[i]);
-          }
-        }
-        tmem_st8(at + (part ? F::SL : F::SH) + (k0 + j) / 2, w);
-      }
-      tmem_st_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bars->s_ready[part]);
-    }
-  };
 #pragma unroll 1
   for (int c = 0; c < x.chunks; ++c) {
-    publish();
+    // S as the next products' operand
+#pragma unroll
+    for (int j = 0; j < kCols; j += 16) {
+      uint32_t hi[8], lo[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) split2(S[j / 2 + i], hi[i], lo[i]);
+      tmem_st8(at + F::SH + (k0 + j) / 2, hi);
+      tmem_st8(at + F::SL + (k0 + j) / 2, lo);
+    }
+    tmem_st_wait();
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&bars->s_ready);
     const TokenFactors& tok = x.tok[c % kTok];   // overwritten after the chunk's last product
     LA_WAIT(f_ready[c % kTok], c / kTok);
-    LA_WAIT(ks_full, c);
-    tc_fence_after();
-    {
-      uint32_t r[32];
-      tmem_ld32(at + F::KS + half * 32, r);
-      tmem_ld_wait();
-#pragma unroll
-      for (int j = 0; j < 16; j += 8) {
-        uint32_t hi[8], lo[8];
-#pragma unroll
-        for (int i = 0; i < 8; i += 2) {
-          const ulonglong2 f = *reinterpret_cast<const ulonglong2*>(&tok.ks[half * 32 + 2 * (j + i)]);
-          split2(mul2(pair_of(r, 2 * (j + i)), f.x), hi[i], lo[i]);
-          split2(mul2(pair_of(r, 2 * (j + i) + 2), f.y), hi[i + 1], lo[i + 1]);
-        }
-        tmem_st8(at + F::KS + half * 32 + j, hi);
-        tmem_st8(at + F::KS + half * 32 + 16 + j, lo);
-      }
-      tmem_st_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bars->ks_ready);
-    }
-    LA_WAIT(w_full[c & 1], c / 2);
-    tc_fence_after();
+    // (kS)ᵀ, then wᵀ, times a factor of each token as operands in two parts, 16 tokens at a time
     const f32x2 carry = pack2(tok.carry, tok.carry);
-    {
-      uint32_t r[32];
-      tmem_ld32(at + F::W + half * 32, r);
-      tmem_ld_wait();
-#pragma unroll
-      for (int j = 0; j < 16; j += 8) {
-        uint32_t hi[8], lo[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          hi[i] = pack_bf16x2(__uint_as_float(r[2 * (j + i)]), __uint_as_float(r[2 * (j + i) + 1]));
-        if (!SUMMARY) tmem_st8(at + F::W + half * 32 + j, hi);   // for the output
+#pragma unroll 1
+    for (int of_w = 0; of_w < 2; ++of_w) {
+      LA_WAIT_AT(of_w ? &bars->w_full[c & 1] : &bars->ks_full, of_w ? c / 2 : c);
+      tc_fence_after();
+      const float* factors = of_w ? tok.left : tok.ks;
+#pragma unroll 1
+      for (int t = half * 32; t < half * 32 + 32; t += 16) {
+        uint32_t r[16], hi[8], lo[8];
+        tmem_ld16(at + (of_w ? F::W : F::KS) + t, r);
+        tmem_ld_wait();
 #pragma unroll
         for (int i = 0; i < 8; i += 2) {
-          const ulonglong2 f = *reinterpret_cast<const ulonglong2*>(&tok.left[half * 32 + 2 * (j + i)]);
-          split2(mul2(pair_of(r, 2 * (j + i)), f.x), hi[i], lo[i]);
-          split2(mul2(pair_of(r, 2 * (j + i) + 2), f.y), hi[i + 1], lo[i + 1]);
+          const ulonglong2 f = *reinterpret_cast<const ulonglong2*>(factors + t + 2 * i);
+          split2(mul2(pair_of(r, 2 * i), f.x), hi[i], lo[i]);
+          split2(mul2(pair_of(r, 2 * i + 2), f.y), hi[i + 1], lo[i + 1]);
         }
-        tmem_st8(at + F::KS + half * 32 + j, hi);
-        tmem_st8(at + F::KS + half * 32 + 16 + j, lo);
+        tmem_st8(at + F::KS + t, hi);
+        tmem_st8(at + F::KS + t + 8, lo);
+        if (!SUMMARY && of_w) {   // for the output
+#pragma unroll
+          for (int i = 0; i < 8; ++i) hi[i] = pack_bf16x2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
+          tmem_st8(at + F::W + t, hi);
+        }
       }
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&bars->w_ready);
+      if (lane == 0) mbar_arrive(of_w ? &bars->w_ready : &bars->ks_ready);
     }
     LA_WAIT(upd_full, c);
     tc_fence_after();
@@ -977,7 +962,7 @@ chunk_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUt
       mbar_init(b, 1);
     for (int i = 0; i < kTok; ++i) mbar_init(&bars->f_ready[i], 2);
     for (uint64_t* b : {&bars->g_empty, &bars->t_ready, &bars->qs_read, &bars->pv_read}) mbar_init(b, 4);
-    for (uint64_t* b : {&bars->s_ready[0], &bars->s_ready[1], &bars->ks_ready, &bars->w_ready}) mbar_init(b, kStateWarps);
+    for (uint64_t* b : {&bars->s_ready, &bars->ks_ready, &bars->w_ready}) mbar_init(b, kStateWarps);
     bars->abort = bars->kq_issued = bars->v_issued = 0;
     fence_barrier_init();
     for (const CUtensorMap* m : {&mq, &mk, &mv, &mo}) tma_prefetch_desc(m);
