@@ -1,11 +1,18 @@
 // The gated delta rule token by token on the CUDA cores:
 //   w_t = β_t(v_t − k_t(α_t S_{t−1})),  S_t = α_t S_{t−1} + k_tᵀ w_t,  o_t = scale·q_t S_t.
 //
-// The columns of S do not meet: a warp has a few of them (16 for dk = 128) with
+// recurrent_kernel (several tokens).  The columns of S do not meet: a warp has a few of them (16 for dk = 128) with
 // all their rows, 16 rows by 4 columns to a lane, and walks the tokens with S in
 // registers.  k·S and q·S of the state before the token are summed together over
 // the P = dk/16 lanes that share a column; o_t = scale·(α q·S_{t−1} + (q·k) w_t)
 // needs no second pass over S, so the next token's sums wait for w_t alone.
+//
+// step_kernel (one token) is bound by reading and writing S, 128 KB for a head of
+// 128×128.  A CTA has 128 columns (or 64) of one head's S with all rows, in the
+// registers of 256 threads: warps read whole rows of 512 bytes, all loads of a thread
+// are issued before anything waits for one, and the sums over rows go through shared
+// memory once.
+//
 // Everything is fp32.
 #include "block.cuh"
 #include "internal.h"
@@ -223,6 +230,114 @@ __global__ void __launch_bounds__(kThreads) recurrent_kernel(const DeltaParams p
   }
 }
 
+// ------------------------------------------------------------------ one token
+
+constexpr int kStepThreads = 256;
+
+// CG groups of four columns, RPT rows per thread.
+template <typename T, int CG, int RPT>
+__global__ void __launch_bounds__(kStepThreads, RPT > 16 ? 1 : 2) step_kernel(const DeltaParams p) {
+  constexpr int RG = kStepThreads / CG, kRows = RG * RPT;
+  __shared__ float4 part[2][RG][CG];
+  __shared__ float ks[kRows], qs[kRows];
+  __shared__ float red[3][kStepThreads / 32];
+  entry();
+  const int slice = (int)(blockIdx.x % p.slices);
+  const int64_t bh = blockIdx.x / p.slices, b = bh / p.Hv;
+  const int h = (int)(bh % p.Hv), hk = h / (p.Hv / p.Hk);
+  const int t = threadIdx.x, cg = t % CG, rg = t / CG;
+  const int col = (slice * CG + cg) * 4;
+  const bool in = col < p.dv;
+  const float* from = p.state_in + bh * p.dk * p.dv + col;
+  float* to = p.state_out + bh * p.dk * p.dv + col;
+  float4 S[RPT];
+#pragma unroll
+  for (int i = 0; i < RPT; ++i) {
+    const int r = i * RG + rg;
+    S[i] = in && r < p.dk ? __ldcs(reinterpret_cast<const float4*>(from + (int64_t)r * p.dv)) : make_float4(0, 0, 0, 0);
+  }
+  // k and q, their lengths and product; one element of each per thread
+  const T* kp = static_cast<const T*>(p.k.data) + b * p.k.sb + (int64_t)hk * p.k.sh;
+  const T* qp = static_cast<const T*>(p.q.data) + b * p.q.sb + (int64_t)hk * p.q.sh;
+  const float ke = t < p.dk ? to_f32(kp[t]) : 0.f, qe = t < p.dk ? to_f32(qp[t]) : 0.f;
+  const float2 g = gates(p, b, 0, h);
+  Raw4<T> vr;
+  if (in) vr.load(static_cast<const T*>(p.v.data) + b * p.v.sb + (int64_t)h * p.v.sh + col);
+  if (t < kRows) ks[t] = ke, qs[t] = qe;
+  const float kk = sum_lanes<32>(ke * ke), qq = sum_lanes<32>(qe * qe), qk = sum_lanes<32>(qe * ke);
+  if (t % 32 == 0) red[0][t / 32] = kk, red[1][t / 32] = qq, red[2][t / 32] = qk;
+  __syncthreads();
+  float4 a = make_float4(0, 0, 0, 0), c = a;   // k·S and q·S
+#pragma unroll
+  for (int i = 0; i < RPT; ++i) {
+    const float k = ks[i * RG + rg], q = qs[i * RG + rg];
+    a.x = fmaf(k, S[i].x, a.x), a.y = fmaf(k, S[i].y, a.y), a.z = fmaf(k, S[i].z, a.z), a.w = fmaf(k, S[i].w, a.w);
+    c.x = fmaf(q, S[i].x, c.x), c.y = fmaf(q, S[i].y, c.y), c.z = fmaf(q, S[i].z, c.z), c.w = fmaf(q, S[i].w, c.w);
+  }
+  part[0][rg][cg] = a;
+  part[1][rg][cg] = c;
+  float s[3] = {};
+#pragma unroll
+  for (int i = 0; i < kStepThreads / 32; ++i) s[0] += red[0][i], s[1] += red[1][i], s[2] += red[2][i];
+  const float rk = p.normalize ? rsqrtf(s[0] + 1e-6f) : 1.f;
+  const float rq = p.scale * (p.normalize ? rsqrtf(s[1] + 1e-6f) : 1.f);
+  __syncthreads();
+  float ksum[4] = {}, qsum[4] = {};
+#pragma unroll
+  for (int r = 0; r < RG; ++r) {
+    const float4 x = part[0][r][cg];
+    ksum[0] += x.x, ksum[1] += x.y, ksum[2] += x.z, ksum[3] += x.w;
+  }
+  if (rg == 0)
+#pragma unroll
+    for (int r = 0; r < RG; ++r) {
+      const float4 x = part[1][r][cg];
+      qsum[0] += x.x, qsum[1] += x.y, qsum[2] += x.z, qsum[3] += x.w;
+    }
+  float v[4], w[4];
+  unpack2(vr.lo(), v[0], v[1]);
+  unpack2(vr.hi(), v[2], v[3]);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) w[j] = rk * (g.y * (v[j] - g.x * (rk * ksum[j])));
+#pragma unroll
+  for (int i = 0; i < RPT; ++i) {
+    const int r = i * RG + rg;
+    const float k = ks[r];
+    const float4 n = make_float4(fmaf(k, w[0], g.x * S[i].x), fmaf(k, w[1], g.x * S[i].y),
+                                 fmaf(k, w[2], g.x * S[i].z), fmaf(k, w[3], g.x * S[i].w));
+    if (in && r < p.dk) __stcs(reinterpret_cast<float4*>(to + (int64_t)r * p.dv), n);
+  }
+  if (rg == 0 && in) {
+    T* op = static_cast<T*>(const_cast<void*>(p.out.data)) + b * p.out.sb + (int64_t)h * p.out.sh + col;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) op[j] = from_f32<T>(rq * (g.x * qsum[j] + s[2] * w[j]));
+  }
+}
+
+template <typename T, int CG, int RPT>
+cudaError_t launch_step(const DeltaArgs& a, DeltaParams p, cudaStream_t s) {
+  p.slices = (a.dv + 4 * CG - 1) / (4 * CG);
+  const int64_t ctas = a.B * a.Hv * p.slices;
+  if (ctas > INT32_MAX) return cudaErrorInvalidConfiguration;
+  return launch(step_kernel<T, CG, RPT>, (unsigned)ctas, kStepThreads, 0, s, 1, p);
+}
+
+template <typename T>
+cudaError_t step(const DeltaArgs& a, const DeltaParams& p, cudaStream_t s) {
+  // 128 columns at a time, 64 where that leaves fewer of them without work
+  const int rest = a.dv % 128;
+  if (rest && rest <= 64) {
+    if (a.dk <= 64) return launch_step<T, 16, 4>(a, p, s);
+    if (a.dk <= 128) return launch_step<T, 16, 8>(a, p, s);
+    return launch_step<T, 16, 16>(a, p, s);
+  }
+  if (a.dk <= 64) return launch_step<T, 32, 8>(a, p, s);
+  if (a.dk <= 128) return launch_step<T, 32, 16>(a, p, s);
+  return launch_step<T, 32, 32>(a, p, s);
+}
+
+// ------------------------------------------------------------------ several tokens
+
 template <typename T, int P>
 cudaError_t launch_recurrent(const DeltaArgs& a, DeltaParams p, cudaStream_t s) {
   p.slices = (a.dv + 128 / P - 1) / (128 / P);
@@ -252,6 +367,7 @@ cudaError_t gated_delta(const DeltaArgs& a, cudaStream_t s) {
   p.scale = a.scale;
   p.gates_f32 = a.gates_f32, p.softplus = a.softplus, p.sigmoid = a.sigmoid;
   p.normalize = a.normalize;
+  if (a.n == 1 && a.state_in && a.state_out && !a.lengths) return a.bf16 ? step<bf16>(a, p, s) : step<float>(a, p, s);
   return a.bf16 ? by_keys<bf16>(a, p, s) : by_keys<float>(a, p, s);
 }
 

@@ -21,8 +21,8 @@
 // are split into two bf16 parts (2^-16 of a value is lost) and T into three (2^-24),
 // which keeps the state within about 3e-6 of itself however long the sequence (4e-6
 // with two parts of T, 1e-6 with three of w as well, whose products would take 256
-// more of a chunk's cycles on the tensor cores).  P and the output's w are rounded
-// to bf16 once, as the output is.
+// more of a chunk's cycles on the tensor cores).  P is rounded to bf16 once, as the
+// output is.
 //
 // Roles: warps 0-7 S (two per quarter of the rows), 8-11 and 12-15 T and P of every
 // other chunk, 16-19 the output, 20 loads, 21 MMAs, 22 and 23 decays and lengths.  Their loops
@@ -395,7 +395,8 @@ __device__ __forceinline__ void role_mma(const Ctx& x, const TcParams& p) {
         if (lead) {
           const Operand P(base + F::oP + c % kPS * kSlab, 16);
 #pragma unroll
-          for (int k = 0; k < KC; ++k) issue_ts<true>(tmem + F::PV, tmem + F::W + tokens(k), P, k * 32, id_nn);
+          for (int i = 0; i < 2 * KC; ++i)
+            issue_ts<true>(tmem + F::PV, tmem + F::W + tokens(i % KC) + i / KC * 8, P, i % KC * 32, id_nn);
           mma_commit(&bars->pv_full);
           mma_commit(&bars->kq_empty[c % kKQ]);   // and the chunk's factors
         }
@@ -522,8 +523,9 @@ __device__ __forceinline__ void role_state(const Ctx& x, const TcParams& p, int 
         tmem_st8(at + F::KS + t + 8, lo);
         if (!SUMMARY && of_w) {   // for the output
 #pragma unroll
-          for (int i = 0; i < 8; ++i) hi[i] = pack_bf16x2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
+          for (int i = 0; i < 8; ++i) split2(pair_of(r, 2 * i), hi[i], lo[i]);
           tmem_st8(at + F::W + t, hi);
+          tmem_st8(at + F::W + t + 8, lo);
         }
       }
       tmem_st_wait();

@@ -22,7 +22,7 @@ using namespace block;
 using bf16 = __nv_bfloat16;
 
 constexpr int kMaxVectors = 8;          // of a thread
-constexpr int kMaxThreads = 1024;
+constexpr int kMaxThreads = 1024, kMidThreads = 256;
 constexpr int kWarpsPerCta = 4;         // rows of a CTA where a warp has one
 
 struct NormParams {
@@ -39,6 +39,9 @@ struct NormParams {
 
 // How a group's sum is taken.
 enum Sums { kLanes, kRow, kShared };
+// What a row has: a warp, up to kMidThreads or up to kMaxThreads (whose registers hold
+// fewer vectors each).
+enum Width { kWarp, kMid, kBig };
 
 __device__ __forceinline__ float max_nan(float a, float b) {   // NaN wins
   float r;
@@ -68,10 +71,11 @@ __device__ __forceinline__ float over_row(float v, float* part, F f) {
   return v;
 }
 
-template <typename T, int NV, bool WARP, int SUMS, bool E4M3>
-__global__ void __launch_bounds__(WARP ? 32 * kWarpsPerCta : kMaxThreads)
+template <typename T, int NV, int WIDTH, int SUMS, bool E4M3, bool GATE>
+__global__ void __launch_bounds__(WIDTH == kWarp ? 32 * kWarpsPerCta : WIDTH == kMid ? kMidThreads : kMaxThreads)
 norm_kernel(const NormParams p) {
   constexpr int V = kVec<T>;
+  constexpr bool WARP = WIDTH == kWarp;
   extern __shared__ float sums[];       // kShared: a vector's sum, then a group's factor
   __shared__ float part[2][32];
   entry();
@@ -81,14 +85,16 @@ norm_kernel(const NormParams p) {
 
   const T* xp = static_cast<const T*>(p.x.data) + row * p.x.sn;
   const T* rp = p.residual.data ? static_cast<const T*>(p.residual.data) + row * p.residual.sn : nullptr;
-  const T* gp = p.gate.data ? static_cast<const T*>(p.gate.data) + row * p.gate.sn : nullptr;
-  uint4 xr[NV], rr[NV];
+  const T* gp = static_cast<const T*>(p.gate.data) + row * p.gate.sn;
+  uint4 xr[NV], rr[NV], gr[NV];
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int c = i * R + at;
     const bool in = c < p.vectors;
     xr[i] = in ? *reinterpret_cast<const uint4*>(xp + c * V) : make_uint4(0, 0, 0, 0);
     if (rp) rr[i] = in ? *reinterpret_cast<const uint4*>(rp + c * V) : make_uint4(0, 0, 0, 0);
+    // the gate is wanted after the sums, and under way before them
+    if (GATE) gr[i] = in ? *reinterpret_cast<const uint4*>(gp + c * V) : make_uint4(0, 0, 0, 0);
   }
   float h[NV][V], sq[NV];
 #pragma unroll
@@ -157,9 +163,9 @@ norm_kernel(const NormParams p) {
 #pragma unroll
       for (int j = 0; j < V; ++j) h[i][j] *= w[j];
     }
-    if (gp) {
+    if constexpr (GATE) {
       float g[V];
-      unpack<T>(*reinterpret_cast<const uint4*>(gp + c * V), g);
+      unpack<T>(gr[i], g);
 #pragma unroll
       for (int j = 0; j < V; ++j) h[i][j] *= silu(g[j]);
     }
@@ -194,36 +200,49 @@ norm_kernel(const NormParams p) {
   }
 }
 
-template <typename T, int NV, bool WARP, bool E4M3>
+template <typename T, int NV, int WIDTH, bool E4M3, bool GATE>
 cudaError_t launch_norm(const NormParams& p, int threads, cudaStream_t s) {
+  constexpr bool WARP = WIDTH == kWarp;
   const int64_t ctas = WARP ? (p.M + kWarpsPerCta - 1) / kWarpsPerCta : p.M;
-  if (ctas > INT32_MAX) return cudaErrorInvalidConfiguration;
+  if (p.M > INT32_MAX) return cudaErrorInvalidConfiguration;
   const unsigned n = (unsigned)ctas, th = WARP ? 32 * kWarpsPerCta : threads;
-  if (p.group == p.vectors) return launch(norm_kernel<T, NV, WARP, kRow, E4M3>, n, th, 0, s, 1, p);
+  if (p.group == p.vectors) return launch(norm_kernel<T, NV, WIDTH, kRow, E4M3, GATE>, n, th, 0, s, 1, p);
   if (p.group <= 32 && (p.group & (p.group - 1)) == 0)
-    return launch(norm_kernel<T, NV, WARP, kLanes, E4M3>, n, th, 0, s, 1, p);
-  return launch(norm_kernel<T, NV, false, kShared, E4M3>, (unsigned)p.M, threads,
+    return launch(norm_kernel<T, NV, WIDTH, kLanes, E4M3, GATE>, n, th, 0, s, 1, p);
+  return launch(norm_kernel<T, NV, WARP ? kMid : WIDTH, kShared, E4M3, GATE>, (unsigned)p.M, threads,
                 (p.vectors + p.vectors / p.group) * sizeof(float), s, 1, p);
 }
 
-template <typename T, bool E4M3>
+template <typename T, bool E4M3, bool GATE>
 cudaError_t by_width(const NormArgs& a, NormParams p, cudaStream_t s) {
   constexpr int V = kVec<T>;
   p.vectors = a.D / V;
   p.group = a.group / V;
-  // threads of a row: a warp while eight vectors of each lane hold it
+  // threads of a row: a warp while eight vectors of each lane hold it (four with a
+  // gate, whose vectors are held too)
   int threads = 32;
-  while (threads < kMaxThreads && p.vectors > kMaxVectors * threads) threads *= 2;
+  const int most = GATE ? kMaxVectors / 2 : kMaxVectors;
+  while (threads < kMaxThreads && p.vectors > most * threads) threads *= 2;
   const int nv = (p.vectors + threads - 1) / threads;
   if (nv > kMaxVectors) return cudaErrorInvalidConfiguration;
   if (threads == 32) {
-    if (nv <= 1) return launch_norm<T, 1, true, E4M3>(p, threads, s);
-    if (nv <= 2) return launch_norm<T, 2, true, E4M3>(p, threads, s);
-    if (nv <= 4) return launch_norm<T, 4, true, E4M3>(p, threads, s);
-    return launch_norm<T, 8, true, E4M3>(p, threads, s);
+    if (nv <= 2) return launch_norm<T, 2, kWarp, E4M3, GATE>(p, threads, s);
+    if (nv <= 4) return launch_norm<T, 4, kWarp, E4M3, GATE>(p, threads, s);
+    return launch_norm<T, 8, kWarp, E4M3, GATE>(p, threads, s);
   }
-  if (nv <= 4) return launch_norm<T, 4, false, E4M3>(p, threads, s);
-  return launch_norm<T, 8, false, E4M3>(p, threads, s);
+  if (threads <= kMidThreads) {
+    if (nv <= 4) return launch_norm<T, 4, kMid, E4M3, GATE>(p, threads, s);
+    return launch_norm<T, 8, kMid, E4M3, GATE>(p, threads, s);
+  }
+  if (nv <= 4) return launch_norm<T, 4, kBig, E4M3, GATE>(p, threads, s);
+  return launch_norm<T, 8, kBig, E4M3, GATE>(p, threads, s);
+}
+
+template <typename T>
+cudaError_t by_kind(const NormArgs& a, const NormParams& p, cudaStream_t s) {
+  const bool gate = p.gate.data != nullptr;
+  if (a.quantize) return gate ? by_width<T, true, true>(a, p, s) : by_width<T, true, false>(a, p, s);
+  return gate ? by_width<T, false, true>(a, p, s) : by_width<T, false, false>(a, p, s);
 }
 
 }  // namespace
@@ -242,8 +261,7 @@ cudaError_t rms_norm(const NormArgs& a, cudaStream_t s) {
   p.M = a.M;
   p.inv_group = 1.f / (float)a.group;
   p.eps = a.eps;
-  if (a.bf16) return a.quantize ? by_width<bf16, true>(a, p, s) : by_width<bf16, false>(a, p, s);
-  return a.quantize ? by_width<float, true>(a, p, s) : by_width<float, false>(a, p, s);
+  return a.bf16 ? by_kind<bf16>(a, p, s) : by_kind<float>(a, p, s);
 }
 
 }  // namespace la
