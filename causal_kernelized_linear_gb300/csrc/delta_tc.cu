@@ -1142,39 +1142,50 @@ cudaError_t launch_chunks(const DeltaArgs& a, TcParams p, cudaStream_t s) {
   p.seg_tokens = (int)(((a.n + kC - 1) / kC + p.segs - 1) / p.segs) * kC;
   const int64_t ctas = heads * p.segs * p.tiles, first = heads * (p.segs - 1) * (p.tiles + 1);
   if (ctas > INT32_MAX || first > INT32_MAX) return cudaErrorInvalidConfiguration;
-  static std::atomic<uint64_t> smem_set[3];
+  static std::atomic<uint64_t> smem_set[2];
   constexpr int kSmem = Cfg<DK>::kSmem;
   if ((e = allow_smem((const void*)chunk_kernel<DK, false>, kSmem, smem_set)) != cudaSuccess) return e;
-  float* ws = nullptr;
+  DeltaParts w{};
   if (p.segs > 1) {
     if ((e = allow_smem((const void*)chunk_kernel<DK, true>, kSmem, smem_set + 1)) != cudaSuccess ||
-        (e = allow_smem((const void*)join_kernel, kJoinSmem, smem_set + 2)) != cudaSuccess)
+        (e = delta_parts(a, p.segs, &w, s)) != cudaSuccess)
       return e;
-    const int64_t state = (int64_t)a.dk * a.dv, each = heads * (p.segs - 1);
-    if ((e = ws_alloc((void**)&ws, each * (2 * state + (int64_t)a.dk * a.dk) * sizeof(float), s)) != cudaSuccess) {
-      cudaGetLastError();
-      return e;
-    }
-    float* entering = ws + each * state;
-    p.added = ws;
-    p.entering = entering;
-    p.transition = entering + each * state;
+    p.added = w.added, p.transition = w.transition, p.entering = w.entering;
     e = launch(chunk_kernel<DK, true>, (unsigned)first, kThreads, kSmem, s, 1, mq, mk, mv, mo, p);
-    const int64_t blocks = (a.dv + kJoinCols - 1) / kJoinCols;
-    if (e == cudaSuccess)
-      e = launch(join_kernel, (unsigned)(heads * blocks), kJoinThreads, kJoinSmem, s, 1, p.state_in, p.added,
-                 p.transition, entering, a.dk, a.dv, p.segs - 1);
+    if (e == cudaSuccess) e = delta_join(a, p.segs, w, s);
   }
   if (e == cudaSuccess)
     e = launch(chunk_kernel<DK, false>, (unsigned)ctas, kThreads, kSmem, s, 1, mq, mk, mv, mo, p);
-  if (ws) {
-    const cudaError_t f = cudaFreeAsync(ws, s);
+  if (w.added) {
+    const cudaError_t f = cudaFreeAsync(w.added, s);
     if (e == cudaSuccess) e = f;
   }
   return e;
 }
 
 }  // namespace
+
+cudaError_t delta_parts(const DeltaArgs& a, int parts, DeltaParts* w, cudaStream_t s) {
+  const int64_t each = a.B * a.Hv * (parts - 1), state = (int64_t)a.dk * a.dv;
+  const cudaError_t e = ws_alloc((void**)&w->added, each * (2 * state + (int64_t)a.dk * a.dk) * sizeof(float), s);
+  if (e != cudaSuccess) {
+    cudaGetLastError();
+    return e;
+  }
+  w->entering = w->added + each * state;
+  w->transition = w->entering + each * state;
+  return e;
+}
+
+cudaError_t delta_join(const DeltaArgs& a, int parts, const DeltaParts& w, cudaStream_t s) {
+  static std::atomic<uint64_t> smem_set{0};
+  const cudaError_t e = allow_smem((const void*)join_kernel, kJoinSmem, &smem_set);
+  if (e != cudaSuccess) return e;
+  const int64_t ctas = a.B * a.Hv * ((a.dv + kJoinCols - 1) / kJoinCols);
+  if (ctas > INT32_MAX) return cudaErrorInvalidConfiguration;
+  return launch(join_kernel, (unsigned)ctas, kJoinThreads, kJoinSmem, s, 1, a.state_in, w.added, w.transition,
+                w.entering, a.dk, a.dv, parts - 1);
+}
 
 bool tc_gated_delta_supported(const DeltaArgs& a) {
   // a tensor map has strides below 2^40 bytes; tokens that are all one row go by themselves

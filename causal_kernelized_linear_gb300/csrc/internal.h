@@ -331,6 +331,15 @@ struct DeltaArgs {
   int num_sms;
 };
 cudaError_t gated_delta(const DeltaArgs& a, cudaStream_t stream);
+// Sequences in parts, where there are few heads: for every part but the last what it
+// makes of a zero state (added, [dk, dv]) and of the identity (transition, [dk, dk]),
+// and by delta_join the states that enter all but the first.  One allocation of the
+// stream, at `added`.  dk ≤ 128.
+struct DeltaParts {
+  float *added, *entering, *transition;
+};
+cudaError_t delta_parts(const DeltaArgs& a, int parts, DeltaParts* w, cudaStream_t stream);
+cudaError_t delta_join(const DeltaArgs& a, int parts, const DeltaParts& w, cudaStream_t stream);
 // In chunks of 64 tokens on the tensor cores (bf16), where the views and sizes allow it.
 bool tc_gated_delta_supported(const DeltaArgs& a);
 cudaError_t tc_gated_delta(const DeltaArgs& a, cudaStream_t stream);
