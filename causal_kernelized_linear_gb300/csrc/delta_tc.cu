@@ -47,8 +47,8 @@ using bf16 = __nv_bfloat16;
 constexpr int kC = 64;                        // tokens of a chunk
 constexpr int kThreads = 24 * 32;
 constexpr int kStateWarps = 8, kPrepWarp = 8, kOutWarp = 16, kLoadWarp = 20, kMmaWarp = 21, kFactorWarp = 22;
-constexpr int kKQ = 3, kVS = 2, kTok = 3, kPS = 2;   // stages: k and q tiles, v tiles, token factors, P
-constexpr int kOutRows = 32;                  // tokens that are stored at once
+constexpr int kKQ = 3, kVS = 2, kTok = 3, kPS = 3;   // stages: k and q tiles, v tiles, token factors, P
+constexpr int kOutRows = 16;                  // tokens that are stored at once
 constexpr int kSlab = kC * 128;               // 8 KB: 64 tokens × 64 features
 constexpr int kAPitch = 68;                   // floats of a row of A
 
@@ -357,9 +357,25 @@ __device__ __forceinline__ void role_mma(const Ctx& x, const TcParams& p) {
         mma_commit(&bars->ks_full);
       }
       __syncwarp();
-      // wᵀ −= (e^b kS)ᵀ (Tβ)ᵀ: hi·hi, hi·mid, lo·hi; and (qS)ᵀ
+      // wᵀ = vᵀ (Tβ)ᵀ, whose columns (P w)ᵀ has read, while (kS)ᵀ is made an operand
+      LA_WAIT(t_ready, c);
+      if (!(SUMMARY && x.identity)) {
+        LA_WAIT(v_full[c % kVS], c / kVS);
+        if (x.partial && c == x.chunks - 1) LA_WAIT(v_clean, 0);
+      }
+      if (!SUMMARY && c >= 1) LA_WAIT(pv_full, c - 1);   // (else the state's warps have read them)
+      tc_fence_after();
+      if (lead) {
+        const Operand V(base + F::oV + c % kVS * 2 * kSlab, kSlab);
+        issue_ss<false>(tmem + F::W, V, 0, T, 0, id_v);
+#pragma unroll
+        for (int i = 1; i < 3 * KC; ++i)
+          issue_ss<true>(tmem + F::W, V, i % KC * 2048, T, i / KC * kSlab + i % KC * 32, id_v);
+        mma_commit(&bars->v_empty[c % kVS]);
+      }
+      __syncwarp();
+      // wᵀ −= (e^b kS)ᵀ (Tβ)ᵀ: hi·hi, hi·mid, lo·hi
       LA_WAIT(ks_ready, c);
-      if (!SUMMARY && c >= 1) LA_WAIT(pv_read, c - 1);
       tc_fence_after();
       if (lead) {
 #pragma unroll
@@ -369,17 +385,41 @@ __device__ __forceinline__ void role_mma(const Ctx& x, const TcParams& p) {
             issue_ts<true>(tmem + F::W, tmem + F::KS + tokens(k) + (part == 2 ? 8 : 0), T,
                            (part == 1 ? kSlab : 0) + k * 32, id_nn);
         mma_commit(&bars->w_full[c & 1]);
-        if constexpr (!SUMMARY) {
+      }
+      __syncwarp();
+      // (qS)ᵀ
+      if constexpr (!SUMMARY) {
+        if (c >= 1) LA_WAIT(pv_read, c - 1);
+        tc_fence_after();
+        if (lead) {
           of_state(tmem + F::PV, K, kSlab);
           mma_commit(&bars->qs_full);
         }
+        __syncwarp();
+      }
+    }
+    // while w is on its way: [k; q]·kᵀ of the chunk after next
+    if (c + 2 < x.chunks) {
+      const int g = c + 2;
+      LA_WAIT(kq_full[g % kKQ], g / kKQ);
+      if (x.partial && g == x.chunks - 1) LA_WAIT(kq_clean, 0);
+      if (g >= 1) LA_WAIT(g_empty, g - 1);
+      tc_fence_after();
+      if (lead) {
+        const Operand d(base + g % kKQ * F::kStage, 16);
+        issue_ss<false>(tmem + F::G, d, 0, d, 0, id_nn);
+#pragma unroll
+        for (int k = 1; k < KD; ++k) issue_ss<true>(tmem + F::G, d, kstep(k), d, kstep(k), id_nn);
+        mma_commit(&bars->g_full[g & 1]);
       }
       __syncwarp();
+    }
+    if (c >= 0) {
       // the state's wᵀk
       LA_WAIT(w_ready, c);
       tc_fence_after();
       if (lead) {
-        const Operand Kt(kq, 2 * kSlab);
+        const Operand Kt(base + c % kKQ * F::kStage, 2 * kSlab);
         issue_ts<false>(tmem + F::UPD, tmem + F::KS, Kt, 0, id_upd);
 #pragma unroll
         for (int i = 1; i < 2 * KC; ++i)
@@ -402,43 +442,6 @@ __device__ __forceinline__ void role_mma(const Ctx& x, const TcParams& p) {
         }
         __syncwarp();
       }
-    }
-    // while S is on its way: the products of the chunks ahead that go without it.
-    // [k; q]·kᵀ
-    if (c + 2 < x.chunks) {
-      const int g = c + 2;
-      LA_WAIT(kq_full[g % kKQ], g / kKQ);
-      if (x.partial && g == x.chunks - 1) LA_WAIT(kq_clean, 0);
-      if (g >= 1) LA_WAIT(g_empty, g - 1);
-      tc_fence_after();
-      if (lead) {
-        const Operand d(base + g % kKQ * F::kStage, 16);
-        issue_ss<false>(tmem + F::G, d, 0, d, 0, id_nn);
-#pragma unroll
-        for (int k = 1; k < KD; ++k) issue_ss<true>(tmem + F::G, d, kstep(k), d, kstep(k), id_nn);
-        mma_commit(&bars->g_full[g & 1]);
-      }
-      __syncwarp();
-    }
-    // wᵀ = vᵀ (Tβ)ᵀ, whose columns (P w)ᵀ has read
-    if (c >= -1 && c + 1 < x.chunks) {
-      const int n = c + 1;
-      LA_WAIT(t_ready, n);
-      if (!(SUMMARY && x.identity)) {
-        LA_WAIT(v_full[n % kVS], n / kVS);
-        if (x.partial && n == x.chunks - 1) LA_WAIT(v_clean, 0);
-      }
-      if (!SUMMARY && n >= 1) LA_WAIT(pv_full, n - 1);   // (else the state's warps have read them)
-      tc_fence_after();
-      if (lead) {
-        const Operand V(base + F::oV + n % kVS * 2 * kSlab, kSlab);
-        issue_ss<false>(tmem + F::W, V, 0, T, 0, id_v);
-#pragma unroll
-        for (int i = 1; i < 3 * KC; ++i)
-          issue_ss<true>(tmem + F::W, V, i % KC * 2048, T, i / KC * kSlab + i % KC * 32, id_v);
-        mma_commit(&bars->v_empty[n % kVS]);
-      }
-      __syncwarp();
     }
   }
 }
@@ -543,7 +546,6 @@ __device__ __forceinline__ void role_state(const Ctx& x, const TcParams& p, int 
 #pragma unroll
       for (int i = 0; i < 16; ++i) S[j / 2 + i] = fma2(S[j / 2 + i], carry, pair_of(r, 2 * i));
     }
-    if (!SUMMARY) LA_WAIT(pv_full, c);   // so that the next chunk's w may start
   }
   if (!x.s_out) return;
 #pragma unroll
@@ -615,10 +617,10 @@ __device__ __forceinline__ void role_out(const Ctx& x, const TcParams& p, const 
     const int rows = min(kC, x.live - c * kC);
 #pragma unroll 1
     for (int j = 0; j < kC; j += kOutRows) {
-      uint32_t v[32];
-      tmem_ld32(at + F::PV + j, v);
+      uint32_t v[kOutRows];
+      tmem_ld16(at + F::PV + j, v);
       tmem_ld_wait();
-      if (j) {
+      if (j + kOutRows == kC) {
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars->pv_read);
@@ -839,6 +841,7 @@ __device__ __forceinline__ void role_prep(const Ctx& x, const TcParams& p, int w
     const float bx = tok.bx[row], by = tok.by[row];
     const float factor = keys ? tok.a[row] : tok.q[row];
     const int upto = row - keys;      // A below the diagonal, P with it
+    // (the products before chunk c's gram matrix have ended with it, (P w)ᵀ of c − 3 among them)
     const uint32_t P = smem_u32(x.sm + F::oP + c % kPS * kSlab);
     named_bar_sync(bar, 128);    // the last chunk's T has been read from A
     // this row of A, or of P, 16 columns at a time
@@ -914,8 +917,7 @@ __device__ __forceinline__ void role_prep(const Ctx& x, const TcParams& p, int w
                        A + (32 + r0) * kAPitch + c0);
     }
     named_bar_sync(bar, 128);
-    // Tβ where the last chunk's was; its w is complete, and so is every product that
-    // was issued before it, with the P of the chunk before
+    // Tβ where the last chunk's was; its w is complete
     if (c >= 1) LA_GO_ON(w_full[(c - 1) & 1], (c - 1) / 2);
     const uint32_t T = smem_u32(x.sm + F::oT);
     const int h0 = keys ? 0 : 32;     // half of the row's columns
@@ -1112,17 +1114,19 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const float* state_i
 // Parts of a sequence: with few heads most SMs would have none, so each sequence is
 // walked twice, first for what every part makes of a state (one CTA more for each
 // part, and no output), then with the states that enter them.  By the µs of a chunk
-// (4.0, and 3.3 without the output) and of joining two parts.
+// (3.9, and 3.6 without the output), of joining two parts (4) and of two launches more:
+// 8 heads of 4096 tokens take 125 µs in 8 parts and 260 undivided, of 1024 tokens 76
+// in 4 and 72.
 int parts_of(const DeltaArgs& a, int tiles) {
   const int64_t heads = a.B * a.Hv, chunks = (a.n + kC - 1) / kC;
   auto rounds = [&](int64_t ctas) { return (double)((ctas + a.num_sms - 1) / a.num_sms); };
   int best = 1;
-  double least = rounds(heads * tiles) * chunks * 4.0;
+  double least = rounds(heads * tiles) * chunks * 3.9;
   for (int g = 2; g <= 64 && g * 4 <= chunks; ++g) {
     const int64_t part = (chunks + g - 1) / g;
     if ((chunks + part - 1) / part != g) continue;
-    const double t = rounds(heads * (g - 1) * (tiles + 1)) * part * 3.3 + rounds(heads * g * tiles) * part * 4.0 +
-                     20.0 + rounds(heads * ((a.dv + kJoinCols - 1) / kJoinCols)) * (g - 1) * 3.0;
+    const double t = rounds(heads * (g - 1) * (tiles + 1)) * part * 3.6 + rounds(heads * g * tiles) * part * 3.9 +
+                     28.0 + rounds(heads * ((a.dv + kJoinCols - 1) / kJoinCols)) * (g - 1) * 4.0;
     if (t < least) least = t, best = g;
   }
   return best;

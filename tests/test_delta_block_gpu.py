@@ -16,6 +16,14 @@ With M ← α·M + ‖w‖ (M starts at ‖S_0‖), which bounds the norm of eve
 sum that q·S is made of, an output row is off by at most
   u·‖o‖ + scale·‖q‖·(E + r·M),  r = f(dk), or 3·2^-8 where S, the chunk's
 scores and its values are rounded to bf16 for the output alone.
+
+A long sequence of few heads is walked in parts, S ← Φ·S + N over one, where Φ
+is what a part makes of the identity and N of a zero state.  A column of Φ has a
+norm of at most the part's decay D, D‖S‖ ≤ M, and ‖N‖ ≤ ‖S'‖ + D‖S‖ ≤ 2M.  What a
+token adds to Φ's error, e·β·α·D per column, meets ‖S‖ by way of Φ's Frobenius norm,
+√dk times as much, so √dk·αM stands in for α‖S‖ above (dk ≥ 8 covers N's 2M).  The
+product and the sum of a join in fp32 are off by f(dk)·‖Φ‖‖S‖ ≤ f(dk)·√dk·M each, which
+decays as M does: there are at most 63 joins, 32 tokens or more apart.
 """
 import math
 
@@ -60,7 +68,7 @@ def _inputs(B, n, hk, hv, dk, dv, dtype, seed, skew=True, gates=None):
             "dt_bias": _randn(g, hv) - 1.0}
 
 
-def _ref(x, softplus=True, sigmoid=True, normalize=True, scale=None, state=None, lengths=None):
+def _ref(x, softplus=True, sigmoid=True, normalize=True, scale=None, state=None, lengths=None, parts=False):
     """(out, state, error of an output row apart from its own rounding, error of the
     state per head) from the recurrence in 64 bits; the errors for e = r = 1."""
     q, k, v, dt, beta = (x[i].double() for i in ("q", "k", "v", "dt", "beta"))
@@ -89,7 +97,7 @@ def _ref(x, softplus=True, sigmoid=True, normalize=True, scale=None, state=None,
         kt = torch.where(live[..., None], k[:, t], 0.0)   # what is not read may be anything
         vt = torch.where(live[..., None], v[:, t], 0.0)
         S = al[..., None, None] * S
-        before = norm(S)
+        before = al * M * dk ** 0.5 if parts else norm(S)
         w = be[..., None] * (vt - torch.einsum("bhk,bhkv->bhv", kt, S))
         S = S + kt[..., None] * w[:, :, None]
         E[0] = al * E[0] + be * (vt.norm(dim=-1) + before)
@@ -98,7 +106,10 @@ def _ref(x, softplus=True, sigmoid=True, normalize=True, scale=None, state=None,
         o = scale * torch.einsum("bhk,bhkv->bhv", q[:, t], S)
         out[:, t] = torch.where(live[..., None], o, 0.0)
         s = scale * q[:, t].norm(dim=-1)
-        tols[:, :, t] = torch.where(live, s * torch.stack([E[0], E[1], M]), 0.0)
+        joins = min(63, t // 32) * dk ** 0.5 * _f(dk) * M if parts else 0.0
+        tols[:, :, t] = torch.where(live, s * torch.stack([E[0], E[1] + joins, M]), 0.0)
+    if parts:
+        E[1] = E[1] + joins
     return out, S, tols, torch.stack(E)
 
 
@@ -277,6 +288,74 @@ def test_gated_delta_in_parts(dtype):
         outs.append(la.gated_delta_step(state, x["q"][:, t], x["k"][:, t], x["v"][:, t], x["dt"][:, t], x["a"],
                                         x["beta"][:, t], dt_bias=x["dt_bias"])[:, None])
     _check((torch.cat(outs, 1), state), x)
+
+
+LONG = [  # B, n, hk, hv, dk, dv, lengths, state; few heads, which are walked in parts where dk allows
+    (1, 4000, 1, 1, 128, 128, None, False), (2, 2051, 1, 2, 64, 192, [2051, 700], True),
+    (1, 2900, 2, 2, 72, 40, None, True), (3, 2500, 1, 1, 128, 136, [0, 1, 2499], True),
+    (2, 2304, 1, 1, 128, 64, [1088, 1153], False), (1, 900, 1, 1, 256, 64, None, True)]
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=IDS)
+@pytest.mark.parametrize("shape", LONG, ids=lambda s: "x".join(map(str, s[:6])))
+def test_gated_delta_long(dtype, shape):
+    B, n, hk, hv, dk, dv, lens, with_state = shape
+    x = _inputs(B, n, hk, hv, dk, dv, dtype, seed=n)
+    x["a"] = x["a"] * 0.002   # the state lasts for thousands of tokens
+    x["beta"] = x["beta"] - 3.0
+    state = _randn(_gen(5), B, hv, dk, dv, scale=0.3) if with_state else None
+    lengths = None if lens is None else torch.tensor(lens, device=DEV, dtype=torch.int32)
+    kw = {"state": state, "lengths": lengths}
+    big = torch.full((B, n + 2, hv, dv), 7.0, device=DEV, dtype=dtype)
+    got = _call(x, out=big[:, 1:-1], **kw)
+    _check(got, x, parts=True, **kw)
+    assert (big[:, 0] == 7).all() and (big[:, -1] == 7).all()
+    again = _call(x, **kw)   # a fixed order of sums
+    assert torch.equal(got[0], again[0]) and torch.equal(got[1], again[1])
+    # the same beside many more heads, where nothing is divided: both within their tolerance
+    wide = {k: (v.repeat(160 // B, *[1] * (v.dim() - 1)) if v.dim() > 1 else v) for k, v in x.items()}
+    whole = _call(wide, state=None if state is None else state.repeat(160 // B, 1, 1, 1),
+                  lengths=None if lens is None else lengths.repeat(160 // B))
+    assert torch.equal(whole[1][:B], whole[1][-B:])
+    _check((whole[0][:B], whole[1][:B]), x, **kw)
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=IDS)
+def test_gated_delta_long_graph(dtype):
+    # parts in captured graphs, which have their workspaces of their own, and NaN in one head of one part
+    x = _inputs(1, 2500, 1, 2, 64, 64, dtype, seed=3)
+    x["a"] = x["a"] * 0.002
+    fixed = {k: v.clone() for k, v in x.items()}
+    ref = _call(x)
+    graphs, outs = [], []
+    for _ in range(2):
+        graph = torch.cuda.CUDAGraph()
+        torch.cuda.synchronize()
+        with torch.cuda.graph(graph):
+            outs.append(_call(fixed))
+        graphs.append(graph)
+    fixed["v"][0, 1500, 1, 3] = float("nan")
+    for graph in graphs:
+        graph.replay()
+    for out, state in outs:
+        assert torch.equal(out[:, :, 0], ref[0][:, :, 0]) and torch.equal(state[:, 0], ref[1][:, 0])
+        assert torch.equal(out[0, :1437, 1], ref[0][0, :1437, 1])
+        assert torch.isnan(out[0, 1500:, 1, 3]).all() and torch.isnan(state[0, 1, :, 3]).all()
+        rest = [i for i in range(64) if i != 3]
+        assert torch.isfinite(state[0, 1][:, rest]).all()
+    fixed["v"].copy_(x["v"])
+    for graph in graphs:
+        graph.replay()
+    for out, state in outs:
+        assert torch.equal(out, ref[0]) and torch.equal(state, ref[1])
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=IDS)
+@pytest.mark.parametrize("n", [14, 15, 16, 17, 18, 31, 33])
+def test_gated_delta_few_tokens(dtype, n):
+    x = _inputs(2, n, 1, 2, 128, 128, dtype, seed=n)
+    state = _randn(_gen(5), 2, 2, 128, 128, scale=0.3)
+    _check(_call(x, state=state), x, state=state)
 
 
 @pytest.mark.parametrize("dtype", DTYPES, ids=IDS)
