@@ -25,7 +25,9 @@ token adds to Φ's error, e·β·α·D per column, meets ‖S‖ by way of Φ's 
 product and the sum of a join in fp32 are off by f(dk)·‖Φ‖‖S‖ ≤ f(dk)·√dk·M each, which
 decays as M does: there are at most 63 joins, 32 tokens or more apart.
 """
+import importlib.util
 import math
+import os
 
 import pytest
 import torch
@@ -684,6 +686,14 @@ def test_block_against_plain():
     z8, zs, total = la.rms_norm(r, residual=u, quantize=True)
     _norm_close((z8, zs, total), r, None, 128, 1e-6, None, u, True)
     _linear8_close(got.flatten(0, 1), z8.flatten(0, 1), zs.flatten(), wo8, wos, None, total.flatten(0, 1))
+
+
+def test_example():
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "gated_delta_block.py")
+    spec = importlib.util.spec_from_file_location("gated_delta_block", path)
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    assert math.isfinite(example.run(width=256, batch=3, prompt=70, tokens=3))
 
 
 def test_far_offsets():
