@@ -29,6 +29,17 @@
 // are kept rolled where they can be: five roles at once run from one instruction
 // cache, and unrolled throughout the kernel spent twice as long on fetching as on
 // issuing (4×4096 tokens of 32 heads in 490 µs).
+//
+// What bounds it: the latency of a chunk's chain, since one CTA has an SM and a chunk waits
+// for the state of the one before.  4×4096 tokens of 32 heads (64 chunks for each of 128
+// CTAs) take 277 µs, 4.2 µs or some 8000 cycles a chunk, of which the tensor pipe is
+// busy a third (2700), and the four conversions between products (S, k·S, w, and S
+// again) with the signals around them take most of the rest; DRAM is at 15 %.  Without
+// the inverse's arithmetic it would take a tenth less, without the norms 3 %.
+//
+// The MMA warp issues what the chain waits for first, and the products beside it into
+// its gaps: v's part of w while k·S is converted, q·S and the next gram matrix while w
+// is.  With the last two between UPD and the next S it took 306 µs.
 #include "block.cuh"
 #include "internal.h"
 #include "tc_pair.cuh"
@@ -728,8 +739,8 @@ __device__ __forceinline__ void small_product(const float* X, const float* Y, in
         make_float4(sign * z[r].x, sign * z[r].y, sign * z[r].z, sign * z[r].w);
 }
 
-// Decays, strengths and lengths of each chunk's tokens, of k by warp 19 and of q by
-// warp 18; lane i has tokens i and i + 32.
+// Decays, strengths and lengths of each chunk's tokens, of k by warp 23 and of q by
+// warp 22; lane i has tokens i and i + 32.
 template <int DK>
 __device__ __forceinline__ void role_factors(const Ctx& x, const TcParams& p, int warp, int lane) {
   using F = Cfg<DK>;

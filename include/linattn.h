@@ -521,6 +521,11 @@ typedef struct {
  *              state_in.
  * dk and dv are multiples of 8, dk ≤ 256, dv ≤ 512 (else LA_ERR_UNSUPPORTED).
  * States, sums, norms and decays are fp32.  Equal inputs give equal bits.
+ * bf16 tokens with dk ≤ 128 go in chunks of 64 from n = 16 on, the states with an
+ * error of a few 1e-6: a NaN or infinity of a token is then seen by all of its
+ * chunk's outputs, those of earlier tokens too, and by everything after it.
+ * Long sequences of few heads are divided: stream-ordered memory is taken for
+ * the states of their parts (LA_ERR_OUT_OF_MEMORY where there is none).
  * Errors as la_linear.
  */
 la_status la_gated_delta(const la_heads* q, const la_heads* k, const la_heads* v,
@@ -628,8 +633,8 @@ int la_debug_build(void);
  * word.  Site numbers: 11–14 the tcgen05 elu+1 forward (tile rows, output
  * rows, the aggregate slot, the entering-state slots), 21–26 the tcgen05
  * backward (item ranges of the loads, rows of the ∂q, ∂k, ∂v stores), 31–32
- * the non-causal readout, 41–42 the Performer forward, 51–52 la_linear's
- * bf16 stores, 90 the self-test.
+ * the non-causal readout, 41–42 the Performer forward, 51–52 la_linear's and
+ * la_linear_e4m3's bf16 stores, 61 la_gated_delta's, 90 the self-test.
  * Errors: LA_ERR_INVALID_ARG (site is NULL), LA_ERR_CUDA.
  */
 la_status la_get_last_device_check(la_stream stream, int* site);

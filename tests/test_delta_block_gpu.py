@@ -227,6 +227,27 @@ def test_gated_delta_views(dtype):
 
 
 @pytest.mark.parametrize("dtype", DTYPES, ids=IDS)
+def test_gated_delta_broadcast_axes(dtype):
+    # one key and query for all heads, one token for all, and rows that overlap
+    x = _inputs(2, 100, 2, 4, 64, 64, dtype, seed=3)
+    y = dict(x)
+    for name in ("q", "k"):
+        y[name] = x[name][:, :, :1].expand(2, 100, 2, 64)
+    z = {k: (v.contiguous() if v.dim() > 1 else v) for k, v in y.items()}
+    for a, b in zip(_call(y), _call(z)):
+        assert torch.equal(a, b)
+    y["v"] = x["v"][:, :1].expand(2, 100, 4, 64)
+    y["dt"], y["beta"] = (x[i][:, :1].expand(2, 100, 4) for i in ("dt", "beta"))
+    _check(_call(y), y)
+    line = x["v"].flatten()
+    y["v"] = line.as_strided((2, 100, 4, 64), (4096, 16, 8, 1))
+    z["v"] = y["v"].contiguous()
+    y["dt"], y["beta"] = z["dt"], z["beta"]
+    for a, b in zip(_call(y), _call(z)):
+        assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=IDS)
 def test_gated_delta_extreme_decays(dtype):
     # no decay at all, decays that clear the state, and steps of zero
     x = _inputs(1, 260, 2, 4, 64, 64, dtype, seed=8, gates=F32)
