@@ -1,17 +1,19 @@
 // The gated delta rule token by token on the CUDA cores:
 //   w_t = β_t(v_t − k_t(α_t S_{t−1})),  S_t = α_t S_{t−1} + k_tᵀ w_t,  o_t = scale·q_t S_t.
 //
-// recurrent_kernel (several tokens).  The columns of S do not meet: a warp has a few of them (16 for dk = 128) with
-// all their rows, 16 rows by 4 columns to a lane, and walks the tokens with S in
-// registers.  k·S and q·S of the state before the token are summed together over
-// the P = dk/16 lanes that share a column; o_t = scale·(α q·S_{t−1} + (q·k) w_t)
+// recurrent_kernel (several tokens).  The columns of S do not meet: a warp has a few of
+// them (16 or 8 for dk = 128) with all their rows, 16 or 8 rows by 4 columns to a lane, and
+// walks the tokens with S in registers, two tokens' q, k and v under way (4×2048 tokens of
+// 32 heads of 128 in fp32: 1.60 ms, 1.76 with one).  Bound by the latency of a token's
+// chain, 0.45 to 0.52 µs, while warps are few, and then by issue.  k·S and q·S of the
+// state before the token are summed together over the P lanes that share a column; o_t = scale·(α q·S_{t−1} + (q·k) w_t)
 // needs no second pass over S, so the next token's sums wait for w_t alone.
 //
 // step_kernel (one token) is bound by reading and writing S, 128 KB for a head of
 // 128×128.  A CTA has 128 columns (or 64) of one head's S with all rows, in the
 // registers of 256 threads: warps read whole rows of 512 bytes, all loads of a thread
 // are issued before anything waits for one, and the sums over rows go through shared
-// memory once.
+// memory once.  256×32 heads of 128×128: 161 µs = 6.7 TB/s, a copy's bandwidth.
 //
 // Everything is fp32.
 #include "block.cuh"
@@ -112,9 +114,9 @@ __device__ __forceinline__ float both(f32x2 v) {
   return lo + hi;
 }
 
-// One warp: 128/P columns of one (b, head), all tokens or a part of them.  SUMMARY:
+// One warp: 128/P columns of one (b, head), 4R rows to a lane, all tokens or a part of them.  SUMMARY:
 // without outputs, from zero, and (dk columns more) from the identity without v.
-template <typename T, int P, bool SUMMARY>
+template <typename T, int P, int R, bool SUMMARY>
 __global__ void __launch_bounds__(kThreads) recurrent_kernel(const DeltaParams p) {
   entry();
   const int64_t wid = (int64_t)blockIdx.x * (kThreads / 32) + threadIdx.x / 32;
@@ -146,10 +148,10 @@ __global__ void __launch_bounds__(kThreads) recurrent_kernel(const DeltaParams p
   }
 
   // rows 4(iP + part) + j of S, in pairs of rows
-  f32x2 S[4][8];
-  bool row_in[4];
+  f32x2 S[4][2 * R];
+  bool row_in[R];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < R; ++i) {
     const int r = 4 * (i * P + part);
     row_in[i] = r < p.dk;
     float4 m[4] = {};
@@ -172,34 +174,38 @@ __global__ void __launch_bounds__(kThreads) recurrent_kernel(const DeltaParams p
   const T* kp = static_cast<const T*>(p.k.data) + b * p.k.sb + t0 * p.k.sn + (int64_t)hk * p.k.sh;
   const T* vp = static_cast<const T*>(p.v.data) + b * p.v.sb + t0 * p.v.sn + (int64_t)h * p.v.sh + mine;
   T* op = static_cast<T*>(const_cast<void*>(p.out.data)) + b * p.out.sb + t0 * p.out.sn + (int64_t)h * p.out.sh + mine;
-  Raw4<T> qr[4], kr[4];
-  T vr = from_f32<T>(0.f);
-  auto load = [&](int t) {   // token t's share of this lane
+  struct Token {
+    Raw4<T> q[R], k[R];
+    T v = from_f32<T>(0.f);
+  };
+  Token even, odd;   // tokens under way
+  auto load = [&](Token& to, int t) {   // token t's share of this lane
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < R; ++i)
       if (row_in[i]) {
         const int r = 4 * (i * P + part);
-        if (!SUMMARY) qr[i].load(qp + t * p.q.sn + r);
-        kr[i].load(kp + t * p.k.sn + r);
+        if (!SUMMARY) to.q[i].load(qp + t * p.q.sn + r);
+        to.k[i].load(kp + t * p.k.sn + r);
       }
-    if (in && !identity) vr = vp[t * p.v.sn];
+    if (in && !identity) to.v = vp[t * p.v.sn];
   };
-  if (live > 0) load(0);
+  if (live > 0) load(even, 0);
+  if (live > 1) load(odd, 1);
   float2 g = {1.f, 0.f};
-  for (int t = 0; t < live; ++t) {
+  auto walk = [&](Token& at, int t) {
     if (t % 32 == 0) g = t + lane < live ? gates(p, b, t0 + t + lane, h) : make_float2(1.f, 0.f);
     const float alpha = __shfl_sync(kAll, g.x, t % 32), beta = __shfl_sync(kAll, g.y, t % 32);
-    f32x2 q[8], k[8];
+    f32x2 q[2 * R], k[2 * R];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      q[2 * i] = qr[i].lo(), q[2 * i + 1] = qr[i].hi();
-      k[2 * i] = kr[i].lo(), k[2 * i + 1] = kr[i].hi();
+    for (int i = 0; i < R; ++i) {
+      q[2 * i] = at.q[i].lo(), q[2 * i + 1] = at.q[i].hi();
+      k[2 * i] = at.k[i].lo(), k[2 * i + 1] = at.k[i].hi();
     }
-    const float v = to_f32(vr);
-    if (t + 1 < live) load(t + 1);
+    const float v = to_f32(at.v);
+    if (t + 2 < live) load(at, t + 2);
     f32x2 qk2 = 0, qq2 = 0, kk2 = 0, ks2[4] = {}, qs2[4] = {};
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < 2 * R; ++i) {
       qk2 = fma2(q[i], k[i], qk2);
       qq2 = fma2(q[i], q[i], qq2);
       kk2 = fma2(k[i], k[i], kk2);
@@ -227,15 +233,20 @@ __global__ void __launch_bounds__(kThreads) recurrent_kernel(const DeltaParams p
     for (int c = 0; c < 4; ++c) {
       const f32x2 w2 = pack2(wc[c], wc[c]);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) S[c][i] = fma2(k[i], w2, mul2(al, S[c][i]));
+      for (int i = 0; i < 2 * R; ++i) S[c][i] = fma2(k[i], w2, mul2(al, S[c][i]));
     }
     if (!SUMMARY && in && part < 4) op[t * p.out.sn] = from_f32<T>(rq * (alpha * qsum + qk * w));
+  };
+#pragma unroll 1
+  for (int t = 0; t < live; t += 2) {
+    walk(even, t);
+    if (t + 1 < live) walk(odd, t + 1);
   }
   if (!SUMMARY && in && part < 4)
     for (int t = live; t < n; ++t) op[t * p.out.sn] = from_f32<T>(0.f);
   if (!state_out || !in) return;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < R; ++i) {
     if (!row_in[i]) continue;
     float* at = state_out + (int64_t)(4 * (i * P + part)) * cols + col0;
 #pragma unroll
@@ -359,29 +370,37 @@ cudaError_t step(const DeltaArgs& a, const DeltaParams& p, cudaStream_t s) {
 
 // ------------------------------------------------------------------ several tokens
 
-// Parts of the sequences: a warp takes 0.6 µs for a token while no more than two share
-// a scheduler, and then as much longer as they are more.
-int parts_of(const DeltaArgs& a, int64_t slices, int64_t more) {
-  if (a.dk > 128) return 1;   // what delta_join holds
+// Parts of the sequences, and the µs that they are taken to need, with P lanes to a
+// column: a warp takes `token` µs for a token while no more than two share a scheduler,
+// and then as much longer as they are more.  Parts measured a seventh above that sum, or
+// more (333 tokens of 8 heads of 128 with 16 lanes: 92 µs in 8 parts, 153 undivided; 2×512 of
+// 16 heads with 8: 299 in 5 parts, 240 in 4, 271 undivided).
+struct Plan {
+  int parts;
+  double us;
+};
+Plan plan_for(const DeltaArgs& a, int P, double token) {
+  const int64_t cols = 128 / P, slices = (a.dv + cols - 1) / cols, more = (a.dk + cols - 1) / cols;
   auto share = [&](int64_t warps) { return std::max(1.0, (double)warps / (8.0 * a.num_sms)); };
   const int64_t heads = a.B * a.Hv;
-  int best = 1;
-  double least = a.n * 0.6 * share(heads * slices);
+  Plan best{1, a.n * token * share(heads * slices)};
+  if (a.dk > 128) return best;   // what delta_join holds
   for (int g = 2; g <= 64 && g * 32 <= a.n; g += g < 8 ? 1 : 4) {
     const int64_t part = (a.n + g - 1) / g;
-    const double t = part * 0.6 * (share(heads * (g - 1) * (slices + more)) + share(heads * g * slices)) + 20.0 +
-                     3.0 * (g - 1);
-    if (t < least) least = t, best = g;
+    const double sum = part * token * (share(heads * (g - 1) * (slices + more)) + share(heads * g * slices)) + 20.0 +
+                       3.0 * (g - 1);
+    const double t = 1.15 * sum;
+    if (t < best.us) best = {g, t};
   }
   return best;
 }
 
-template <typename T, int P>
-cudaError_t launch_recurrent(const DeltaArgs& a, DeltaParams p, cudaStream_t s) {
+template <typename T, int P, int R>
+cudaError_t launch_recurrent(const DeltaArgs& a, DeltaParams p, int parts, cudaStream_t s) {
   constexpr int kCols = 128 / P;
   const int64_t more = (a.dk + kCols - 1) / kCols, heads = a.B * a.Hv;
   p.slices = (a.dv + kCols - 1) / kCols;
-  p.parts = parts_of(a, p.slices, more);
+  p.parts = parts;
   p.part_tokens = (int)((a.n + p.parts - 1) / p.parts);
   p.parts = (int)((a.n + p.part_tokens - 1) / p.part_tokens);
   auto ctas = [](int64_t warps) { return (warps + kThreads / 32 - 1) / (kThreads / 32); };
@@ -393,11 +412,11 @@ cudaError_t launch_recurrent(const DeltaArgs& a, DeltaParams p, cudaStream_t s) 
     if ((e = delta_parts(a, p.parts, &w, s)) != cudaSuccess) return e;
     p.added = w.added, p.transition = w.transition, p.entering = w.entering;
     p.warps = first;
-    e = launch(recurrent_kernel<T, P, true>, (unsigned)ctas(first), kThreads, 0, s, 1, p);
+    e = launch(recurrent_kernel<T, P, R, true>, (unsigned)ctas(first), kThreads, 0, s, 1, p);
     if (e == cudaSuccess) e = delta_join(a, p.parts, w, s);
   }
   p.warps = warps;
-  if (e == cudaSuccess) e = launch(recurrent_kernel<T, P, false>, (unsigned)ctas(warps), kThreads, 0, s, 1, p);
+  if (e == cudaSuccess) e = launch(recurrent_kernel<T, P, R, false>, (unsigned)ctas(warps), kThreads, 0, s, 1, p);
   if (w.added) {
     const cudaError_t f = cudaFreeAsync(w.added, s);
     if (e == cudaSuccess) e = f;
@@ -407,16 +426,26 @@ cudaError_t launch_recurrent(const DeltaArgs& a, DeltaParams p, cudaStream_t s) 
 
 template <typename T>
 cudaError_t by_keys(const DeltaArgs& a, const DeltaParams& p, cudaStream_t s) {
-  if (a.dk <= 64) return launch_recurrent<T, 4>(a, p, s);
-  if (a.dk <= 128) return launch_recurrent<T, 8>(a, p, s);
-  return launch_recurrent<T, 16>(a, p, s);
+  // Sixteen rows to a lane; or eight, with twice the warps, where each of them has a
+  // scheduler to itself: 2×512 tokens of 16 heads of 128 (512 warps) in 235 µs against
+  // 271, 4×512 in 337 against 272.
+  const int lanes = a.dk <= 64 ? 4 : a.dk <= 128 ? 8 : 16;
+  const Plan wide = plan_for(a, lanes, 0.6);
+  if (a.dk <= 128 && a.B * a.Hv * ((a.dv * 2 * lanes + 127) / 128) <= 4 * (int64_t)a.num_sms) {
+    const Plan fine = plan_for(a, 2 * lanes, 0.45);
+    if (fine.us < wide.us)
+      return a.dk <= 64 ? launch_recurrent<T, 8, 2>(a, p, fine.parts, s) : launch_recurrent<T, 16, 2>(a, p, fine.parts, s);
+  }
+  if (a.dk <= 64) return launch_recurrent<T, 4, 4>(a, p, wide.parts, s);
+  if (a.dk <= 128) return launch_recurrent<T, 8, 4>(a, p, wide.parts, s);
+  return launch_recurrent<T, 16, 4>(a, p, wide.parts, s);
 }
 
 }  // namespace
 
 cudaError_t gated_delta(const DeltaArgs& a, cudaStream_t s) {
-  // A chunk takes 13.5 µs whatever its tokens, the kernels here 0.65 µs for each of one
-  // sequence of 32 heads (1.1 for four such sequences): 16 tokens 15.0 µs, 37 tokens 28.9.
+  // A chunk takes 12.5 µs whatever its tokens, the kernels here some 5 µs and 0.4 to 0.65
+  // for each of one sequence of 32 heads: 12 tokens 8.6 µs, 12.8 for four such sequences.
   if (a.n >= 16 && tc_gated_delta_supported(a)) return tc_gated_delta(a, s);
   DeltaParams p{};
   p.q = a.q, p.k = a.k, p.v = a.v, p.out = a.out;

