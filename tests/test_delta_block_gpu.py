@@ -28,6 +28,8 @@ decays as M does: there are at most 63 joins, 32 tokens or more apart.
 import importlib.util
 import math
 import os
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -725,6 +727,48 @@ def test_example():
     example = importlib.util.module_from_spec(spec)
     spec.loader.exec_module(example)
     assert math.isfinite(example.run(width=256, batch=3, prompt=70, tokens=3))
+
+
+def test_debug_build_gives_the_same_bits(tmp_path):
+    # the LA_DEBUG library in a child process: no check fails, equal outputs
+    code = (
+        "import sys, torch, causal_kernelized_linear_gb300 as la\n"
+        "g = torch.Generator(device='cuda').manual_seed(5)\n"
+        "r = lambda *s: torch.randn(*s, device='cuda', generator=g).bfloat16()\n"
+        "out = {}\n"
+        "def delta(B, n, hk, hv, dk, dv, f32=False, lens=None):\n"
+        "    x = [r(B, n, hk, dk), r(B, n, hk, dk), r(B, n, hv, dv), r(B, n, hv), -torch.rand(hv, device='cuda',"
+        " generator=g), r(B, n, hv)]\n"
+        "    x = [t.float() for t in x] if f32 else x\n"
+        "    lens = None if lens is None else torch.tensor(lens, device='cuda', dtype=torch.int32)\n"
+        "    return la.gated_delta(*x, lengths=lens, return_state=True)\n"
+        "for i, c in enumerate(((1, 200, 1, 2, 128, 136), (2, 77, 1, 1, 64, 40, False, [77, 30]), (1, 2500, 1, 1, 128, 128),"
+        " (1, 300, 1, 1, 64, 64, True), (1, 9, 2, 2, 128, 128))):\n"
+        "    out[f'delta{i}'], out[f'state{i}'] = delta(*c)\n"
+        "for m, k, n in ((5, 208, 136), (130, 528, 1000), (1500, 272, 2056)):\n"
+        "    y, s = la.rms_norm(r(m, k), r(k), quantize=True)\n"
+        "    w = r(n, k).to(torch.float8_e4m3fn)\n"
+        "    out[f'norm{m}'], out[f'scale{m}'] = y.float(), s\n"
+        "    out[f'linear{m}'] = la.linear_e4m3(y, s, w, torch.rand(n, device='cuda', generator=g), bias=r(n),"
+        " activation='silu', residual=r(m, n))\n"
+        "out['status'] = torch.tensor(la.last_device_check())\n"
+        "out['debug'] = torch.tensor(int(la.debug_build()))\n"
+        "torch.save({k: v.cpu() for k, v in out.items()}, sys.argv[1])\n")
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    la.build()
+    la.build(debug=True)
+    got = []
+    for debug in ("0", "1"):
+        path = str(tmp_path / debug)
+        env = dict(os.environ, LA_DEBUG=debug, PYTHONPATH=root)
+        p = subprocess.run([sys.executable, "-c", code, path], env=env, capture_output=True, text=True, timeout=300)
+        assert p.returncode == 0, p.stderr[-2000:]
+        got.append(torch.load(path))
+    rel, dbg = got
+    assert rel.pop("debug").item() == 0 and dbg.pop("debug").item() == 1
+    assert rel["status"].tolist() == [0, 0]
+    for k in rel:
+        assert torch.equal(rel[k], dbg[k]), k
 
 
 def test_far_offsets():
