@@ -17,12 +17,14 @@
 // (kS)ᵀe^b)(Tβ)ᵀ, and wᵀk for the new state; everything else (the gram matrix and the
 // inverse of the chunk after next, the output) runs beside them.
 //
-// Rounding.  The state, sums, decays, A and T are fp32.  As MMA operands S, kS and w
-// are split into two bf16 parts (2^-16 of a value is lost) and T into three (2^-24),
-// which keeps the state within about 3e-6 of itself however long the sequence (4e-6
-// with two parts of T, 1e-6 with three of w as well, whose products would take 256
-// more of a chunk's cycles on the tensor cores).  P is rounded to bf16 once, as the
-// output is.
+// Rounding.  The state, sums, decays, A and T are fp32.  As MMA operands S, kS, w and T
+// are split into three bf16 parts, which keep 24 bits, and those of their products are
+// taken that reach 2^-24.  What the output alone sees, which is bf16, goes by two parts
+// (2^-16): S for q·S, w and P for P·w.  Whenever the tensor cores add to a sum they cut it
+// towards zero, so small parts are added first: the state is then 1.5e-7 off after 4096 or
+// 16384 tokens (fp32 products 1.7e-7), 1.0e-6 with the large parts first.  With two parts
+// of S, kS and w and one of P it was 2.9e-6, the output off by 1.3 times its own
+// rounding, and 4×4096 tokens of 32 heads took 283 µs, not 321.
 //
 // Roles: warps 0-7 S (two per quarter of the rows), 8-11 and 12-15 T and P of every
 // other chunk, 16-19 the output, 20 loads, 21 MMAs, 22 and 23 decays and lengths.  Their loops
@@ -32,20 +34,20 @@
 //
 // What bounds it: the latency of a chunk's chain, since one CTA has an SM and a chunk waits
 // for the state of the one before.  4×4096 tokens of 32 heads (64 chunks for each of 128
-// CTAs) take 277 µs, 4.2 µs or some 8000 cycles a chunk, of which the tensor pipe is
-// busy a third (2700), and the four conversions between products (S, k·S, w, and S
-// again) with the signals around them take most of the rest; DRAM is at 15 %.  Without
-// the inverse's arithmetic it would take a tenth less, without the norms 3 %.
+// CTAs) take 321 µs, 4.9 µs or some 9300 cycles a chunk, of which the tensor pipe is
+// busy 4200, and the four conversions between products (S, k·S, w, and S
+// again) with the signals around them take most of the rest; DRAM is at 13 %.
 //
 // The MMA warp issues what the chain waits for first, and the products beside it into
-// its gaps: v's part of w while k·S is converted, q·S and the next gram matrix while w
-// is.  With the last two between UPD and the next S it took 306 µs.
+// its gaps: the small parts of v's share of w while k·S is converted, q·S and the next
+// gram matrix while w is.
 #include "block.cuh"
 #include "internal.h"
 #include "tc_pair.cuh"
 
 #include <algorithm>
 #include <atomic>
+#include <type_traits>
 
 namespace la {
 namespace {
@@ -58,7 +60,7 @@ using bf16 = __nv_bfloat16;
 constexpr int kC = 64;                        // tokens of a chunk
 constexpr int kThreads = 24 * 32;
 constexpr int kStateWarps = 8, kPrepWarp = 8, kOutWarp = 16, kLoadWarp = 20, kMmaWarp = 21, kFactorWarp = 22;
-constexpr int kKQ = 3, kVS = 2, kTok = 3, kPS = 3;   // stages: k and q tiles, v tiles, token factors, P
+constexpr int kKQ = 3, kVS = 1, kTok = 3, kPS = 2;   // stages: k and q tiles, v tiles, token factors, P
 constexpr int kOutRows = 16;                  // tokens that are stored at once
 constexpr int kSlab = kC * 128;               // 8 KB: 64 tokens × 64 features
 constexpr int kAPitch = 68;                   // floats of a row of A
@@ -81,7 +83,8 @@ struct alignas(16) TokenFactors {
 
 struct Bars {
   uint64_t kq_full[kKQ], kq_empty[kKQ], v_full[kVS], v_empty[kVS], f_ready[kTok];
-  uint64_t g_full[2], w_full[2];              // by the chunk's parity: each prep warpgroup sees every other one
+  // by the chunk's parity: each prep warpgroup sees every other one
+  uint64_t g_full[2], w_full[2], p_empty[2];
   uint64_t kq_clean, v_clean;                 // the last chunk's rows past the length are zero
   uint64_t g_empty, t_ready, s_ready, ks_full, ks_ready, qs_full, qs_read, w_ready,
       upd_full, pv_full, pv_read, done;
@@ -95,8 +98,8 @@ template <int DK> struct Cfg {
   static constexpr int kStage = 2 * kSlabs * kSlab;          // k and q: per 64 features, k's rows, then q's
   static constexpr int oV = kKQ * kStage;
   static constexpr int oT = oV + kVS * 2 * kSlab;            // Tβ in three parts
-  static constexpr int oP = oT + 3 * kSlab;
-  static constexpr int oOut = oP + kPS * kSlab;              // kOutRows tokens, by 64 columns
+  static constexpr int oP = oT + 3 * kSlab;                  // P in two parts
+  static constexpr int oOut = oP + kPS * 2 * kSlab;          // kOutRows tokens, by 64 columns
   static constexpr int oA = oOut + 2 * kOutRows * 128;
   static constexpr int oTok = oA + 2 * kC * kAPitch * 4;     // of each prep warpgroup
   static constexpr int oBars = oTok + kTok * (int)sizeof(TokenFactors);
@@ -105,6 +108,9 @@ template <int DK> struct Cfg {
   // tensor memory columns
   static constexpr uint32_t SH = 0, SL = DK / 2, UPD = DK, KS = 2 * DK, W = KS + kC, PV = W + kC,
                             G = PV + kC;
+  // third parts: of S and of k·S before the update takes their place, of w where S's
+  // second part was (q·S has been taken)
+  static constexpr uint32_t S3 = UPD, KS3 = UPD, W3 = SL;
   static_assert(G + kC <= 512, "tensor memory");
 };
 
@@ -258,20 +264,38 @@ __device__ __forceinline__ void role_load(const Ctx& x, const TcParams& p, const
   volatile int* abort = &x.bars->abort;
   const int hk = x.h / (p.Hv / p.Hk);
   const int vslabs = p.dv - x.tile * 128 > 64 ? 2 : 1;
-  for (int c = 0; c < x.chunks; ++c) {
-    const int s = c % kKQ, vs = c % kVS, t = x.t0 + c * kC;
-    if (c >= kKQ) LA_WAIT(kq_empty[s], c / kKQ - 1);
-    if (lane == 0) {
-      uint8_t* to = x.sm + s * F::kStage;
-      mbar_arrive_expect_tx(&x.bars->kq_full[s], F::kStage);
+  // the rows past the length may hold anything: zeros, so that they add nothing
+  const int last = x.live - (x.chunks - 1) * kC;
+  auto clear = [&](uint8_t* slab) {
+    for (int i = last * 8 + lane; i < kC * 8; i += 32)
+      *reinterpret_cast<uint4*>(slab + i * 16) = make_uint4(0, 0, 0, 0);
+  };
+  // k and q a chunk ahead of v, whose one stage is given back in the middle of a chunk
+#pragma unroll 1
+  for (int g = 0; g <= x.chunks; ++g) {
+    if (g < x.chunks) {
+      const int s = g % kKQ, t = x.t0 + g * kC;
+      if (g >= kKQ) LA_WAIT(kq_empty[s], g / kKQ - 1);
+      if (lane == 0) {
+        uint8_t* to = x.sm + s * F::kStage;
+        mbar_arrive_expect_tx(&x.bars->kq_full[s], F::kStage);
 #pragma unroll
-      for (int i = 0; i < F::kSlabs; ++i) {
-        tma_load_4d(to + i * 2 * kSlab, mk, &x.bars->kq_full[s], i * 64, hk * p.k_h, t, x.b * p.k_b);
-        tma_load_4d(to + i * 2 * kSlab + kSlab, mq, &x.bars->kq_full[s], i * 64, hk * p.q_h, t, x.b * p.q_b);
+        for (int i = 0; i < F::kSlabs; ++i) {
+          tma_load_4d(to + i * 2 * kSlab, mk, &x.bars->kq_full[s], i * 64, hk * p.k_h, t, x.b * p.k_b);
+          tma_load_4d(to + i * 2 * kSlab + kSlab, mq, &x.bars->kq_full[s], i * 64, hk * p.q_h, t, x.b * p.q_b);
+        }
+        x.bars->kq_issued = g + 1;
+      }
+      if (x.partial && g == x.chunks - 1) {   // (its gram matrix comes before its v)
+        LA_WAIT(kq_full[s], g / kKQ);
+        for (int i = 0; i < 2 * F::kSlabs; ++i) clear(x.sm + s * F::kStage + i * kSlab);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&x.bars->kq_clean);
       }
     }
-    if (lane == 0) x.bars->kq_issued = c + 1;
-    if (SUMMARY && x.identity) continue;
+    const int c = g - 1, vs = c % kVS, t = x.t0 + c * kC;
+    if (c < 0 || (SUMMARY && x.identity)) continue;
     if (c >= kVS) LA_WAIT(v_empty[vs], c / kVS - 1);
     if (lane == 0) {
       uint8_t* to = x.sm + F::oV + vs * 2 * kSlab;
@@ -281,19 +305,8 @@ __device__ __forceinline__ void role_load(const Ctx& x, const TcParams& p, const
     }
     if (lane == 0) x.bars->v_issued = c + 1;
   }
-  // the rows past the length may hold anything: zeros, so that they add nothing
-  if (!x.partial) return;
-  const int c = x.chunks - 1, r0 = x.live - c * kC;
-  auto clear = [&](uint8_t* slab) {
-    for (int i = r0 * 8 + lane; i < kC * 8; i += 32)
-      *reinterpret_cast<uint4*>(slab + i * 16) = make_uint4(0, 0, 0, 0);
-  };
-  LA_WAIT(kq_full[c % kKQ], c / kKQ);
-  for (int i = 0; i < 2 * F::kSlabs; ++i) clear(x.sm + c % kKQ * F::kStage + i * kSlab);
-  fence_proxy_async_smem();
-  __syncwarp();
-  if (lane == 0) mbar_arrive(&x.bars->kq_clean);
-  if (SUMMARY && x.identity) return;
+  if (!x.partial || (SUMMARY && x.identity)) return;
+  const int c = x.chunks - 1;
   LA_WAIT(v_full[c % kVS], c / kVS);
   for (int i = 0; i < vslabs; ++i) clear(x.sm + F::oV + (c % kVS * 2 + i) * kSlab);
   fence_proxy_async_smem();
@@ -347,13 +360,17 @@ __device__ __forceinline__ void role_mma(const Ctx& x, const TcParams& p) {
   const Operand T(base + F::oT, 16);
   // K-step k of a tile with 64 features per slab
   auto kstep = [](int k) { return (uint32_t)((k >> 2) * 2 * kSlab + (k & 3) * 32); };
-  // S's hi parts, then its lo parts, with k (at 0) or q
-  auto of_state = [&](uint32_t to, const Operand& b, uint32_t at) {
-    issue_ts<false>(to, tmem + F::SH, b, at, id_nn);
+  // S's second and first parts with k (at 0) or q; the second on top of the third
+  auto of_state = [&](auto acc, uint32_t to, const Operand& b, uint32_t at) {
+    issue_ts<decltype(acc)::value>(to, tmem + F::SL, b, at, id_nn);
 #pragma unroll
-    for (int i = 1; i < 2 * KD; ++i) issue_ts<true>(to, tmem + F::SH + i * 8, b, at + kstep(i % KD), id_nn);
+    for (int i = 1; i < KD; ++i) issue_ts<true>(to, tmem + F::SL + i * 8, b, at + kstep(i), id_nn);
+#pragma unroll
+    for (int i = 0; i < KD; ++i) issue_ts<true>(to, tmem + F::SH + i * 8, b, at + kstep(i), id_nn);
   };
-  // K-step k of (kS)ᵀ or wᵀ: 16 tokens' hi parts, then their lo parts
+  // S's third part is in two halves, each where its warps have read the update
+  auto third = [](int k) { return (uint32_t)(k / (KD / 2) * (DK / 2) + k % (KD / 2) * 8); };
+  // K-step k of (kS)ᵀ or wᵀ: 16 tokens' first parts, then their second parts
   auto tokens = [](int k) { return (uint32_t)(k * 16); };
 #pragma unroll 1
   for (int c = -2; c < x.chunks; ++c) {
@@ -364,11 +381,14 @@ __device__ __forceinline__ void role_mma(const Ctx& x, const TcParams& p) {
       LA_WAIT(s_ready, c);
       tc_fence_after();
       if (lead) {
-        of_state(tmem + F::KS, K, 0);
+        issue_ts<false>(tmem + F::KS, tmem + F::S3, K, 0, id_nn);
+#pragma unroll
+        for (int i = 1; i < KD; ++i) issue_ts<true>(tmem + F::KS, tmem + F::S3 + third(i), K, kstep(i), id_nn);
+        of_state(std::true_type(), tmem + F::KS, K, 0);
         mma_commit(&bars->ks_full);
       }
       __syncwarp();
-      // wᵀ = vᵀ (Tβ)ᵀ, whose columns (P w)ᵀ has read, while (kS)ᵀ is made an operand
+      // the small parts of wᵀ = vᵀ (Tβ)ᵀ, whose columns (P w)ᵀ has read, while (kS)ᵀ is made an operand
       LA_WAIT(t_ready, c);
       if (!(SUMMARY && x.identity)) {
         LA_WAIT(v_full[c % kVS], c / kVS);
@@ -378,23 +398,28 @@ __device__ __forceinline__ void role_mma(const Ctx& x, const TcParams& p) {
       tc_fence_after();
       if (lead) {
         const Operand V(base + F::oV + c % kVS * 2 * kSlab, kSlab);
-        issue_ss<false>(tmem + F::W, V, 0, T, 0, id_v);
+        issue_ss<false>(tmem + F::W, V, 0, T, 2 * kSlab, id_v);
 #pragma unroll
-        for (int i = 1; i < 3 * KC; ++i)
-          issue_ss<true>(tmem + F::W, V, i % KC * 2048, T, i / KC * kSlab + i % KC * 32, id_v);
-        mma_commit(&bars->v_empty[c % kVS]);
+        for (int i = 1; i < 2 * KC; ++i)
+          issue_ss<true>(tmem + F::W, V, i % KC * 2048, T, (2 - i / KC) * kSlab + i % KC * 32, id_v);
       }
       __syncwarp();
-      // wᵀ −= (e^b kS)ᵀ (Tβ)ᵀ: hi·hi, hi·mid, lo·hi
+      // wᵀ −= (e^b kS)ᵀ (Tβ)ᵀ, of the parts whose products reach 2^-24, and v's large one
       LA_WAIT(ks_ready, c);
       tc_fence_after();
       if (lead) {
+        const Operand V(base + F::oV + c % kVS * 2 * kSlab, kSlab);
 #pragma unroll
-        for (int part = 0; part < 3; ++part)
+        for (int sum = 2; sum >= 0; --sum)
 #pragma unroll
-          for (int k = 0; k < KC; ++k)
-            issue_ts<true>(tmem + F::W, tmem + F::KS + tokens(k) + (part == 2 ? 8 : 0), T,
-                           (part == 1 ? kSlab : 0) + k * 32, id_nn);
+          for (int a = sum; a >= 0; --a)
+#pragma unroll
+            for (int k = 0; k < KC; ++k)
+              issue_ts<true>(tmem + F::W, tmem + (a < 2 ? F::KS + tokens(k) + a * 8 : F::KS3 + k * 8), T,
+                             (sum - a) * kSlab + k * 32, id_nn);
+#pragma unroll
+        for (int k = 0; k < KC; ++k) issue_ss<true>(tmem + F::W, V, k * 2048, T, k * 32, id_v);
+        mma_commit(&bars->v_empty[c % kVS]);
         mma_commit(&bars->w_full[c & 1]);
       }
       __syncwarp();
@@ -403,7 +428,7 @@ __device__ __forceinline__ void role_mma(const Ctx& x, const TcParams& p) {
         if (c >= 1) LA_WAIT(pv_read, c - 1);
         tc_fence_after();
         if (lead) {
-          of_state(tmem + F::PV, K, kSlab);
+          of_state(std::false_type(), tmem + F::PV, K, kSlab);
           mma_commit(&bars->qs_full);
         }
         __syncwarp();
@@ -431,10 +456,12 @@ __device__ __forceinline__ void role_mma(const Ctx& x, const TcParams& p) {
       tc_fence_after();
       if (lead) {
         const Operand Kt(base + c % kKQ * F::kStage, 2 * kSlab);
-        issue_ts<false>(tmem + F::UPD, tmem + F::KS, Kt, 0, id_upd);
+        issue_ts<false>(tmem + F::UPD, tmem + F::W3, Kt, 0, id_upd);
 #pragma unroll
-        for (int i = 1; i < 2 * KC; ++i)
-          issue_ts<true>(tmem + F::UPD, tmem + F::KS + tokens(i % KC) + i / KC * 8, Kt, i % KC * 2048, id_upd);
+        for (int k = 1; k < KC; ++k) issue_ts<true>(tmem + F::UPD, tmem + F::W3 + k * 8, Kt, k * 2048, id_upd);
+#pragma unroll
+        for (int i = 0; i < 2 * KC; ++i)
+          issue_ts<true>(tmem + F::UPD, tmem + F::KS + tokens(i % KC) + (1 - i / KC) * 8, Kt, i % KC * 2048, id_upd);
         mma_commit(&bars->upd_full);
         if (SUMMARY) mma_commit(&bars->kq_empty[c % kKQ]);
       }
@@ -444,11 +471,14 @@ __device__ __forceinline__ void role_mma(const Ctx& x, const TcParams& p) {
         LA_WAIT(qs_read, c);
         tc_fence_after();
         if (lead) {
-          const Operand P(base + F::oP + c % kPS * kSlab, 16);
+          // hi·lo, lo·hi, hi·hi
+          const Operand P(base + F::oP + c % kPS * 2 * kSlab, 16);
 #pragma unroll
-          for (int i = 0; i < 2 * KC; ++i)
-            issue_ts<true>(tmem + F::PV, tmem + F::W + tokens(i % KC) + i / KC * 8, P, i % KC * 32, id_nn);
+          for (int i = 0; i < 3 * KC; ++i)
+            issue_ts<true>(tmem + F::PV, tmem + F::W + tokens(i % KC) + (i / KC == 1 ? 8 : 0), P,
+                           (i < KC ? kSlab : 0) + i % KC * 32, id_nn);
           mma_commit(&bars->pv_full);
+          mma_commit(&bars->p_empty[c & 1]);
           mma_commit(&bars->kq_empty[c % kKQ]);   // and the chunk's factors
         }
         __syncwarp();
@@ -503,11 +533,12 @@ __device__ __forceinline__ void role_state(const Ctx& x, const TcParams& p, int 
     // S as the next products' operand
 #pragma unroll
     for (int j = 0; j < kCols; j += 16) {
-      uint32_t hi[8], lo[8];
+      uint32_t hi[8], mid[8], lo[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) split2(S[j / 2 + i], hi[i], lo[i]);
+      for (int i = 0; i < 8; ++i) split3(S[j / 2 + i], hi[i], mid[i], lo[i]);
       tmem_st8(at + F::SH + (k0 + j) / 2, hi);
-      tmem_st8(at + F::SL + (k0 + j) / 2, lo);
+      tmem_st8(at + F::SL + (k0 + j) / 2, mid);
+      tmem_st8(at + F::S3 + k0 + j / 2, lo);
     }
     tmem_st_wait();
     tc_fence_before();
@@ -515,7 +546,7 @@ __device__ __forceinline__ void role_state(const Ctx& x, const TcParams& p, int 
     if (lane == 0) mbar_arrive(&bars->s_ready);
     const TokenFactors& tok = x.tok[c % kTok];   // overwritten after the chunk's last product
     LA_WAIT(f_ready[c % kTok], c / kTok);
-    // (kS)ᵀ, then wᵀ, times a factor of each token as operands in two parts, 16 tokens at a time
+    // (kS)ᵀ, then wᵀ, times a factor of each token as operands in three parts, 16 tokens at a time
     const f32x2 carry = pack2(tok.carry, tok.carry);
 #pragma unroll 1
     for (int of_w = 0; of_w < 2; ++of_w) {
@@ -524,23 +555,26 @@ __device__ __forceinline__ void role_state(const Ctx& x, const TcParams& p, int 
       const float* factors = of_w ? tok.left : tok.ks;
 #pragma unroll 1
       for (int t = half * 32; t < half * 32 + 32; t += 16) {
-        uint32_t r[16], hi[8], lo[8];
+        uint32_t r[16], hi[8], mid[8], lo[8];
         tmem_ld16(at + (of_w ? F::W : F::KS) + t, r);
         tmem_ld_wait();
 #pragma unroll
         for (int i = 0; i < 8; i += 2) {
           const ulonglong2 f = *reinterpret_cast<const ulonglong2*>(factors + t + 2 * i);
-          split2(mul2(pair_of(r, 2 * i), f.x), hi[i], lo[i]);
-          split2(mul2(pair_of(r, 2 * i + 2), f.y), hi[i + 1], lo[i + 1]);
+          split3(mul2(pair_of(r, 2 * i), f.x), hi[i], mid[i], lo[i]);
+          split3(mul2(pair_of(r, 2 * i + 2), f.y), hi[i + 1], mid[i + 1], lo[i + 1]);
         }
         tmem_st8(at + F::KS + t, hi);
-        tmem_st8(at + F::KS + t + 8, lo);
+        tmem_st8(at + F::KS + t + 8, mid);
         if (!SUMMARY && of_w) {   // for the output
 #pragma unroll
-          for (int i = 0; i < 8; ++i) split2(pair_of(r, 2 * i), hi[i], lo[i]);
+          for (int i = 0; i < 8; ++i) split2(pair_of(r, 2 * i), hi[i], mid[i]);
           tmem_st8(at + F::W + t, hi);
-          tmem_st8(at + F::W + t + 8, lo);
+          tmem_st8(at + F::W + t + 8, mid);
+          LA_WAIT(qs_full, c);    // (complete by now: q·S follows w on the tensor cores)
+          tc_fence_after();
         }
+        tmem_st8(at + (of_w ? F::W3 : F::KS3) + t / 2, lo);
       }
       tmem_st_wait();
       tc_fence_before();
@@ -852,11 +886,11 @@ __device__ __forceinline__ void role_prep(const Ctx& x, const TcParams& p, int w
     const float bx = tok.bx[row], by = tok.by[row];
     const float factor = keys ? tok.a[row] : tok.q[row];
     const int upto = row - keys;      // A below the diagonal, P with it
-    // (the products before chunk c's gram matrix have ended with it, (P w)ᵀ of c − 3 among them)
-    const uint32_t P = smem_u32(x.sm + F::oP + c % kPS * kSlab);
+    const uint32_t P = smem_u32(x.sm + F::oP + c % kPS * 2 * kSlab);
     named_bar_sync(bar, 128);    // the last chunk's T has been read from A
     // this row of A, or of P, 16 columns at a time
     LA_GO_ON(g_full[c & 1], c / 2);
+    if (!SUMMARY && !keys && c >= kPS) LA_GO_ON(p_empty[c & 1], c / kPS - 1);
     tc_fence_after();
     const float far = factor * tok.far[row];
     const f32x2 f2 = pack2(factor, factor), bx2 = pack2(bx, bx), by2 = pack2(by, by), minus = pack2(-1.f, -1.f);
@@ -896,11 +930,15 @@ __device__ __forceinline__ void role_prep(const Ctx& x, const TcParams& p, int w
         float4* to = reinterpret_cast<float4*>(A + row * kAPitch + j0);
 #pragma unroll
         for (int j = 0; j < 4; ++j) to[j] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
-      } else {
+      } else if (!SUMMARY) {
 #pragma unroll
         for (int j = 0; j < 16; j += 8) {
-          const float w[8] = {v[j], v[j + 1], v[j + 2], v[j + 3], v[j + 4], v[j + 5], v[j + 6], v[j + 7]};
-          if (!SUMMARY) sts128(P + sw_chunk(kC, row, 0, (j0 + j) / 8), pack8(w));
+          uint32_t hi[4], lo[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) split2(pack2(v[j + 2 * i], v[j + 2 * i + 1]), hi[i], lo[i]);
+          const uint32_t to = P + sw_chunk(kC, row, 0, (j0 + j) / 8);
+          sts128(to, make_uint4(hi[0], hi[1], hi[2], hi[3]));
+          sts128(to + kSlab, make_uint4(lo[0], lo[1], lo[2], lo[3]));
         }
       }
     }
@@ -972,8 +1010,8 @@ chunk_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUt
   if (threadIdx.x == 0) {
     for (int i = 0; i < kKQ; ++i) mbar_init(&bars->kq_full[i], 1), mbar_init(&bars->kq_empty[i], 1);
     for (int i = 0; i < kVS; ++i) mbar_init(&bars->v_full[i], 1), mbar_init(&bars->v_empty[i], 1);
-    for (uint64_t* b : {&bars->kq_clean, &bars->v_clean, &bars->g_full[0], &bars->g_full[1], &bars->ks_full,
-                        &bars->qs_full, &bars->w_full[0], &bars->w_full[1], &bars->upd_full, &bars->pv_full, &bars->done})
+    for (uint64_t* b : {&bars->kq_clean, &bars->v_clean, &bars->g_full[0], &bars->g_full[1], &bars->p_empty[0],
+                        &bars->p_empty[1], &bars->ks_full, &bars->qs_full, &bars->w_full[0], &bars->w_full[1], &bars->upd_full, &bars->pv_full, &bars->done})
       mbar_init(b, 1);
     for (int i = 0; i < kTok; ++i) mbar_init(&bars->f_ready[i], 2);
     for (uint64_t* b : {&bars->g_empty, &bars->t_ready, &bars->qs_read, &bars->pv_read}) mbar_init(b, 4);
