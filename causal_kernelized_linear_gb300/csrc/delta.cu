@@ -21,6 +21,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <type_traits>
 
 namespace la {
 namespace {
@@ -69,13 +70,17 @@ __device__ __forceinline__ float gate_value(const Rows& r, bool f32, int64_t at)
 }
 
 // α and β of a token.  A step of zero leaves the state alone whatever the rate.
-__device__ __forceinline__ float2 gates(const DeltaParams& p, int64_t b, int64_t t, int h) {
+struct Gates {
+  Decay alpha;
+  float beta;
+};
+__device__ __forceinline__ Gates gates(const DeltaParams& p, int64_t b, int64_t t, int h) {
   float d = gate_value(p.dt, p.gates_f32, b * p.dt.sb + t * p.dt.sn + h);
   if (p.dt_bias) d += p.dt_bias[h];
   if (p.softplus) d = softplus(d);
   float be = gate_value(p.beta, p.gates_f32, b * p.beta.sb + t * p.beta.sn + h);
   if (p.sigmoid) be = 1.f / (1.f + expf(-be));
-  return make_float2(d == 0.f ? 1.f : expf(d * p.a[h]), be);
+  return {decay_of(d == 0.f ? 0.f : d * p.a[h]), be};
 }
 
 // Sums over a column's P lanes, of four columns: lane i gets column
@@ -191,10 +196,16 @@ __global__ void __launch_bounds__(kThreads) recurrent_kernel(const DeltaParams p
   };
   if (live > 0) load(even, 0);
   if (live > 1) load(odd, 1);
-  float2 g = {1.f, 0.f};
+  Gates g = {{1.f, 0.f}, 0.f};   // of 32 tokens, one to a lane
+  uint32_t near = 0;             // those whose α is near 1
   auto walk = [&](Token& at, int t) {
-    if (t % 32 == 0) g = t + lane < live ? gates(p, b, t0 + t + lane, h) : make_float2(1.f, 0.f);
-    const float alpha = __shfl_sync(kAll, g.x, t % 32), beta = __shfl_sync(kAll, g.y, t % 32);
+    if (t % 32 == 0) {
+      if (t + lane < live) g = gates(p, b, t0 + t + lane, h);
+      near = __ballot_sync(kAll, g.alpha.keep != 0.f);
+    }
+    const bool keep = near >> t % 32 & 1;
+    const Decay alpha{keep ? 1.f : 0.f, __shfl_sync(kAll, g.alpha.more, t % 32)};
+    const float beta = __shfl_sync(kAll, g.beta, t % 32);
     f32x2 q[2 * R], k[2 * R];
 #pragma unroll
     for (int i = 0; i < R; ++i) {
@@ -225,17 +236,21 @@ __global__ void __launch_bounds__(kThreads) recurrent_kernel(const DeltaParams p
     }
     const float qk = sum_lanes<P>(both(qk2));
     const float ksum = sum_columns<P>(ks, lane), qsum = sum_columns<P>(qs, lane);
-    const float w = rk * (beta * (v - alpha * (rk * ksum)));
+    const float w = rk * (beta * (v - decayed(alpha, rk * ksum)));
     float wc[4];
     spread_columns(w, lane, wc);
-    const f32x2 al = pack2(alpha, alpha);
+    const f32x2 more = pack2(alpha.more, alpha.more);
+    auto update = [&](auto near_one) {
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      const f32x2 w2 = pack2(wc[c], wc[c]);
+      for (int c = 0; c < 4; ++c) {
+        const f32x2 w2 = pack2(wc[c], wc[c]);
 #pragma unroll
-      for (int i = 0; i < 2 * R; ++i) S[c][i] = fma2(k[i], w2, mul2(al, S[c][i]));
-    }
-    if (!SUMMARY && in && part < 4) op[t * p.out.sn] = from_f32<T>(rq * (alpha * qsum + qk * w));
+        for (int i = 0; i < 2 * R; ++i)
+          S[c][i] = fma2(k[i], w2, decltype(near_one)::value ? fma2(more, S[c][i], S[c][i]) : mul2(more, S[c][i]));
+      }
+    };
+    if (keep) update(std::true_type()); else update(std::false_type());   // (the same for the whole warp)
+    if (!SUMMARY && in && part < 4) op[t * p.out.sn] = from_f32<T>(rq * decayed(alpha, qsum, qk * w));
   };
 #pragma unroll 1
   for (int t = 0; t < live; t += 2) {
@@ -292,7 +307,7 @@ __global__ void __launch_bounds__(kStepThreads, RPT > 16 ? 1 : 2) step_kernel(co
   const T* kp = static_cast<const T*>(p.k.data) + b * p.k.sb + (int64_t)hk * p.k.sh;
   const T* qp = static_cast<const T*>(p.q.data) + b * p.q.sb + (int64_t)hk * p.q.sh;
   const float ke = t < p.dk ? to_f32(kp[t]) : 0.f, qe = t < p.dk ? to_f32(qp[t]) : 0.f;
-  const float2 g = gates(p, b, 0, h);
+  const Gates g = gates(p, b, 0, h);
   Raw4<T> vr;
   if (in) vr.load(static_cast<const T*>(p.v.data) + b * p.v.sb + (int64_t)h * p.v.sh + col);
   if (t < kRows) ks[t] = ke, qs[t] = qe;
@@ -330,19 +345,19 @@ __global__ void __launch_bounds__(kStepThreads, RPT > 16 ? 1 : 2) step_kernel(co
   unpack2(vr.lo(), v[0], v[1]);
   unpack2(vr.hi(), v[2], v[3]);
 #pragma unroll
-  for (int j = 0; j < 4; ++j) w[j] = rk * (g.y * (v[j] - g.x * (rk * ksum[j])));
+  for (int j = 0; j < 4; ++j) w[j] = rk * (g.beta * (v[j] - decayed(g.alpha, rk * ksum[j])));
 #pragma unroll
   for (int i = 0; i < RPT; ++i) {
     const int r = i * RG + rg;
     const float k = ks[r];
-    const float4 n = make_float4(fmaf(k, w[0], g.x * S[i].x), fmaf(k, w[1], g.x * S[i].y),
-                                 fmaf(k, w[2], g.x * S[i].z), fmaf(k, w[3], g.x * S[i].w));
+    const float4 n = make_float4(decayed(g.alpha, S[i].x, k * w[0]), decayed(g.alpha, S[i].y, k * w[1]),
+                                 decayed(g.alpha, S[i].z, k * w[2]), decayed(g.alpha, S[i].w, k * w[3]));
     if (in && r < p.dk) __stcs(reinterpret_cast<float4*>(to + (int64_t)r * p.dv), n);
   }
   if (rg == 0 && in) {
     T* op = static_cast<T*>(const_cast<void*>(p.out.data)) + b * p.out.sb + (int64_t)h * p.out.sh + col;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) op[j] = from_f32<T>(rq * (g.x * qsum[j] + s[2] * w[j]));
+    for (int j = 0; j < 4; ++j) op[j] = from_f32<T>(rq * decayed(g.alpha, qsum[j], s[2] * w[j]));
   }
 }
 

@@ -61,6 +61,7 @@ constexpr int kC = 64;                        // tokens of a chunk
 constexpr int kThreads = 24 * 32;
 constexpr int kStateWarps = 8, kPrepWarp = 8, kOutWarp = 16, kLoadWarp = 20, kMmaWarp = 21, kFactorWarp = 22;
 constexpr int kKQ = 3, kVS = 1, kTok = 3, kPS = 2;   // stages: k and q tiles, v tiles, token factors, P
+constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kOutRows = 16;                  // tokens that are stored at once
 constexpr int kSlab = kC * 128;               // 8 KB: 64 tokens × 64 features
 constexpr int kAPitch = 68;                   // floats of a row of A
@@ -78,7 +79,7 @@ struct alignas(16) TokenFactors {
   float ks[kC];         // −e^b r_k: a row of k·S
   float left[kC];       // r_k e^{b_C − b}: a row of w for the state
   float out[kC];        // scale r_q e^b: a row of q·S
-  float carry;          // e^{b_C}
+  Decay carry;          // e^{b_C}
 };
 
 struct Bars {
@@ -547,7 +548,7 @@ __device__ __forceinline__ void role_state(const Ctx& x, const TcParams& p, int 
     const TokenFactors& tok = x.tok[c % kTok];   // overwritten after the chunk's last product
     LA_WAIT(f_ready[c % kTok], c / kTok);
     // (kS)ᵀ, then wᵀ, times a factor of each token as operands in three parts, 16 tokens at a time
-    const f32x2 carry = pack2(tok.carry, tok.carry);
+    const f32x2 keep = pack2(tok.carry.keep, tok.carry.keep), more = pack2(tok.carry.more, tok.carry.more);
 #pragma unroll 1
     for (int of_w = 0; of_w < 2; ++of_w) {
       LA_WAIT_AT(of_w ? &bars->w_full[c & 1] : &bars->ks_full, of_w ? c / 2 : c);
@@ -589,7 +590,7 @@ __device__ __forceinline__ void role_state(const Ctx& x, const TcParams& p, int 
       tmem_ld32(at + F::UPD + k0 + j, r);
       tmem_ld_wait();
 #pragma unroll
-      for (int i = 0; i < 16; ++i) S[j / 2 + i] = fma2(S[j / 2 + i], carry, pair_of(r, 2 * i));
+      for (int i = 0; i < 16; ++i) S[j / 2 + i] = fma2(S[j / 2 + i], keep, fma2(S[j / 2 + i], more, pair_of(r, 2 * i)));
     }
   }
   if (!x.s_out) return;
@@ -862,7 +863,7 @@ __device__ __forceinline__ void role_factors(const Ctx& x, const TcParams& p, in
         tok.q[t] = p.scale * r[i];
       }
     }
-    if (keys && lane == 0) tok.carry = ex2_f32(last.x + last.y);
+    if (keys && lane == 0) tok.carry = decay_of(kLn2 * (last.x + last.y));
     __syncwarp();
     if (lane == 0) mbar_arrive(&x.bars->f_ready[c % kTok]);
   }

@@ -91,3 +91,50 @@ def test_single_writes_keep_24_bits(dtype, n, dk, writes):
     tol = (2.0 ** -19 + (n * 2.0 ** -24 if dtype == F32 else 0.0)) * terms + 1e-30
     off = (got.double() - S).abs()
     assert (off <= tol).all(), f"off by {(off / tol).max().item():.2f} of what is allowed"
+
+
+def _slow(n, x):
+    """How far n roundings of 2^-24 take a state that decays by e^x (x < 0) at each, relative to
+    it and in the root mean square of its elements, twice over.  They are as good as independent
+    but for runs in which what is taken off lies alike between two values of fp32: it is
+    |x|·2^23 to 2^24 steps, and shrinks by |x| of that from one time to the next.  An exponent's
+    roundings are 2^-23 of it, four of them."""
+    run = max(1.0, 1 / (x * x * 2.0 ** 23))
+    return 2 * 2.0 ** -24 * math.sqrt(n * run) + 4 * 2.0 ** -23 * -x * n
+
+
+SLOW = [(3000, 1e-3, -1.0), (30000, 1e-3, -0.1), (65536, 1e-3, -0.016)]
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=IDS)
+@pytest.mark.parametrize("hv,n,dt,a", [(1, *s) for s in SLOW] + [(1300, *SLOW[0])])   # in parts; undivided
+def test_slow_decays(dtype, hv, n, dt, a):
+    # nothing is written: the state is decayed n times by factors next to 1
+    d = 32
+    state = _randn(_gen(n), 1, hv, d, d)
+    zero = torch.zeros(1, n, 1, d, device=DEV, dtype=dtype)
+    step = torch.full((1, n, hv), dt, device=DEV)
+    _, got = la.gated_delta(zero, zero, zero.expand(1, n, hv, d), step, torch.full((hv,), a, device=DEV),
+                            torch.zeros_like(step), softplus=False, sigmoid=False, state=state, return_state=True)
+    x = step[0, 0, 0].double() * float(torch.tensor(a))
+    want = state.double() * torch.exp(n * x)
+    off = ((got.double() - want).norm() / want.norm()).item()
+    chunks = (n + 63) // 64
+    tol = _slow(chunks, 64 * x.item()) if dtype == BF16 else _slow(n, x.item())
+    assert off <= tol, f"off by {off:.2e} where {tol:.2e} is allowed"
+
+
+@pytest.mark.parametrize("dk", [64, 128, 256])
+def test_slow_decays_step_by_step(dk):
+    n, dt, a = SLOW[0]
+    state = _randn(_gen(n), 1, 2, dk, 64)
+    start = state.clone()
+    zero = torch.zeros(1, 2, dk, device=DEV)
+    step, rate = torch.full((1, 2), dt, device=DEV), torch.full((2,), a, device=DEV)
+    v, none = zero[..., :64].contiguous(), torch.zeros_like(step)
+    for _ in range(n):
+        la.gated_delta_step(state, zero, zero, v, step, rate, none, softplus=False, sigmoid=False)
+    x = step[0, 0].double() * a
+    want = start.double() * torch.exp(n * x)
+    off = ((state.double() - want).norm() / want.norm()).item()
+    assert off <= _slow(n, x.item()), f"off by {off:.2e}"
