@@ -134,9 +134,8 @@ def gated_delta(q, k, v, dt, a, beta, dt_bias=None, softplus=True, sigmoid=True,
     ``normalize`` takes q and k to unit length first; ``scale`` dk^-½ unless
     given; ``state`` [B, Hv, dk, dv] fp32 (None: zeros); ``lengths`` [B] int32:
     later tokens are not read, leave the state alone and give 0.  dk and dv
-    are multiples of 8, at most 256 and 512.  In bf16 from 16 tokens on, chunks of
-    64 tokens share a NaN or infinity of one of them.  Returns out [B, n, Hv, dv], or
-    (out, state after the prompt)."""
+    are multiples of 8, at most 256 and 512.  Returns out [B, n, Hv, dv], or (out,
+    state after the prompt)."""
     return (_ext or _load_ext()).gated_delta(q, k, v, dt, a, beta, dt_bias, softplus, sigmoid,
                                              normalize, scale, state, lengths, out, return_state,
                                              stream)

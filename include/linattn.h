@@ -522,8 +522,8 @@ typedef struct {
  * dk and dv are multiples of 8, dk ≤ 256, dv ≤ 512 (else LA_ERR_UNSUPPORTED).
  * States, sums, norms and decays are fp32.  Equal inputs give equal bits.
  * bf16 tokens with dk ≤ 128 go in chunks of 64 from n = 16 on, the states as near
- * as fp32 sums bring them: a NaN or infinity of a token is then seen by all of its
- * chunk's outputs, those of earlier tokens too, and by everything after it.
+ * as fp32 sums bring them.  A NaN or infinity of v reaches its column from its token
+ * on, of k, dt or beta all of the head from there on, of q its token's output.
  * Long sequences of few heads are divided: stream-ordered memory is taken for
  * the states of their parts (LA_ERR_OUT_OF_MEMORY where there is none).
  * Errors as la_linear.
