@@ -64,13 +64,15 @@ __host__ __device__ constexpr uint32_t idesc_of(uint32_t M, uint32_t N) {
   return F8 ? (1u << 4) | ((N >> 3) << 17) | ((M >> 4) << 24) : idesc_bf16_f32(M, N, false, false);
 }
 
-// The sums of 8-bit operands times the scales of their row and columns.
+// The sums of 8-bit operands times the scales of their row and columns, the column's
+// first: the product of two scales may be subnormal where the result is not.
 __device__ __forceinline__ float4 scales4(const float* ws) {
   return __ldg(reinterpret_cast<const float4*>(ws));
 }
 __device__ __forceinline__ void rescale8(float xs, const float4& lo, const float4& hi, float (&v)[8]) {
-  v[0] *= xs * lo.x, v[1] *= xs * lo.y, v[2] *= xs * lo.z, v[3] *= xs * lo.w;
-  v[4] *= xs * hi.x, v[5] *= xs * hi.y, v[6] *= xs * hi.z, v[7] *= xs * hi.w;
+  const float w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = v[i] * w[i] * xs;
 }
 
 // bias, activation and residual on 8 neighbouring columns of a row.

@@ -573,7 +573,7 @@ la_status la_rms_norm(const la_rows* x, const void* weight, int64_t group, float
 
 /*
  * la_linear_e4m3 — la_linear on 8-bit operands with scales:
- *   out[m,n] = act(x_scale[m]·weight_scale[n]·Σ_k x[m,k]·weight[n,k] + bias[n]) + residual[m,n]
+ *   out[m,n] = act(x_scale[m]·(weight_scale[n]·Σ_k x[m,k]·weight[n,k]) + bias[n]) + residual[m,n]
  *   x, weight       [1, M, K] and [1, N, K], LA_E4M3.
  *   x_scale         device fp32 [M];  weight_scale  device fp32 [N].
  *   bias, residual, out  as la_linear, bf16.
