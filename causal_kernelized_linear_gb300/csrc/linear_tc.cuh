@@ -75,15 +75,16 @@ __device__ __forceinline__ void rescale8(float xs, const float4& lo, const float
   for (int i = 0; i < 8; ++i) v[i] = v[i] * w[i] * xs;
 }
 
-// bias, activation and residual on 8 neighbouring columns of a row.
-template <int ACT>
-__device__ __forceinline__ void finish8(bool biased, const uint4& bias, bool added, const uint4& res, float (&v)[8]) {
-  if (biased) {
-    float b[8];
-    unpack<bf16>(bias, b);
+// bias, activation and residual on 8 neighbouring columns of a row: where they lie, or
+// as they have been fetched.
+__device__ __forceinline__ void add8(const uint4& a, float (&v)[8]) {
+  float b[8];
+  unpack<bf16>(a, b);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] += b[i];
-  }
+  for (int i = 0; i < 8; ++i) v[i] += b[i];
+}
+template <int ACT>
+__device__ __forceinline__ void activate8(float (&v)[8]) {
   if constexpr (ACT == LA_ACT_GELU) {
 #pragma unroll
     for (int i = 0; i < 8; i += 2) {
@@ -94,12 +95,18 @@ __device__ __forceinline__ void finish8(bool biased, const uint4& bias, bool add
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = activate<ACT>(v[i]);
   }
-  if (added) {
-    float r[8];
-    unpack<bf16>(res, r);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] += r[i];
-  }
+}
+template <int ACT>
+__device__ __forceinline__ void finish8(bool biased, const uint4& bias, bool added, const uint4& res, float (&v)[8]) {
+  if (biased) add8(bias, v);
+  activate8<ACT>(v);
+  if (added) add8(res, v);
+}
+template <int ACT>
+__device__ __forceinline__ void finish8(const bf16* bias, const bf16* res, float (&v)[8]) {
+  if (bias) add8(__ldg(reinterpret_cast<const uint4*>(bias)), v);
+  activate8<ACT>(v);
+  if (res) add8(*reinterpret_cast<const uint4*>(res), v);
 }
 
 // ------------------------------------------------------------------ many tokens
@@ -245,9 +252,11 @@ pair_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUte
       const int cols = min(BN / 2, p.N - n0);
       const bf16* res = p.residual && m < p.M ? p.residual + m * p.res_sn + n0 : nullptr;
       const float xs = F8 && m < p.M ? p.x_scale[m] : 0.f;
-      // what the sums meet is fetched before they are waited for, then 32 columns ahead:
-      // with loads where they are used, 16384×2048×8192 of e4m3 took 180 µs and not
-      // 163, with bias and residual 276 and not 209 (bf16 the same, 285 and 311)
+      // With e4m3 operands what the sums meet is fetched before they are waited for, then
+      // 32 columns ahead: with loads where they are used, 16384×2048×8192 took 180 µs and
+      // not 163, with bias and residual 276 and not 209.  bf16 has them where they are
+      // used: the same at that size (285 and 322), and 9.5 µs, not 11, for 777×128×4096
+      // with both, which is all epilogue.
       float4 ws[F8 ? 8 : 1];
       uint4 bias[4], added[4];
       auto fetch = [&](int c) {
@@ -259,7 +268,7 @@ pair_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUte
             if (res) added[j] = *reinterpret_cast<const uint4*>(res + c + 8 * j);
           }
       };
-      if (m0 < p.M) fetch(0);
+      if (F8 && m0 < p.M) fetch(0);
       if (!warp_wait(&bars->acc_full[buf], (n >> 1) & 1, p.status, abort)) break;
       tc_fence_after();
       if (m0 < p.M) {
@@ -271,21 +280,33 @@ pair_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUte
           tmem_ld_wait();
           if (lane == 0) tma_store_wait_read0();
           __syncwarp();
+          if constexpr (F8) {
 #pragma unroll
-          for (int h = 0; h < 8; h += 4) {
-            uint4 o[4];
+            for (int h = 0; h < 8; h += 4) {
+              uint4 o[4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
+              for (int j = 0; j < 4; ++j) {
+                float v[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[8 * (h + j) + i]);
+                rescale8(xs, ws[2 * j], ws[2 * j + 1], v);
+                finish8<ACT>(p.bias != nullptr, bias[j], res != nullptr, added[j], v);
+                o[j] = pack8(v);
+              }
+              fetch(c + 8 * h + 32);
+#pragma unroll
+              for (int j = 0; j < 4; ++j) sts128(sa + sw_chunk(32, lane, 0, h + j), o[j]);
+            }
+          } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
               float v[8];
 #pragma unroll
-              for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[8 * (h + j) + i]);
-              if constexpr (F8) rescale8(xs, ws[2 * j], ws[2 * j + 1], v);
-              finish8<ACT>(p.bias != nullptr, bias[j], res != nullptr, added[j], v);
-              o[j] = pack8(v);
+              for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[8 * j + i]);
+              const bool in = c + 8 * j < cols;
+              finish8<ACT>(p.bias && in ? p.bias + n0 + c + 8 * j : nullptr, res && in ? res + c + 8 * j : nullptr, v);
+              sts128(sa + sw_chunk(32, lane, 0, j), pack8(v));
             }
-            fetch(c + 8 * h + 32);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) sts128(sa + sw_chunk(32, lane, 0, h + j), o[j]);
           }
           fence_proxy_async_smem();
           __syncwarp();
@@ -479,10 +500,7 @@ few_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUten
       }
       const int64_t m = m0 + t;
       if constexpr (F8) rescale8(p.x_scale[m], scales4(p.w_scale + n), scales4(p.w_scale + n + 4), v);
-      uint4 bias{}, added{};
-      if (p.bias) bias = __ldg(reinterpret_cast<const uint4*>(p.bias + n));
-      if (p.residual) added = *reinterpret_cast<const uint4*>(p.residual + m * p.res_sn + n);
-      finish8<ACT>(p.bias != nullptr, bias, p.residual != nullptr, added, v);
+      finish8<ACT>(p.bias ? p.bias + n : nullptr, p.residual ? p.residual + m * p.res_sn + n : nullptr, v);
       if (LA_DCHECK(p.status, m < p.M && n + 8 <= p.N, 52))
         *reinterpret_cast<uint4*>(p.out + m * p.out_sn + n) = pack8(v);
     }
