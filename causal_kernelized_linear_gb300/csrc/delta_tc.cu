@@ -294,9 +294,10 @@ __device__ __forceinline__ void role_load(const Ctx& x, const TcParams& p, const
       if (g >= kKQ) LA_WAIT(kq_empty[s], g / kKQ - 1);
       if (lane == 0) {
         uint8_t* to = x.sm + s * F::kStage;
-        mbar_arrive_expect_tx(&x.bars->kq_full[s], F::kStage);
+        const bool ok = LA_DCHECK(p.status, t >= x.t0 && t < x.t0 + x.live && hk < p.Hk, 62);
+        mbar_arrive_expect_tx(&x.bars->kq_full[s], ok ? F::kStage : 0);
 #pragma unroll
-        for (int i = 0; i < F::kSlabs; ++i) {
+        for (int i = 0; ok && i < F::kSlabs; ++i) {
           tma_load_4d(to + i * 2 * kSlab, mk, &x.bars->kq_full[s], i * 64, hk * p.k_h, t, x.b * p.k_b);
           tma_load_4d(to + i * 2 * kSlab + kSlab, mq, &x.bars->kq_full[s], i * 64, hk * p.q_h, t, x.b * p.q_b);
         }
@@ -315,8 +316,9 @@ __device__ __forceinline__ void role_load(const Ctx& x, const TcParams& p, const
     if (c >= kVS) LA_WAIT(v_empty[vs], c / kVS - 1);
     if (lane == 0) {
       uint8_t* to = x.sm + F::oV + vs * 2 * kSlab;
-      mbar_arrive_expect_tx(&x.bars->v_full[vs], vslabs * kSlab);
-      for (int i = 0; i < vslabs; ++i)
+      const bool ok = LA_DCHECK(p.status, t >= x.t0 && t < x.t0 + x.live && x.tile * 128 + (vslabs - 1) * 64 < p.dv, 62);
+      mbar_arrive_expect_tx(&x.bars->v_full[vs], ok ? vslabs * kSlab : 0);
+      for (int i = 0; ok && i < vslabs; ++i)
         tma_load_4d(to + i * kSlab, mv, &x.bars->v_full[vs], x.tile * 128 + i * 64, x.h * p.v_h, t, x.b * p.v_b);
     }
     if (lane == 0) x.bars->v_issued = c + 1;
@@ -850,7 +852,7 @@ __device__ __forceinline__ void role_out(const Ctx& x, const TcParams& p, const 
         for (int i = 0; i < 2; ++i) {
           const int col = x.tile * 128 + i * 64;
           const int t = x.t0 + c * kC + j;
-          if (!stored && col < p.dv && t < p.n && LA_DCHECK(p.status, t >= 0, 61))
+          if (!stored && col < p.dv && t < p.n && LA_DCHECK(p.status, t >= x.t0 && min(t + kOutRows, p.n) <= x.t0 + x.end, 61))
             tma_store_4d(mo, stage + i * kOutRows * 128, col, x.h * p.o_h, t, x.b * p.o_b);
         }
         tma_store_commit();

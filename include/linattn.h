@@ -634,7 +634,8 @@ int la_debug_build(void);
  * rows, the aggregate slot, the entering-state slots), 21–26 the tcgen05
  * backward (item ranges of the loads, rows of the ∂q, ∂k, ∂v stores), 31–32
  * the non-causal readout, 41–42 the Performer forward, 51–52 la_linear's and
- * la_linear_e4m3's bf16 stores, 61 la_gated_delta's, 90 the self-test.
+ * la_linear_e4m3's bf16 stores, 61–62 la_gated_delta's stores (rows of
+ * the CTA's part) and loads (tokens that count), 90 the self-test.
  * Errors: LA_ERR_INVALID_ARG (site is NULL), LA_ERR_CUDA.
  */
 la_status la_get_last_device_check(la_stream stream, int* site);
