@@ -569,10 +569,11 @@ def _num_sms(num_sms):
 
 
 def selftest_linear_kernel(dtype, m, n, k, num_sms=None):
-    """la_selftest_linear_kernel: the name of the kernel that ``linear`` runs for
-    x [m, k] and weight [n, k] on a GPU with num_sms multiprocessors (default: the
-    current device's)."""
-    name = load().la_selftest_linear_kernel(_DT[dtype], m, n, k, _num_sms(num_sms))
+    """la_selftest_linear_kernel: the name of the kernel that ``linear`` (or, for
+    float8_e4m3fn, ``linear_e4m3``) runs for x [m, k] and weight [n, k] on a GPU with
+    num_sms multiprocessors (default: the current device's)."""
+    code = LA_E4M3 if dtype == torch.float8_e4m3fn else _DT[dtype]
+    name = load().la_selftest_linear_kernel(code, m, n, k, _num_sms(num_sms))
     if name is None:
         raise ValueError("sizes out of range")
     return name.decode()

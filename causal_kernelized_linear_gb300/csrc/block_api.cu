@@ -270,7 +270,7 @@ la_status la_selective_step(float* state, const la_rows* x, const la_rows* dt, c
 }
 
 const char* la_selftest_linear_kernel(la_dtype dtype, int64_t M, int64_t N, int64_t K, int num_sms) {
-  if ((dtype != LA_BF16 && dtype != LA_F32) || M < 1 || N < 1 || K < 1 || M > kMaxDim || N > kMaxDim ||
+  if ((dtype != LA_BF16 && dtype != LA_F32 && dtype != LA_E4M3) || M < 1 || N < 1 || K < 1 || M > kMaxDim || N > kMaxDim ||
       K > kMaxDim || num_sms < 1)
     return nullptr;
   LinearArgs a{};
@@ -279,7 +279,7 @@ const char* la_selftest_linear_kernel(la_dtype dtype, int64_t M, int64_t N, int6
   a.K = K;
   a.bf16 = dtype == LA_BF16;
   a.num_sms = num_sms;
-  return linear_kernel(a);
+  return dtype == LA_E4M3 ? tc_linear_e4m3_kernel(a) : linear_kernel(a);
 }
 
 const char* la_selftest_step_kernel(int64_t B, int64_t D, int states, int num_sms) {

@@ -374,6 +374,8 @@ struct LinearE4m3Args {
   const float* w_scale;     // [N]
 };
 cudaError_t tc_linear_e4m3(const LinearE4m3Args& a, cudaStream_t stream);
+// The name of its kernel, by M, N, K and num_sms alone.
+const char* tc_linear_e4m3_kernel(const LinearArgs& a);
 
 // Memory-bound recurrent decode step.
 cudaError_t decode_step(const DecodeArgs& a, cudaStream_t stream);

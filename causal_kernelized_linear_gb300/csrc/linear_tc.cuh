@@ -636,6 +636,11 @@ Choice choose(const LinearArgs& a, int kblocks) {
   return p256 == least ? kPair256 : kPair128;
 }
 
+template <bool F8> const char* kernel_name(const LinearArgs& a) {
+  static const char* const names[] = {"few16", "few32", "few64", "few128", "pair128", "pair256"};
+  return names[choose(a, kblocks_of<F8>(a))];
+}
+
 template <int ACT, bool F8>
 cudaError_t by_shape(const LinearArgs& a, const float* x_scale, const float* w_scale,
                      cudaStream_t s) {

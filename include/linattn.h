@@ -587,8 +587,8 @@ la_status la_linear_e4m3(const la_rows* x, const float* x_scale, const la_rows* 
 
 /*
  * la_selftest_linear_kernel, la_selftest_step_kernel — test hooks: the name of the
- * kernel that la_linear or la_selective_step would run for these sizes on a GPU
- * with num_sms multiprocessors ("few64", "pair256", "tile8x2", "rows8", "step4",
+ * kernel that la_linear (LA_E4M3: la_linear_e4m3) or la_selective_step would run
+ * for these sizes on a GPU with num_sms multiprocessors ("few64", "pair256", "tile8x2", "rows8", "step4",
  * …; a static string), or NULL for sizes out of range.  Host only: no device is
  * needed, nothing is queued.
  */
