@@ -133,7 +133,8 @@ def gated_delta(q, k, v, dt, a, beta, dt_bias=None, softplus=True, sigmoid=True,
     dt, beta [B, n, Hv] of the same type or fp32; a, dt_bias [Hv] fp32, a ≤ 0;
     ``normalize`` takes q and k to unit length first; ``scale`` dk^-½ unless
     given; ``state`` [B, Hv, dk, dv] fp32 (None: zeros); ``lengths`` [B] int32:
-    later tokens are not read, leave the state alone and give 0.  dk and dv
+    later tokens have no part in any result, leave the state alone and give 0
+    (up to 63 of them may be fetched).  dk and dv
     are multiples of 8, at most 256 and 512.  Returns out [B, n, Hv, dv], or (out,
     state after the prompt)."""
     return (_ext or _load_ext()).gated_delta(q, k, v, dt, a, beta, dt_bias, softplus, sigmoid,

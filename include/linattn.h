@@ -514,9 +514,11 @@ typedef struct {
  *   a          device fp32 [Hv], zero or negative (−∞ clears the state).
  *   dt_bias    device fp32 [Hv], or NULL.
  *   state_in   device fp32 [B, Hv, dk, dv] dense, or NULL for zeros.
- *   lengths    device [B] int32, or NULL for n: tokens t ≥ lengths[b] are not
- *              read, leave the state alone, and their outputs are 0 (values
- *              are taken into [0, n]).
+ *   lengths    device [B] int32, or NULL for n: tokens t ≥ lengths[b] have no
+ *              part in any result, leave the state alone, and their outputs
+ *              are 0 (values are taken into [0, n]).  Up to 63 of them may be
+ *              fetched all the same: their memory is to be valid and not
+ *              written while the call runs.
  *   state_out  device fp32 [B, Hv, dk, dv] dense, or NULL.  Must not overlap
  *              state_in.
  * dk and dv are multiples of 8, dk ≤ 256, dv ≤ 512 (else LA_ERR_UNSUPPORTED).
