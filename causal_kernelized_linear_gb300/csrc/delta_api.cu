@@ -289,10 +289,6 @@ la_status la_rms_norm(const la_rows* x, const void* weight, int64_t group, float
   a.eps = eps;
   a.bf16 = x->dtype == LA_BF16;
   a.quantize = quantize;
-  DeviceInfo di;
-  const la_status st = device_info(&di);
-  if (st != LA_OK) return st;
-  a.num_sms = di.num_sms;
   return launch_status(rms_norm(a, (cudaStream_t)stream));
 }
 

@@ -361,7 +361,6 @@ struct NormArgs {
   int D, group;
   float eps;
   bool bf16, quantize;
-  int num_sms;
 };
 // Whether a row of D features fits a CTA's registers.
 bool rms_norm_supported(int64_t D, bool bf16);
