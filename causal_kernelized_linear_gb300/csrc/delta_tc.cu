@@ -1328,19 +1328,19 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const float* state_i
 // Parts of a sequence: with few heads most SMs would have none, so each sequence is
 // walked twice, first for what every part makes of a state (one CTA more for each
 // part, and no output), then with the states that enter them.  By the µs of a chunk
-// (3.9, and 3.6 without the output), of joining two parts (4) and of two launches more:
-// 8 heads of 4096 tokens take 125 µs in 8 parts and 260 undivided, of 1024 tokens 76
-// in 4 and 72.
+// (5.1, and 4.3 without the output), of joining two parts (4.8) and of two launches more:
+// 8 heads of 4096 tokens take 123 µs in 8 parts, 180 in 4 and 329 undivided, of 1024
+// tokens 67, 69 and 89.
 int parts_of(const DeltaArgs& a, int tiles) {
   const int64_t heads = a.B * a.Hv, chunks = (a.n + kC - 1) / kC;
   auto rounds = [&](int64_t ctas) { return (double)((ctas + a.num_sms - 1) / a.num_sms); };
   int best = 1;
-  double least = rounds(heads * tiles) * chunks * 3.9;
+  double least = rounds(heads * tiles) * chunks * 5.1;
   for (int g = 2; g <= 64 && g * 4 <= chunks; ++g) {
     const int64_t part = (chunks + g - 1) / g;
     if ((chunks + part - 1) / part != g) continue;
-    const double t = rounds(heads * (g - 1) * (tiles + 1)) * part * 3.6 + rounds(heads * g * tiles) * part * 3.9 +
-                     28.0 + rounds(heads * ((a.dv + kJoinCols - 1) / kJoinCols)) * (g - 1) * 4.0;
+    const double t = rounds(heads * (g - 1) * (tiles + 1)) * part * 4.3 + rounds(heads * g * tiles) * part * 5.1 +
+                     15.0 + rounds(heads * ((a.dv + kJoinCols - 1) / kJoinCols)) * (g - 1) * 4.8;
     if (t < least) least = t, best = g;
   }
   return best;
