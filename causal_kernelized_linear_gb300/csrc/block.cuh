@@ -148,7 +148,7 @@ __device__ __forceinline__ int live_tokens(const int32_t* lengths, int64_t b, in
 
 // A factor α = e^x of a state that is applied again and again, as keep + more with a keep
 // of 0 or 1.  Near 1 it is 1 and what α lacks of it: rounded itself, α would be off by up to
-// 2^-25 the same way at every token (30000 times e^-0.0001 left the state 1.2e-3 off, now 2e-5).
+// 2^-25 the same way at every token (30000 times e^-0.0001 left the state 1.2e-3 off, now 1.2e-5).
 struct Decay {
   float keep, more;
 };

@@ -4,8 +4,8 @@
 // recurrent_kernel (several tokens).  The columns of S do not meet: a warp has a few of
 // them (16 or 8 for dk = 128) with all their rows, 16 or 8 rows by 4 columns to a lane, and
 // walks the tokens with S in registers, two tokens' q, k and v under way (4×2048 tokens of
-// 32 heads of 128 in fp32: 1.60 ms, 1.76 with one).  Bound by the latency of a token's
-// chain, 0.45 to 0.52 µs, while warps are few, and then by issue.  k·S and q·S of the
+// 32 heads of 128 in fp32: 1.61 ms).  Bound by the latency of a token's
+// chain, 0.49 to 0.58 µs, while warps are few, and then by issue.  k·S and q·S of the
 // state before the token are summed together over the P lanes that share a column; o_t = scale·(α q·S_{t−1} + (q·k) w_t)
 // needs no second pass over S, so the next token's sums wait for w_t alone.
 //
@@ -13,7 +13,7 @@
 // 128×128.  A CTA has 128 columns (or 64) of one head's S with all rows, in the
 // registers of 256 threads: warps read whole rows of 512 bytes, all loads of a thread
 // are issued before anything waits for one, and the sums over rows go through shared
-// memory once.  256×32 heads of 128×128: 161 µs = 6.7 TB/s, a copy's bandwidth.
+// memory once.  256×32 heads of 128×128: 165 µs = 6.5 TB/s, 0.98 of a copy's bandwidth.
 //
 // Everything is fp32.
 #include "block.cuh"
@@ -388,8 +388,8 @@ cudaError_t step(const DeltaArgs& a, const DeltaParams& p, cudaStream_t s) {
 // Parts of the sequences, and the µs that they are taken to need, with P lanes to a
 // column: a warp takes `token` µs for a token while no more than two share a scheduler,
 // and then as much longer as they are more.  Parts measured a seventh above that sum, or
-// more (333 tokens of 8 heads of 128 with 16 lanes: 92 µs in 8 parts, 153 undivided; 2×512 of
-// 16 heads with 8: 299 in 5 parts, 240 in 4, 271 undivided).
+// more (333 tokens of 8 heads of 128 with 16 lanes: 93 µs in 8 parts, 166 undivided; 2×512 of
+// 16 heads with 8: 314 in 5 parts, 249 in 4, 297 undivided).
 struct Plan {
   int parts;
   double us;
@@ -442,8 +442,8 @@ cudaError_t launch_recurrent(const DeltaArgs& a, DeltaParams p, int parts, cudaS
 template <typename T>
 cudaError_t by_keys(const DeltaArgs& a, const DeltaParams& p, cudaStream_t s) {
   // Sixteen rows to a lane; or eight, with twice the warps, where each of them has a
-  // scheduler to itself: 2×512 tokens of 16 heads of 128 (512 warps) in 235 µs against
-  // 271, 4×512 in 337 against 272.
+  // scheduler to itself: 2×512 tokens of 16 heads of 128 (512 warps) in 252 µs undivided
+  // against 297 (4×512, while a decay was one factor, in 337 against 272).
   const int lanes = a.dk <= 64 ? 4 : a.dk <= 128 ? 8 : 16;
   const Plan wide = plan_for(a, lanes, 0.6);
   if (a.dk <= 128 && a.B * a.Hv * ((a.dv * 2 * lanes + 127) / 128) <= 4 * (int64_t)a.num_sms) {

@@ -509,8 +509,9 @@ typedef struct {
  * With normalize, q_t and k_t are divided by sqrt(Σ x² + 1e-6) first.
  *   q, k       [B, n, Hk, dk], bf16 or fp32 (one dtype for all la_heads here).
  *   v, out     [B, n, Hv, dv]; Hv is a multiple of Hk.  out is written in full.
- *   dt, beta   [B, n, Hv] (la_rows), both of q's dtype or both fp32; here
- *              strides and data need only be aligned to an element.
+ *   dt, beta   [B, n, Hv] (la_rows: the heads of a token lie next to one
+ *              another), both of q's dtype or both fp32; here strides and data
+ *              need only be aligned to an element.
  *   a          device fp32 [Hv], zero or negative (−∞ clears the state).
  *   dt_bias    device fp32 [Hv], or NULL.
  *   state_in   device fp32 [B, Hv, dk, dv] dense, or NULL for zeros.
